@@ -1,7 +1,9 @@
 """TIDE layout-aware FSDP2 collectives, single-GPU hot path for GB300 (sm_103a).
 
 ``tide_rs_reduce`` and ``tide_ag_place`` run in hand-written CUDA kernels in
-``libtide.so`` (C ABI: include/tide.h); this package only binds them.
+``libtide.so`` (C ABI: include/tide.h); this package only binds them.  So do the
+training block's operators that run between the two (include/tide_ops.h): RMS
+norm, linear layer, 8-bit activation checkpoints.
 """
 
 from .tide import (  # noqa: F401
@@ -17,3 +19,23 @@ from .tide import (  # noqa: F401
     TIDE_OPT_RD_EXCHANGE, TIDE_OPT_AG_TRANSPORT,
     TIDE_SUM_LANDING, TIDE_SUM_RELATIVE, TIDE_AG_SM, TIDE_AG_COPY_ENGINES, TIDE_AG_BULK,
 )
+
+# The operators take torch tensors; the collectives do not need torch, so it is
+# imported when the first operator is asked for.
+_OPS = frozenset((
+    "Checkpoint8", "TIDE_CKPT_BLOCK", "tide_checkpoint_store", "tide_checkpoint_load", "tide_rms_norm",
+    "tide_rms_norm_backward", "tide_linear", "tide_linear_grad_input", "tide_linear_grad_weight",
+    "TIDE_ACT_NONE", "TIDE_ACT_RELU", "TIDE_ACT_GELU", "TIDE_ACT_GELU_ERF", "TIDE_ACT_SILU",
+))
+
+
+def __getattr__(name):
+    if name not in _OPS:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import ops
+    globals().update({n: getattr(ops, n) for n in _OPS})
+    return globals()[name]
+
+
+def __dir__():
+    return sorted(set(globals()) | _OPS)

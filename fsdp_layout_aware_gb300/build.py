@@ -1,14 +1,16 @@
 """In-tree build of the CUDA libraries for sm_103a (GB300).
 
 ``build_all()`` compiles, with nvcc and in parallel:
-  * ``fsdp_layout_aware_gb300/libtide.so``  -- the C-ABI library (include/tide.h)
+  * ``fsdp_layout_aware_gb300/libtide.so``  -- the C-ABI library (include/tide.h,
+                                               include/tide_ops.h)
   * ``synth/libtide_synth.so``              -- the seeded input generator's
                                                device twin (tests and bench only)
 and, on request (``build_lib("tide_checked")``, ``--checked``):
   * ``fsdp_layout_aware_gb300/libtide_checked.so`` -- the same library compiled
-                                               with TIDE_CHECKED: every kernel
-                                               store checked against its work
-                                               item (check.cuh; tests only)
+                                               with TIDE_CHECKED: every store
+                                               of the collectives' kernels checked
+                                               against its work item (check.cuh;
+                                               tests only)
 A library is rebuilt only when its sources, headers or flags changed (a
 content hash is kept next to the objects in ``_build/``).
 """
@@ -38,9 +40,11 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]
 
 TIDE_SRCS = [os.path.join(HERE, "csrc", f) for f in ("plan.cpp", "runtime.cu", "rs_kernel.cu", "rs_bulk.cu",
-                                                     "rs_staged.cu", "ag_kernel.cu", "ag_bulk.cu", "rs_noalloc.cu")]
+                                                     "rs_staged.cu", "ag_kernel.cu", "ag_bulk.cu", "rs_noalloc.cu",
+                                                     "ops_norm.cu", "ops_ckpt.cu", "ops_linear.cu")]
 TIDE_DEPS = [os.path.join(HERE, "csrc", f) for f in ("tide_internal.h", "rs_device.cuh", "bulk_ptx.cuh",
-                                                     "check.cuh")] + [os.path.join(ROOT, "include", "tide.h")]
+                                                     "check.cuh", "ops_common.cuh")] + \
+            [os.path.join(ROOT, "include", f) for f in ("tide.h", "tide_ops.h")]
 
 LIBS = {
     "tide": {

@@ -1,0 +1,231 @@
+// Device helpers and host-side argument checks shared by the training-block
+// operators (ops_norm.cu, ops_ckpt.cu, ops_linear.cu).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <string>
+
+#include "../../include/tide_ops.h"
+#include "tide_internal.h"
+
+namespace tide {
+
+using bf16 = __nv_bfloat16;
+
+// Columns that share one scale of an 8-bit checkpoint.
+constexpr int kMxBlock = 32;
+
+// ---------------------------------------------------------------- host side
+
+inline tide_status cuda_status(cudaError_t err, const char* what) {
+  return err == cudaSuccess ? TIDE_OK : fail(TIDE_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(err));
+}
+
+inline int64_t elem_bytes_of(int32_t dtype) { return dtype == TIDE_BF16 ? 2 : 4; }
+
+inline tide_status check_sizes(int64_t rows, int64_t cols, const char* what) {
+  if (rows < 0 || cols < 0) return fail(TIDE_ERR_INVALID_ARG, std::string(what) + ": negative size");
+  return TIDE_OK;
+}
+
+// One matrix argument: non-null, aligned to its element, rows of at least
+// `cols` elements, and byte offsets that fit int64.
+inline tide_status check_matrix(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t elem, const char* what) {
+  if (rows == 0 || cols == 0) return TIDE_OK;
+  if (!p) return fail(TIDE_ERR_INVALID_ARG, std::string(what) + " is NULL");
+  if ((uintptr_t)p % elem) return fail(TIDE_ERR_ALIGNMENT, std::string(what) + " is not aligned to its element size");
+  if (rows > 1 && ld < cols) return fail(TIDE_ERR_INVALID_ARG, std::string(what) + ": row stride shorter than a row");
+  if (cols > INT64_MAX / elem || (rows > 1 && (ld > INT64_MAX / elem || rows - 1 > (INT64_MAX - cols * elem) / (ld * elem))))
+    return fail(TIDE_ERR_OVERFLOW, std::string(what) + " does not fit int64 bytes");
+  return TIDE_OK;
+}
+
+inline tide_status check_checkpoint(const void* codes, int64_t ld_codes, const void* scales, int64_t ld_scales,
+                                    int64_t rows, int64_t cols) {
+  tide_status st = check_matrix(codes, rows, cols, ld_codes, 1, "codes");
+  if (st == TIDE_OK) st = check_matrix(scales, rows, (cols + kMxBlock - 1) / kMxBlock, ld_scales, 1, "scales");
+  return st;
+}
+
+inline tide_status check_act(int32_t act) {
+  return act < TIDE_ACT_NONE || act > TIDE_ACT_SILU ? fail(TIDE_ERR_INVALID_ARG, "unknown activation") : TIDE_OK;
+}
+
+inline tide_status check_dtype(int32_t dtype) {
+  return dtype != TIDE_BF16 && dtype != TIDE_F32 ? fail(TIDE_ERR_INVALID_ARG, "unknown element type") : TIDE_OK;
+}
+
+// Whether rows of a matrix start on 16-byte boundaries (NULL counts: it is
+// not touched).
+inline bool rows_aligned(const void* p, int64_t ld, int64_t elem, int64_t rows) {
+  return !p || ((uintptr_t)p % 16 == 0 && (rows <= 1 || ld * elem % 16 == 0));
+}
+
+// SMs of the current device (asked once per device); 0 if the query failed.
+int ops_num_sms();
+
+#define TIDE_TRY(expr)                    \
+  do {                                    \
+    tide_status st_ = (expr);             \
+    if (st_ != TIDE_OK) return st_;       \
+  } while (0)
+
+// ---------------------------------------------------------------- device side
+
+// V consecutive elements as fp32.  V = 8: 16-byte accesses; V = 1: one element.
+template <int V>
+__device__ __forceinline__ void load_vec(const bf16* p, float (&v)[V]) {
+  if constexpr (V == 8) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = __bfloat162float(p[i]);
+  }
+}
+
+template <int V>
+__device__ __forceinline__ void load_vec(const float* p, float (&v)[V]) {
+  if constexpr (V == 8) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = p[i];
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&t);
+}
+
+template <int V>
+__device__ __forceinline__ void store_vec(bf16* p, const float (&v)[V]) {
+  if constexpr (V == 8) {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) p[i] = __float2bfloat16_rn(v[i]);
+  }
+}
+
+template <int V>
+__device__ __forceinline__ void store_vec(float* p, const float (&v)[V]) {
+  if constexpr (V == 8) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) p[i] = v[i];
+  }
+}
+
+// ---- 8-bit checkpoints
+
+// Infinities become NaN (0 * inf); finite values and NaN stay.
+__device__ __forceinline__ float finite_or_nan(float v) { return __fmaf_rn(0.0f, v, v); }
+
+// Scale byte of a block whose largest finite magnitude is `a`: the smallest
+// e >= -127 with a <= 448 * 2^e, plus 127.  With a = 1.m * 2^E and
+// 448 = 1.75 * 2^8, e = E - 8 if 1.m <= 1.75, else E - 7.
+__device__ __forceinline__ int scale_byte(float a) {
+  const uint32_t u = __float_as_uint(a);
+  const int b = (int)(u >> 23) - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return b > 0 ? b : 0;
+}
+// 2^(127 - byte) and 2^(byte - 127); byte is at most 247.
+__device__ __forceinline__ float scale_inverse(int byte) { return __uint_as_float((uint32_t)(254 - byte) << 23); }
+__device__ __forceinline__ float scale_value(int byte) {
+  return __uint_as_float(byte > 0 ? (uint32_t)byte << 23 : 0x400000u);
+}
+
+// Two codes of values already divided by the scale (lo in the low byte).
+__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
+// The topmost scale's codes stop at 240: the next value, 256 * 2^120, is
+// beyond fp32.
+__device__ __forceinline__ float clamp_top(float q, int byte) {
+  return byte >= 247 && fabsf(q) > 240.0f ? copysignf(240.0f, q) : q;
+}
+
+// fp32 values of two codes (exact: e4m3 is a subset of fp16).
+__device__ __forceinline__ float2 e4m3_values(uint32_t pair) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)pair, __NV_E4M3);
+  return __half22float2(__half2(h));
+}
+
+// ---- activations
+
+constexpr float kGeluA = 0.7978845608028654f;  // sqrt(2/pi)
+constexpr float kGeluB = 0.044715f;
+constexpr float kInvSqrt2 = 0.7071067811865475f;
+constexpr float kInvSqrt2Pi = 0.3989422804014327f;
+
+// FAST: the approximate exponential and division, good to a few units in the
+// last place of fp32 over the range that matters, for results that are then
+// rounded to bf16 or 8 bits.  fp32 results take the accurate ones.
+template <bool FAST>
+__device__ __forceinline__ float exp_of(float t) {
+  return FAST ? __expf(t) : expf(t);
+}
+
+// 1 / (1 + exp(-t)): 0 at -inf (and where the exponential overflows), 1 at
+// +inf, NaN at NaN.
+template <bool FAST>
+__device__ __forceinline__ float sigmoid(float t) {
+  const float d = 1.0f + exp_of<FAST>(-t);
+  return FAST ? __fdividef(1.0f, d) : 1.0f / d;
+}
+
+// GELU, GELU_ERF and SILU are z * p(z) with p from 0 to 1; where p has come
+// down to 0 the product is 0 (not -inf * 0).
+template <bool FAST>
+__device__ __forceinline__ float act_value(int act, float z) {
+  float p;
+  switch (act) {
+    case TIDE_ACT_RELU: return z < 0.0f ? 0.0f : z;
+    case TIDE_ACT_GELU: p = sigmoid<FAST>(2.0f * kGeluA * (z + kGeluB * z * z * z)); break;
+    case TIDE_ACT_GELU_ERF: p = 0.5f * erfcf(-kInvSqrt2 * z); break;
+    case TIDE_ACT_SILU: p = sigmoid<FAST>(z); break;
+    default: return z;
+  }
+  return p == 0.0f ? 0.0f : z * p;
+}
+
+// f' = p + z p'; where p' has come down to 0 it is p (not inf * 0).
+template <bool FAST>
+__device__ __forceinline__ float act_grad(int act, float z) {
+  float p, d;
+  switch (act) {
+    case TIDE_ACT_RELU: return z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;
+    case TIDE_ACT_GELU:
+      p = sigmoid<FAST>(2.0f * kGeluA * (z + kGeluB * z * z * z));
+      d = p * (1.0f - p);
+      return d == 0.0f ? p : p + z * d * (2.0f * kGeluA * (1.0f + 3.0f * kGeluB * z * z));
+    case TIDE_ACT_GELU_ERF:
+      p = 0.5f * erfcf(-kInvSqrt2 * z);
+      d = exp_of<FAST>(-0.5f * z * z);
+      return d == 0.0f ? p : p + z * d * kInvSqrt2Pi;
+    case TIDE_ACT_SILU:
+      p = sigmoid<FAST>(z);
+      d = p * (1.0f - p);
+      return d == 0.0f ? p : p + z * d;
+    default: return 1.0f;
+  }
+}
+
+}  // namespace tide
