@@ -25,6 +25,7 @@ from .tide import (  # noqa: F401
 _OPS = frozenset((
     "Checkpoint8", "TIDE_CKPT_BLOCK", "tide_checkpoint_store", "tide_checkpoint_load", "tide_rms_norm",
     "tide_rms_norm_backward", "tide_linear", "tide_linear_grad_input", "tide_linear_grad_weight",
+    "tide_ops_check", "tide_ops_set_option", "TIDE_OPS_OPT_WAIT_LIMIT_NS", "TIDE_OPS_OPT_TEST_DROP_LOAD",
     "TIDE_ACT_NONE", "TIDE_ACT_RELU", "TIDE_ACT_GELU", "TIDE_ACT_GELU_ERF", "TIDE_ACT_SILU",
 ))
 

@@ -41,9 +41,10 @@ CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler",
 
 TIDE_SRCS = [os.path.join(HERE, "csrc", f) for f in ("plan.cpp", "runtime.cu", "rs_kernel.cu", "rs_bulk.cu",
                                                      "rs_staged.cu", "ag_kernel.cu", "ag_bulk.cu", "rs_noalloc.cu",
-                                                     "ops_norm.cu", "ops_ckpt.cu", "ops_linear.cu")]
+                                                     "ops_norm.cu", "ops_ckpt.cu", "ops_linear.cu", "ops_linear_forward.cu",
+                                                     "ops_linear_grad_input.cu", "ops_linear_grad_weight.cu")]
 TIDE_DEPS = [os.path.join(HERE, "csrc", f) for f in ("tide_internal.h", "rs_device.cuh", "bulk_ptx.cuh",
-                                                     "check.cuh", "ops_common.cuh")] + \
+                                                     "check.cuh", "ops_common.cuh", "gemm_tc.cuh", "tc_ptx.cuh")] + \
             [os.path.join(ROOT, "include", f) for f in ("tide.h", "tide_ops.h")]
 
 LIBS = {

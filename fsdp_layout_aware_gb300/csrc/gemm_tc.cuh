@@ -1,0 +1,482 @@
+// Tensor-core products of the linear layer, out = epilogue(A B^T).
+//
+// A is [m, k] and B [n, k], each either with k contiguous (K-major) or with
+// its other axis contiguous (MN-major), in bf16; sums are fp32 in tensor
+// memory.  A tile is 128 * CG rows by BN columns; with CG = 2 two CTAs of a
+// cluster share it, each holding 128 rows of A, half of B's rows and its 128
+// rows of the accumulator, so that every byte staged in shared memory feeds
+// twice the arithmetic.
+//
+// One persistent CTA per SM.  Warp 0 streams 64-deep blocks of A and B into a
+// ring of shared-memory stages with TMA; warp 1 (of the first CTA of a pair)
+// issues the matrix instructions; warps 4-7 take a finished accumulator out of
+// tensor memory and run the epilogue while the next tile accumulates in the
+// other half.  Every wait is bounded: a wait that runs out sets the status
+// word, and the CTA drains its copies, frees its tensor memory and returns.
+#pragma once
+
+#include "ops_common.cuh"
+#include "tc_ptx.cuh"
+
+namespace tide {
+
+enum Epilogue { EPI_FORWARD, EPI_GRAD_INPUT, EPI_PLAIN, EPI_PARTIAL };
+
+// What becomes of a sum v at (row, col):
+//   FORWARD      v += bias; z, and its checkpoint, get v; out = f(v) + residual
+//   GRAD_INPUT   out = v * f'(kept z)
+//   PLAIN        out = v
+//   PARTIAL      v in fp32 to partial[split], for epilogue_kernel
+struct EpilogueArgs {
+  int64_t rows, cols;
+  int32_t act;
+  bool vec;  // every matrix below has 16-byte aligned rows (cols may still be odd)
+  const bf16* bias;
+  const bf16* residual;
+  int64_t ldr;
+  bf16* out;
+  int64_t ldo;
+  bf16* z;
+  int64_t ldz;
+  uint8_t* codes;
+  int64_t ldc;
+  uint8_t* scales;
+  int64_t lds;
+  const bf16* zin;
+  int64_t ldzin;
+  const uint8_t* cin;
+  int64_t ldcin;
+  const uint8_t* sin;
+  int64_t ldsin;
+  float* partial;  // [splits][rows][ldp]
+  int64_t ldp;
+};
+
+struct TcArgs {
+  CUtensorMap a, b;
+  EpilogueArgs e;
+  int32_t tiles_m, tiles_n;
+  int32_t k_blocks;        // of 64, over the whole sum
+  int32_t split_blocks;    // k blocks of one split (all of them without splitting)
+  int32_t splits;
+  int32_t* status;
+  uint64_t wait_limit_ns;
+  int64_t test_drop;       // k block (counted per CTA) whose loads are withheld (tests); -1: none
+};
+
+constexpr int kTcThreads = 256;
+constexpr int kTcK = 64;           // values of k a stage holds: 128 bytes, one swizzle row
+constexpr int kTcStages = 6;
+constexpr int kTcGroupM = 8;       // tile rows walked together, for reuse of B in L2
+
+template <int CG, int BN>
+struct TcShape {
+  static constexpr int a_bytes = 128 * kTcK * 2;
+  static constexpr int b_rows = BN / CG;
+  static constexpr int b_bytes = b_rows * kTcK * 2;
+  static constexpr int stage_bytes = a_bytes + b_bytes;
+  static constexpr int transpose_bytes = 4 * 32 * 33 * 4;  // a [32][33] fp32 block per epilogue warp
+  static constexpr int columns = 2 * BN;                   // two accumulators
+  static constexpr int smem_bytes = 1024 + kTcStages * stage_bytes + transpose_bytes + 256;
+};
+
+// ---- epilogues
+
+template <int ACT>
+struct ActTag {
+  static constexpr int value = ACT;
+};
+// f called with the activation as a constant.
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F&& f) {
+  switch (act) {
+    case TIDE_ACT_RELU: f(ActTag<TIDE_ACT_RELU>()); break;
+    case TIDE_ACT_GELU: f(ActTag<TIDE_ACT_GELU>()); break;
+    case TIDE_ACT_GELU_ERF: f(ActTag<TIDE_ACT_GELU_ERF>()); break;
+    case TIDE_ACT_SILU: f(ActTag<TIDE_ACT_SILU>()); break;
+    default: break;
+  }
+}
+
+__device__ __forceinline__ void load32(const bf16* p, float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float t[8];
+    load_vec<8>(p + 8 * i, t);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[8 * i + k] = t[k];
+  }
+}
+__device__ __forceinline__ void store32(bf16* p, const float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float t[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) t[k] = v[8 * i + k];
+    store_vec<8>(p + 8 * i, t);
+  }
+}
+
+// 32 neighbouring columns of one row, held by one thread; every matrix's rows
+// are 16-byte aligned and col is a multiple of 32.
+template <int EPI>
+__device__ __forceinline__ void epilogue_row(const EpilogueArgs& e, int split, int64_t row, int64_t col,
+                                             float (&v)[32]) {
+  float t[32];
+  if constexpr (EPI == EPI_FORWARD) {
+    if (e.bias) {
+      load32(e.bias + col, t);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] += t[i];
+    }
+    if (e.z) store32(e.z + row * e.ldz + col, v);
+    if (e.codes) {
+      float m = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        t[i] = finite_or_nan(v[i]);
+        m = fmaxf(m, fabsf(t[i]));
+      }
+      const int byte = scale_byte(m);
+      const float inv = scale_inverse(byte);
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        w[i] = e4m3_pair(clamp_top(t[4 * i] * inv, byte), clamp_top(t[4 * i + 1] * inv, byte)) |
+               e4m3_pair(clamp_top(t[4 * i + 2] * inv, byte), clamp_top(t[4 * i + 3] * inv, byte)) << 16;
+      }
+      uint4* c = reinterpret_cast<uint4*>(e.codes + row * e.ldc + col);
+      c[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      c[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      e.scales[row * e.lds + col / kMxBlock] = (uint8_t)byte;
+    }
+    with_act(e.act, [&](auto a) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = act_value<true>(a.value, v[i]);
+    });
+    if (e.residual) {
+      load32(e.residual + row * e.ldr + col, t);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] += t[i];
+    }
+  }
+  if constexpr (EPI == EPI_GRAD_INPUT) {
+    if (e.act != TIDE_ACT_NONE) {
+      if (e.zin) {
+        load32(e.zin + row * e.ldzin + col, t);
+      } else {
+        const uint4* c = reinterpret_cast<const uint4*>(e.cin + row * e.ldcin + col);
+        const uint4 c0 = c[0], c1 = c[1];
+        const float s = scale_value(e.sin[row * e.ldsin + col / kMxBlock]);
+        const uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 q = e4m3_values((w[i / 2] >> (16 * (i % 2))) & 0xffffu);
+          t[2 * i] = q.x * s;
+          t[2 * i + 1] = q.y * s;
+        }
+      }
+      with_act(e.act, [&](auto a) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] *= act_grad<true>(a.value, t[i]);
+      });
+    }
+  }
+  if constexpr (EPI == EPI_PARTIAL) {
+    float4* p = reinterpret_cast<float4*>(e.partial + (split * e.rows + row) * e.ldp + col);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  } else {
+    store32(e.out + row * e.ldo + col, v);
+  }
+}
+
+// One element of a row per lane, a whole warp on one block of 32 columns; any
+// alignment.  `in`: the element exists (the row does for every lane).
+template <int EPI>
+__device__ __forceinline__ void epilogue_element(const EpilogueArgs& e, int64_t row, int64_t col, bool in, float v,
+                                                 float bias) {
+  if constexpr (EPI == EPI_FORWARD) {
+    v += bias;
+    if (e.z && in) e.z[row * e.ldz + col] = __float2bfloat16_rn(v);
+    if (e.codes) {
+      const float t = finite_or_nan(v);
+      const uint32_t m = __reduce_max_sync(0xffffffffu, in ? __float_as_uint(fmaxf(fabsf(t), 0.0f)) : 0u);
+      const int byte = scale_byte(__uint_as_float(m));
+      if (in) {
+        e.codes[row * e.ldc + col] = (uint8_t)e4m3_pair(clamp_top(t * scale_inverse(byte), byte), 0.0f);
+        if (col % kMxBlock == 0) e.scales[row * e.lds + col / kMxBlock] = (uint8_t)byte;
+      }
+    }
+    v = act_value<true>(e.act, v);
+    if (e.residual && in) v += __bfloat162float(e.residual[row * e.ldr + col]);
+  }
+  if constexpr (EPI == EPI_GRAD_INPUT) {
+    if (e.act != TIDE_ACT_NONE && in) {
+      const float z = e.zin ? __bfloat162float(e.zin[row * e.ldzin + col])
+                            : e4m3_values(e.cin[row * e.ldcin + col]).x *
+                                  scale_value(e.sin[row * e.ldsin + col / kMxBlock]);
+      v *= act_grad<true>(e.act, z);
+    }
+  }
+  if (in) e.out[row * e.ldo + col] = __float2bfloat16_rn(v);
+}
+
+// ---- the kernel
+
+struct TileAt {
+  int m, n;
+};
+// Tiles in groups of kTcGroupM tile rows, down the rows first: CTAs at work at
+// one time share few rows of A and B.
+__device__ __forceinline__ TileAt tile_at(const TcArgs& p, int t) {
+  const int per_group = kTcGroupM * p.tiles_n;
+  const int g = t / per_group, first = g * kTcGroupM;
+  const int height = min(kTcGroupM, p.tiles_m - first);
+  const int i = t - g * per_group;
+  return {first + i % height, i / height};
+}
+
+template <int CG, int BN, bool A_MN, bool B_MN, int EPI>
+__global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_constant__ TcArgs p) {
+  using Shape = TcShape<CG, BN>;
+  extern __shared__ unsigned char raw[];
+  // 1024-byte aligned: the swizzle pattern follows address bits.
+  unsigned char* smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+  unsigned char* transpose = smem + kTcStages * Shape::stage_bytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(transpose + Shape::transpose_bytes);
+  uint64_t* empty = full + kTcStages;
+  uint64_t* acc_full = empty + kTcStages;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* drained = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kTcStages; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(acc_full + i, 1);
+      mbar_init(acc_empty + i, 4 * CG);
+    }
+    mbar_init(drained, 1);
+    fence_mbar_init_cluster();
+    tma_prefetch_map(&p.a);
+    tma_prefetch_map(&p.b);
+  }
+  if (warp == 2) tmem_alloc<CG>(tmem_slot, Shape::columns);
+  tc_fence_before();
+  if constexpr (CG == 2)
+    cluster_sync();
+  else
+    __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  const int tiles = p.tiles_m * p.tiles_n;
+  const int units = tiles * p.splits;
+  const int first = blockIdx.x / CG, step = gridDim.x / CG;
+  bool ok = true;
+
+  if (warp == 0 && lane == 0) {
+    // Producer.  The pair's loads all count on the first CTA's barrier.
+    int stage = 0;
+    uint32_t phase = 0;
+    int64_t issued = 0;
+    for (int u = first; u < units && ok; u += step) {
+      const TileAt at = tile_at(p, u % tiles);
+      const int split = u / tiles;
+      const int kb0 = split * p.split_blocks, kb1 = min(p.k_blocks, kb0 + p.split_blocks);
+      const int m0 = (at.m * CG + (int)rank) * 128, n0 = at.n * BN + (int)rank * Shape::b_rows;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!(ok = mbar_wait_bounded(empty + stage, phase ^ 1, p.wait_limit_ns))) break;
+        unsigned char* a = smem + stage * Shape::stage_bytes;
+        unsigned char* b = a + Shape::a_bytes;
+        if (rank == 0) mbar_arrive_expect_tx(full + stage, CG * Shape::stage_bytes);
+        const uint32_t bar = CG == 2 ? mapped_addr(smem_addr(full + stage), 0) : smem_addr(full + stage);
+        if (issued != p.test_drop) {
+          if constexpr (A_MN) {
+            tma_load_2d<CG>(a, &p.a, m0, kb * kTcK, bar);
+            tma_load_2d<CG>(a + 8192, &p.a, m0 + 64, kb * kTcK, bar);
+          } else {
+            tma_load_2d<CG>(a, &p.a, kb * kTcK, m0, bar);
+          }
+          if constexpr (B_MN) {
+#pragma unroll
+            for (int i = 0; i < Shape::b_rows / 64; ++i)
+              tma_load_2d<CG>(b + 8192 * i, &p.b, n0 + 64 * i, kb * kTcK, bar);
+          } else {
+            tma_load_2d<CG>(b, &p.b, kb * kTcK, n0, bar);
+          }
+        }
+        ++issued;
+        if (++stage == kTcStages) stage = 0, phase ^= 1;
+      }
+    }
+    // Before leaving, every stage is handed back (no commit's arrival is still
+    // under way), or, after a wait that ran out, the loads in flight landed.
+    for (int s = 0; s < kTcStages; ++s) {
+      const int64_t uses = (issued - s + kTcStages - 1) / kTcStages;  // times stage s was filled
+      if (uses <= 0) break;
+      if (ok) ok = mbar_wait_bounded(empty + s, (uint32_t)(uses - 1) & 1, p.wait_limit_ns);
+      if (!ok && rank == 0) mbar_wait_bounded(full + s, (uint32_t)(uses - 1) & 1, p.wait_limit_ns);
+    }
+    if (!ok) {  // the pair's other CTA counts on barriers it cannot ask: a millisecond is ample for a load
+      const uint64_t t = global_ns();
+      while (global_ns() - t < 1000000) __nanosleep(1000);
+    }
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    // Matrix instructions, for both CTAs of a pair.
+    constexpr uint32_t idesc = instruction_desc(128 * CG, BN, A_MN, B_MN);
+    int stage = 0;
+    uint32_t phase = 0;
+    int turn = 0;
+    for (int u = first; u < units && ok; u += step, ++turn) {
+      const int split = u / tiles;
+      const int kb0 = split * p.split_blocks, kb1 = min(p.k_blocks, kb0 + p.split_blocks);
+      const int acc = turn & 1;
+      if (!(ok = mbar_wait_bounded(acc_empty + acc, ((turn >> 1) & 1) ^ 1, p.wait_limit_ns))) break;
+      tc_fence_after();
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!(ok = mbar_wait_bounded(full + stage, phase, p.wait_limit_ns))) break;
+        tc_fence_after();
+        const uint32_t a = smem_addr(smem + stage * Shape::stage_bytes);
+        const uint64_t da = operand_desc<A_MN>(a), db = operand_desc<B_MN>(a + Shape::a_bytes);
+#pragma unroll
+        for (int k = 0; k < kTcK / 16; ++k)
+          tc_mma<CG>(tmem + acc * BN, da + k * kDescStep<A_MN>, db + k * kDescStep<B_MN>, idesc, kb > kb0 || k > 0);
+        tc_commit<CG>(empty + stage);
+        if (++stage == kTcStages) stage = 0, phase ^= 1;
+      }
+      if (ok) tc_commit<CG>(acc_full + acc);
+    }
+    if (!ok) {
+      tc_commit<CG>(drained);
+      mbar_wait_bounded(drained, 0, p.wait_limit_ns);
+    }
+  } else if (warp >= 4) {
+    // Epilogue: warp w reads lanes 32 (w mod 4) onwards, one row of the tile a
+    // lane, 32 columns at a time.
+    const int quad = warp - 4;
+    float* block = reinterpret_cast<float*>(transpose) + quad * 32 * 33;
+    int turn = 0;
+    for (int u = first; u < units; u += step, ++turn) {
+      const TileAt at = tile_at(p, u % tiles);
+      const int split = u / tiles;
+      const int acc = turn & 1;
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(acc_full + acc, (turn >> 1) & 1, p.wait_limit_ns));
+      if (!ok) break;
+      tc_fence_after();
+      const int64_t row0 = (int64_t)(at.m * CG + (int)rank) * 128 + quad * 32;
+      const EpilogueArgs& e = p.e;
+      const uint32_t from = tmem + acc * BN + ((uint32_t)(quad * 32) << 16);
+#pragma unroll 1
+      for (int c = 0; c < BN; c += 32) {
+        const int64_t col = (int64_t)at.n * BN + c;
+        float v[32];
+        __syncwarp();
+        tmem_load32(from + c, v);
+        if (c + 32 == BN) {  // the accumulator may be written again
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (CG == 2)
+              mbar_arrive_cluster(mapped_addr(smem_addr(acc_empty + acc), 0));
+            else
+              mbar_arrive(acc_empty + acc);
+          }
+        }
+        if (row0 >= e.rows || (EPI != EPI_PARTIAL && col >= e.cols)) continue;
+        if (EPI == EPI_PARTIAL || (e.vec && col + 32 <= e.cols)) {
+          if (row0 + lane < e.rows) epilogue_row<EPI>(e, split, row0 + lane, col, v);
+        } else if constexpr (EPI != EPI_PARTIAL) {
+          // Turned in shared memory: lane l then has column l of each row.
+#pragma unroll
+          for (int i = 0; i < 32; ++i) block[lane * 33 + i] = v[i];
+          __syncwarp();
+          const bool in = col + lane < e.cols;
+          float bias = 0.0f;
+          if (EPI == EPI_FORWARD && e.bias && in) bias = __bfloat162float(e.bias[col + lane]);
+          const int n = (int)min((int64_t)32, e.rows - row0);
+          for (int r = 0; r < n; ++r) epilogue_element<EPI>(e, row0 + r, col + lane, in, block[r * 33 + lane], bias);
+          __syncwarp();
+        }
+      }
+    }
+  }
+  if (!ok) atomicOr(p.status, TIDE_DEVICE_TIMEOUT);
+  __syncwarp();
+  tc_fence_before();
+  if constexpr (CG == 2)
+    cluster_sync();
+  else
+    __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_free<CG>(tmem, Shape::columns);
+  }
+}
+
+// The sums of the splits, in order, through the epilogue: a warp takes blocks
+// of 32 columns of a row.  With no splits (nothing to sum) the sums are zero.
+template <int EPI>
+__global__ void __launch_bounds__(256) epilogue_kernel(const EpilogueArgs e, int splits) {
+  const int lane = threadIdx.x % 32;
+  const int64_t blocks = (e.cols + 31) / 32;
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) / 32;
+  const int64_t row = i / blocks;
+  if (row >= e.rows) return;
+  const int64_t col = (i - row * blocks) * 32 + lane;
+  const bool in = col < e.cols;
+  float v = 0.0f;
+  const float* q = e.partial + row * e.ldp + col;
+  if (in)
+    for (int s = 0; s < splits; ++s) v += q[(int64_t)s * e.rows * e.ldp];
+  float bias = 0.0f;
+  if (EPI == EPI_FORWARD && e.bias && in) bias = __bfloat162float(e.bias[col]);
+  epilogue_element<EPI>(e, row, col, in, v, bias);
+}
+
+// Launches the product kernel of one operand layout; `kind` an Epilogue.
+// Defined per layout in ops_linear_*.cu.
+struct TcLaunch {
+  int cg, bn;
+  int grid;
+};
+cudaError_t launch_forward(const TcArgs& p, const TcLaunch& l, bool partial, cudaStream_t stream);
+cudaError_t launch_grad_input(const TcArgs& p, const TcLaunch& l, bool partial, cudaStream_t stream);
+cudaError_t launch_grad_weight(const TcArgs& p, const TcLaunch& l, bool partial, cudaStream_t stream);
+
+template <int CG, int BN, bool A_MN, bool B_MN, int EPI>
+cudaError_t launch_tc(const TcArgs& p, int grid, cudaStream_t stream) {
+  auto kernel = gemm_tc_kernel<CG, BN, A_MN, B_MN, EPI>;
+  constexpr int smem = TcShape<CG, BN>::smem_bytes;
+  // Set for each device once; the call is cheap and host-only.
+  const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kTcThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CG;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CG == 2 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <bool A_MN, bool B_MN, int EPI>
+cudaError_t launch_layout(const TcArgs& p, const TcLaunch& l, bool partial, cudaStream_t stream) {
+  if (l.cg == 2) return launch_tc<2, 256, A_MN, B_MN, EPI>(p, l.grid, stream);
+  if (partial) return launch_tc<1, 128, A_MN, B_MN, EPI_PARTIAL>(p, l.grid, stream);
+  return launch_tc<1, 128, A_MN, B_MN, EPI>(p, l.grid, stream);
+}
+
+}  // namespace tide

@@ -2,7 +2,10 @@
 // with the previous activation's derivative, weight and bias gradients
 // (include/tide_ops.h).
 
-#include "ops_common.cuh"
+#include <algorithm>
+#include <atomic>
+
+#include "gemm_tc.cuh"
 
 namespace tide {
 
@@ -12,112 +15,184 @@ tide_status launch_checkpoint_load_bf16(int64_t rows, int64_t cols, const uint8_
 
 namespace {
 
-// out[m, n] = epilogue(sum over k of A(m, k) * B(n, k)), with element strides.
-struct GemmArgs {
-  int64_t m, n, k;
-  const bf16* a;
-  int64_t a_m, a_k;
-  const bf16* b;
-  int64_t b_n, b_k;
-  // Epilogue: v = sum + bias[n]; z and its checkpoint get v; then
-  // v = f(v) + residual, or v * f'(kept z), to out.
-  const bf16* bias;
-  int32_t act;
-  bool grad;  // multiply by f'(zin) instead of applying f
-  const bf16* residual;
-  int64_t ldr;
-  bf16* out;
-  int64_t ldo;
-  bf16* z;
-  int64_t ldz;
-  uint8_t* codes;
-  int64_t ldc;
-  uint8_t* scales;
-  int64_t lds;
-  const bf16* zin;
-  int64_t ldzin;
-  const uint8_t* cin;
-  int64_t ldcin;
-  const uint8_t* sin;
-  int64_t ldsin;
-};
+// Set where a product's kernel gave up a wait (tide_ops_check).
+__device__ int32_t g_status;
+std::atomic<int64_t> g_wait_limit_ns{2000000000};
+std::atomic<int64_t> g_test_drop{-1};
 
-constexpr int kTile = 64, kStep = 16;
-
-__global__ void __launch_bounds__(256) gemm_kernel(const GemmArgs g) {
-  __shared__ float sa[kStep][kTile + 4], sb[kStep][kTile + 4];
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  const int64_t tiles_n = (g.n + kTile - 1) / kTile;
-  const int64_t m0 = blockIdx.x / tiles_n * kTile, n0 = blockIdx.x % tiles_n * kTile;
-  float acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < g.k; k0 += kStep) {
-    for (int i = threadIdx.x; i < kTile * kStep; i += 256) {
-      // Neighbouring threads follow whichever axis is contiguous.
-      const int ma = g.a_k == 1 ? i / kStep : i % kTile, ka = g.a_k == 1 ? i % kStep : i / kTile;
-      const int nb = g.b_k == 1 ? i / kStep : i % kTile, kb = g.b_k == 1 ? i % kStep : i / kTile;
-      sa[ka][ma] = m0 + ma < g.m && k0 + ka < g.k ? __bfloat162float(g.a[(m0 + ma) * g.a_m + (k0 + ka) * g.a_k]) : 0.0f;
-      sb[kb][nb] = n0 + nb < g.n && k0 + kb < g.k ? __bfloat162float(g.b[(n0 + nb) * g.b_n + (k0 + kb) * g.b_k]) : 0.0f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kStep; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[k][ty * 4 + i], sb[k][tx * 4 + j], acc[i][j]);
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t m = m0 + ty * 4 + i;
-    float most = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t n = n0 + tx * 4 + j;
-      if (m < g.m && n < g.n) {
-        float v = acc[i][j] + (g.bias ? __bfloat162float(g.bias[n]) : 0.0f);
-        acc[i][j] = v;
-        if (g.z) g.z[m * g.ldz + n] = __float2bfloat16_rn(v);
-        if (g.grad) {
-          if (g.act != TIDE_ACT_NONE) {
-            const float z = g.zin ? __bfloat162float(g.zin[m * g.ldzin + n])
-                                  : e4m3_values(g.cin[m * g.ldcin + n]).x *
-                                        scale_value(g.sin[m * g.ldsin + n / kMxBlock]);
-            v *= act_grad<true>(g.act, z);
-          }
-        } else {
-          v = act_value<true>(g.act, v);
-        }
-        if (g.residual) v += __bfloat162float(g.residual[m * g.ldr + n]);
-        if (g.out) g.out[m * g.ldo + n] = __float2bfloat16_rn(v);
-      } else {
-        acc[i][j] = 0.0f;
-      }
-      acc[i][j] = finite_or_nan(acc[i][j]);
-      most = fmaxf(most, fabsf(acc[i][j]));
-    }
-    if (g.codes) {
-#pragma unroll
-      for (int d = 1; d < 8; d <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-      const int byte = scale_byte(most);
-      const float inv = scale_inverse(byte);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t n = n0 + tx * 4 + j;
-        if (m < g.m && n < g.n) {
-          g.codes[m * g.ldc + n] = (uint8_t)e4m3_pair(clamp_top(acc[i][j] * inv, byte), 0.0f);
-          if (n % kMxBlock == 0) g.scales[m * g.lds + n / kMxBlock] = (uint8_t)byte;
-        }
-      }
-    }
-  }
+tide_status ops_status_word(int32_t** word) {
+  static std::atomic<int32_t*> known[64];
+  int dev = -1;
+  TIDE_TRY(cuda_status(cudaGetDevice(&dev), "cudaGetDevice"));
+  if (dev < 64 && (*word = known[dev].load(std::memory_order_relaxed))) return TIDE_OK;
+  void* p = nullptr;
+  TIDE_TRY(cuda_status(cudaGetSymbolAddress(&p, g_status), "cudaGetSymbolAddress"));
+  *word = (int32_t*)p;
+  if (dev < 64) known[dev].store(*word, std::memory_order_relaxed);
+  return TIDE_OK;
 }
 
-tide_status gemm(const GemmArgs& g, cudaStream_t stream) {
-  const int64_t tiles_m = (g.m + kTile - 1) / kTile, tiles_n = (g.n + kTile - 1) / kTile;
-  if (tiles_m > INT32_MAX / tiles_n) return fail(TIDE_ERR_UNIMPLEMENTED, "product has too many tiles for one launch");
-  gemm_kernel<<<(unsigned)(tiles_m * tiles_n), 256, 0, stream>>>(g);
-  return cuda_status(cudaGetLastError(), "linear product");
+// One operand: `rows` rows of `cols` contiguous elements.
+struct Operand {
+  const bf16* p;
+  int64_t rows, cols, ld;
+};
+
+// Whether TMA can read the operand in place: 16-byte aligned base and rows, and
+// a row stride that its descriptor holds.
+bool readable(const void* p, int64_t rows, int64_t ld) {
+  return (uintptr_t)p % 16 == 0 && (rows <= 1 || (ld % 8 == 0 && ld < (int64_t)1 << 38));
+}
+
+int64_t packed_ld(int64_t cols) { return (cols + 7) / 8 * 8; }
+int64_t packed_bytes(int64_t rows, int64_t cols) { return (rows * packed_ld(cols) * 2 + 255) / 256 * 256; }
+
+// How a product [m, k] x [n, k] runs.
+struct Shape {
+  int cg = 1, bn = 128;
+  int32_t tiles_m = 0, tiles_n = 0, k_blocks = 0, split_blocks = 0, splits = 1;
+  int64_t partial_bytes = 0;
+};
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Picks the tile and the number of splits with the smallest estimated time, in
+// SM clocks: the turns of the busiest SM times the clocks of a turn.
+Shape pick_shape(int64_t m, int64_t n, int64_t k, int sms) {
+  Shape best;
+  double best_cost = 1e300;
+  const int64_t kb = ceil_div(k, kTcK);
+  {
+    Shape s;
+    s.cg = 2, s.bn = 256;
+    s.tiles_m = (int32_t)ceil_div(m, 256), s.tiles_n = (int32_t)ceil_div(n, 256);
+    s.k_blocks = s.split_blocks = (int32_t)kb;
+    const double turns = (double)ceil_div((int64_t)s.tiles_m * s.tiles_n, sms / 2);
+    best_cost = turns * (kb * 540.0 + 600.0) + 6000.0;
+    best = s;
+  }
+  for (int64_t splits = 1; splits <= 16 && splits <= std::max<int64_t>(1, kb / 4); ++splits) {
+    Shape s;
+    s.tiles_m = (int32_t)ceil_div(m, 128), s.tiles_n = (int32_t)ceil_div(n, 128);
+    s.k_blocks = (int32_t)kb;
+    s.split_blocks = (int32_t)ceil_div(kb, splits);
+    s.splits = (int32_t)ceil_div(kb, s.split_blocks);
+    const double turns = (double)ceil_div((int64_t)s.tiles_m * s.tiles_n * s.splits, sms);
+    double cost = turns * (s.split_blocks * (m <= 128 ? 650.0 : 340.0) + 500.0) + 3500.0;
+    if (s.splits > 1) {
+      s.partial_bytes = s.splits * m * (int64_t)s.tiles_n * 128 * 4;
+      cost += 4000.0 + (double)s.partial_bytes * 2.0 / 2500.0;
+    }
+    if (cost < best_cost) best = s, best_cost = cost;
+  }
+  return best;
+}
+
+tide_status check_extent(int64_t m, int64_t n, int64_t k) {
+  const int64_t most = INT32_MAX - 1024;
+  if (m > most || n > most || k > most || ceil_div(m, 128) * ceil_div(n, 128) > most / 16)
+    return fail(TIDE_ERR_UNIMPLEMENTED, "linear: sizes beyond 2^31, or too many tiles");
+  return TIDE_OK;
+}
+
+// Workspace of a product: packed copies of operands that TMA cannot read (or
+// that a checkpoint holds), then the splits' partial sums.
+int64_t product_workspace(int64_t m, int64_t n, int64_t k, bool pack_a, int64_t a_rows, int64_t a_cols, bool pack_b,
+                          int64_t b_rows, int64_t b_cols) {
+  if (m <= 0 || n <= 0 || k <= 0) return 0;
+  const int sms = ops_num_sms();
+  return (pack_a ? packed_bytes(a_rows, a_cols) : 0) + (pack_b ? packed_bytes(b_rows, b_cols) : 0) +
+         (sms > 0 ? pick_shape(m, n, k, sms).partial_bytes : 0);
+}
+
+// Rows of any alignment to rows of packed_ld(cols), eight elements a thread.
+// (What lies between a row's end and the next row is not read by the product.)
+__global__ void __launch_bounds__(256) pack_kernel(int64_t rows, int64_t cols, const bf16* __restrict__ x, int64_t ldx,
+                                                   bf16* __restrict__ out, int64_t ldo) {
+  const int64_t per_row = ldo / 8;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t row = i / per_row, col = (i - row * per_row) * 8;
+  if (row >= rows) return;
+  float v[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = col + k < cols ? __bfloat162float(x[row * ldx + col + k]) : 0.0f;
+  store_vec<8>(out + row * ldo + col, v);
+}
+
+tide_status pack(Operand* o, unsigned char** at, cudaStream_t stream) {
+  const int64_t ld = packed_ld(o->cols);
+  const int64_t grid = ceil_div(o->rows * (ld / 8), 256);
+  if (grid > INT32_MAX) return fail(TIDE_ERR_UNIMPLEMENTED, "linear: operand too large to lay out anew");
+  pack_kernel<<<(unsigned)grid, 256, 0, stream>>>(o->rows, o->cols, o->p, o->ld, (bf16*)*at, ld);
+  o->p = (const bf16*)*at;
+  o->ld = ld;
+  *at += packed_bytes(o->rows, o->cols);
+  return cuda_status(cudaGetLastError(), "laying out an operand");
+}
+
+using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
+EncodeTiled encode_tiled() {
+  static const EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return (EncodeTiled)p;
+  }();
+  return fn;
+}
+
+// A 2-D map with 128-byte swizzle; elements outside the matrix read as zero.
+tide_status make_map(CUtensorMap* map, const Operand& o, int box_rows) {
+  const EncodeTiled encode = encode_tiled();
+  if (!encode) return fail(TIDE_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  const cuuint64_t dims[2] = {(cuuint64_t)o.cols, (cuuint64_t)o.rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)(o.rows > 1 ? o.ld : packed_ld(o.cols)) * 2};
+  const cuuint32_t box[2] = {kTcK, (cuuint32_t)box_rows}, steps[2] = {1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<bf16*>(o.p), dims, strides, box, steps,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? TIDE_OK : fail(TIDE_ERR_CUDA, "cuTensorMapEncodeTiled failed: " + std::to_string((int)r));
+}
+
+using Launch = cudaError_t (*)(const TcArgs&, const TcLaunch&, bool, cudaStream_t);
+
+// out [m, n] = epilogue(sum over k); a_mn / b_mn: the operand's rows run along
+// k (its contiguous axis is m or n).
+template <int EPI>
+tide_status product(int64_t m, int64_t n, int64_t k, Operand a, bool a_mn, Operand b, bool b_mn, EpilogueArgs e,
+                    Launch launch, unsigned char* workspace, cudaStream_t stream) {
+  const int sms = ops_num_sms();
+  if (sms <= 0) return fail(TIDE_ERR_CUDA, "the current device could not be queried");
+  TIDE_TRY(check_extent(m, n, k));
+  e.rows = m, e.cols = n;
+  int splits = 0;
+  if (k > 0) {
+    const Shape s = pick_shape(m, n, k, sms);
+    if (!readable(a.p, a.rows, a.ld)) TIDE_TRY(pack(&a, &workspace, stream));
+    if (!readable(b.p, b.rows, b.ld)) TIDE_TRY(pack(&b, &workspace, stream));
+    TcArgs p{};
+    TIDE_TRY(make_map(&p.a, a, a_mn ? kTcK : 128));
+    TIDE_TRY(make_map(&p.b, b, b_mn ? kTcK : s.bn / s.cg));
+    const bool partial = s.splits > 1;
+    if (partial) e.partial = (float*)workspace, e.ldp = (int64_t)s.tiles_n * s.bn;
+    p.e = e;
+    p.tiles_m = s.tiles_m, p.tiles_n = s.tiles_n;
+    p.k_blocks = s.k_blocks, p.split_blocks = s.split_blocks, p.splits = s.splits;
+    TIDE_TRY(ops_status_word(&p.status));
+    p.wait_limit_ns = (uint64_t)g_wait_limit_ns.load(std::memory_order_relaxed);
+    p.test_drop = g_test_drop.load(std::memory_order_relaxed);
+    const int64_t units = (int64_t)s.tiles_m * s.tiles_n * s.splits;
+    const TcLaunch l{s.cg, s.bn, (int)std::min<int64_t>(units * s.cg, sms / s.cg * s.cg)};
+    TIDE_TRY(cuda_status(launch(p, l, partial, stream), "linear product"));
+    if (!partial) return TIDE_OK;
+    splits = s.splits;
+  }
+  const int64_t grid = ceil_div(m * ceil_div(n, 32), 8);
+  if (grid > INT32_MAX) return fail(TIDE_ERR_UNIMPLEMENTED, "linear: too many elements for one launch");
+  epilogue_kernel<EPI><<<(unsigned)grid, 256, 0, stream>>>(e, splits);
+  return cuda_status(cudaGetLastError(), "linear epilogue");
 }
 
 // db: a block sums 32 columns over all rows, in a fixed order.
@@ -150,8 +225,6 @@ tide_status check_workspace(const void* workspace, int64_t bytes, int64_t need) 
   return TIDE_OK;
 }
 
-int64_t packed_ld(int64_t cols) { return (cols + 7) / 8 * 8; }
-
 }  // namespace
 }  // namespace tide
 
@@ -159,7 +232,11 @@ using namespace tide;
 
 extern "C" {
 
-int64_t tide_linear_workspace(int64_t, int64_t, int64_t, const void*, int64_t, const void*, int64_t) { return 0; }
+int64_t tide_linear_workspace(int64_t rows, int64_t inner, int64_t outer, const void* x, int64_t ldx, const void* w,
+                              int64_t ldw) {
+  return product_workspace(rows, outer, inner, !readable(x, rows, ldx), rows, inner, !readable(w, outer, ldw), outer,
+                           inner);
+}
 
 tide_status tide_linear(int64_t rows, int64_t inner, int64_t outer, const void* x, int64_t ldx, const void* w,
                         int64_t ldw, const void* bias, int32_t act, const void* residual, int64_t ldr, void* y,
@@ -177,19 +254,24 @@ tide_status tide_linear(int64_t rows, int64_t inner, int64_t outer, const void* 
   if (z) TIDE_TRY(check_matrix(z, rows, outer, ldz, 2, "z"));
   if (codes || scales) TIDE_TRY(check_checkpoint(codes, ld_codes, scales, ld_scales, rows, outer));
   TIDE_TRY(check_workspace(workspace, workspace_bytes, tide_linear_workspace(rows, inner, outer, x, ldx, w, ldw)));
-  GemmArgs g{};
-  g.m = rows, g.n = outer, g.k = inner;
-  g.a = (const bf16*)x, g.a_m = ldx, g.a_k = 1;
-  g.b = (const bf16*)w, g.b_n = ldw, g.b_k = 1;
-  g.bias = (const bf16*)bias, g.act = act;
-  g.residual = (const bf16*)residual, g.ldr = ldr;
-  g.out = (bf16*)y, g.ldo = ldy, g.z = (bf16*)z, g.ldz = ldz;
-  g.codes = codes, g.ldc = ld_codes, g.scales = scales, g.lds = ld_scales;
-  return gemm(g, (cudaStream_t)stream);
+  EpilogueArgs e{};
+  e.act = act;
+  e.bias = (const bf16*)bias;
+  e.residual = (const bf16*)residual, e.ldr = ldr;
+  e.out = (bf16*)y, e.ldo = ldy;
+  e.z = (bf16*)z, e.ldz = ldz;
+  e.codes = codes, e.ldc = ld_codes, e.scales = scales, e.lds = ld_scales;
+  e.vec = (uintptr_t)bias % 16 == 0 && rows_aligned(residual, ldr, 2, rows) && rows_aligned(y, ldy, 2, rows) &&
+          rows_aligned(z, ldz, 2, rows) && rows_aligned(codes, ld_codes, 1, rows);
+  return product<EPI_FORWARD>(rows, outer, inner, {(const bf16*)x, rows, inner, ldx}, false,
+                              {(const bf16*)w, outer, inner, ldw}, false, e, launch_forward, (unsigned char*)workspace,
+                              (cudaStream_t)stream);
 }
 
-int64_t tide_linear_grad_input_workspace(int64_t, int64_t, int64_t, const void*, int64_t, const void*, int64_t) {
-  return 0;
+int64_t tide_linear_grad_input_workspace(int64_t rows, int64_t inner, int64_t outer, const void* dy, int64_t lddy,
+                                         const void* w, int64_t ldw) {
+  return product_workspace(rows, inner, outer, !readable(dy, rows, lddy), rows, outer, !readable(w, outer, ldw), outer,
+                           inner);
 }
 
 tide_status tide_linear_grad_input(int64_t rows, int64_t inner, int64_t outer, const void* dy, int64_t lddy,
@@ -213,28 +295,30 @@ tide_status tide_linear_grad_input(int64_t rows, int64_t inner, int64_t outer, c
   TIDE_TRY(check_matrix(dx, rows, inner, lddx, 2, "dx"));
   TIDE_TRY(check_workspace(workspace, workspace_bytes,
                            tide_linear_grad_input_workspace(rows, inner, outer, dy, lddy, w, ldw)));
-  GemmArgs g{};
-  g.m = rows, g.n = inner, g.k = outer;
-  g.a = (const bf16*)dy, g.a_m = lddy, g.a_k = 1;
-  g.b = (const bf16*)w, g.b_n = 1, g.b_k = ldw;
-  g.act = act, g.grad = true;
-  g.zin = (const bf16*)z, g.ldzin = ldz;
-  g.cin = codes, g.ldcin = ld_codes, g.sin = scales, g.ldsin = ld_scales;
-  g.out = (bf16*)dx, g.ldo = lddx;
-  return gemm(g, (cudaStream_t)stream);
+  EpilogueArgs e{};
+  e.act = act;
+  e.zin = (const bf16*)z, e.ldzin = ldz;
+  e.cin = codes, e.ldcin = ld_codes, e.sin = scales, e.ldsin = ld_scales;
+  e.out = (bf16*)dx, e.ldo = lddx;
+  e.vec = rows_aligned(dx, lddx, 2, rows) &&
+          (act == TIDE_ACT_NONE || (z ? rows_aligned(z, ldz, 2, rows) : rows_aligned(codes, ld_codes, 1, rows)));
+  return product<EPI_GRAD_INPUT>(rows, inner, outer, {(const bf16*)dy, rows, outer, lddy}, false,
+                                 {(const bf16*)w, outer, inner, ldw}, true, e, launch_grad_input,
+                                 (unsigned char*)workspace, (cudaStream_t)stream);
 }
 
-int64_t tide_linear_grad_weight_workspace(int64_t rows, int64_t inner, int64_t outer, const void*, int64_t,
-                                          const void* x, int64_t) {
-  if (rows <= 0 || inner <= 0 || outer <= 0 || x) return 0;
-  return rows * packed_ld(inner) * 2;
+int64_t tide_linear_grad_weight_workspace(int64_t rows, int64_t inner, int64_t outer, const void* dy, int64_t lddy,
+                                          const void* x, int64_t ldx) {
+  return product_workspace(outer, inner, rows, !readable(dy, rows, lddy), rows, outer, !x || !readable(x, rows, ldx),
+                           rows, inner);
 }
 
 tide_status tide_linear_grad_weight(int64_t rows, int64_t inner, int64_t outer, const void* dy, int64_t lddy,
                                     const void* x, int64_t ldx, const uint8_t* codes, int64_t ld_codes,
                                     const uint8_t* scales, int64_t ld_scales, int32_t act, void* dw, int64_t lddw,
-                                    void* db, void* workspace, int64_t workspace_bytes, void* stream) {
+                                    void* db, void* workspace, int64_t workspace_bytes, void* stream_) {
   clear_error();
+  const cudaStream_t stream = (cudaStream_t)stream_;
   TIDE_TRY(check_product(rows, inner, outer));
   TIDE_TRY(check_act(act));
   if (outer == 0) return TIDE_OK;
@@ -251,24 +335,54 @@ tide_status tide_linear_grad_weight(int64_t rows, int64_t inner, int64_t outer, 
   TIDE_TRY(check_workspace(workspace, workspace_bytes,
                            tide_linear_grad_weight_workspace(rows, inner, outer, dy, lddy, x, ldx)));
   if (inner > 0) {
-    GemmArgs g{};
-    g.m = outer, g.n = inner, g.k = rows;
-    g.a = (const bf16*)dy, g.a_m = 1, g.a_k = lddy;
-    g.b = (const bf16*)x, g.b_n = 1, g.b_k = ldx;
+    unsigned char* at = (unsigned char*)workspace;
+    Operand b{(const bf16*)x, rows, inner, ldx};
     if (!x && rows > 0) {
-      TIDE_TRY(launch_checkpoint_load_bf16(rows, inner, codes, ld_codes, scales, ld_scales, act, workspace,
-                                           packed_ld(inner), (cudaStream_t)stream));
-      g.b = (const bf16*)workspace, g.b_k = packed_ld(inner);
+      TIDE_TRY(launch_checkpoint_load_bf16(rows, inner, codes, ld_codes, scales, ld_scales, act, at, packed_ld(inner),
+                                           stream));
+      b.p = (const bf16*)at, b.ld = packed_ld(inner);
+      at += packed_bytes(rows, inner);
     }
-    g.out = (bf16*)dw, g.ldo = lddw;
-    TIDE_TRY(gemm(g, (cudaStream_t)stream));
+    EpilogueArgs e{};
+    e.out = (bf16*)dw, e.ldo = lddw;
+    e.vec = rows_aligned(dw, lddw, 2, outer);
+    TIDE_TRY(product<EPI_PLAIN>(outer, inner, rows, {(const bf16*)dy, rows, outer, lddy}, true, b, true, e,
+                                launch_grad_weight, at, stream));
   }
   if (db) {
-    column_sum_kernel<<<(unsigned)((outer + 31) / 32), 1024, 0, (cudaStream_t)stream>>>(
-        rows, outer, (const bf16*)dy, lddy, (bf16*)db);
+    column_sum_kernel<<<(unsigned)((outer + 31) / 32), 1024, 0, stream>>>(rows, outer, (const bf16*)dy, lddy, (bf16*)db);
     return cuda_status(cudaGetLastError(), "bias gradient");
   }
   return TIDE_OK;
+}
+
+tide_status tide_ops_check(void) {
+  clear_error();
+  int32_t* word = nullptr;
+  TIDE_TRY(ops_status_word(&word));
+  cudaError_t err = cudaDeviceSynchronize();
+  int32_t got = 0;
+  if (err == cudaSuccess) err = cudaMemcpy(&got, word, sizeof got, cudaMemcpyDeviceToHost);
+  if (err == cudaSuccess && got) err = cudaMemset(word, 0, sizeof got);
+  TIDE_TRY(cuda_status(err, "reading the operators' status word"));
+  if (got & TIDE_DEVICE_TIMEOUT)
+    return fail(TIDE_ERR_TIMEOUT, "an operator's kernel gave up a bounded wait; its outputs are undefined");
+  return TIDE_OK;
+}
+
+tide_status tide_ops_set_option(int32_t option, int64_t value) {
+  clear_error();
+  switch (option) {
+    case TIDE_OPS_OPT_WAIT_LIMIT_NS:
+      if (value <= 0) return fail(TIDE_ERR_INVALID_ARG, "the wait limit must be positive");
+      g_wait_limit_ns.store(value);
+      return TIDE_OK;
+    case TIDE_OPS_OPT_TEST_DROP_LOAD:
+      if (value < -1) return fail(TIDE_ERR_INVALID_ARG, "the load to withhold must be -1 or more");
+      g_test_drop.store(value);
+      return TIDE_OK;
+    default: return fail(TIDE_ERR_INVALID_ARG, "unknown option");
+  }
 }
 
 }  // extern "C"

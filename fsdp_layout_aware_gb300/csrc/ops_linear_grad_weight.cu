@@ -1,0 +1,10 @@
+// dW = dy^T X: the summed axis (tokens) outermost in both.
+#include "gemm_tc.cuh"
+
+namespace tide {
+
+cudaError_t launch_grad_weight(const TcArgs& p, const TcLaunch& l, bool partial, cudaStream_t stream) {
+  return launch_layout<true, true, EPI_PLAIN>(p, l, partial, stream);
+}
+
+}  // namespace tide

@@ -19,6 +19,7 @@ from .tide import TideError, _check, _lib, _stream
 TIDE_BF16, TIDE_F32 = 0, 1
 TIDE_ACT_NONE, TIDE_ACT_RELU, TIDE_ACT_GELU, TIDE_ACT_GELU_ERF, TIDE_ACT_SILU = range(5)
 ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_erf": 3, "silu": 4, None: 0, 0: 0, 1: 1, 2: 2, 3: 3, 4: 4}
+TIDE_OPS_OPT_WAIT_LIMIT_NS, TIDE_OPS_OPT_TEST_DROP_LOAD = 1, 2
 TIDE_CKPT_BLOCK = 32  # columns that share a scale
 
 _DTYPES = {torch.bfloat16: TIDE_BF16, torch.float32: TIDE_F32}
@@ -28,6 +29,8 @@ _MAT = [_vp, _i64]  # address, row stride
 
 def _declare():
     sig = {
+        "tide_ops_check": (_i32, []),
+        "tide_ops_set_option": (_i32, [_i32, _i64]),
         "tide_checkpoint_store": (_i32, [_i64, _i64, _i32] + 3 * _MAT + [_vp]),
         "tide_checkpoint_load": (_i32, [_i64, _i64] + 2 * _MAT + [_i32, _i32] + 2 * _MAT + [_vp]),
         "tide_rms_norm": (_i32, [_i64, _i64, _i32] + 2 * _MAT + [_vp, ctypes.c_float] + 2 * _MAT + [_vp] + 2 * _MAT +
@@ -160,6 +163,15 @@ def _workspace(given, need, stream):
         # The block must not go to another call of the allocating stream while this one still uses it.
         ws.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream))
     return ws, ws.data_ptr(), need
+
+
+def tide_ops_check():
+    """Synchronise and raise TideError(TIDE_ERR_TIMEOUT) if an operator's kernel gave up a wait on this device."""
+    _check(_lib.tide_ops_check())
+
+
+def tide_ops_set_option(option, value):
+    _check(_lib.tide_ops_set_option(option, value))
 
 
 def tide_checkpoint_store(x, ckpt, stream=None):

@@ -13,8 +13,9 @@
  *     pointers are aligned to their element size; no other alignment is asked
  *     for (16-byte aligned rows are faster).
  *   - All calls enqueue work on `stream` of the current device, allocate
- *     nothing and can be captured into a CUDA graph.  A call with nothing to
- *     write returns TIDE_OK.
+ *     nothing and can be captured into a CUDA graph (after a first call of
+ *     the kind, which loads its kernels).  A call with nothing to write
+ *     returns TIDE_OK.
  *   - Arithmetic is fp32 whatever the tensors' type; each output is rounded
  *     once, to nearest even, when it is stored.  Results do not depend on
  *     timing: the same call gives the same bits.
@@ -53,6 +54,23 @@ typedef enum tide_act {
   TIDE_ACT_GELU_ERF = 3,
   TIDE_ACT_SILU = 4
 } tide_act;
+
+/* Synchronise the current device and report whether a kernel of the linear
+ * layer gave up a bounded wait there since the last check (TIDE_ERR_TIMEOUT;
+ * the flag is then cleared).  Such a call's outputs are undefined.  Errors:
+ * CUDA. */
+tide_status tide_ops_check(void);
+
+/* Process-wide options.
+ *   TIDE_OPS_OPT_WAIT_LIMIT_NS   bound, in nanoseconds, on every wait inside
+ *                                the linear layer's kernels (default 2e9)
+ *   TIDE_OPS_OPT_TEST_DROP_LOAD  test hook: a product's CTAs withhold the
+ *                                loads of the given block of 64 of the summed
+ *                                axis (counted per CTA from 0), so a bounded
+ *                                wait runs out; -1 (default) disables
+ * Errors: INVALID_ARG. */
+typedef enum tide_ops_option { TIDE_OPS_OPT_WAIT_LIMIT_NS = 1, TIDE_OPS_OPT_TEST_DROP_LOAD = 2 } tide_ops_option;
+tide_status tide_ops_set_option(int32_t option, int64_t value);
 
 /* ---- 8-bit checkpoints ----------------------------------------------------
  * A matrix kept in 8 bits: `codes` [rows, cols] e4m3 bytes (row stride

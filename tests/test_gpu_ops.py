@@ -621,3 +621,76 @@ def test_refusals():
     torch.cuda.synchronize()
     tide.tide_linear(x, w, y, bias=b)
     torch.cuda.synchronize()
+
+
+# ---------------------------------------------------------------- the pair-of-CTAs product, and bounded waits
+
+BIG = [(2100, 200, 3100), (4096, 520, 2304), (2049, 1030, 2570), (3333, 72, 4100)]  # rows, inner, outer
+
+
+@pytest.mark.parametrize("rows,inner,outer", BIG)
+def test_large_products(rows, inner, outer):
+    """Sizes that take 256 x 256 tiles, whole and ragged, against fp64 on the GPU."""
+    x, w = rand((rows, inner), BF, 1).to(DEV), rand((outer, inner), BF, 2, scale=inner ** -0.5).to(DEV)
+    b, r = rand((outer,), BF, 3).to(DEV), rand((rows, outer), BF, 4).to(DEV)
+    xd, wd = x.double(), w.double()
+
+    def near(got, want, size, k, what):
+        # the output's rounding and the accumulation's (R.product_bound)
+        tol = R.BF16 * want.abs() + ((k / 16 + 16) * R.FP32) * size + 64 * R.FP32 * (want.abs() + 20)
+        over = (got.double() - want).abs() - tol
+        assert over.max().item() <= 0, (what, over.max().item())
+
+    z = xd @ wd.t() + b.double()
+    size = xd.abs() @ wd.abs().t() + b.double().abs()
+    y, kz, k8 = (torch.empty(rows, outer, dtype=BF, device=DEV), torch.empty(rows, outer, dtype=BF, device=DEV),
+                 tide.Checkpoint8.empty(rows, outer))
+    tide.tide_linear(x, w, y, bias=b, act="silu", residual=r, z=kz)
+    near(kz, z, size, inner, "z")
+    near(y, z * torch.sigmoid(z) + r.double(), 1.13 * size, inner, "y")
+    tide.tide_linear(x, w, y, bias=b, z=k8)
+    near(y, z, size, inner, "plain y")
+    back = torch.empty(rows, outer, device=DEV)
+    tide.tide_checkpoint_load(k8, back)
+    s = torch.exp2(k8.scales.double() - 127).repeat_interleave(32, 1)[:, :outer]
+    # half the gap between codes, and the product's own error
+    over = (back.double() - z).abs() - torch.maximum(2.0 ** -4 * z.abs(), 2.0 ** -10 * s) - (inner / 16 + 16) * R.FP32 * size
+    assert over.max().item() <= 0
+    zv = back.double()
+    dx = torch.empty(rows, outer, dtype=BF, device=DEV)
+    wt = rand((inner, outer), BF, 5, scale=inner ** -0.5).to(DEV)
+    tide.tide_linear_grad_input(x, wt, dx, act="silu", z=k8)
+    p = torch.sigmoid(zv)
+    f = p + zv * p * (1 - p)
+    near(dx, (xd @ wt.double()) * f, 1.13 * (xd.abs() @ wt.double().abs()), inner, "dx")
+    dw, db = torch.empty(outer, inner, dtype=BF, device=DEV), torch.empty(outer, dtype=BF, device=DEV)
+    tide.tide_linear_grad_weight(r, x, dw, db=db)
+    near(dw, r.double().t() @ xd, r.double().abs().t() @ xd.abs(), rows, "dw")
+    near(db, r.double().sum(0), r.double().abs().sum(0), rows, "db")
+    big = torch.empty(outer, outer, dtype=BF, device=DEV)
+    tide.tide_linear_grad_weight(r, k8, big)
+    near(big, r.double().t() @ zv, r.double().abs().t() @ zv.abs(), rows, "dw of a checkpoint")
+    tide.tide_ops_check()
+
+
+@pytest.mark.parametrize("rows,inner,outer", [(64, 4096, 256), (2100, 1024, 3100)])
+def test_a_wait_that_runs_out_is_reported(rows, inner, outer):
+    """A block whose loads are withheld: the kernels give up in time, say so once, and the next call is right."""
+    x, w = rand((rows, inner), BF, 1).to(DEV), rand((outer, inner), BF, 2).to(DEV)
+    y, want = (torch.empty(rows, outer, dtype=BF, device=DEV) for _ in range(2))
+    tide.tide_linear(x, w, want)
+    tide.tide_ops_check()
+    tide.tide_ops_set_option(tide.TIDE_OPS_OPT_WAIT_LIMIT_NS, 20_000_000)
+    tide.tide_ops_set_option(tide.TIDE_OPS_OPT_TEST_DROP_LOAD, 2)
+    try:
+        tide.tide_linear(x, w, y)
+        with pytest.raises(tide.TideError) as e:
+            tide.tide_ops_check()
+        assert e.value.status == 8
+    finally:
+        tide.tide_ops_set_option(tide.TIDE_OPS_OPT_TEST_DROP_LOAD, -1)
+        tide.tide_ops_set_option(tide.TIDE_OPS_OPT_WAIT_LIMIT_NS, 2_000_000_000)
+    tide.tide_ops_check()
+    tide.tide_linear(x, w, y)
+    tide.tide_ops_check()
+    assert torch.equal(y, want)

@@ -106,9 +106,9 @@ def test_arguments_are_checked_on_the_host(f, args, status):
 def test_every_declared_operator_is_exported_and_bound():
     text = open(os.path.join(ROOT, "include", "tide_ops.h")).read()
     names = set(re.findall(r"^\w+ (tide_\w+)\(", text, re.M))
-    assert len(names) == 11
+    assert len(names) == 13
     for n in names:
-        assert getattr(lib(), n).argtypes, n
+        assert getattr(lib(), n).argtypes is not None, n
 
 
 def test_header_is_plain_c(tmp_path):
@@ -146,3 +146,9 @@ def test_reference_derivatives(name):
     num = (R.act(name, z + d) - R.act(name, z - d)) / (2 * d)
     assert np.abs(num - R.act_grad(name, z)).max() < 1e-8
     assert R.act_grad(name, np.array([np.inf]))[0] == 1
+
+
+def test_options():
+    for option, value, status in ((1, 0, INVALID), (1, -5, INVALID), (2, -2, INVALID), (3, 1, INVALID), (2, -1, OK),
+                                  (1, 2_000_000_000, OK)):
+        assert lib().tide_ops_set_option(option, value) == status
