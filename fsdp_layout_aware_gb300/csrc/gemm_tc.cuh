@@ -131,20 +131,11 @@ __device__ __forceinline__ void epilogue_row(const EpilogueArgs& e, int split, i
     }
     if (e.z) store32(e.z + row * e.ldz + col, v);
     if (e.codes) {
-      float m = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        t[i] = finite_or_nan(v[i]);
-        m = fmaxf(m, fabsf(t[i]));
-      }
-      const int byte = scale_byte(m);
-      const float inv = scale_inverse(byte);
+      for (int i = 0; i < 32; ++i) t[i] = v[i];
+      const int byte = scale_byte(block_magnitude<1>(t));
       uint32_t w[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        w[i] = e4m3_pair(clamp_top(t[4 * i] * inv, byte), clamp_top(t[4 * i + 1] * inv, byte)) |
-               e4m3_pair(clamp_top(t[4 * i + 2] * inv, byte), clamp_top(t[4 * i + 3] * inv, byte)) << 16;
-      }
+      encode(t, byte, w);
       uint4* c = reinterpret_cast<uint4*>(e.codes + row * e.ldc + col);
       c[0] = make_uint4(w[0], w[1], w[2], w[3]);
       c[1] = make_uint4(w[4], w[5], w[6], w[7]);
@@ -204,7 +195,7 @@ __device__ __forceinline__ void epilogue_element(const EpilogueArgs& e, int64_t 
       const uint32_t m = __reduce_max_sync(0xffffffffu, in ? __float_as_uint(fmaxf(fabsf(t), 0.0f)) : 0u);
       const int byte = scale_byte(__uint_as_float(m));
       if (in) {
-        e.codes[row * e.ldc + col] = (uint8_t)e4m3_pair(clamp_top(t * scale_inverse(byte), byte), 0.0f);
+        e.codes[row * e.ldc + col] = encode_one(t, byte);
         if (col % kMxBlock == 0) e.scales[row * e.lds + col / kMxBlock] = (uint8_t)byte;
       }
     }

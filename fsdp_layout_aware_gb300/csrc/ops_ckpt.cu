@@ -4,6 +4,8 @@
 // so they are bound by memory traffic: store reads s bytes and writes 1 + 1/32
 // per element, load reads 1 + 1/32 (and s for a gradient) and writes s.
 
+#include <algorithm>
+
 #include "ops_common.cuh"
 
 namespace tide {
@@ -11,133 +13,202 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// A thread owns eight neighbouring columns, four neighbouring lanes a block of
-// 32: the block's largest magnitude takes two shuffles.  Rows start on 16-byte
-// boundaries (x) and 8-byte ones (codes).
+struct StoreArgs {
+  uint32_t items;   // units of work (store_vec: 8 columns, store_any: kAnyBlocks blocks) in this launch
+  FastDiv per_row;  // of them in a row
+  int64_t cols;
+  const void* x;
+  int64_t ldx;
+  uint8_t* codes;
+  int64_t ldc;
+  uint8_t* scales;
+  int64_t lds;
+};
+
+struct LoadArgs {
+  uint32_t items;
+  FastDiv per_row;
+  int64_t cols;
+  const uint8_t* codes;
+  int64_t ldc;
+  const uint8_t* scales;
+  int64_t lds;
+  int act;
+  const void* grad;
+  int64_t ldg;
+  void* out;
+  int64_t ldo;
+};
+
+// Aligned rows: a thread owns eight neighbouring columns, four neighbouring
+// lanes a block of 32, whose largest magnitude takes two shuffles.  kItems such
+// groups a thread, all loads first, keep enough bytes in flight.  Rows start
+// on 16-byte boundaries (x) and 8-byte ones (codes).
+constexpr int kItems = 4;
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads) store_vec_kernel(int64_t rows, int64_t cols, const T* __restrict__ x,
-                                                             int64_t ldx, uint8_t* __restrict__ codes, int64_t ldc,
-                                                             uint8_t* __restrict__ scales, int64_t lds) {
-  const int64_t per_row = (cols + kMxBlock - 1) / kMxBlock * 4;  // threads a row
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int64_t row = i / per_row;
-  const int64_t col = (i - row * per_row) * 8;
-  float v[8];
-  float a = 0.0f;
-  const bool here = row < rows && col < cols;
-  if (here) {
-    load_vec<8>(x + row * ldx + col, v);
+__global__ void __launch_bounds__(kThreads) store_vec_kernel(const StoreArgs a) {
+  float v[kItems][8];
+  int64_t row[kItems], col[kItems];
+  bool here[kItems];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      v[k] = finite_or_nan(v[k]);
-      a = fmaxf(a, fabsf(v[k]));
+  for (int j = 0; j < kItems; ++j) {
+    const uint32_t i = (blockIdx.x * kItems + j) * kThreads + threadIdx.x;
+    const uint32_t r = a.per_row.quotient(i);
+    row[j] = r;
+    col[j] = (int64_t)(i - r * a.per_row.d) * 8;
+    here[j] = i < a.items && col[j] < a.cols;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[j][k] = 0.0f;
+    if (here[j]) load_vec<8>((const T*)a.x + row[j] * a.ldx + col[j], v[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < kItems; ++j) {
+    const int byte = scale_byte(block_magnitude<4>(v[j]));
+    uint32_t w[2];
+    encode(v[j], byte, w);
+    if (!here[j]) continue;
+    *reinterpret_cast<uint2*>(a.codes + row[j] * a.ldc + col[j]) = make_uint2(w[0], w[1]);
+    if (col[j] % kMxBlock == 0) a.scales[row[j] * a.lds + col[j] / kMxBlock] = (uint8_t)byte;
+  }
+}
+
+// Any alignment: a warp takes kAnyBlocks neighbouring blocks of a row, one
+// element a lane.
+constexpr int kAnyBlocks = 4;
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) store_any_kernel(const StoreArgs a) {
+  const uint32_t i = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+  if (i >= a.items) return;
+  const uint32_t lane = threadIdx.x % 32;
+  const int64_t row = a.per_row.quotient(i);
+  const int64_t first = (int64_t)(i - (uint32_t)row * a.per_row.d) * (kAnyBlocks * kMxBlock);
+  float v[kAnyBlocks][1];
+#pragma unroll
+  for (int j = 0; j < kAnyBlocks; ++j) {
+    const int64_t col = first + j * kMxBlock + lane;
+    v[j][0] = 0.0f;
+    if (col < a.cols) load_vec<1>((const T*)a.x + row * a.ldx + col, v[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < kAnyBlocks; ++j) {
+    const int64_t col = first + j * kMxBlock + lane;
+    const float t = finite_or_nan(v[j][0]);
+    // Magnitudes order as their bits do; fmaxf leaves NaN out.
+    const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fabsf(t), 0.0f)));
+    const int byte = scale_byte(__uint_as_float(m));
+    if (col < a.cols) {
+      a.codes[row * a.ldc + col] = encode_one(t, byte);
+      if (lane == 0) a.scales[row * a.lds + col / kMxBlock] = (uint8_t)byte;
     }
   }
-  a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-  a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
-  if (!here) return;
-  const int byte = scale_byte(a);
-  const float inv = scale_inverse(byte);
-  uint32_t w[2] = {0, 0};
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    w[k / 2] |= e4m3_pair(clamp_top(v[2 * k] * inv, byte), clamp_top(v[2 * k + 1] * inv, byte)) << (16 * (k % 2));
-  *reinterpret_cast<uint2*>(codes + row * ldc + col) = make_uint2(w[0], w[1]);
-  if (col % kMxBlock == 0) scales[row * lds + col / kMxBlock] = (uint8_t)byte;
 }
 
-// Any alignment: a warp takes a block of 32 columns, one element a lane.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) store_any_kernel(int64_t rows, int64_t cols, const T* __restrict__ x,
-                                                             int64_t ldx, uint8_t* __restrict__ codes, int64_t ldc,
-                                                             uint8_t* __restrict__ scales, int64_t lds) {
-  const int64_t blocks = (cols + kMxBlock - 1) / kMxBlock;
-  const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / 32;
-  const int64_t row = i / blocks;
-  if (row >= rows) return;
-  const int64_t b = i - row * blocks, col = b * kMxBlock + threadIdx.x % 32;
-  float v[1] = {0.0f};
-  if (col < cols) load_vec<1>(x + row * ldx + col, v);
-  v[0] = finite_or_nan(v[0]);
-  // Magnitudes order as their bits do.
-  const uint32_t a = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fabsf(v[0]), 0.0f)));
-  const int byte = scale_byte(__uint_as_float(a));
-  if (col < cols)
-    codes[row * ldc + col] = (uint8_t)e4m3_pair(clamp_top(v[0] * scale_inverse(byte), byte), 0.0f);
-  if (threadIdx.x % 32 == 0) scales[row * lds + b] = (uint8_t)byte;
-}
-
-template <typename T>
-__device__ __forceinline__ float loaded(float value, int act, bool has_grad, float grad) {
+// fp32 outputs take the accurate exponential and division.
+template <typename T, int N>
+__device__ __forceinline__ void loaded(float (&v)[N], int act, bool has_grad, const float (&g)[N]) {
   constexpr bool fast = sizeof(T) == 2;
-  return has_grad ? grad * act_grad<fast>(act, value) : act_value<fast>(act, value);
-}
-
-// Eight neighbouring columns a thread; rows on 16-byte (out, grad) and 8-byte
-// (codes) boundaries.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) load_vec_kernel(int64_t rows, int64_t cols,
-                                                            const uint8_t* __restrict__ codes, int64_t ldc,
-                                                            const uint8_t* __restrict__ scales, int64_t lds, int act,
-                                                            const T* grad, int64_t ldg, T* out, int64_t ldo) {
-  const int64_t per_row = cols / 8;
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int64_t row = i / per_row;
-  if (row >= rows) return;
-  const int64_t col = (i - row * per_row) * 8;
-  const uint2 c = *reinterpret_cast<const uint2*>(codes + row * ldc + col);
-  const float s = scale_value(scales[row * lds + col / kMxBlock]);
-  float g[8] = {};
-  if (grad) load_vec<8>(grad + row * ldg + col, g);
-  float v[8];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float2 t = e4m3_values(((k < 2 ? c.x : c.y) >> (16 * (k % 2))) & 0xffffu);
-    v[2 * k] = loaded<T>(t.x * s, act, grad != nullptr, g[2 * k]);
-    v[2 * k + 1] = loaded<T>(t.y * s, act, grad != nullptr, g[2 * k + 1]);
+  for (int k = 0; k < N; ++k) v[k] = has_grad ? g[k] * act_grad<fast>(act, v[k]) : act_value<fast>(act, v[k]);
+}
+
+// Eight neighbouring columns a thread and item; rows on 16-byte (out, grad)
+// and 8-byte (codes) boundaries.
+template <typename T, bool GRAD>
+__global__ void __launch_bounds__(kThreads) load_vec_kernel(const LoadArgs a) {
+  uint2 c[kItems];
+  uint8_t s[kItems];
+  float g[kItems][8];
+  int64_t row[kItems], col[kItems];
+  bool here[kItems];
+#pragma unroll
+  for (int j = 0; j < kItems; ++j) {
+    const uint32_t i = (blockIdx.x * kItems + j) * kThreads + threadIdx.x;
+    const uint32_t r = a.per_row.quotient(i);
+    row[j] = r;
+    here[j] = i < a.items;
+    col[j] = (int64_t)(i - r * a.per_row.d) * 8;
+    if (here[j]) {
+      c[j] = *reinterpret_cast<const uint2*>(a.codes + row[j] * a.ldc + col[j]);
+      s[j] = a.scales[row[j] * a.lds + col[j] / kMxBlock];
+      if (GRAD) load_vec<8>((const T*)a.grad + row[j] * a.ldg + col[j], g[j]);
+    }
   }
-  store_vec<8>(out + row * ldo + col, v);
+#pragma unroll
+  for (int j = 0; j < kItems; ++j) {
+    if (!here[j]) continue;
+    float v[8];
+    decode8(c[j], scale_value(s[j]), v);
+    loaded<T>(v, a.act, GRAD, g[j]);
+    store_vec<8>((T*)a.out + row[j] * a.ldo + col[j], v);
+  }
 }
 
-// Any alignment: neighbouring lanes on neighbouring elements.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) load_any_kernel(int64_t rows, int64_t cols,
-                                                            const uint8_t* __restrict__ codes, int64_t ldc,
-                                                            const uint8_t* __restrict__ scales, int64_t lds, int act,
-                                                            const T* grad, int64_t ldg, T* out, int64_t ldo) {
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int64_t row = i / cols;
-  if (row >= rows) return;
-  const int64_t col = i - row * cols;
-  const float value = e4m3_values(codes[row * ldc + col]).x * scale_value(scales[row * lds + col / kMxBlock]);
-  float g[1] = {0.0f};
-  if (grad) load_vec<1>(grad + row * ldg + col, g);
-  const float v[1] = {loaded<T>(value, act, grad != nullptr, g[0])};
-  store_vec<1>(out + row * ldo + col, v);
+// Any alignment: a warp takes kAnyBlocks neighbouring blocks of a row, one
+// element a lane.
+template <typename T, bool GRAD>
+__global__ void __launch_bounds__(kThreads) load_any_kernel(const LoadArgs a) {
+  const uint32_t i = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+  if (i >= a.items) return;
+  const uint32_t lane = threadIdx.x % 32;
+  const int64_t row = a.per_row.quotient(i);
+  const int64_t first = (int64_t)(i - (uint32_t)row * a.per_row.d) * (kAnyBlocks * kMxBlock);
+  uint8_t c[kAnyBlocks], s[kAnyBlocks];
+  float g[kAnyBlocks][1];
+#pragma unroll
+  for (int j = 0; j < kAnyBlocks; ++j) {
+    const int64_t col = first + j * kMxBlock + lane;
+    g[j][0] = 0.0f;
+    c[j] = s[j] = 0;
+    if (col < a.cols) {
+      c[j] = a.codes[row * a.ldc + col];
+      s[j] = a.scales[row * a.lds + col / kMxBlock];
+      if (GRAD) load_vec<1>((const T*)a.grad + row * a.ldg + col, g[j]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kAnyBlocks; ++j) {
+    const int64_t col = first + j * kMxBlock + lane;
+    if (col >= a.cols) continue;
+    float v[1] = {e4m3_values(c[j]).x * scale_value(s[j])};
+    loaded<T>(v, a.act, GRAD, g[j]);
+    store_vec<1>((T*)a.out + row * a.ldo + col, v);
+  }
 }
 
-// Blocks for rows * per_row threads; UNIMPLEMENTED past the grid limit (over
-// 1.7e10 blocks of 32).
-tide_status grid_for(int64_t rows, int64_t per_row, unsigned int* grid) {
-  if (rows > (int64_t)INT32_MAX * kThreads / per_row)
-    return fail(TIDE_ERR_UNIMPLEMENTED, "matrix has too many elements for one launch");
-  *grid = (unsigned int)((rows * per_row + kThreads - 1) / kThreads);
+// Calls launch(first row, rows, items, grid) until every row is done: a launch
+// has fewer than 2^31 items (per_row in a row, per_block in a block).
+template <typename F>
+tide_status in_launches(int64_t rows, int64_t per_row, int per_block, F&& launch) {
+  const int64_t most = ((int64_t)1 << 31) - 65536;
+  if (per_row > most || rows > ((int64_t)1 << 42) / per_row) return fail(TIDE_ERR_UNIMPLEMENTED, "matrix has more elements than any GPU holds");
+  const int64_t step = most / per_row;
+  for (int64_t r = 0; r < rows; r += step) {
+    const int64_t n = std::min(step, rows - r), items = n * per_row;
+    launch(r, (uint32_t)items, (unsigned)((items + per_block - 1) / per_block));
+    TIDE_TRY(cuda_status(cudaGetLastError(), "checkpoint"));
+  }
   return TIDE_OK;
 }
+
+int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 template <typename T>
 tide_status store(int64_t rows, int64_t cols, const void* x, int64_t ldx, uint8_t* codes, int64_t ldc, uint8_t* scales,
                   int64_t lds, cudaStream_t stream) {
-  const int64_t blocks = (cols + kMxBlock - 1) / kMxBlock;
+  const int64_t blocks = div_up(cols, kMxBlock);
   const bool vec = cols % 8 == 0 && rows_aligned(x, ldx, sizeof(T), rows) && (uintptr_t)codes % 8 == 0 &&
                    (rows <= 1 || ldc % 8 == 0);
-  unsigned int grid;
-  TIDE_TRY(grid_for(rows, blocks * (vec ? 4 : 32), &grid));
-  if (vec)
-    store_vec_kernel<T><<<grid, kThreads, 0, stream>>>(rows, cols, (const T*)x, ldx, codes, ldc, scales, lds);
-  else
-    store_any_kernel<T><<<grid, kThreads, 0, stream>>>(rows, cols, (const T*)x, ldx, codes, ldc, scales, lds);
-  return cuda_status(cudaGetLastError(), "checkpoint store");
+  const int64_t per_row = vec ? blocks * 4 : div_up(blocks, kAnyBlocks);
+  return in_launches(rows, per_row, vec ? kThreads * kItems : kThreads / 32, [&](int64_t r, uint32_t items, unsigned grid) {
+    const StoreArgs a{items, FastDiv((uint32_t)per_row), cols, (const T*)x + r * ldx, ldx, codes + r * ldc, ldc,
+                      scales + r * lds, lds};
+    if (vec)
+      store_vec_kernel<T><<<grid, kThreads, 0, stream>>>(a);
+    else
+      store_any_kernel<T><<<grid, kThreads, 0, stream>>>(a);
+  });
 }
 
 template <typename T>
@@ -145,15 +216,19 @@ tide_status load(int64_t rows, int64_t cols, const uint8_t* codes, int64_t ldc, 
                  int32_t act, const void* grad, int64_t ldg, void* out, int64_t ldo, cudaStream_t stream) {
   const bool vec = cols % 8 == 0 && rows_aligned(grad, ldg, sizeof(T), rows) &&
                    rows_aligned(out, ldo, sizeof(T), rows) && (uintptr_t)codes % 8 == 0 && (rows <= 1 || ldc % 8 == 0);
-  unsigned int grid;
-  TIDE_TRY(grid_for(rows, vec ? cols / 8 : cols, &grid));
-  if (vec)
-    load_vec_kernel<T><<<grid, kThreads, 0, stream>>>(rows, cols, codes, ldc, scales, lds, act, (const T*)grad, ldg,
-                                                      (T*)out, ldo);
-  else
-    load_any_kernel<T><<<grid, kThreads, 0, stream>>>(rows, cols, codes, ldc, scales, lds, act, (const T*)grad, ldg,
-                                                      (T*)out, ldo);
-  return cuda_status(cudaGetLastError(), "checkpoint load");
+  const int64_t per_row = vec ? cols / 8 : div_up(div_up(cols, kMxBlock), kAnyBlocks);
+  return in_launches(rows, per_row, vec ? kThreads * kItems : kThreads / 32, [&](int64_t r, uint32_t items, unsigned grid) {
+    const LoadArgs a{items, FastDiv((uint32_t)per_row), cols, codes + r * ldc, ldc, scales + r * lds, lds, act,
+                     grad ? (const T*)grad + r * ldg : nullptr, ldg, (T*)out + r * ldo, ldo};
+    if (vec && grad)
+      load_vec_kernel<T, true><<<grid, kThreads, 0, stream>>>(a);
+    else if (vec)
+      load_vec_kernel<T, false><<<grid, kThreads, 0, stream>>>(a);
+    else if (grad)
+      load_any_kernel<T, true><<<grid, kThreads, 0, stream>>>(a);
+    else
+      load_any_kernel<T, false><<<grid, kThreads, 0, stream>>>(a);
+  });
 }
 
 }  // namespace

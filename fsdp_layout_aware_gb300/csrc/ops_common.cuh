@@ -69,6 +69,24 @@ inline bool rows_aligned(const void* p, int64_t ld, int64_t elem, int64_t rows) 
 // SMs of the current device (asked once per device); 0 if the query failed.
 int ops_num_sms();
 
+// Division of 32-bit numbers below 2^31 by a fixed one: a multiplication and a
+// shift.  For 2^(s-1) < d <= 2^s, m = ceil(2^(31+s) / d) is below 2^32 and the
+// quotient is floor(n * m / 2^(31+s)): the error n * (m d - 2^(31+s)) / (d
+// 2^(31+s)) is below n / 2^(31+s) <= 1 / d for n < 2^31.
+struct FastDiv {
+  uint32_t d = 1, m = 1u << 31, s = 0;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t div) : d(div) {
+    while ((1ull << s) < d) ++s;
+    m = (uint32_t)(((1ull << (31 + s)) + d - 1) / d);
+  }
+#if defined(__CUDACC__)
+  __device__ __forceinline__ uint32_t quotient(uint32_t n) const {
+    return (uint32_t)(((uint64_t)n * m) >> 31 >> s);
+  }
+#endif
+};
+
 #define TIDE_TRY(expr)                    \
   do {                                    \
     tide_status st_ = (expr);             \
@@ -134,9 +152,6 @@ __device__ __forceinline__ void store_vec(float* p, const float (&v)[V]) {
 
 // ---- 8-bit checkpoints
 
-// Infinities become NaN (0 * inf); finite values and NaN stay.
-__device__ __forceinline__ float finite_or_nan(float v) { return __fmaf_rn(0.0f, v, v); }
-
 // Scale byte of a block whose largest finite magnitude is `a`: the smallest
 // e >= -127 with a <= 448 * 2^e, plus 127.  With a = 1.m * 2^E and
 // 448 = 1.75 * 2^8, e = E - 8 if 1.m <= 1.75, else E - 7.
@@ -151,21 +166,76 @@ __device__ __forceinline__ float scale_value(int byte) {
   return __uint_as_float(byte > 0 ? (uint32_t)byte << 23 : 0x400000u);
 }
 
+// What a checkpoint keeps of a value: infinities become NaN (0 * inf), finite
+// values and NaN stay.
+__device__ __forceinline__ float finite_or_nan(float v) { return __fmaf_rn(0.0f, v, v); }
+
+// Largest magnitude over the N values of each of LANES neighbouring lanes (a
+// power of two) that hold a block; NaN does not count.  Infinities, which are
+// rare, are made NaN in v and the finite values looked at again.  With LANES
+// above 1 the whole warp calls it.
+template <int LANES, int N>
+__device__ __forceinline__ float block_magnitude(float (&v)[N]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int k = 0; k < N; ++k) m = fmaxf(m, fabsf(v[k]));
+#pragma unroll
+  for (int d = 1; d < LANES; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  if (LANES > 1 ? __any_sync(0xffffffffu, isinf(m)) : isinf(m)) {
+    m = 0.0f;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      v[k] = finite_or_nan(v[k]);
+      m = fmaxf(m, fabsf(v[k]));
+    }
+#pragma unroll
+    for (int d = 1; d < LANES; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  }
+  return m;
+}
+
 // Two codes of values already divided by the scale (lo in the low byte).
 __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
 
-// The topmost scale's codes stop at 240: the next value, 256 * 2^120, is
-// beyond fp32.
-__device__ __forceinline__ float clamp_top(float q, int byte) {
-  return byte >= 247 && fabsf(q) > 240.0f ? copysignf(240.0f, q) : q;
+// N values (a multiple of 4) of a block with scale byte `byte` to N / 4 words
+// of codes.  The topmost scale's codes stop at 240: the next value, 256 * 2^120,
+// is beyond fp32.
+template <int N>
+__device__ __forceinline__ void encode(float (&v)[N], int byte, uint32_t (&w)[N / 4]) {
+  const float inv = scale_inverse(byte);
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] *= inv;
+  if (byte >= 247) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = fabsf(v[k]) > 240.0f ? copysignf(240.0f, v[k]) : v[k];
+  }
+#pragma unroll
+  for (int k = 0; k < N / 4; ++k)
+    w[k] = e4m3_pair(v[4 * k], v[4 * k + 1]) | e4m3_pair(v[4 * k + 2], v[4 * k + 3]) << 16;
+}
+// One value.
+__device__ __forceinline__ uint8_t encode_one(float v, int byte) {
+  v *= scale_inverse(byte);
+  if (byte >= 247 && fabsf(v) > 240.0f) v = copysignf(240.0f, v);
+  return (uint8_t)e4m3_pair(v, 0.0f);
 }
 
 // fp32 values of two codes (exact: e4m3 is a subset of fp16).
 __device__ __forceinline__ float2 e4m3_values(uint32_t pair) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)pair, __NV_E4M3);
   return __half22float2(__half2(h));
+}
+
+// Eight values from two words of codes.
+__device__ __forceinline__ void decode8(uint2 c, float scale, float (&v)[8]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 t = e4m3_values(((k < 2 ? c.x : c.y) >> (16 * (k % 2))) & 0xffffu);
+    v[2 * k] = t.x * scale;
+    v[2 * k + 1] = t.y * scale;
+  }
 }
 
 // ---- activations

@@ -14,7 +14,6 @@ namespace tide {
 namespace {
 
 constexpr int kMaxCols = 16384;
-constexpr int kMinBlock = 256;
 
 struct NormArgs {
   int64_t rows, cols;
@@ -51,41 +50,43 @@ struct NormGradArgs {
   int64_t ldres;
   void* dx;
   int64_t lddx;
-  float* partial;  // [groups][cols]: each row group's sum of dy * n; NULL: not wanted
+  float* partial;  // [row groups][cols]: each one's sum of dy * n; NULL: not wanted
 };
 
-// Sum of v over the TPR threads that share a row (TPR a power of two, at least
-// 32); `scratch` has a float per warp.  The order is fixed.
-template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float* scratch) {
+// Sum of v over the threads of a row (blockDim.x, a multiple of 32; threadIdx.y
+// is the row).  One barrier: `turn` alternates the scratch floats, one per
+// warp, so a sum is read before its place is written again.  The order is
+// fixed.
+__device__ __forceinline__ float row_sum(float v, float (&scratch)[2][32], int& turn) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  if constexpr (TPR > 32) {
-    constexpr int warps = TPR / 32;
-    const int warp = threadIdx.x / 32, first = warp / warps * warps;
-    __syncthreads();  // the previous row's sums have been read
-    if (threadIdx.x % 32 == 0) scratch[warp] = v;
+  const int warps = blockDim.x / 32;
+  if (warps > 1) {
+    const int first = threadIdx.y * warps;
+    float* s = scratch[turn];
+    turn ^= 1;
+    if (threadIdx.x % 32 == 0) s[first + threadIdx.x / 32] = v;
     __syncthreads();
     v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < warps; ++w) v += scratch[first + w];
+    for (int w = 0; w < warps; ++w) v += s[first + w];
   }
   return v;
 }
 
-// A row takes TPR threads, each NV vectors of V columns; a block holds
-// blockDim.x / TPR rows.
-template <typename T, int TPR, int V, int NV>
-__global__ void __launch_bounds__(TPR < kMinBlock ? kMinBlock : TPR) norm_kernel(const NormArgs a) {
-  __shared__ float scratch[32];
-  const int lane = threadIdx.x % TPR;
-  const int64_t row = (int64_t)blockIdx.x * (blockDim.x / TPR) + threadIdx.x / TPR;
+// A row takes blockDim.x threads, each NV vectors of V columns; a block holds
+// blockDim.y rows.
+template <typename T, int V, int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a) {
+  __shared__ float scratch[2][32];
+  int turn = 0;
+  const int lane = threadIdx.x;
+  const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const bool here = row < a.rows;
   float s[NV][V];
   float sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int col = (i * TPR + lane) * V;
+    const int col = (i * blockDim.x + lane) * V;
 #pragma unroll
     for (int k = 0; k < V; ++k) s[i][k] = 0.0f;
     if (here && col < a.cols) {
@@ -97,49 +98,39 @@ __global__ void __launch_bounds__(TPR < kMinBlock ? kMinBlock : TPR) norm_kernel
         for (int k = 0; k < V; ++k) s[i][k] += r[k];
       }
     }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int k = 0; k < V; ++k) sum = fmaf(s[i][k], s[i][k], sum);
-  }
-  sum = row_sum<TPR>(sum, scratch);
+  sum = row_sum(sum, scratch, turn);
   const float rstd = 1.0f / sqrtf(sum / (float)a.cols + a.eps);
   if (here && lane == 0 && a.rstd) a.rstd[row] = rstd;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int col = (i * TPR + lane) * V;
+    const int col = (i * blockDim.x + lane) * V;
     const bool in = here && col < a.cols;
     float y[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) y[k] = 0.0f;
     if (in) {
       if (a.h) store_vec<V>((T*)a.h + row * a.ldh + col, s[i]);
       load_vec<V>((const T*)a.weight + col, y);
 #pragma unroll
       for (int k = 0; k < V; ++k) y[k] *= s[i][k] * rstd;
       if (a.y) store_vec<V>((T*)a.y + row * a.ldy + col, y);
-    } else {
-#pragma unroll
-      for (int k = 0; k < V; ++k) y[k] = 0.0f;
     }
     if (a.codes) {
       // 32 / V neighbouring lanes hold a block of 32 columns.
-      float m = 0.0f;
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        y[k] = finite_or_nan(y[k]);
-        m = fmaxf(m, fabsf(y[k]));
-      }
-#pragma unroll
-      for (int d = 1; d < kMxBlock / V; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-      const int byte = scale_byte(m);
-      const float inv = scale_inverse(byte);
+      const int byte = scale_byte(block_magnitude<kMxBlock / V>(y));
       if (in) {
         uint8_t* c = a.codes + row * a.ldc + col;
         if constexpr (V == 8) {
-          uint32_t w[2] = {0, 0};
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            w[k / 2] |= e4m3_pair(clamp_top(y[2 * k] * inv, byte), clamp_top(y[2 * k + 1] * inv, byte)) << (16 * (k % 2));
+          uint32_t w[2];
+          encode(y, byte, w);
           *reinterpret_cast<uint2*>(c) = make_uint2(w[0], w[1]);
         } else {
-          *c = (uint8_t)e4m3_pair(clamp_top(y[0] * inv, byte), 0.0f);
+          *c = encode_one(y[0], byte);
         }
         if (col % kMxBlock == 0) a.scales[row * a.lds + col / kMxBlock] = (uint8_t)byte;
       }
@@ -147,81 +138,219 @@ __global__ void __launch_bounds__(TPR < kMinBlock ? kMinBlock : TPR) norm_kernel
   }
 }
 
-// Row groups (TPR threads each) walk the rows with a fixed stride, so a thread
-// keeps its columns and their share of dweight in registers.
-template <typename T, int TPR, int V, int NV>
-__global__ void __launch_bounds__(TPR < kMinBlock ? kMinBlock : TPR) norm_grad_kernel(const NormGradArgs a) {
-  __shared__ float scratch[32];
-  const int lane = threadIdx.x % TPR;
-  const int64_t group = (int64_t)blockIdx.x * (blockDim.x / TPR) + threadIdx.x / TPR;
-  const int64_t groups = (int64_t)gridDim.x * (blockDim.x / TPR);
-  float acc[NV][V] = {};
-  // Every group of a block makes the same number of turns (row_sum's barriers).
-  for (int64_t first = (int64_t)blockIdx.x * (blockDim.x / TPR); first < a.rows; first += groups) {
-    const int64_t row = first + threadIdx.x / TPR;
+// ---- backward
+
+// dx of one row's columns and their share of dweight, once n = h (still without
+// rstd) and g = dy are in registers.
+template <typename T, int V, int NV>
+__device__ __forceinline__ void grad_row(const NormGradArgs& a, int64_t row, bool here, float rstd, float (&n)[NV][V],
+                                         float (&g)[NV][V], const float (&w)[NV][V], float (&acc)[NV][V],
+                                         float (&scratch)[2][32], int& turn, const float (&dres)[NV][V]) {
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      n[i][k] *= rstd;
+      acc[i][k] = fmaf(g[i][k], n[i][k], acc[i][k]);
+      g[i][k] *= w[i][k];
+      sum = fmaf(g[i][k], n[i][k], sum);
+    }
+  if (!a.dx) return;
+  const float mean = row_sum(sum, scratch, turn) / (float)a.cols;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int col = (i * blockDim.x + threadIdx.x) * V;
+    if (here && col < a.cols) {
+      float d[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k) d[k] = fmaf(rstd, fmaf(-n[i][k], mean, g[i][k]), dres[i][k]);
+      store_vec<V>((T*)a.dx + row * a.lddx + col, d);
+    }
+  }
+}
+
+template <int V, int NV>
+__device__ __forceinline__ void store_partial(const NormGradArgs& a, const float (&acc)[NV][V]) {
+  if (!a.partial) return;
+  float* p = a.partial + ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * a.cols;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int col = (i * blockDim.x + threadIdx.x) * V;
+    if (col < a.cols) store_vec<V>(p + col, acc[i]);
+  }
+}
+
+// Row groups (blockDim.x threads) walk the rows with a fixed stride, so a
+// thread keeps its columns' weights and their share of dweight in registers.
+// Any alignment (V = 1), and rows too long for the ring below.
+template <typename T, int V, int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_grad_kernel(const NormGradArgs a) {
+  __shared__ float scratch[2][32];
+  int turn = 0;
+  float acc[NV][V] = {}, w[NV][V] = {};
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int col = (i * blockDim.x + threadIdx.x) * V;
+    if (col < a.cols) load_vec<V>((const T*)a.weight + col, w[i]);
+  }
+  // Every group of a block makes the same number of turns (row_sum's barrier).
+  for (int64_t first = (int64_t)blockIdx.x * blockDim.y; first < a.rows; first += (int64_t)gridDim.x * blockDim.y) {
+    const int64_t row = first + threadIdx.y;
     const bool here = row < a.rows;
     const float rstd = here ? a.rstd[row] : 0.0f;
-    float n[NV][V], g[NV][V];
-    float sum = 0.0f;
+    float n[NV][V] = {}, g[NV][V] = {}, dres[NV][V] = {};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = (i * TPR + lane) * V;
-#pragma unroll
-      for (int k = 0; k < V; ++k) n[i][k] = g[i][k] = 0.0f;
+      const int col = (i * blockDim.x + threadIdx.x) * V;
       if (here && col < a.cols) {
         if (a.h) {
           load_vec<V>((const T*)a.h + row * a.ldh + col, n[i]);
         } else {
-          const float sc = scale_value(a.scales[row * a.lds + col / kMxBlock]);
+          const float scale = scale_value(a.scales[row * a.lds + col / kMxBlock]);
           const uint8_t* c = a.codes + row * a.ldc + col;
-          if constexpr (V == 8) {
-            const uint2 u = *reinterpret_cast<const uint2*>(c);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 t = e4m3_values(((k < 2 ? u.x : u.y) >> (16 * (k % 2))) & 0xffffu);
-              n[i][2 * k] = t.x * sc;
-              n[i][2 * k + 1] = t.y * sc;
-            }
-          } else {
-            n[i][0] = e4m3_values(*c).x * sc;
-          }
+          if constexpr (V == 8)
+            decode8(*reinterpret_cast<const uint2*>(c), scale, n[i]);
+          else
+            n[i][0] = e4m3_values(*c).x * scale;
         }
         load_vec<V>((const T*)a.dy + row * a.lddy + col, g[i]);
-        float w[V];
-        load_vec<V>((const T*)a.weight + col, w);
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          n[i][k] *= rstd;
-          acc[i][k] = fmaf(g[i][k], n[i][k], acc[i][k]);
-          g[i][k] *= w[k];
-          sum = fmaf(g[i][k], n[i][k], sum);
-        }
+        if (a.dres) load_vec<V>((const T*)a.dres + row * a.ldres + col, dres[i]);
       }
     }
-    if (!a.dx) continue;
-    sum = row_sum<TPR>(sum, scratch);
-    const float mean = sum / (float)a.cols;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int col = (i * TPR + lane) * V;
-      if (here && col < a.cols) {
-        float d[V] = {};
-        if (a.dres) load_vec<V>((const T*)a.dres + row * a.ldres + col, d);
-#pragma unroll
-        for (int k = 0; k < V; ++k) d[k] = fmaf(rstd, fmaf(-n[i][k], mean, g[i][k]), d[k]);
-        store_vec<V>((T*)a.dx + row * a.lddx + col, d);
-      }
-    }
+    grad_row<T, V, NV>(a, row, here, rstd, n, g, w, acc, scratch, turn, dres);
   }
-  if (!a.partial) return;
+  store_partial<V, NV>(a, acc);
+}
+
+__device__ __forceinline__ void copy_async16(uint32_t smem, const void* gmem) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
+}
+__device__ __forceinline__ void copy_async8(uint32_t smem, const void* gmem) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem), "l"(gmem) : "memory");
+}
+
+// Shared memory a ring slot (one row of the block) takes: for every thread and
+// vector, its h (or codes), dy and dres.
+inline int ring_slot_bytes(int threads, int nv, int elem, bool kept, bool dres) {
+  return threads * nv * ((kept ? 8 : 8 * elem) + 8 * elem * (dres ? 2 : 1));
+}
+
+// As above with aligned rows, eight columns a vector, DEPTH rows of a group in
+// flight: each thread copies its own columns of the rows to come into a ring in
+// shared memory and reads nothing else from it, so the copies need no barrier
+// and cost no registers.  What is in flight then is DEPTH - 1 rows a block,
+// whatever the one barrier of a row costs.
+template <typename T, int NV, int DEPTH, bool KEPT, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_grad_ring_kernel(const NormGradArgs a) {
+  extern __shared__ __align__(16) unsigned char ring[];
+  __shared__ float scratch[2][32];
+  constexpr int kWords = sizeof(T) / 2;                        // 16-byte words of a vector
+  const int threads = blockDim.x * blockDim.y, tid = threadIdx.y * blockDim.x + threadIdx.x;
+  const int h_bytes = KEPT ? 8 : 16 * kWords;
+  const uint32_t slot = (uint32_t)(threads * NV * (h_bytes + 16 * kWords * (a.dres ? 2 : 1)));
+  const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring);
+  // Within a slot: dy, dres, h; within each, word by word over the threads, so
+  // neighbouring threads use neighbouring banks.
+  const uint32_t vec_bytes = (uint32_t)threads * 16;
+  const uint32_t off_dres = NV * kWords * vec_bytes, off_h = off_dres * (a.dres ? 2 : 1);
+
+  int turn = 0;
+  float acc[NV][8] = {}, w[NV][8] = {};
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int col = (i * TPR + lane) * V;
-    if (col < a.cols) {
-#pragma unroll
-      for (int k = 0; k < V; ++k) a.partial[group * a.cols + col + k] = acc[i][k];
-    }
+    const int col = (i * blockDim.x + threadIdx.x) * 8;
+    if (col < a.cols) load_vec<8>((const T*)a.weight + col, w[i]);
   }
+  const int64_t step = (int64_t)gridDim.x * blockDim.y;
+  const int64_t first = (int64_t)blockIdx.x * blockDim.y;
+
+  auto fetch = [&](int64_t row, uint32_t at) {
+    if (row < a.rows) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int col = (i * blockDim.x + threadIdx.x) * 8;
+        if (col >= a.cols) continue;
+        const T* dy = (const T*)a.dy + row * a.lddy + col;
+#pragma unroll
+        for (int q = 0; q < kWords; ++q) {
+          const uint32_t o = at + (i * kWords + q) * vec_bytes + tid * 16;
+          copy_async16(o, dy + q * (16 / sizeof(T)));
+          if (a.dres) copy_async16(o + off_dres, (const T*)a.dres + row * a.ldres + col + q * (16 / sizeof(T)));
+          if (!KEPT) copy_async16(o + off_h, (const T*)a.h + row * a.ldh + col + q * (16 / sizeof(T)));
+        }
+        if (KEPT) copy_async8(at + off_h + (i * threads + tid) * 8, a.codes + row * a.ldc + col);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // rstd and the scales of a row, one row ahead.
+  float rstd = 0.0f;
+  uint8_t scale[NV] = {};
+  auto fetch_small = [&](int64_t row) {
+    if (row >= a.rows) return;
+    rstd = a.rstd[row];
+    if constexpr (KEPT) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int col = (i * blockDim.x + threadIdx.x) * 8;
+        if (col < a.cols) scale[i] = a.scales[row * a.lds + col / kMxBlock];
+      }
+    }
+  };
+  auto word = [&](uint32_t o, float (&v)[8]) {  // a vector of T at ring offset o
+    load_vec<8>(reinterpret_cast<const T*>(ring + o), v);
+  };
+
+#pragma unroll
+  for (int d = 0; d < DEPTH - 1; ++d) fetch(first + threadIdx.y + d * step, base + d * slot);
+  fetch_small(first + threadIdx.y);
+  int at = 0;
+  for (int64_t r0 = first; r0 < a.rows; r0 += step) {
+    const int64_t row = r0 + threadIdx.y;
+    const bool here = row < a.rows;
+    int next = at + DEPTH - 1;
+    if (next >= DEPTH) next -= DEPTH;
+    fetch(row + (DEPTH - 1) * step, base + next * slot);
+    const float row_rstd = here ? rstd : 0.0f;
+    uint8_t row_scale[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) row_scale[i] = scale[i];
+    fetch_small(row + step);
+    asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+    float n[NV][8] = {}, g[NV][8] = {}, dres[NV][8] = {};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int col = (i * blockDim.x + threadIdx.x) * 8;
+      if (!here || col >= a.cols) continue;
+      const unsigned char* s = ring + at * slot;
+      if constexpr (kWords == 1) {
+        word(at * slot + i * vec_bytes + tid * 16, g[i]);
+        if (a.dres) word(at * slot + off_dres + i * vec_bytes + tid * 16, dres[i]);
+        if (!KEPT) word(at * slot + off_h + i * vec_bytes + tid * 16, n[i]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const uint32_t o = (i * 2 + q) * vec_bytes + tid * 16;
+          const float4 x = *reinterpret_cast<const float4*>(s + o);
+          g[i][4 * q] = x.x, g[i][4 * q + 1] = x.y, g[i][4 * q + 2] = x.z, g[i][4 * q + 3] = x.w;
+          if (a.dres) {
+            const float4 y = *reinterpret_cast<const float4*>(s + off_dres + o);
+            dres[i][4 * q] = y.x, dres[i][4 * q + 1] = y.y, dres[i][4 * q + 2] = y.z, dres[i][4 * q + 3] = y.w;
+          }
+          if (!KEPT) {
+            const float4 z = *reinterpret_cast<const float4*>(s + off_h + o);
+            n[i][4 * q] = z.x, n[i][4 * q + 1] = z.y, n[i][4 * q + 2] = z.z, n[i][4 * q + 3] = z.w;
+          }
+        }
+      }
+      if (KEPT) decode8(*reinterpret_cast<const uint2*>(s + off_h + (i * threads + tid) * 8), scale_value(row_scale[i]), n[i]);
+    }
+    grad_row<T, 8, NV>(a, row, here, row_rstd, n, g, w, acc, scratch, turn, dres);
+    if (++at == DEPTH) at = 0;
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  store_partial<8, NV>(a, acc);
 }
 
 // dweight: the sum of the groups' partials, in a fixed order.  A block takes
@@ -233,8 +362,17 @@ __global__ void __launch_bounds__(1024) norm_weight_kernel(const float* __restri
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int64_t col = (int64_t)blockIdx.x * 32 + lane;
   float v = 0.0f;
-  if (col < cols)
-    for (int64_t g = warp; g < groups; g += 32) v += partial[g * cols + col];
+  if (col < cols) {
+    int64_t g = warp;
+    for (; g + 7 * 32 < groups; g += 8 * 32) {  // eight loads at a time
+      float t[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[j] = partial[(g + j * 32) * cols + col];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v += t[j];
+    }
+    for (; g < groups; g += 32) v += partial[g * cols + col];
+  }
   s[warp][lane] = v;
   __syncthreads();
   v = s[lane][warp];  // lane l of warp w: column w's sum over warp l's groups
@@ -247,32 +385,35 @@ __global__ void __launch_bounds__(1024) norm_weight_kernel(const float* __restri
   }
 }
 
-// Calls f(TPR, V, NV as constants) for the smallest instance that holds a row.
-template <typename F>
-void with_shape(bool vec, int64_t cols, F&& f) {
-#define TIDE_SHAPE(tpr, v, nv) \
-  if (cols <= (int64_t)(tpr) * (v) * (nv)) \
-    return f(std::integral_constant<int, tpr>(), std::integral_constant<int, v>(), std::integral_constant<int, nv>())
-  if (vec) {
-    TIDE_SHAPE(32, 8, 1);
-    TIDE_SHAPE(32, 8, 2);
-    TIDE_SHAPE(128, 8, 1);
-    TIDE_SHAPE(128, 8, 2);
-    TIDE_SHAPE(256, 8, 2);
-    TIDE_SHAPE(512, 8, 2);
-    TIDE_SHAPE(1024, 8, 2);
-  } else {
-    TIDE_SHAPE(32, 1, 8);
-    TIDE_SHAPE(128, 1, 8);
-    TIDE_SHAPE(256, 1, 8);
-    TIDE_SHAPE(512, 1, 8);
-    TIDE_SHAPE(1024, 1, 8);
-    TIDE_SHAPE(1024, 1, 16);
-  }
-#undef TIDE_SHAPE
+// How a row is spread: V columns a vector, NV vectors a thread, `threads`
+// threads a row, `rows` rows a block.  NV grows with the row so that a block
+// stays at 512 threads or fewer where it can (several blocks an SM).
+struct RowShape {
+  int nv, threads, rows;
+};
+RowShape row_shape(bool vec, int64_t cols) {
+  RowShape s{};
+  if (vec)
+    s.nv = cols <= 2048 ? 1 : cols <= 8192 ? 2 : 4;
+  else
+    s.nv = cols <= 1024 ? 4 : cols <= 4096 ? 8 : 16;
+  const int64_t each = (int64_t)s.nv * (vec ? 8 : 1);
+  s.threads = (int)((cols + each * 32 - 1) / (each * 32) * 32);
+  s.rows = std::max(1, 256 / s.threads);
+  return s;
 }
 
-int rows_per_block(int tpr) { return tpr < kMinBlock ? kMinBlock / tpr : 1; }
+template <int N>
+using Int = std::integral_constant<int, N>;
+
+// f(V, NV, most threads of a block), as constants.
+template <typename F>
+void with_shape(bool vec, const RowShape& s, F&& f) {
+  if (vec)
+    s.nv == 1 ? f(Int<8>(), Int<1>(), Int<256>()) : s.nv == 2 ? f(Int<8>(), Int<2>(), Int<512>()) : f(Int<8>(), Int<4>(), Int<512>());
+  else
+    s.nv == 4 ? f(Int<1>(), Int<4>(), Int<256>()) : s.nv == 8 ? f(Int<1>(), Int<8>(), Int<512>()) : f(Int<1>(), Int<16>(), Int<1024>());
+}
 
 template <typename T>
 tide_status norm(const NormArgs& a, cudaStream_t stream) {
@@ -280,26 +421,23 @@ tide_status norm(const NormArgs& a, cudaStream_t stream) {
                    rows_aligned(a.residual, a.ldr, sizeof(T), a.rows) && rows_aligned(a.h, a.ldh, sizeof(T), a.rows) &&
                    rows_aligned(a.y, a.ldy, sizeof(T), a.rows) && (uintptr_t)a.weight % 16 == 0 &&
                    (uintptr_t)a.codes % 8 == 0 && (!a.codes || a.rows <= 1 || a.ldc % 8 == 0);
-  tide_status st = TIDE_OK;
-  with_shape(vec, a.cols, [&](auto tpr, auto v, auto nv) {
-    const int rpb = rows_per_block(tpr);
-    const int64_t grid = (a.rows + rpb - 1) / rpb;
-    if (grid > INT32_MAX) {
-      st = fail(TIDE_ERR_UNIMPLEMENTED, "too many rows for one launch");
-      return;
-    }
-    norm_kernel<T, tpr(), v(), nv()><<<(unsigned)grid, tpr() * rpb, 0, stream>>>(a);
-    st = cuda_status(cudaGetLastError(), "rms norm");
+  const RowShape s = row_shape(vec, a.cols);
+  const int64_t grid = (a.rows + s.rows - 1) / s.rows;
+  if (grid > INT32_MAX) return fail(TIDE_ERR_UNIMPLEMENTED, "too many rows for one launch");
+  with_shape(vec, s, [&](auto v, auto nv, auto threads) {
+    norm_kernel<T, v(), nv(), threads()><<<(unsigned)grid, dim3(s.threads, s.rows), 0, stream>>>(a);
   });
-  return st;
+  return cuda_status(cudaGetLastError(), "rms norm");
 }
 
-// Row groups of the backward pass: what fills the GPU, at most one a row.
-int64_t grad_groups(int64_t rows, int tpr, int sms) {
-  const int rpb = rows_per_block(tpr);
-  const int64_t blocks = std::min<int64_t>((rows + rpb - 1) / rpb, (int64_t)sms * (2048 / (tpr * rpb)));
-  return blocks * rpb;
+// Blocks of the backward pass: up to `per_sm` an SM, but past 64 row groups at
+// least four rows a group, so that the partial sums stay few.
+int64_t grad_blocks(int64_t rows, const RowShape& s, int per_sm, int sms) {
+  const int64_t most = (rows + s.rows - 1) / s.rows;
+  const int64_t few = std::max<int64_t>(64 / s.rows, (rows + 4 * s.rows - 1) / (4 * s.rows));
+  return std::min(std::min(most, few), (int64_t)sms * per_sm);
 }
+int most_per_sm(const RowShape& s) { return std::max(1, 1024 / (s.threads * s.rows)); }
 
 template <typename T>
 tide_status norm_grad(NormGradArgs a, void* dweight, cudaStream_t stream) {
@@ -311,13 +449,40 @@ tide_status norm_grad(NormGradArgs a, void* dweight, cudaStream_t stream) {
                    (uintptr_t)a.codes % 8 == 0 && (a.h || a.rows <= 1 || a.ldc % 8 == 0);
   tide_status st = TIDE_OK;
   int64_t groups = 0;
-  if (a.rows > 0)
-    with_shape(vec, a.cols, [&](auto tpr, auto v, auto nv) {
-      const int rpb = rows_per_block(tpr);
-      groups = grad_groups(a.rows, tpr, sms);
-      norm_grad_kernel<T, tpr(), v(), nv()><<<(unsigned)(groups / rpb), tpr() * rpb, 0, stream>>>(a);
+  if (a.rows > 0) {
+    const RowShape s = row_shape(vec, a.cols);
+    const dim3 block(s.threads, s.rows);
+    const int slot = ring_slot_bytes(s.threads * s.rows, s.nv, sizeof(T), !a.h, a.dres != nullptr);
+    constexpr int kRoom = 200 * 1024;  // shared memory of an SM that rings may take
+    const int depth = 4 * slot <= kRoom ? 4 : 2 * slot <= kRoom ? 2 : 0;
+    const int per_sm = vec && depth ? std::min(most_per_sm(s), kRoom / (depth * slot)) : most_per_sm(s);
+    const int64_t blocks = grad_blocks(a.rows, s, per_sm, sms);
+    groups = blocks * s.rows;
+    with_shape(vec, s, [&](auto v, auto nv, auto threads) {
+      if constexpr (v() == 8) {
+        auto ring = [&](auto kernel) {
+          const int smem = depth * slot;
+          cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+          if (err == cudaSuccess) {
+            kernel<<<(unsigned)blocks, block, smem, stream>>>(a);
+            err = cudaGetLastError();
+          }
+          st = cuda_status(err, "rms norm backward");
+        };
+        constexpr int kT = threads();
+        if (depth == 4) {
+          a.h ? ring(norm_grad_ring_kernel<T, nv(), 4, false, kT>) : ring(norm_grad_ring_kernel<T, nv(), 4, true, kT>);
+          return;
+        }
+        if (depth == 2) {
+          a.h ? ring(norm_grad_ring_kernel<T, nv(), 2, false, kT>) : ring(norm_grad_ring_kernel<T, nv(), 2, true, kT>);
+          return;
+        }
+      }
+      norm_grad_kernel<T, v(), nv(), threads()><<<(unsigned)blocks, block, 0, stream>>>(a);
       st = cuda_status(cudaGetLastError(), "rms norm backward");
     });
+  }
   if (st == TIDE_OK && dweight) {
     norm_weight_kernel<T><<<(unsigned)((a.cols + 31) / 32), 1024, 0, stream>>>(a.partial, groups, a.cols, (T*)dweight);
     st = cuda_status(cudaGetLastError(), "rms norm weight gradient");
@@ -373,9 +538,11 @@ tide_status tide_rms_norm(int64_t rows, int64_t cols, int32_t dtype, const void*
 int64_t tide_rms_norm_backward_workspace(int64_t rows, int64_t cols) {
   if (rows <= 0 || cols <= 0 || cols > kMaxCols) return 0;
   const int sms = ops_num_sms();
-  int64_t most = 0;  // whichever instance the alignment of the call's rows selects
-  for (const bool vec : {true, false})
-    with_shape(vec, cols, [&](auto tpr, auto, auto) { most = std::max(most, grad_groups(rows, tpr, sms)); });
+  int64_t most = 0;  // whichever the alignment of the call's rows selects
+  for (const bool vec : {true, false}) {
+    const RowShape s = row_shape(vec, cols);
+    most = std::max(most, grad_blocks(rows, s, most_per_sm(s), sms) * s.rows);
+  }
   return most * cols * 4;
 }
 
