@@ -14,7 +14,8 @@ import ctypes
 
 import torch
 
-from .tide import TideError, _check, _lib, _stream
+from .tide import TideError, _check, _lib
+from .tide import _stream as _stream_of
 
 TIDE_BF16, TIDE_F32 = 0, 1
 TIDE_ACT_NONE, TIDE_ACT_RELU, TIDE_ACT_GELU, TIDE_ACT_GELU_ERF, TIDE_ACT_SILU = range(5)
@@ -53,6 +54,17 @@ def _declare():
 _declare()
 
 
+# The current stream's handle without building a Stream object (a microsecond
+# of a call), where this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(_device())
+    return _stream_of(stream)
+
+
 def _refuse(message, status=1):
     raise TideError(status, message)
 
@@ -83,51 +95,61 @@ class Checkpoint8:
 
 
 _NO_MAT = (None, 0)
+_NO_CKPT = (None, 0, None, 0)
+_device = torch.cuda.current_device
 
 
-def _mat(t, name, shape, dtype):
-    """(address, row stride) of a 2-D tensor, after checking it."""
+def _wrong(t, name, shape, dtype, dev):
+    """What is wrong with a tensor that _mat or _vec did not take."""
     if t.dtype is not dtype:
         _refuse(f"{name} is {t.dtype}, not {dtype}")
-    if t.shape != shape:
-        _refuse(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if tuple(t.shape) != shape:
+        _refuse(f"{name} has shape {tuple(t.shape)}, not {shape}")
     if not t.is_cuda:
         _refuse(f"{name} is not on the GPU")
-    if t.get_device() != torch.cuda.current_device():
+    if t.get_device() != dev:
         _refuse(f"{name} is on device {t.get_device()}, which is not the current one", 7)
-    ld, step = t.stride()
-    if step != 1 and shape[1] > 1:
-        _refuse(f"{name}: the last axis is not contiguous")
-    return t.data_ptr(), ld
+    _refuse(f"{name}: the last axis is not contiguous")
 
 
-def _vec(t, name, n, dtype):
-    if t.dtype is not dtype:
-        _refuse(f"{name} is {t.dtype}, not {dtype}")
-    if t.dim() != 1 or t.shape[0] != n:
-        _refuse(f"{name} has shape {tuple(t.shape)}, not ({n},)")
-    if not t.is_cuda:
-        _refuse(f"{name} is not on the GPU")
-    if t.get_device() != torch.cuda.current_device():
-        _refuse(f"{name} is on device {t.get_device()}, which is not the current one", 7)
-    if n > 1 and t.stride(0) != 1:
-        _refuse(f"{name} is not contiguous")
-    return t.data_ptr()
+def _mat(t, name, rows, cols, dtype, dev):
+    """(address, row stride) of a (rows, cols) tensor on device dev."""
+    if t.dtype is dtype and t.get_device() == dev and t.shape == (rows, cols):
+        ld, step = t.stride()
+        if step == 1 or cols <= 1:
+            return t.data_ptr(), ld
+    _wrong(t, name, (rows, cols), dtype, dev)
 
 
-def _ckpt(c, name, shape):
+def _vec(t, name, n, dtype, dev):
+    """Address of an (n,) tensor on device dev."""
+    if t.dtype is dtype and t.get_device() == dev and t.shape == (n,) and (n <= 1 or t.stride(0) == 1):
+        return t.data_ptr()
+    _wrong(t, name, (n,), dtype, dev)
+
+
+def _ckpt(c, name, rows, cols, dev):
     """codes and scales of a checkpoint: (address, stride, address, stride)."""
-    rows, cols = shape
-    return _mat(c.codes, name + ".codes", shape, torch.uint8) + _mat(
-        c.scales, name + ".scales", (rows, -(-cols // TIDE_CKPT_BLOCK)), torch.uint8)
+    u8 = torch.uint8
+    return (*_mat(c.codes, name + ".codes", rows, cols, u8, dev),
+            *_mat(c.scales, name + ".scales", rows, -(-cols // TIDE_CKPT_BLOCK), u8, dev))
 
 
-def _opt(t, name, shape, dtype):
-    return _NO_MAT if t is None else _mat(t, name, shape, dtype)
+def _opt(t, name, rows, cols, dtype, dev):
+    return _NO_MAT if t is None else _mat(t, name, rows, cols, dtype, dev)
 
 
-def _optv(t, name, n, dtype):
-    return None if t is None else _vec(t, name, n, dtype)
+def _optv(t, name, n, dtype, dev):
+    return None if t is None else _vec(t, name, n, dtype, dev)
+
+
+def _plain_or_kept(t, name, rows, cols, dtype, dev):
+    """Arguments of a matrix given plain, as a Checkpoint8, or not at all: (address, stride) and _ckpt's four."""
+    if t is None:
+        return _NO_MAT + _NO_CKPT
+    if isinstance(t, Checkpoint8):
+        return _NO_MAT + _ckpt(t, name, rows, cols, dev)
+    return _mat(t, name, rows, cols, dtype, dev) + _NO_CKPT
 
 
 def _dtype(t, name):
@@ -150,15 +172,15 @@ def _act(act):
     return code
 
 
-def _workspace(given, need, stream):
+def _workspace(given, need, stream, dev):
     """(tensor that keeps it alive, address, bytes)."""
     if given is not None:
-        if not given.is_cuda or not given.is_contiguous():
-            _refuse("workspace is not a contiguous tensor on the GPU")
+        if given.get_device() != dev or not given.is_contiguous():
+            _refuse("workspace is not a contiguous tensor on the current device")
         return given, given.data_ptr(), given.numel() * given.element_size()
     if need == 0:
         return None, None, 0
-    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
     if stream is not None:
         # The block must not go to another call of the allocating stream while this one still uses it.
         ws.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream))
@@ -176,81 +198,83 @@ def tide_ops_set_option(option, value):
 
 def tide_checkpoint_store(x, ckpt, stream=None):
     """Keep x (rows, cols; bf16 or fp32) in ckpt (a Checkpoint8 of that shape)."""
-    shape = _shape2(x, "x")
-    _check(_lib.tide_checkpoint_store(*shape, _dtype(x, "x"), *_mat(x, "x", shape, x.dtype),
-                                      *_ckpt(ckpt, "ckpt", shape), _stream(stream)))
+    dev = _device()
+    rows, cols = _shape2(x, "x")
+    _check(_lib.tide_checkpoint_store(rows, cols, _dtype(x, "x"), *_mat(x, "x", rows, cols, x.dtype, dev),
+                                      *_ckpt(ckpt, "ckpt", rows, cols, dev), _stream(stream)))
 
 
 def tide_checkpoint_load(ckpt, out, act=TIDE_ACT_NONE, grad=None, stream=None):
     """out = f(values), or grad * f'(values) when grad is given (out may be grad)."""
-    shape = ckpt.shape
-    _check(_lib.tide_checkpoint_load(*shape, *_ckpt(ckpt, "ckpt", shape), _act(act), _dtype(out, "out"),
-                                     *_opt(grad, "grad", shape, out.dtype), *_mat(out, "out", shape, out.dtype),
+    dev = _device()
+    rows, cols = ckpt.shape
+    t = out.dtype
+    _check(_lib.tide_checkpoint_load(rows, cols, *_ckpt(ckpt, "ckpt", rows, cols, dev), _act(act), _dtype(out, "out"),
+                                     *_opt(grad, "grad", rows, cols, t, dev), *_mat(out, "out", rows, cols, t, dev),
                                      _stream(stream)))
 
 
 def tide_rms_norm(x, weight, eps, y=None, residual=None, h=None, rstd=None, y8=None, stream=None):
     """h = x + residual; y (and y8, a Checkpoint8) = h * rstd * weight, rstd = (mean(h^2) + eps)^-1/2 per row."""
-    shape = _shape2(x, "x")
+    dev = _device()
+    rows, cols = _shape2(x, "x")
     t = x.dtype
-    _check(_lib.tide_rms_norm(*shape, _dtype(x, "x"), *_mat(x, "x", shape, t), *_opt(residual, "residual", shape, t),
-                              _vec(weight, "weight", shape[1], t), eps, *_opt(h, "h", shape, t),
-                              *_opt(y, "y", shape, t), _optv(rstd, "rstd", shape[0], torch.float32),
-                              *(_NO_MAT + _NO_MAT if y8 is None else _ckpt(y8, "y8", shape)), _stream(stream)))
+    _check(_lib.tide_rms_norm(rows, cols, _dtype(x, "x"), *_mat(x, "x", rows, cols, t, dev),
+                              *_opt(residual, "residual", rows, cols, t, dev), _vec(weight, "weight", cols, t, dev), eps,
+                              *_opt(h, "h", rows, cols, t, dev), *_opt(y, "y", rows, cols, t, dev),
+                              _optv(rstd, "rstd", rows, torch.float32, dev),
+                              *(_NO_CKPT if y8 is None else _ckpt(y8, "y8", rows, cols, dev)), _stream(stream)))
 
 
 def tide_rms_norm_backward(dy, h, weight, rstd, dx=None, dweight=None, dres=None, workspace=None, stream=None):
     """Gradients of tide_rms_norm: dx (of x and of residual, dres added) and dweight; h may be a Checkpoint8."""
-    shape = _shape2(dy, "dy")
-    rows, cols = shape
+    dev = _device()
+    rows, cols = _shape2(dy, "dy")
     t = dy.dtype
-    kept = (_NO_MAT + _ckpt(h, "h", shape) if isinstance(h, Checkpoint8)
-            else _mat(h, "h", shape, t) + _NO_MAT + _NO_MAT)
-    args = (rows, cols, _dtype(dy, "dy"), *_mat(dy, "dy", shape, t), *kept, _vec(weight, "weight", cols, t),
-            _vec(rstd, "rstd", rows, torch.float32), *_opt(dres, "dres", shape, t), *_opt(dx, "dx", shape, t),
-            _optv(dweight, "dweight", cols, t))
+    args = (rows, cols, _dtype(dy, "dy"), *_mat(dy, "dy", rows, cols, t, dev),
+            *_plain_or_kept(h, "h", rows, cols, t, dev), _vec(weight, "weight", cols, t, dev),
+            _vec(rstd, "rstd", rows, torch.float32, dev), *_opt(dres, "dres", rows, cols, t, dev),
+            *_opt(dx, "dx", rows, cols, t, dev), _optv(dweight, "dweight", cols, t, dev))
     need = 0 if dweight is None else _lib.tide_rms_norm_backward_workspace(rows, cols)
-    keep, ws, ws_bytes = _workspace(workspace, need, stream)
+    keep, ws, ws_bytes = _workspace(workspace, need, stream, dev)
     _check(_lib.tide_rms_norm_backward(*args, ws, ws_bytes, _stream(stream)))
 
 
 def tide_linear(x, w, y, bias=None, act=TIDE_ACT_NONE, residual=None, z=None, workspace=None, stream=None):
     """y = f(x w^T + bias) + residual; z (bf16, or a Checkpoint8) keeps x w^T + bias for the backward pass."""
+    dev = _device()
     rows, inner = _shape2(x, "x")
     outer = _shape2(w, "w")[0]
-    bf, out = torch.bfloat16, (rows, outer)
-    a, b = _mat(x, "x", (rows, inner), bf), _mat(w, "w", (outer, inner), bf)
-    kept = (_NO_MAT + _ckpt(z, "z", out) if isinstance(z, Checkpoint8) else _opt(z, "z", out, bf) + _NO_MAT + _NO_MAT)
-    args = (*a, *b, _optv(bias, "bias", outer, bf), _act(act), *_opt(residual, "residual", out, bf),
-            *_mat(y, "y", out, bf), *kept)
-    keep, ws, ws_bytes = _workspace(workspace, _lib.tide_linear_workspace(rows, inner, outer, *a, *b), stream)
-    _check(_lib.tide_linear(rows, inner, outer, *args, ws, ws_bytes, _stream(stream)))
+    bf = torch.bfloat16
+    size = (rows, inner, outer)
+    ab = (*_mat(x, "x", rows, inner, bf, dev), *_mat(w, "w", outer, inner, bf, dev))
+    args = (_optv(bias, "bias", outer, bf, dev), _act(act), *_opt(residual, "residual", rows, outer, bf, dev),
+            *_mat(y, "y", rows, outer, bf, dev), *_plain_or_kept(z, "z", rows, outer, bf, dev))
+    keep, ws, ws_bytes = _workspace(workspace, _lib.tide_linear_workspace(*size, *ab), stream, dev)
+    _check(_lib.tide_linear(*size, *ab, *args, ws, ws_bytes, _stream(stream)))
 
 
 def tide_linear_grad_input(dy, w, dx, act=TIDE_ACT_NONE, z=None, workspace=None, stream=None):
     """dx = (dy w) * f'(z): z (bf16 or Checkpoint8) is the pre-activation behind this layer's input."""
+    dev = _device()
     rows, outer = _shape2(dy, "dy")
     inner = _shape2(w, "w")[1]
-    bf, out = torch.bfloat16, (rows, inner)
-    a, b = _mat(dy, "dy", (rows, outer), bf), _mat(w, "w", (outer, inner), bf)
-    kept = (_NO_MAT + _ckpt(z, "z", out) if isinstance(z, Checkpoint8) else _opt(z, "z", out, bf) + _NO_MAT + _NO_MAT)
-    args = (*a, *b, _act(act), *kept, *_mat(dx, "dx", out, bf))
-    keep, ws, ws_bytes = _workspace(workspace, _lib.tide_linear_grad_input_workspace(rows, inner, outer, *a, *b), stream)
-    _check(_lib.tide_linear_grad_input(rows, inner, outer, *args, ws, ws_bytes, _stream(stream)))
+    bf = torch.bfloat16
+    size = (rows, inner, outer)
+    ab = (*_mat(dy, "dy", rows, outer, bf, dev), *_mat(w, "w", outer, inner, bf, dev))
+    args = (_act(act), *_plain_or_kept(z, "z", rows, inner, bf, dev), *_mat(dx, "dx", rows, inner, bf, dev))
+    keep, ws, ws_bytes = _workspace(workspace, _lib.tide_linear_grad_input_workspace(*size, *ab), stream, dev)
+    _check(_lib.tide_linear_grad_input(*size, *ab, *args, ws, ws_bytes, _stream(stream)))
 
 
 def tide_linear_grad_weight(dy, x, dw, db=None, act=TIDE_ACT_NONE, workspace=None, stream=None):
     """dw = dy^T X, db = column sums of dy; X is x, or f(values) of a Checkpoint8 x."""
+    dev = _device()
     rows, outer = _shape2(dy, "dy")
+    inner = x.shape[1] if isinstance(x, Checkpoint8) else _shape2(x, "x")[1]
     bf = torch.bfloat16
-    a = _mat(dy, "dy", (rows, outer), bf)
-    if isinstance(x, Checkpoint8):
-        inner = x.shape[1]
-        plain, kept = _NO_MAT, _ckpt(x, "x", (rows, inner))
-    else:
-        inner = _shape2(x, "x")[1]
-        plain, kept = _mat(x, "x", (rows, inner), bf), _NO_MAT + _NO_MAT
-    args = (*a, *plain, *kept, _act(act), *_mat(dw, "dw", (outer, inner), bf), _optv(db, "db", outer, bf))
-    keep, ws, ws_bytes = _workspace(workspace, _lib.tide_linear_grad_weight_workspace(rows, inner, outer, *a, *plain),
-                                    stream)
-    _check(_lib.tide_linear_grad_weight(rows, inner, outer, *args, ws, ws_bytes, _stream(stream)))
+    size = (rows, inner, outer)
+    a, kept = _mat(dy, "dy", rows, outer, bf, dev), _plain_or_kept(x, "x", rows, inner, bf, dev)
+    args = (_act(act), *_mat(dw, "dw", outer, inner, bf, dev), _optv(db, "db", outer, bf, dev))
+    keep, ws, ws_bytes = _workspace(workspace, _lib.tide_linear_grad_weight_workspace(*size, *a, *kept[:2]), stream, dev)
+    _check(_lib.tide_linear_grad_weight(*size, *a, *kept, *args, ws, ws_bytes, _stream(stream)))
