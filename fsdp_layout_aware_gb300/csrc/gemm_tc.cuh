@@ -1,11 +1,13 @@
 // Tensor-core products of the linear layer, out = epilogue(A B^T).
 //
-// A is [m, k] and B [n, k], each either with k contiguous (K-major) or with
-// its other axis contiguous (MN-major), in bf16; sums are fp32 in tensor
-// memory.  A tile is 128 * CG rows by BN columns; with CG = 2 two CTAs of a
-// cluster share it, each holding 128 rows of A, half of B's rows and its 128
-// rows of the accumulator, so that every byte staged in shared memory feeds
-// twice the arithmetic.
+// A and B are bf16, each either with k contiguous (K-major) or with its other
+// axis contiguous (MN-major); sums are fp32 in tensor memory.  A tile is 128 *
+// CG rows of A by BN rows of B; with CG = 2 two CTAs of a cluster share it, each
+// holding 128 rows of A, half of B's rows and its 128 rows of the accumulator,
+// so that every byte staged in shared memory feeds twice the arithmetic.
+// Normally A's rows are the output's rows.  With SWAP they are its columns (A is
+// then the weight): for outputs of few rows, whose tiles would be mostly empty,
+// 128 weight rows fill a tile however few tokens there are.
 //
 // One persistent CTA per SM.  Warp 0 streams 64-deep blocks of A and B into a
 // ring of shared-memory stages with TMA; warp 1 (of the first CTA of a pair)
@@ -55,7 +57,7 @@ struct EpilogueArgs {
 struct TcArgs {
   CUtensorMap a, b;
   EpilogueArgs e;
-  int32_t tiles_m, tiles_n;
+  int32_t tiles_a, tiles_b;  // tiles along A's and B's rows
   int32_t k_blocks;        // of 64, over the whole sum
   int32_t split_blocks;    // k blocks of one split (all of them without splitting)
   int32_t splits;
@@ -66,8 +68,8 @@ struct TcArgs {
 
 constexpr int kTcThreads = 256;
 constexpr int kTcK = 64;           // values of k a stage holds: 128 bytes, one swizzle row
-constexpr int kTcStages = 6;
-constexpr int kTcGroupM = 8;       // tile rows walked together, for reuse of B in L2
+constexpr int kTcGroup = 8;        // tile rows walked together, for reuse of B in L2
+constexpr int kTcRoom = 224 * 1024;  // shared memory a CTA may take
 
 template <int CG, int BN>
 struct TcShape {
@@ -77,7 +79,9 @@ struct TcShape {
   static constexpr int stage_bytes = a_bytes + b_bytes;
   static constexpr int transpose_bytes = 4 * 32 * 33 * 4;  // a [32][33] fp32 block per epilogue warp
   static constexpr int columns = 2 * BN;                   // two accumulators
-  static constexpr int smem_bytes = 1024 + kTcStages * stage_bytes + transpose_bytes + 256;
+  static constexpr int fixed_bytes = 1024 + transpose_bytes + 512;
+  static constexpr int stages = (kTcRoom - fixed_bytes) / stage_bytes < 12 ? (kTcRoom - fixed_bytes) / stage_bytes : 12;
+  static constexpr int smem_bytes = fixed_bytes + stages * stage_bytes;
 };
 
 // ---- epilogues
@@ -216,28 +220,30 @@ __device__ __forceinline__ void epilogue_element(const EpilogueArgs& e, int64_t 
 // ---- the kernel
 
 struct TileAt {
-  int m, n;
+  int a, b;
 };
-// Tiles in groups of kTcGroupM tile rows, down the rows first: CTAs at work at
+// Tiles in groups of kTcGroup along A, down A's rows first: CTAs at work at
 // one time share few rows of A and B.
 __device__ __forceinline__ TileAt tile_at(const TcArgs& p, int t) {
-  const int per_group = kTcGroupM * p.tiles_n;
-  const int g = t / per_group, first = g * kTcGroupM;
-  const int height = min(kTcGroupM, p.tiles_m - first);
+  const int per_group = kTcGroup * p.tiles_b;
+  const int g = t / per_group, first = g * kTcGroup;
+  const int height = min(kTcGroup, p.tiles_a - first);
   const int i = t - g * per_group;
   return {first + i % height, i / height};
 }
 
-template <int CG, int BN, bool A_MN, bool B_MN, int EPI>
+template <int CG, int BN, bool A_MN, bool B_MN, int EPI, bool SWAP>
 __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_constant__ TcArgs p) {
   using Shape = TcShape<CG, BN>;
+  constexpr int kStages = Shape::stages;
+  static_assert((2 * kStages + 5) * 8 + 4 <= 512, "barriers");
   extern __shared__ unsigned char raw[];
   // 1024-byte aligned: the swizzle pattern follows address bits.
   unsigned char* smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
-  unsigned char* transpose = smem + kTcStages * Shape::stage_bytes;
+  unsigned char* transpose = smem + kStages * Shape::stage_bytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(transpose + Shape::transpose_bytes);
-  uint64_t* empty = full + kTcStages;
-  uint64_t* acc_full = empty + kTcStages;
+  uint64_t* empty = full + kStages;
+  uint64_t* acc_full = empty + kStages;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* drained = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
@@ -246,7 +252,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_con
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kTcStages; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       mbar_init(full + s, 1);
       mbar_init(empty + s, 1);
     }
@@ -267,8 +273,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_con
     __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // Only now is anything read that an earlier kernel of the call wrote; what
+  // follows may be launched while this runs (it waits likewise).
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  const int tiles = p.tiles_m * p.tiles_n;
+  const int tiles = p.tiles_a * p.tiles_b;
   const int units = tiles * p.splits;
   const int first = blockIdx.x / CG, step = gridDim.x / CG;
   bool ok = true;
@@ -282,7 +292,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_con
       const TileAt at = tile_at(p, u % tiles);
       const int split = u / tiles;
       const int kb0 = split * p.split_blocks, kb1 = min(p.k_blocks, kb0 + p.split_blocks);
-      const int m0 = (at.m * CG + (int)rank) * 128, n0 = at.n * BN + (int)rank * Shape::b_rows;
+      const int a0 = (at.a * CG + (int)rank) * 128, b0 = at.b * BN + (int)rank * Shape::b_rows;
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!(ok = mbar_wait_bounded(empty + stage, phase ^ 1, p.wait_limit_ns))) break;
         unsigned char* a = smem + stage * Shape::stage_bytes;
@@ -291,27 +301,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_con
         const uint32_t bar = CG == 2 ? mapped_addr(smem_addr(full + stage), 0) : smem_addr(full + stage);
         if (issued != p.test_drop) {
           if constexpr (A_MN) {
-            tma_load_2d<CG>(a, &p.a, m0, kb * kTcK, bar);
-            tma_load_2d<CG>(a + 8192, &p.a, m0 + 64, kb * kTcK, bar);
+            tma_load_2d<CG>(a, &p.a, a0, kb * kTcK, bar);
+            tma_load_2d<CG>(a + 8192, &p.a, a0 + 64, kb * kTcK, bar);
           } else {
-            tma_load_2d<CG>(a, &p.a, kb * kTcK, m0, bar);
+            tma_load_2d<CG>(a, &p.a, kb * kTcK, a0, bar);
           }
           if constexpr (B_MN) {
 #pragma unroll
             for (int i = 0; i < Shape::b_rows / 64; ++i)
-              tma_load_2d<CG>(b + 8192 * i, &p.b, n0 + 64 * i, kb * kTcK, bar);
+              tma_load_2d<CG>(b + 8192 * i, &p.b, b0 + 64 * i, kb * kTcK, bar);
           } else {
-            tma_load_2d<CG>(b, &p.b, kb * kTcK, n0, bar);
+            tma_load_2d<CG>(b, &p.b, kb * kTcK, b0, bar);
           }
         }
         ++issued;
-        if (++stage == kTcStages) stage = 0, phase ^= 1;
+        if (++stage == kStages) stage = 0, phase ^= 1;
       }
     }
     // Before leaving, every stage is handed back (no commit's arrival is still
     // under way), or, after a wait that ran out, the loads in flight landed.
-    for (int s = 0; s < kTcStages; ++s) {
-      const int64_t uses = (issued - s + kTcStages - 1) / kTcStages;  // times stage s was filled
+    for (int s = 0; s < kStages; ++s) {
+      const int64_t uses = (issued - s + kStages - 1) / kStages;  // times stage s was filled
       if (uses <= 0) break;
       if (ok) ok = mbar_wait_bounded(empty + s, (uint32_t)(uses - 1) & 1, p.wait_limit_ns);
       if (!ok && rank == 0) mbar_wait_bounded(full + s, (uint32_t)(uses - 1) & 1, p.wait_limit_ns);
@@ -341,7 +351,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_con
         for (int k = 0; k < kTcK / 16; ++k)
           tc_mma<CG>(tmem + acc * BN, da + k * kDescStep<A_MN>, db + k * kDescStep<B_MN>, idesc, kb > kb0 || k > 0);
         tc_commit<CG>(empty + stage);
-        if (++stage == kTcStages) stage = 0, phase ^= 1;
+        if (++stage == kStages) stage = 0, phase ^= 1;
       }
       if (ok) tc_commit<CG>(acc_full + acc);
     }
@@ -362,12 +372,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_con
       ok = __all_sync(0xffffffffu, mbar_wait_bounded(acc_full + acc, (turn >> 1) & 1, p.wait_limit_ns));
       if (!ok) break;
       tc_fence_after();
-      const int64_t row0 = (int64_t)(at.m * CG + (int)rank) * 128 + quad * 32;
+      const int64_t a_row = (int64_t)(at.a * CG + (int)rank) * 128 + quad * 32;  // lane 0's row of A
       const EpilogueArgs& e = p.e;
       const uint32_t from = tmem + acc * BN + ((uint32_t)(quad * 32) << 16);
+      float lane_bias = 0.0f;
+      if (SWAP && EPI == EPI_FORWARD && e.bias && a_row + lane < e.cols) lane_bias = __bfloat162float(e.bias[a_row + lane]);
 #pragma unroll 1
       for (int c = 0; c < BN; c += 32) {
-        const int64_t col = (int64_t)at.n * BN + c;
+        const int64_t b_row = (int64_t)at.b * BN + c;  // the first of 32 rows of B
         float v[32];
         __syncwarp();
         tmem_load32(from + c, v);
@@ -381,20 +393,37 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_con
               mbar_arrive(acc_empty + acc);
           }
         }
-        if (row0 >= e.rows || (EPI != EPI_PARTIAL && col >= e.cols)) continue;
-        if (EPI == EPI_PARTIAL || (e.vec && col + 32 <= e.cols)) {
-          if (row0 + lane < e.rows) epilogue_row<EPI>(e, split, row0 + lane, col, v);
-        } else if constexpr (EPI != EPI_PARTIAL) {
-          // Turned in shared memory: lane l then has column l of each row.
+        if constexpr (SWAP) {
+          // Lane l has column a_row + l of the output in 32 rows: neighbouring
+          // lanes on neighbouring elements.
+          if (a_row >= e.cols || b_row >= e.rows) continue;
 #pragma unroll
           for (int i = 0; i < 32; ++i) block[lane * 33 + i] = v[i];
           __syncwarp();
-          const bool in = col + lane < e.cols;
-          float bias = 0.0f;
-          if (EPI == EPI_FORWARD && e.bias && in) bias = __bfloat162float(e.bias[col + lane]);
-          const int n = (int)min((int64_t)32, e.rows - row0);
-          for (int r = 0; r < n; ++r) epilogue_element<EPI>(e, row0 + r, col + lane, in, block[r * 33 + lane], bias);
-          __syncwarp();
+          const int n = (int)min((int64_t)32, e.rows - b_row);
+          const bool in = a_row + lane < e.cols;
+          for (int r = 0; r < n; ++r) {
+            if constexpr (EPI == EPI_PARTIAL)
+              e.partial[(split * e.rows + b_row + r) * e.ldp + a_row + lane] = block[lane * 33 + r];
+            else
+              epilogue_element<EPI>(e, b_row + r, a_row + lane, in, block[lane * 33 + r], lane_bias);
+          }
+        } else {
+          if (a_row >= e.rows || (EPI != EPI_PARTIAL && b_row >= e.cols)) continue;
+          if (EPI == EPI_PARTIAL || (e.vec && b_row + 32 <= e.cols)) {
+            if (a_row + lane < e.rows) epilogue_row<EPI>(e, split, a_row + lane, b_row, v);
+          } else if constexpr (EPI != EPI_PARTIAL) {
+            // Turned in shared memory: lane l then has column l of each row.
+#pragma unroll
+            for (int i = 0; i < 32; ++i) block[lane * 33 + i] = v[i];
+            __syncwarp();
+            const bool in = b_row + lane < e.cols;
+            float bias = 0.0f;
+            if (EPI == EPI_FORWARD && e.bias && in) bias = __bfloat162float(e.bias[b_row + lane]);
+            const int n = (int)min((int64_t)32, e.rows - a_row);
+            for (int r = 0; r < n; ++r)
+              epilogue_element<EPI>(e, a_row + r, b_row + lane, in, block[r * 33 + lane], bias);
+          }
         }
       }
     }
@@ -416,6 +445,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_con
 // of 32 columns of a row.  With no splits (nothing to sum) the sums are zero.
 template <int EPI>
 __global__ void __launch_bounds__(256) epilogue_kernel(const EpilogueArgs e, int splits) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x % 32;
   const int64_t blocks = (e.cols + 31) / 32;
   const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) / 32;
@@ -432,21 +462,34 @@ __global__ void __launch_bounds__(256) epilogue_kernel(const EpilogueArgs e, int
   epilogue_element<EPI>(e, row, col, in, v, bias);
 }
 
-// Launches the product kernel of one operand layout; `kind` an Epilogue.
-// Defined per layout in ops_linear_*.cu.
-struct TcLaunch {
-  int cg, bn;
-  int grid;
+// The tiles that are built: pairs of CTAs on 256 x 256 and 256 x 128, and, with
+// A and B swapped, single CTAs on 128 weight rows by kSmallB or 128 tokens.
+enum TcTile { TILE_256x256, TILE_256x128, TILE_SWAP_128, TILE_SWAP_SMALL };
+struct TcTileShape {
+  int a, b, ctas;  // rows of A and of B in a tile, CTAs on it
+  bool swap;
 };
-cudaError_t launch_forward(const TcArgs& p, const TcLaunch& l, bool partial, cudaStream_t stream);
-cudaError_t launch_grad_input(const TcArgs& p, const TcLaunch& l, bool partial, cudaStream_t stream);
-cudaError_t launch_grad_weight(const TcArgs& p, const TcLaunch& l, bool partial, cudaStream_t stream);
+// Rows of B in the small swapped tile; an MN-major operand comes in 64s.
+constexpr int small_b(bool mn) { return mn ? 64 : 32; }
+inline TcTileShape tile_shape(TcTile t, bool b_mn_when_swapped) {
+  switch (t) {
+    case TILE_256x256: return {256, 256, 2, false};
+    case TILE_256x128: return {256, 128, 2, false};
+    case TILE_SWAP_128: return {128, 128, 1, true};
+    default: return {128, small_b(b_mn_when_swapped), 1, true};
+  }
+}
 
-template <int CG, int BN, bool A_MN, bool B_MN, int EPI>
-cudaError_t launch_tc(const TcArgs& p, int grid, cudaStream_t stream) {
-  auto kernel = gemm_tc_kernel<CG, BN, A_MN, B_MN, EPI>;
+// Launches the product kernel of one operand layout (ops_linear_*.cu).  `after`:
+// the kernel before it on the stream belongs to the same call.
+cudaError_t launch_forward(const TcArgs& p, TcTile t, int grid, bool after, cudaStream_t stream);
+cudaError_t launch_grad_input(const TcArgs& p, TcTile t, int grid, bool after, cudaStream_t stream);
+cudaError_t launch_grad_weight(const TcArgs& p, TcTile t, int grid, bool after, cudaStream_t stream);
+
+template <int CG, int BN, bool A_MN, bool B_MN, int EPI, bool SWAP>
+cudaError_t launch_tc(const TcArgs& p, int grid, bool after, cudaStream_t stream) {
+  auto kernel = gemm_tc_kernel<CG, BN, A_MN, B_MN, EPI, SWAP>;
   constexpr int smem = TcShape<CG, BN>::smem_bytes;
-  // Set for each device once; the call is cheap and host-only.
   const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg{};
@@ -454,20 +497,42 @@ cudaError_t launch_tc(const TcArgs& p, int grid, cudaStream_t stream) {
   cfg.blockDim = dim3(kTcThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CG;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  if (CG == 2) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = CG;
+    attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
+  if (after) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
+  }
   cfg.attrs = attr;
-  cfg.numAttrs = CG == 2 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+// A_MN, B_MN: the operands' majors unswapped.  Sums of several splits go to
+// p.e.partial.
 template <bool A_MN, bool B_MN, int EPI>
-cudaError_t launch_layout(const TcArgs& p, const TcLaunch& l, bool partial, cudaStream_t stream) {
-  if (l.cg == 2) return launch_tc<2, 256, A_MN, B_MN, EPI>(p, l.grid, stream);
-  if (partial) return launch_tc<1, 128, A_MN, B_MN, EPI_PARTIAL>(p, l.grid, stream);
-  return launch_tc<1, 128, A_MN, B_MN, EPI>(p, l.grid, stream);
+cudaError_t launch_layout(const TcArgs& p, TcTile t, int grid, bool after, cudaStream_t stream) {
+  const bool partial = p.splits > 1;
+  constexpr int kSmall = small_b(A_MN);
+  switch (t) {
+    case TILE_256x256:
+      return partial ? launch_tc<2, 256, A_MN, B_MN, EPI_PARTIAL, false>(p, grid, after, stream)
+                     : launch_tc<2, 256, A_MN, B_MN, EPI, false>(p, grid, after, stream);
+    case TILE_256x128:
+      return partial ? launch_tc<2, 128, A_MN, B_MN, EPI_PARTIAL, false>(p, grid, after, stream)
+                     : launch_tc<2, 128, A_MN, B_MN, EPI, false>(p, grid, after, stream);
+    case TILE_SWAP_128:
+      return partial ? launch_tc<1, 128, B_MN, A_MN, EPI_PARTIAL, true>(p, grid, after, stream)
+                     : launch_tc<1, 128, B_MN, A_MN, EPI, true>(p, grid, after, stream);
+    default:
+      return partial ? launch_tc<1, kSmall, B_MN, A_MN, EPI_PARTIAL, true>(p, grid, after, stream)
+                     : launch_tc<1, kSmall, B_MN, A_MN, EPI, true>(p, grid, after, stream);
+  }
 }
 
 }  // namespace tide

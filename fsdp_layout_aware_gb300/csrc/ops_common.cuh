@@ -66,6 +66,11 @@ inline bool rows_aligned(const void* p, int64_t ld, int64_t elem, int64_t rows) 
   return !p || ((uintptr_t)p % 16 == 0 && (rows <= 1 || ld * elem % 16 == 0));
 }
 
+// out[c] (of `dtype`) = the sum of partial[g][c] over the groups, in a fixed
+// order; zero with none.  `after`: the stream's last kernel is this call's.
+tide_status launch_sum_groups(const float* partial, int64_t groups, int64_t cols, int32_t dtype, void* out, bool after,
+                              cudaStream_t stream);
+
 // SMs of the current device (asked once per device); 0 if the query failed.
 int ops_num_sms();
 

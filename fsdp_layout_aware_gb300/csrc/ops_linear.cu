@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <utility>
 
 #include "gemm_tc.cuh"
 
@@ -48,42 +49,48 @@ int64_t packed_ld(int64_t cols) { return (cols + 7) / 8 * 8; }
 int64_t packed_bytes(int64_t rows, int64_t cols) { return (rows * packed_ld(cols) * 2 + 255) / 256 * 256; }
 
 // How a product [m, k] x [n, k] runs.
-struct Shape {
-  int cg = 1, bn = 128;
-  int32_t tiles_m = 0, tiles_n = 0, k_blocks = 0, split_blocks = 0, splits = 1;
+struct Plan {
+  TcTile tile = TILE_256x256;
+  int32_t tiles_a = 0, tiles_b = 0, k_blocks = 0, split_blocks = 0, splits = 1;
+  int64_t ldp = 0;            // columns of a partial sum, whole tiles
   int64_t partial_bytes = 0;
 };
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Picks the tile and the number of splits with the smallest estimated time, in
-// SM clocks: the turns of the busiest SM times the clocks of a turn.
-Shape pick_shape(int64_t m, int64_t n, int64_t k, int sms) {
-  Shape best;
+// The tile and the number of splits with the smallest estimated time, in SM
+// clocks: what a CTA sets up and winds down, the turns of the busiest CTA times
+// the clocks of a turn, and the joining of splits.
+//   A block of 64 of the sum takes a pair 540 clocks on 256 x 256 (the tensor
+//   cores' rate is 512), and 390 on 256 x 128: there 24 KB a CTA at the 63 bytes
+//   a clock that an SM was seen to draw from L2 bind (256 at the tensor cores'
+//   rate).  A single CTA's block of 16 KB of weights and its tokens comes at
+//   that rate too, but not faster than DRAM delivers the weights to all SMs.
+Plan pick_plan(int64_t m, int64_t n, int64_t k, bool a_mn, int sms) {
+  Plan best;
   double best_cost = 1e300;
   const int64_t kb = ceil_div(k, kTcK);
-  {
-    Shape s;
-    s.cg = 2, s.bn = 256;
-    s.tiles_m = (int32_t)ceil_div(m, 256), s.tiles_n = (int32_t)ceil_div(n, 256);
-    s.k_blocks = s.split_blocks = (int32_t)kb;
-    const double turns = (double)ceil_div((int64_t)s.tiles_m * s.tiles_n, sms / 2);
-    best_cost = turns * (kb * 540.0 + 600.0) + 6000.0;
-    best = s;
-  }
-  for (int64_t splits = 1; splits <= 16 && splits <= std::max<int64_t>(1, kb / 4); ++splits) {
-    Shape s;
-    s.tiles_m = (int32_t)ceil_div(m, 128), s.tiles_n = (int32_t)ceil_div(n, 128);
+  for (const TcTile t : {TILE_256x256, TILE_256x128, TILE_SWAP_128, TILE_SWAP_SMALL}) {
+    const TcTileShape ts = tile_shape(t, a_mn);
+    if (ts.swap && (m > ts.b || (t == TILE_SWAP_128 && m <= small_b(a_mn)))) continue;
+    Plan s;
+    s.tile = t;
+    s.tiles_a = (int32_t)ceil_div(ts.swap ? n : m, ts.a);
+    s.tiles_b = (int32_t)ceil_div(ts.swap ? m : n, ts.b);
     s.k_blocks = (int32_t)kb;
-    s.split_blocks = (int32_t)ceil_div(kb, splits);
-    s.splits = (int32_t)ceil_div(kb, s.split_blocks);
-    const double turns = (double)ceil_div((int64_t)s.tiles_m * s.tiles_n * s.splits, sms);
-    double cost = turns * (s.split_blocks * (m <= 128 ? 650.0 : 340.0) + 500.0) + 3500.0;
-    if (s.splits > 1) {
-      s.partial_bytes = s.splits * m * (int64_t)s.tiles_n * 128 * 4;
-      cost += 4000.0 + (double)s.partial_bytes * 2.0 / 2500.0;
+    s.ldp = ts.swap ? s.tiles_a * (int64_t)ts.a : s.tiles_b * (int64_t)ts.b;
+    const double block = t == TILE_256x256 ? 540 : t == TILE_256x128 ? 390 : 260 + ts.b * 2.0;
+    const double wind_down = t == TILE_256x256 ? 4000 : t == TILE_256x128 ? 2500 : 1000 + ts.b * 10.0;
+    for (int64_t want = 1; want <= 32 && want <= std::max<int64_t>(1, kb / 4); ++want) {
+      s.split_blocks = (int32_t)ceil_div(kb, want);
+      s.splits = (int32_t)ceil_div(kb, s.split_blocks);
+      if (s.splits != want) continue;  // the same split as a smaller number's
+      const double turns = (double)ceil_div((int64_t)s.tiles_a * s.tiles_b * s.splits, sms / ts.ctas);
+      double cost = turns * (s.split_blocks * block + 300.0) + wind_down + 6000.0;
+      s.partial_bytes = s.splits > 1 ? s.splits * m * s.ldp * 4 : 0;
+      if (s.splits > 1) cost += 5000.0 + (double)s.partial_bytes / 1500.0;
+      if (cost < best_cost) best = s, best_cost = cost;
     }
-    if (cost < best_cost) best = s, best_cost = cost;
   }
   return best;
 }
@@ -97,18 +104,19 @@ tide_status check_extent(int64_t m, int64_t n, int64_t k) {
 
 // Workspace of a product: packed copies of operands that TMA cannot read (or
 // that a checkpoint holds), then the splits' partial sums.
-int64_t product_workspace(int64_t m, int64_t n, int64_t k, bool pack_a, int64_t a_rows, int64_t a_cols, bool pack_b,
+int64_t product_workspace(int64_t m, int64_t n, int64_t k, bool a_mn, bool pack_a, int64_t a_rows, int64_t a_cols, bool pack_b,
                           int64_t b_rows, int64_t b_cols) {
   if (m <= 0 || n <= 0 || k <= 0) return 0;
-  const int sms = ops_num_sms();
+  const int sms = std::max(2, ops_num_sms());
   return (pack_a ? packed_bytes(a_rows, a_cols) : 0) + (pack_b ? packed_bytes(b_rows, b_cols) : 0) +
-         (sms > 0 ? pick_shape(m, n, k, sms).partial_bytes : 0);
+         pick_plan(m, n, k, a_mn, sms).partial_bytes;
 }
 
 // Rows of any alignment to rows of packed_ld(cols), eight elements a thread.
 // (What lies between a row's end and the next row is not read by the product.)
 __global__ void __launch_bounds__(256) pack_kernel(int64_t rows, int64_t cols, const bf16* __restrict__ x, int64_t ldx,
                                                    bf16* __restrict__ out, int64_t ldo) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t per_row = ldo / 8;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t row = i / per_row, col = (i - row * per_row) * 8;
@@ -156,61 +164,128 @@ tide_status make_map(CUtensorMap* map, const Operand& o, int box_rows) {
   return r == CUDA_SUCCESS ? TIDE_OK : fail(TIDE_ERR_CUDA, "cuTensorMapEncodeTiled failed: " + std::to_string((int)r));
 }
 
-using Launch = cudaError_t (*)(const TcArgs&, const TcLaunch&, bool, cudaStream_t);
+using Launch = cudaError_t (*)(const TcArgs&, TcTile, int, bool, cudaStream_t);
 
 // out [m, n] = epilogue(sum over k); a_mn / b_mn: the operand's rows run along
-// k (its contiguous axis is m or n).
+// k (its contiguous axis is m or n).  `after`: the stream's last kernel is this
+// call's.
 template <int EPI>
 tide_status product(int64_t m, int64_t n, int64_t k, Operand a, bool a_mn, Operand b, bool b_mn, EpilogueArgs e,
-                    Launch launch, unsigned char* workspace, cudaStream_t stream) {
+                    Launch launch, unsigned char* workspace, bool after, cudaStream_t stream) {
   const int sms = ops_num_sms();
   if (sms <= 0) return fail(TIDE_ERR_CUDA, "the current device could not be queried");
   TIDE_TRY(check_extent(m, n, k));
   e.rows = m, e.cols = n;
   int splits = 0;
   if (k > 0) {
-    const Shape s = pick_shape(m, n, k, sms);
-    if (!readable(a.p, a.rows, a.ld)) TIDE_TRY(pack(&a, &workspace, stream));
-    if (!readable(b.p, b.rows, b.ld)) TIDE_TRY(pack(&b, &workspace, stream));
+    const Plan s = pick_plan(m, n, k, a_mn, sms);
+    const TcTileShape ts = tile_shape(s.tile, a_mn);
+    for (Operand* o : {&a, &b}) {
+      if (readable(o->p, o->rows, o->ld)) continue;
+      TIDE_TRY(pack(o, &workspace, stream));
+      after = true;
+    }
+    if (ts.swap) std::swap(a, b), std::swap(a_mn, b_mn);
     TcArgs p{};
     TIDE_TRY(make_map(&p.a, a, a_mn ? kTcK : 128));
-    TIDE_TRY(make_map(&p.b, b, b_mn ? kTcK : s.bn / s.cg));
-    const bool partial = s.splits > 1;
-    if (partial) e.partial = (float*)workspace, e.ldp = (int64_t)s.tiles_n * s.bn;
+    TIDE_TRY(make_map(&p.b, b, b_mn ? kTcK : ts.b / ts.ctas));
+    if (s.splits > 1) e.partial = (float*)workspace, e.ldp = s.ldp;
     p.e = e;
-    p.tiles_m = s.tiles_m, p.tiles_n = s.tiles_n;
+    p.tiles_a = s.tiles_a, p.tiles_b = s.tiles_b;
     p.k_blocks = s.k_blocks, p.split_blocks = s.split_blocks, p.splits = s.splits;
     TIDE_TRY(ops_status_word(&p.status));
     p.wait_limit_ns = (uint64_t)g_wait_limit_ns.load(std::memory_order_relaxed);
     p.test_drop = g_test_drop.load(std::memory_order_relaxed);
-    const int64_t units = (int64_t)s.tiles_m * s.tiles_n * s.splits;
-    const TcLaunch l{s.cg, s.bn, (int)std::min<int64_t>(units * s.cg, sms / s.cg * s.cg)};
-    TIDE_TRY(cuda_status(launch(p, l, partial, stream), "linear product"));
-    if (!partial) return TIDE_OK;
+    const int64_t units = (int64_t)s.tiles_a * s.tiles_b * s.splits;
+    const int grid = (int)std::min<int64_t>(units * ts.ctas, sms / ts.ctas * ts.ctas);
+    TIDE_TRY(cuda_status(launch(p, s.tile, grid, after, stream), "linear product"));
+    if (s.splits == 1) return TIDE_OK;
     splits = s.splits;
+    after = true;
   }
   const int64_t grid = ceil_div(m * ceil_div(n, 32), 8);
   if (grid > INT32_MAX) return fail(TIDE_ERR_UNIMPLEMENTED, "linear: too many elements for one launch");
-  epilogue_kernel<EPI><<<(unsigned)grid, 256, 0, stream>>>(e, splits);
-  return cuda_status(cudaGetLastError(), "linear epilogue");
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = after ? 1 : 0;
+  return cuda_status(cudaLaunchKernelEx(&cfg, epilogue_kernel<EPI>, e, splits), "linear epilogue");
 }
 
-// db: a block sums 32 columns over all rows, in a fixed order.
-__global__ void __launch_bounds__(1024) column_sum_kernel(int64_t rows, int64_t cols, const bf16* __restrict__ x,
-                                                          int64_t ldx, bf16* __restrict__ out) {
-  __shared__ float s[32][33];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int64_t col = (int64_t)blockIdx.x * 32 + lane;
-  float v = 0.0f;
-  if (col < cols)
-    for (int64_t r = warp; r < rows; r += 32) v += __bfloat162float(x[r * ldx + col]);
-  s[warp][lane] = v;
-  __syncthreads();
-  v = s[lane][warp];
+// db: column sums.  A thread sums V neighbouring columns over its block's rows
+// (one in four of them), and the block's four are joined in shared memory;
+// block row y gives partial[y], summed by launch_sum_groups.
+constexpr int kSumLanes = 64;
+
+template <int V>
+__global__ void __launch_bounds__(256) column_sum_kernel(int64_t rows, int64_t cols, const bf16* __restrict__ x,
+                                                         int64_t ldx, int64_t rows_per_block,
+                                                         float* __restrict__ partial) {
+  __shared__ float s[4][kSumLanes * V];
+  const int lane = threadIdx.x % kSumLanes, part = threadIdx.x / kSumLanes;
+  const int64_t col = ((int64_t)blockIdx.x * kSumLanes + lane) * V;
+  const int64_t r0 = blockIdx.y * rows_per_block, r1 = min(rows, r0 + rows_per_block);
+  float v[V] = {};
+  if (col < cols) {
+    int64_t r = r0 + part;
+    constexpr int kAhead = V == 8 ? 4 : 8;
+    for (; r + 4 * (kAhead - 1) < r1; r += 4 * kAhead) {
+      float t[kAhead][V];
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  const int64_t o = (int64_t)blockIdx.x * 32 + warp;
-  if (lane == 0 && o < cols) out[o] = __float2bfloat16_rn(v);
+      for (int j = 0; j < kAhead; ++j) load_vec<V>(x + (r + 4 * j) * ldx + col, t[j]);
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[k] += t[j][k];
+    }
+    for (; r < r1; r += 4) {
+      float t[V];
+      load_vec<V>(x + r * ldx + col, t);
+#pragma unroll
+      for (int k = 0; k < V; ++k) v[k] += t[k];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < V; ++k) s[part][lane * V + k] = v[k];
+  __syncthreads();
+  for (int i = threadIdx.x; i < kSumLanes * V; i += 256) {
+    const int64_t c = (int64_t)blockIdx.x * kSumLanes * V + i;
+    if (c < cols) partial[blockIdx.y * cols + c] = s[0][i] + s[1][i] + s[2][i] + s[3][i];
+  }
+}
+
+// Rows of blocks that column sums take: enough blocks to fill the GPU, of at
+// least 64 rows.
+int64_t sum_groups(int64_t rows, int64_t cols, bool vec, int sms) {
+  const int64_t across = ceil_div(cols, kSumLanes * (vec ? 8 : 1));
+  return std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(ceil_div(rows, 64), ceil_div(sms * 8, across)), 1024));
+}
+
+bool sums_by_vector(int64_t rows, int64_t cols, const void* x, int64_t ldx) {
+  return cols % 8 == 0 && rows_aligned(x, ldx, 2, rows);
+}
+
+tide_status column_sums(int64_t rows, int64_t cols, const bf16* x, int64_t ldx, float* partial, bf16* out, int sms,
+                        cudaStream_t stream) {
+  int64_t groups = 0;
+  if (rows > 0) {
+    const bool vec = sums_by_vector(rows, cols, x, ldx);
+    groups = sum_groups(rows, cols, vec, sms);
+    const int64_t per = ceil_div(rows, groups);
+    groups = ceil_div(rows, per);
+    const dim3 grid((unsigned)ceil_div(cols, kSumLanes * (vec ? 8 : 1)), (unsigned)groups);
+    if (vec)
+      column_sum_kernel<8><<<grid, 256, 0, stream>>>(rows, cols, x, ldx, per, partial);
+    else
+      column_sum_kernel<1><<<grid, 256, 0, stream>>>(rows, cols, x, ldx, per, partial);
+    TIDE_TRY(cuda_status(cudaGetLastError(), "bias gradient"));
+  }
+  return launch_sum_groups(partial, groups, cols, TIDE_BF16, out, groups > 0, stream);
 }
 
 tide_status check_product(int64_t rows, int64_t inner, int64_t outer) {
@@ -234,7 +309,7 @@ extern "C" {
 
 int64_t tide_linear_workspace(int64_t rows, int64_t inner, int64_t outer, const void* x, int64_t ldx, const void* w,
                               int64_t ldw) {
-  return product_workspace(rows, outer, inner, !readable(x, rows, ldx), rows, inner, !readable(w, outer, ldw), outer,
+  return product_workspace(rows, outer, inner, false, !readable(x, rows, ldx), rows, inner, !readable(w, outer, ldw), outer,
                            inner);
 }
 
@@ -264,13 +339,13 @@ tide_status tide_linear(int64_t rows, int64_t inner, int64_t outer, const void* 
   e.vec = (uintptr_t)bias % 16 == 0 && rows_aligned(residual, ldr, 2, rows) && rows_aligned(y, ldy, 2, rows) &&
           rows_aligned(z, ldz, 2, rows) && rows_aligned(codes, ld_codes, 1, rows);
   return product<EPI_FORWARD>(rows, outer, inner, {(const bf16*)x, rows, inner, ldx}, false,
-                              {(const bf16*)w, outer, inner, ldw}, false, e, launch_forward, (unsigned char*)workspace,
+                              {(const bf16*)w, outer, inner, ldw}, false, e, launch_forward, (unsigned char*)workspace, false,
                               (cudaStream_t)stream);
 }
 
 int64_t tide_linear_grad_input_workspace(int64_t rows, int64_t inner, int64_t outer, const void* dy, int64_t lddy,
                                          const void* w, int64_t ldw) {
-  return product_workspace(rows, inner, outer, !readable(dy, rows, lddy), rows, outer, !readable(w, outer, ldw), outer,
+  return product_workspace(rows, inner, outer, false, !readable(dy, rows, lddy), rows, outer, !readable(w, outer, ldw), outer,
                            inner);
 }
 
@@ -304,13 +379,17 @@ tide_status tide_linear_grad_input(int64_t rows, int64_t inner, int64_t outer, c
           (act == TIDE_ACT_NONE || (z ? rows_aligned(z, ldz, 2, rows) : rows_aligned(codes, ld_codes, 1, rows)));
   return product<EPI_GRAD_INPUT>(rows, inner, outer, {(const bf16*)dy, rows, outer, lddy}, false,
                                  {(const bf16*)w, outer, inner, ldw}, true, e, launch_grad_input,
-                                 (unsigned char*)workspace, (cudaStream_t)stream);
+                                 (unsigned char*)workspace, false, (cudaStream_t)stream);
 }
 
 int64_t tide_linear_grad_weight_workspace(int64_t rows, int64_t inner, int64_t outer, const void* dy, int64_t lddy,
                                           const void* x, int64_t ldx) {
-  return product_workspace(outer, inner, rows, !readable(dy, rows, lddy), rows, outer, !x || !readable(x, rows, ldx),
-                           rows, inner);
+  const int sms = std::max(2, ops_num_sms());
+  if (rows <= 0 || outer <= 0) return 0;
+  // The product's, and the bias gradient's partial sums in the same place after it.
+  const int64_t sums = sum_groups(rows, outer, sums_by_vector(rows, outer, dy, lddy), sms) * outer * 4;
+  return std::max(sums, product_workspace(outer, inner, rows, true, !readable(dy, rows, lddy), rows, outer,
+                                          !x || !readable(x, rows, ldx), rows, inner));
 }
 
 tide_status tide_linear_grad_weight(int64_t rows, int64_t inner, int64_t outer, const void* dy, int64_t lddy,
@@ -347,12 +426,10 @@ tide_status tide_linear_grad_weight(int64_t rows, int64_t inner, int64_t outer, 
     e.out = (bf16*)dw, e.ldo = lddw;
     e.vec = rows_aligned(dw, lddw, 2, outer);
     TIDE_TRY(product<EPI_PLAIN>(outer, inner, rows, {(const bf16*)dy, rows, outer, lddy}, true, b, true, e,
-                                launch_grad_weight, at, stream));
+                                launch_grad_weight, at, !x && rows > 0, stream));
   }
-  if (db) {
-    column_sum_kernel<<<(unsigned)((outer + 31) / 32), 1024, 0, stream>>>(rows, outer, (const bf16*)dy, lddy, (bf16*)db);
-    return cuda_status(cudaGetLastError(), "bias gradient");
-  }
+  if (db)
+    TIDE_TRY(column_sums(rows, outer, (const bf16*)dy, lddy, (float*)workspace, (bf16*)db, ops_num_sms(), stream));
   return TIDE_OK;
 }
 

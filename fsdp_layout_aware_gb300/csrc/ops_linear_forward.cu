@@ -3,8 +3,8 @@
 
 namespace tide {
 
-cudaError_t launch_forward(const TcArgs& p, const TcLaunch& l, bool partial, cudaStream_t stream) {
-  return launch_layout<false, false, EPI_FORWARD>(p, l, partial, stream);
+cudaError_t launch_forward(const TcArgs& p, TcTile t, int grid, bool after, cudaStream_t stream) {
+  return launch_layout<false, false, EPI_FORWARD>(p, t, grid, after, stream);
 }
 
 }  // namespace tide

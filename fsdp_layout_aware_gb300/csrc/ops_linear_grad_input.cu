@@ -3,8 +3,8 @@
 
 namespace tide {
 
-cudaError_t launch_grad_input(const TcArgs& p, const TcLaunch& l, bool partial, cudaStream_t stream) {
-  return launch_layout<false, true, EPI_GRAD_INPUT>(p, l, partial, stream);
+cudaError_t launch_grad_input(const TcArgs& p, TcTile t, int grid, bool after, cudaStream_t stream) {
+  return launch_layout<false, true, EPI_GRAD_INPUT>(p, t, grid, after, stream);
 }
 
 }  // namespace tide

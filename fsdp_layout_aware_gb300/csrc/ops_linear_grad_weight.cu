@@ -3,8 +3,8 @@
 
 namespace tide {
 
-cudaError_t launch_grad_weight(const TcArgs& p, const TcLaunch& l, bool partial, cudaStream_t stream) {
-  return launch_layout<true, true, EPI_PLAIN>(p, l, partial, stream);
+cudaError_t launch_grad_weight(const TcArgs& p, TcTile t, int grid, bool after, cudaStream_t stream) {
+  return launch_layout<true, true, EPI_PLAIN>(p, t, grid, after, stream);
 }
 
 }  // namespace tide

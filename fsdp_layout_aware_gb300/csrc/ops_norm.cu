@@ -353,12 +353,12 @@ __global__ void __launch_bounds__(THREADS) norm_grad_ring_kernel(const NormGradA
   store_partial<8, NV>(a, acc);
 }
 
-// dweight: the sum of the groups' partials, in a fixed order.  A block takes
-// 32 columns; warp w adds partials w, w + 32, ...
+// A block takes 32 columns; warp w adds partials w, w + 32, ...
 template <typename T>
-__global__ void __launch_bounds__(1024) norm_weight_kernel(const float* __restrict__ partial, int64_t groups,
-                                                           int64_t cols, T* __restrict__ dweight) {
+__global__ void __launch_bounds__(1024) sum_groups_kernel(const float* __restrict__ partial, int64_t groups,
+                                                          int64_t cols, T* __restrict__ out) {
   __shared__ float s[32][33];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int64_t col = (int64_t)blockIdx.x * 32 + lane;
   float v = 0.0f;
@@ -378,10 +378,10 @@ __global__ void __launch_bounds__(1024) norm_weight_kernel(const float* __restri
   v = s[lane][warp];  // lane l of warp w: column w's sum over warp l's groups
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  const int64_t out = (int64_t)blockIdx.x * 32 + warp;
-  if (lane == 0 && out < cols) {
+  const int64_t o = (int64_t)blockIdx.x * 32 + warp;
+  if (lane == 0 && o < cols) {
     const float t[1] = {v};
-    store_vec<1>(dweight + out, t);
+    store_vec<1>(out + o, t);
   }
 }
 
@@ -483,10 +483,8 @@ tide_status norm_grad(NormGradArgs a, void* dweight, cudaStream_t stream) {
       st = cuda_status(cudaGetLastError(), "rms norm backward");
     });
   }
-  if (st == TIDE_OK && dweight) {
-    norm_weight_kernel<T><<<(unsigned)((a.cols + 31) / 32), 1024, 0, stream>>>(a.partial, groups, a.cols, (T*)dweight);
-    st = cuda_status(cudaGetLastError(), "rms norm weight gradient");
-  }
+  if (st == TIDE_OK && dweight)
+    st = launch_sum_groups(a.partial, groups, a.cols, sizeof(T) == 2 ? TIDE_BF16 : TIDE_F32, dweight, groups > 0, stream);
   return st;
 }
 
@@ -495,6 +493,23 @@ tide_status check_cols(int64_t cols) {
 }
 
 }  // namespace
+
+tide_status launch_sum_groups(const float* partial, int64_t groups, int64_t cols, int32_t dtype, void* out, bool after,
+                              cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((cols + 31) / 32));
+  cfg.blockDim = dim3(1024);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = after ? 1 : 0;
+  return cuda_status(dtype == TIDE_BF16
+                         ? cudaLaunchKernelEx(&cfg, sum_groups_kernel<bf16>, partial, groups, cols, (bf16*)out)
+                         : cudaLaunchKernelEx(&cfg, sum_groups_kernel<float>, partial, groups, cols, (float*)out),
+                     "joining partial sums");
+}
 
 int ops_num_sms() {
   static int known[64];
