@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_con
   uint64_t* drained = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
 
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
 
   if (threadIdx.x == 0) {
@@ -283,37 +283,41 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_con
   const int first = blockIdx.x / CG, step = gridDim.x / CG;
   bool ok = true;
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     // Producer.  The pair's loads all count on the first CTA's barrier.
     int stage = 0;
     uint32_t phase = 0;
     int64_t issued = 0;
+    const uint32_t full0 = CG == 2 ? mapped_addr(smem_addr(full), 0) : smem_addr(full);
     for (int u = first; u < units && ok; u += step) {
       const TileAt at = tile_at(p, u % tiles);
       const int split = u / tiles;
       const int kb0 = split * p.split_blocks, kb1 = min(p.k_blocks, kb0 + p.split_blocks);
       const int a0 = (at.a * CG + (int)rank) * 128, b0 = at.b * BN + (int)rank * Shape::b_rows;
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!(ok = mbar_wait_bounded(empty + stage, phase ^ 1, p.wait_limit_ns))) break;
+        if (!(ok = warp_wait_bounded(empty + stage, phase ^ 1, p.wait_limit_ns))) break;
         unsigned char* a = smem + stage * Shape::stage_bytes;
         unsigned char* b = a + Shape::a_bytes;
-        if (rank == 0) mbar_arrive_expect_tx(full + stage, CG * Shape::stage_bytes);
-        const uint32_t bar = CG == 2 ? mapped_addr(smem_addr(full + stage), 0) : smem_addr(full + stage);
-        if (issued != p.test_drop) {
-          if constexpr (A_MN) {
-            tma_load_2d<CG>(a, &p.a, a0, kb * kTcK, bar);
-            tma_load_2d<CG>(a + 8192, &p.a, a0 + 64, kb * kTcK, bar);
-          } else {
-            tma_load_2d<CG>(a, &p.a, kb * kTcK, a0, bar);
-          }
-          if constexpr (B_MN) {
+        const uint32_t bar = full0 + stage * 8;
+        if (elect_one()) {
+          if (rank == 0) mbar_arrive_expect_tx(full + stage, CG * Shape::stage_bytes);
+          if (issued != p.test_drop) {
+            if constexpr (A_MN) {
+              tma_load_2d<CG>(a, &p.a, a0, kb * kTcK, bar);
+              tma_load_2d<CG>(a + 8192, &p.a, a0 + 64, kb * kTcK, bar);
+            } else {
+              tma_load_2d<CG>(a, &p.a, kb * kTcK, a0, bar);
+            }
+            if constexpr (B_MN) {
 #pragma unroll
-            for (int i = 0; i < Shape::b_rows / 64; ++i)
-              tma_load_2d<CG>(b + 8192 * i, &p.b, b0 + 64 * i, kb * kTcK, bar);
-          } else {
-            tma_load_2d<CG>(b, &p.b, kb * kTcK, b0, bar);
+              for (int i = 0; i < Shape::b_rows / 64; ++i)
+                tma_load_2d<CG>(b + 8192 * i, &p.b, b0 + 64 * i, kb * kTcK, bar);
+            } else {
+              tma_load_2d<CG>(b, &p.b, kb * kTcK, b0, bar);
+            }
           }
         }
+        __syncwarp();
         ++issued;
         if (++stage == kStages) stage = 0, phase ^= 1;
       }
@@ -323,16 +327,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_con
     for (int s = 0; s < kStages; ++s) {
       const int64_t uses = (issued - s + kStages - 1) / kStages;  // times stage s was filled
       if (uses <= 0) break;
-      if (ok) ok = mbar_wait_bounded(empty + s, (uint32_t)(uses - 1) & 1, p.wait_limit_ns);
-      if (!ok && rank == 0) mbar_wait_bounded(full + s, (uint32_t)(uses - 1) & 1, p.wait_limit_ns);
+      if (ok) ok = warp_wait_bounded(empty + s, (uint32_t)(uses - 1) & 1, p.wait_limit_ns);
+      if (!ok && rank == 0) warp_wait_bounded(full + s, (uint32_t)(uses - 1) & 1, p.wait_limit_ns);
     }
     if (!ok) {  // the pair's other CTA counts on barriers it cannot ask: a millisecond is ample for a load
       const uint64_t t = global_ns();
       while (global_ns() - t < 1000000) __nanosleep(1000);
     }
-  } else if (warp == 1 && lane == 0 && rank == 0) {
+  } else if (warp == 1 && rank == 0) {
     // Matrix instructions, for both CTAs of a pair.
     constexpr uint32_t idesc = instruction_desc(128 * CG, BN, A_MN, B_MN);
+    const uint64_t desc_a0 = operand_desc<A_MN>(smem_addr(smem));
+    const uint64_t desc_b0 = operand_desc<B_MN>(smem_addr(smem) + Shape::a_bytes);
     int stage = 0;
     uint32_t phase = 0;
     int turn = 0;
@@ -340,24 +346,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_con
       const int split = u / tiles;
       const int kb0 = split * p.split_blocks, kb1 = min(p.k_blocks, kb0 + p.split_blocks);
       const int acc = turn & 1;
-      if (!(ok = mbar_wait_bounded(acc_empty + acc, ((turn >> 1) & 1) ^ 1, p.wait_limit_ns))) break;
+      if (!(ok = warp_wait_bounded(acc_empty + acc, ((turn >> 1) & 1) ^ 1, p.wait_limit_ns))) break;
       tc_fence_after();
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!(ok = mbar_wait_bounded(full + stage, phase, p.wait_limit_ns))) break;
+        if (!(ok = warp_wait_bounded(full + stage, phase, p.wait_limit_ns))) break;
         tc_fence_after();
-        const uint32_t a = smem_addr(smem + stage * Shape::stage_bytes);
-        const uint64_t da = operand_desc<A_MN>(a), db = operand_desc<B_MN>(a + Shape::a_bytes);
+        const uint64_t da = desc_a0 + stage * (Shape::stage_bytes >> 4), db = desc_b0 + stage * (Shape::stage_bytes >> 4);
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < kTcK / 16; ++k)
-          tc_mma<CG>(tmem + acc * BN, da + k * kDescStep<A_MN>, db + k * kDescStep<B_MN>, idesc, kb > kb0 || k > 0);
-        tc_commit<CG>(empty + stage);
+          for (int k = 0; k < kTcK / 16; ++k)
+            tc_mma<CG>(tmem + acc * BN, da + k * kDescStep<A_MN>, db + k * kDescStep<B_MN>, idesc, kb > kb0 || k > 0);
+          tc_commit<CG>(empty + stage);
+        }
+        __syncwarp();
         if (++stage == kStages) stage = 0, phase ^= 1;
       }
-      if (ok) tc_commit<CG>(acc_full + acc);
+      if (ok && elect_one()) tc_commit<CG>(acc_full + acc);
+      __syncwarp();
     }
     if (!ok) {
-      tc_commit<CG>(drained);
-      mbar_wait_bounded(drained, 0, p.wait_limit_ns);
+      if (elect_one()) tc_commit<CG>(drained);
+      __syncwarp();
+      warp_wait_bounded(drained, 0, p.wait_limit_ns);
     }
   } else if (warp >= 4) {
     // Epilogue: warp w reads lanes 32 (w mod 4) onwards, one row of the tile a
@@ -369,7 +379,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_con
       const TileAt at = tile_at(p, u % tiles);
       const int split = u / tiles;
       const int acc = turn & 1;
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(acc_full + acc, (turn >> 1) & 1, p.wait_limit_ns));
+      ok = warp_wait_bounded(acc_full + acc, (turn >> 1) & 1, p.wait_limit_ns);
       if (!ok) break;
       tc_fence_after();
       const int64_t a_row = (int64_t)(at.a * CG + (int)rank) * 128 + quad * 32;  // lane 0's row of A
@@ -428,7 +438,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_con
       }
     }
   }
-  if (!ok) atomicOr(p.status, TIDE_DEVICE_TIMEOUT);
+  if (!ok && lane == 0) atomicOr(p.status, TIDE_DEVICE_TIMEOUT);
   __syncwarp();
   tc_fence_before();
   if constexpr (CG == 2)

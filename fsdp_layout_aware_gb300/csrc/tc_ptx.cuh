@@ -38,18 +38,29 @@ __device__ __forceinline__ void fence_mbar_init_cluster() {
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
 
-// Waits for the phase with the given parity to complete, at most limit_ns;
-// false when that ran out.  The clock is only read once try_wait has come back
-// empty a number of times.
-__device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
-  if (mbar_try_wait(bar, parity)) return true;
+// One lane of a whole, converged warp (the same one each time).  The roles below
+// run with all 32 lanes and let this lane issue: the matrix instructions' and
+// copies' operands must be uniform over the warp, and inside a branch that one
+// lane takes by its index the compiler cannot tell that they are (the issue
+// loop then took 540 clocks for four matrix instructions, whatever their size).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
+// A whole warp waits for the phase with the given parity to complete, at most
+// limit_ns; false (on every lane) when that ran out.  The clock is only read
+// once the wait has come back empty a number of times.
+__device__ __forceinline__ bool warp_wait_bounded(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   uint64_t start = 0;
   for (uint32_t n = 1;; ++n) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     if (n % 64 == 0) {
       const uint64_t now = global_ns();
       if (start == 0) start = now;
-      if (now - start > limit_ns) return false;
+      if (__any_sync(0xffffffffu, now - start > limit_ns)) return false;
     }
   }
 }
