@@ -28,7 +28,7 @@ enum Epilogue { EPI_FORWARD, EPI_GRAD_INPUT, EPI_PLAIN, EPI_PARTIAL };
 //   FORWARD      v += bias; z, and its checkpoint, get v; out = f(v) + residual
 //   GRAD_INPUT   out = v * f'(kept z)
 //   PLAIN        out = v
-//   PARTIAL      v in fp32 to partial[split], for epilogue_kernel
+//   PARTIAL      v in fp32 to partial[split], for join_kernel
 struct EpilogueArgs {
   int64_t rows, cols;
   int32_t act;
@@ -50,7 +50,10 @@ struct EpilogueArgs {
   int64_t ldcin;
   const uint8_t* sin;
   int64_t ldsin;
-  float* partial;  // [splits][rows][ldp]
+  // Sums of the splits: with swapped operands [splits][rows][ldp]; otherwise in
+  // blocks of 32 x 32, [splits][blocks of rows][ldp / 32][8][32 rows][4], so that
+  // a warp that holds a row a lane writes and reads 512 bytes at a time.
+  float* partial;
   int64_t ldp;
 };
 
@@ -124,8 +127,7 @@ __device__ __forceinline__ void store32(bf16* p, const float (&v)[32]) {
 // 32 neighbouring columns of one row, held by one thread; every matrix's rows
 // are 16-byte aligned and col is a multiple of 32.
 template <int EPI>
-__device__ __forceinline__ void epilogue_row(const EpilogueArgs& e, int split, int64_t row, int64_t col,
-                                             float (&v)[32]) {
+__device__ __forceinline__ void epilogue_row(const EpilogueArgs& e, int64_t row, int64_t col, float (&v)[32]) {
   float t[32];
   if constexpr (EPI == EPI_FORWARD) {
     if (e.bias) {
@@ -177,44 +179,104 @@ __device__ __forceinline__ void epilogue_row(const EpilogueArgs& e, int split, i
       });
     }
   }
-  if constexpr (EPI == EPI_PARTIAL) {
-    float4* p = reinterpret_cast<float4*>(e.partial + (split * e.rows + row) * e.ldp + col);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-  } else {
-    store32(e.out + row * e.ldo + col, v);
-  }
+  store32(e.out + row * e.ldo + col, v);
 }
 
-// One element of a row per lane, a whole warp on one block of 32 columns; any
-// alignment.  `in`: the element exists (the row does for every lane).
-template <int EPI>
-__device__ __forceinline__ void epilogue_element(const EpilogueArgs& e, int64_t row, int64_t col, bool in, float v,
-                                                 float bias) {
+// Where lane `lane`'s row of the 32 x 32 block at (row, col) keeps its partial
+// sums: columns 4 q to 4 q + 3 are the float4 at 32 q.
+__device__ __forceinline__ float4* partial_block(const EpilogueArgs& e, int split, int64_t row, int64_t col, int lane) {
+  const int64_t block = (split * ((e.rows + 31) / 32) + row / 32) * (e.ldp / 32) + col / 32;
+  return reinterpret_cast<float4*>(e.partial) + block * 256 + lane;
+}
+
+// N rows from `row` (the first n of them exist), a whole warp on one block of 32
+// columns of each, an element a lane; any alignment.  `in`: the column exists.
+// The rows' steps are independent, which keeps a lone warp busy.
+template <int EPI, int N>
+__device__ __forceinline__ void epilogue_columns(const EpilogueArgs& e, int64_t row, int n, int64_t col, bool in,
+                                                 float (&v)[N], float bias) {
   if constexpr (EPI == EPI_FORWARD) {
-    v += bias;
-    if (e.z && in) e.z[row * e.ldz + col] = __float2bfloat16_rn(v);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += bias;
+    if (e.z) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (in && i < n) e.z[(row + i) * e.ldz + col] = __float2bfloat16_rn(v[i]);
+    }
     if (e.codes) {
-      const float t = finite_or_nan(v);
-      const uint32_t m = __reduce_max_sync(0xffffffffu, in ? __float_as_uint(fmaxf(fabsf(t), 0.0f)) : 0u);
-      const int byte = scale_byte(__uint_as_float(m));
-      if (in) {
-        e.codes[row * e.ldc + col] = encode_one(t, byte);
-        if (col % kMxBlock == 0) e.scales[row * e.lds + col / kMxBlock] = (uint8_t)byte;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float t = finite_or_nan(v[i]);
+        const uint32_t m = __reduce_max_sync(0xffffffffu, in ? __float_as_uint(fmaxf(fabsf(t), 0.0f)) : 0u);
+        const int byte = scale_byte(__uint_as_float(m));
+        if (in && i < n) {
+          e.codes[(row + i) * e.ldc + col] = encode_one(t, byte);
+          if (col % kMxBlock == 0) e.scales[(row + i) * e.lds + col / kMxBlock] = (uint8_t)byte;
+        }
       }
     }
-    v = act_value<true>(e.act, v);
-    if (e.residual && in) v += __bfloat162float(e.residual[row * e.ldr + col]);
-  }
-  if constexpr (EPI == EPI_GRAD_INPUT) {
-    if (e.act != TIDE_ACT_NONE && in) {
-      const float z = e.zin ? __bfloat162float(e.zin[row * e.ldzin + col])
-                            : e4m3_values(e.cin[row * e.ldcin + col]).x *
-                                  scale_value(e.sin[row * e.ldsin + col / kMxBlock]);
-      v *= act_grad<true>(e.act, z);
+    float r[N] = {};
+    if (e.residual) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (in && i < n) r[i] = __bfloat162float(e.residual[(row + i) * e.ldr + col]);
+    }
+    with_act(e.act, [&](auto a) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = act_value<true>(a.value, v[i]);
+    });
+    if (e.residual) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += r[i];
     }
   }
-  if (in) e.out[row * e.ldo + col] = __float2bfloat16_rn(v);
+  if constexpr (EPI == EPI_GRAD_INPUT) {
+    if (e.act != TIDE_ACT_NONE) {
+      float z[N] = {};
+      if (e.zin) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (in && i < n) z[i] = __bfloat162float(e.zin[(row + i) * e.ldzin + col]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (in && i < n)
+            z[i] = e4m3_values(e.cin[(row + i) * e.ldcin + col]).x * scale_value(e.sin[(row + i) * e.ldsin + col / kMxBlock]);
+      }
+      with_act(e.act, [&](auto a) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] *= act_grad<true>(a.value, z[i]);
+      });
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (in && i < n) e.out[(row + i) * e.ldo + col] = __float2bfloat16_rn(v[i]);
+}
+
+// A 32 x 32 block of the output at (row, col), lane l holding row l; any
+// alignment.  Where a row cannot take whole vectors it is turned in `block`
+// ([32][33], this warp's): lane l then has column l of each row.
+template <int EPI>
+__device__ __forceinline__ void epilogue_block(const EpilogueArgs& e, int64_t row, int64_t col, int lane, float (&v)[32],
+                                               float* block) {
+  if (e.vec && col + 32 <= e.cols) {
+    if (row + lane < e.rows) epilogue_row<EPI>(e, row + lane, col, v);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 32; ++i) block[lane * 33 + i] = v[i];
+  __syncwarp();
+  const bool in = col + lane < e.cols;
+  float bias = 0.0f;
+  if (EPI == EPI_FORWARD && e.bias && in) bias = __bfloat162float(e.bias[col + lane]);
+  const int n = (int)min((int64_t)32, e.rows - row);
+  for (int r = 0; r < n; r += 8) {
+    float t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = block[(r + i) * 33 + lane];
+    epilogue_columns<EPI>(e, row + r, n - r, col + lane, in, t, bias);
+  }
 }
 
 // ---- the kernel
@@ -412,27 +474,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_con
           __syncwarp();
           const int n = (int)min((int64_t)32, e.rows - b_row);
           const bool in = a_row + lane < e.cols;
-          for (int r = 0; r < n; ++r) {
-            if constexpr (EPI == EPI_PARTIAL)
-              e.partial[(split * e.rows + b_row + r) * e.ldp + a_row + lane] = block[lane * 33 + r];
-            else
-              epilogue_element<EPI>(e, b_row + r, a_row + lane, in, block[lane * 33 + r], lane_bias);
+          for (int r = 0; r < n; r += 8) {
+            float t[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t[i] = block[lane * 33 + r + i];
+            if constexpr (EPI == EPI_PARTIAL) {
+              float* q = e.partial + (split * e.rows + b_row + r) * e.ldp + a_row + lane;
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (r + i < n) q[i * e.ldp] = t[i];
+            } else {
+              epilogue_columns<EPI>(e, b_row + r, n - r, a_row + lane, in, t, lane_bias);
+            }
           }
         } else {
           if (a_row >= e.rows || (EPI != EPI_PARTIAL && b_row >= e.cols)) continue;
-          if (EPI == EPI_PARTIAL || (e.vec && b_row + 32 <= e.cols)) {
-            if (a_row + lane < e.rows) epilogue_row<EPI>(e, split, a_row + lane, b_row, v);
-          } else if constexpr (EPI != EPI_PARTIAL) {
-            // Turned in shared memory: lane l then has column l of each row.
+          if constexpr (EPI == EPI_PARTIAL) {
+            float4* q = partial_block(e, split, a_row, b_row, lane);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) block[lane * 33 + i] = v[i];
-            __syncwarp();
-            const bool in = b_row + lane < e.cols;
-            float bias = 0.0f;
-            if (EPI == EPI_FORWARD && e.bias && in) bias = __bfloat162float(e.bias[b_row + lane]);
-            const int n = (int)min((int64_t)32, e.rows - a_row);
-            for (int r = 0; r < n; ++r)
-              epilogue_element<EPI>(e, a_row + r, b_row + lane, in, block[r * 33 + lane], bias);
+            for (int i = 0; i < 8; ++i) q[32 * i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          } else {
+            epilogue_block<EPI>(e, a_row, b_row, lane, v, block);
           }
         }
       }
@@ -451,25 +513,44 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_con
   }
 }
 
-// The sums of the splits, in order, through the epilogue: a warp takes blocks
-// of 32 columns of a row.  With no splits (nothing to sum) the sums are zero.
-template <int EPI>
-__global__ void __launch_bounds__(256) epilogue_kernel(const EpilogueArgs e, int splits) {
+// The sums of the splits, in order, through the epilogue.  Swapped: a warp
+// takes 32 columns of a row; without splits (nothing to sum) the sums are zero.
+// Otherwise a warp takes a block of 32 x 32.
+constexpr int kJoinThreads = 128;
+
+template <int EPI, bool SWAP>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const EpilogueArgs e, int splits) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x % 32;
-  const int64_t blocks = (e.cols + 31) / 32;
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) / 32;
-  const int64_t row = i / blocks;
-  if (row >= e.rows) return;
-  const int64_t col = (i - row * blocks) * 32 + lane;
-  const bool in = col < e.cols;
-  float v = 0.0f;
-  const float* q = e.partial + row * e.ldp + col;
-  if (in)
-    for (int s = 0; s < splits; ++s) v += q[(int64_t)s * e.rows * e.ldp];
-  float bias = 0.0f;
-  if (EPI == EPI_FORWARD && e.bias && in) bias = __bfloat162float(e.bias[col]);
-  epilogue_element<EPI>(e, row, col, in, v, bias);
+  const int64_t across = (e.cols + 31) / 32;
+  const int64_t i = ((int64_t)blockIdx.x * kJoinThreads + threadIdx.x) / 32;
+  if constexpr (SWAP) {
+    const int64_t row = i / across;
+    if (row >= e.rows) return;
+    const int64_t col = (i - row * across) * 32 + lane;
+    const bool in = col < e.cols;
+    float v[1] = {0.0f};
+    const float* q = e.partial + row * e.ldp + col;
+    if (in)
+      for (int s = 0; s < splits; ++s) v[0] += q[(int64_t)s * e.rows * e.ldp];
+    float bias = 0.0f;
+    if (EPI == EPI_FORWARD && e.bias && in) bias = __bfloat162float(e.bias[col]);
+    epilogue_columns<EPI>(e, row, 1, col, in, v, bias);
+  } else {
+    __shared__ float blocks[kJoinThreads / 32][32 * 33];
+    const int64_t row = i / across * 32, col = i % across * 32;
+    if (row >= e.rows) return;
+    float v[32] = {};
+    for (int s = 0; s < splits; ++s) {
+      const float4* q = partial_block(e, s, row, col, lane);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float4 t = q[32 * k];
+        v[4 * k] += t.x, v[4 * k + 1] += t.y, v[4 * k + 2] += t.z, v[4 * k + 3] += t.w;
+      }
+    }
+    epilogue_block<EPI>(e, row, col, lane, v, blocks[threadIdx.x / 32]);
+  }
 }
 
 // The tiles that are built: pairs of CTAs on 256 x 256 and 256 x 128, and, with

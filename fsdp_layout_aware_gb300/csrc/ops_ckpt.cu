@@ -14,7 +14,7 @@ namespace {
 constexpr int kThreads = 256;
 
 struct StoreArgs {
-  uint32_t items;   // units of work (store_vec: 8 columns, store_any: kAnyBlocks blocks) in this launch
+  uint32_t items;   // units of work (store_vec: 8 columns, store_any: 256) in this launch
   FastDiv per_row;  // of them in a row
   int64_t cols;
   const void* x;
@@ -73,36 +73,52 @@ __global__ void __launch_bounds__(kThreads) store_vec_kernel(const StoreArgs a) 
   }
 }
 
-// Any alignment: a warp takes kAnyBlocks neighbouring blocks of a row, one
-// element a lane.
-constexpr int kAnyBlocks = 4;
-
+// Any alignment: a warp takes 256 columns of a row, a lane eight of them as
+// above.  Codes are stored as aligned 8-byte words: with the row's codes `p`
+// bytes past a boundary, a lane's word is the last p codes of the lane before
+// and its own first 8 - p.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) store_any_kernel(const StoreArgs a) {
   const uint32_t i = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
   if (i >= a.items) return;
-  const uint32_t lane = threadIdx.x % 32;
+  const int lane = threadIdx.x % 32;
   const int64_t row = a.per_row.quotient(i);
-  const int64_t first = (int64_t)(i - (uint32_t)row * a.per_row.d) * (kAnyBlocks * kMxBlock);
-  float v[kAnyBlocks][1];
+  const int64_t col = (int64_t)(i - (uint32_t)row * a.per_row.d) * 256 + lane * 8;
+  const int n = (int)max((int64_t)0, min((int64_t)8, a.cols - col));  // columns that exist
+  const T* x = (const T*)a.x + row * a.ldx + col;
+  float v[8];
+  if (n == 8) {
+    load_any8(x, v);
+  } else {
 #pragma unroll
-  for (int j = 0; j < kAnyBlocks; ++j) {
-    const int64_t col = first + j * kMxBlock + lane;
-    v[j][0] = 0.0f;
-    if (col < a.cols) load_vec<1>((const T*)a.x + row * a.ldx + col, v[j]);
-  }
-#pragma unroll
-  for (int j = 0; j < kAnyBlocks; ++j) {
-    const int64_t col = first + j * kMxBlock + lane;
-    const float t = finite_or_nan(v[j][0]);
-    // Magnitudes order as their bits do; fmaxf leaves NaN out.
-    const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fabsf(t), 0.0f)));
-    const int byte = scale_byte(__uint_as_float(m));
-    if (col < a.cols) {
-      a.codes[row * a.ldc + col] = encode_one(t, byte);
-      if (lane == 0) a.scales[row * a.lds + col / kMxBlock] = (uint8_t)byte;
+    for (int k = 0; k < 8; ++k) {
+      float t[1] = {0.0f};
+      if (k < n) load_vec<1>(x + k, t);
+      v[k] = t[0];
     }
   }
+  const int byte = scale_byte(block_magnitude<4>(v));
+  uint32_t w[2];
+  encode(v, byte, w);
+  if (n > 0 && lane % 4 == 0) a.scales[row * a.lds + col / kMxBlock] = (uint8_t)byte;
+
+  uint8_t* c = a.codes + row * a.ldc + col;
+  const int p = (int)((uintptr_t)c & 7);  // the same for every lane
+  const uint64_t cur = (uint64_t)w[1] << 32 | w[0];
+  const uint64_t before = __shfl_up_sync(0xffffffffu, cur, 1);
+  int n_before = __shfl_up_sync(0xffffffffu, n, 1);
+  if (lane == 0) n_before = 0;
+  const uint64_t word = p ? cur << (8 * p) | before >> (64 - 8 * p) : cur;
+  // Byte j of the word is column j - p; valid from `lo` to below `hi`.
+  const int lo = lane == 0 ? p : 0;
+  const int hi = n > 0 ? min(8, p + n) : n_before - (8 - p);
+  if (lo == 0 && hi == 8) {
+    *reinterpret_cast<uint64_t*>(c - p) = word;
+  } else {
+    for (int j = lo; j < hi; ++j) (c - p)[j] = (uint8_t)(word >> (8 * j));
+  }
+  if (lane == 31)
+    for (int k = 8 - p; k < n; ++k) c[k] = (uint8_t)(cur >> (8 * k));
 }
 
 // fp32 outputs take the accurate exponential and division.
@@ -145,35 +161,44 @@ __global__ void __launch_bounds__(kThreads) load_vec_kernel(const LoadArgs a) {
   }
 }
 
-// Any alignment: a warp takes kAnyBlocks neighbouring blocks of a row, one
-// element a lane.
+// Any alignment: a thread takes the eight columns of an aligned word of out
+// (the row's first and last words may be partial), so that out is stored whole,
+// and grad read whole where it lies as out does.
 template <typename T, bool GRAD>
 __global__ void __launch_bounds__(kThreads) load_any_kernel(const LoadArgs a) {
-  const uint32_t i = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+  const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
   if (i >= a.items) return;
-  const uint32_t lane = threadIdx.x % 32;
   const int64_t row = a.per_row.quotient(i);
-  const int64_t first = (int64_t)(i - (uint32_t)row * a.per_row.d) * (kAnyBlocks * kMxBlock);
-  uint8_t c[kAnyBlocks], s[kAnyBlocks];
-  float g[kAnyBlocks][1];
-#pragma unroll
-  for (int j = 0; j < kAnyBlocks; ++j) {
-    const int64_t col = first + j * kMxBlock + lane;
-    g[j][0] = 0.0f;
-    c[j] = s[j] = 0;
-    if (col < a.cols) {
-      c[j] = a.codes[row * a.ldc + col];
-      s[j] = a.scales[row * a.lds + col / kMxBlock];
-      if (GRAD) load_vec<1>((const T*)a.grad + row * a.ldg + col, g[j]);
+  T* out = (T*)a.out + row * a.ldo;
+  const int phase = (int)((uintptr_t)out % 16 / sizeof(T));
+  const int64_t col = (int64_t)(i - (uint32_t)row * a.per_row.d) * 8 - phase;
+  if (col >= a.cols) return;
+  const uint8_t* codes = a.codes + row * a.ldc;
+  const uint8_t* scales = a.scales + row * a.lds;
+  const T* grad = GRAD ? (const T*)a.grad + row * a.ldg : nullptr;
+  float v[8], g[8] = {};
+  if (col >= 0 && col + 8 <= a.cols) {
+    const uint2 c = load_any_bytes(codes + col);
+    const float s0 = scale_value(scales[col / kMxBlock]), s1 = scale_value(scales[(col + 7) / kMxBlock]);
+    const int first = kMxBlock - (int)(col % kMxBlock);  // columns of the first block
+    if (GRAD) {
+      if ((uintptr_t)(grad + col) % 16 == 0)
+        load_vec<8>(grad + col, g);
+      else
+        load_any8(grad + col, g);
     }
-  }
+    decode8(c, 1.0f, v);
 #pragma unroll
-  for (int j = 0; j < kAnyBlocks; ++j) {
-    const int64_t col = first + j * kMxBlock + lane;
-    if (col >= a.cols) continue;
-    float v[1] = {e4m3_values(c[j]).x * scale_value(s[j])};
-    loaded<T>(v, a.act, GRAD, g[j]);
-    store_vec<1>((T*)a.out + row * a.ldo + col, v);
+    for (int k = 0; k < 8; ++k) v[k] *= k < first ? s0 : s1;
+    loaded<T>(v, a.act, GRAD, g);
+    store_vec<8>(out + col, v);
+  } else {
+    for (int64_t k = max(col, (int64_t)0); k < min(col + 8, a.cols); ++k) {
+      float t[1] = {e4m3_values(codes[k]).x * scale_value(scales[k / kMxBlock])}, u[1] = {0.0f};
+      if (GRAD) load_vec<1>(grad + k, u);
+      loaded<T>(t, a.act, GRAD, u);
+      store_vec<1>(out + k, t);
+    }
   }
 }
 
@@ -200,7 +225,7 @@ tide_status store(int64_t rows, int64_t cols, const void* x, int64_t ldx, uint8_
   const int64_t blocks = div_up(cols, kMxBlock);
   const bool vec = cols % 8 == 0 && rows_aligned(x, ldx, sizeof(T), rows) && (uintptr_t)codes % 8 == 0 &&
                    (rows <= 1 || ldc % 8 == 0);
-  const int64_t per_row = vec ? blocks * 4 : div_up(blocks, kAnyBlocks);
+  const int64_t per_row = vec ? blocks * 4 : div_up(cols, 256);
   return in_launches(rows, per_row, vec ? kThreads * kItems : kThreads / 32, [&](int64_t r, uint32_t items, unsigned grid) {
     const StoreArgs a{items, FastDiv((uint32_t)per_row), cols, (const T*)x + r * ldx, ldx, codes + r * ldc, ldc,
                       scales + r * lds, lds};
@@ -216,8 +241,8 @@ tide_status load(int64_t rows, int64_t cols, const uint8_t* codes, int64_t ldc, 
                  int32_t act, const void* grad, int64_t ldg, void* out, int64_t ldo, cudaStream_t stream) {
   const bool vec = cols % 8 == 0 && rows_aligned(grad, ldg, sizeof(T), rows) &&
                    rows_aligned(out, ldo, sizeof(T), rows) && (uintptr_t)codes % 8 == 0 && (rows <= 1 || ldc % 8 == 0);
-  const int64_t per_row = vec ? cols / 8 : div_up(div_up(cols, kMxBlock), kAnyBlocks);
-  return in_launches(rows, per_row, vec ? kThreads * kItems : kThreads / 32, [&](int64_t r, uint32_t items, unsigned grid) {
+  const int64_t per_row = vec ? cols / 8 : (cols + 14) / 8;  // words that any phase of a row touches
+  return in_launches(rows, per_row, vec ? kThreads * kItems : kThreads, [&](int64_t r, uint32_t items, unsigned grid) {
     const LoadArgs a{items, FastDiv((uint32_t)per_row), cols, codes + r * ldc, ldc, scales + r * lds, lds, act,
                      grad ? (const T*)grad + r * ldg : nullptr, ldg, (T*)out + r * ldo, ldo};
     if (vec && grad)

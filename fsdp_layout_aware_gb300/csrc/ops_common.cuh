@@ -155,6 +155,54 @@ __device__ __forceinline__ void store_vec(float* p, const float (&v)[V]) {
   }
 }
 
+// Eight elements at any alignment, as fp32: the widest loads that stay inside
+// them.
+__device__ __forceinline__ void load_any8(const bf16* p, float (&v)[8]) {
+  const uint16_t* x = reinterpret_cast<const uint16_t*>(p);
+  uint32_t w[4];
+  if ((uintptr_t)x % 4 == 0) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = reinterpret_cast<const uint32_t*>(x)[j];
+  } else {  // an element, three aligned pairs, an element
+    const uint32_t first = x[0], last = x[7];
+    uint32_t q[3];
+#pragma unroll
+    for (int j = 0; j < 3; ++j) q[j] = reinterpret_cast<const uint32_t*>(x + 1)[j];
+    w[0] = first | q[0] << 16;
+    w[1] = __funnelshift_r(q[0], q[1], 16);
+    w[2] = __funnelshift_r(q[1], q[2], 16);
+    w[3] = q[2] >> 16 | last << 16;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = __uint_as_float(w[j] << 16);
+    v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load_any8(const float* p, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = p[j];
+}
+
+// Eight bytes at any alignment.
+__device__ __forceinline__ uint2 load_any_bytes(const uint8_t* p) {
+  const uint32_t phase = (uint32_t)(uintptr_t)p & 3u;
+  if (phase == 0) return make_uint2(reinterpret_cast<const uint32_t*>(p)[0], reinterpret_cast<const uint32_t*>(p)[1]);
+  if (phase == 2) {
+    const uint32_t a = reinterpret_cast<const uint16_t*>(p)[0], b = *reinterpret_cast<const uint32_t*>(p + 2),
+                   c = reinterpret_cast<const uint16_t*>(p)[3];
+    return make_uint2(a | b << 16, b >> 16 | c << 16);
+  }
+  if (phase == 3) {  // 1, 4, 2, 1
+    const uint32_t a = p[0], b = *reinterpret_cast<const uint32_t*>(p + 1), c = *reinterpret_cast<const uint16_t*>(p + 5),
+                   d = p[7];
+    return make_uint2(a | b << 8, b >> 24 | c << 8 | d << 24);
+  }
+  const uint32_t a = p[0], b = *reinterpret_cast<const uint16_t*>(p + 1), c = *reinterpret_cast<const uint32_t*>(p + 3),
+                 d = p[7];  // 1, 2, 4, 1
+  return make_uint2(a | b << 8 | c << 24, c >> 8 | d << 24);
+}
+
 // ---- 8-bit checkpoints
 
 // Scale byte of a block whose largest finite magnitude is `a`: the smallest

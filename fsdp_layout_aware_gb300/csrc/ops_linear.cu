@@ -60,35 +60,39 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // The tile and the number of splits with the smallest estimated time, in SM
 // clocks: what a CTA sets up and winds down, the turns of the busiest CTA times
-// the clocks of a turn, and the joining of splits.
-//   A block of 64 of the sum takes a pair 540 clocks on 256 x 256 (the tensor
-//   cores' rate is 512), and 390 on 256 x 128: there 24 KB a CTA at the 63 bytes
-//   a clock that an SM was seen to draw from L2 bind (256 at the tensor cores'
-//   rate).  A single CTA's block of 16 KB of weights and its tokens comes at
-//   that rate too, but not faster than DRAM delivers the weights to all SMs.
-Plan pick_plan(int64_t m, int64_t n, int64_t k, bool a_mn, int sms) {
+// the clocks of a turn (or what DRAM takes to deliver the operands), and the
+// joining of splits.  Clocks of a block of 64 of the sum, measured with every SM
+// at work (alone, the first two run at the tensor cores' rate, 512 and 256):
+// 570 on 256 x 256, 340 on 256 x 128, and 275 to 420 on the single CTA's tiles.
+Plan pick_plan(int64_t m, int64_t n, int64_t k, bool a_mn, bool vec, int sms) {
   Plan best;
   double best_cost = 1e300;
   const int64_t kb = ceil_div(k, kTcK);
   for (const TcTile t : {TILE_256x256, TILE_256x128, TILE_SWAP_128, TILE_SWAP_SMALL}) {
     const TcTileShape ts = tile_shape(t, a_mn);
-    if (ts.swap && (m > ts.b || (t == TILE_SWAP_128 && m <= small_b(a_mn)))) continue;
+    if (t == TILE_SWAP_128 && m <= small_b(a_mn)) continue;
     Plan s;
     s.tile = t;
     s.tiles_a = (int32_t)ceil_div(ts.swap ? n : m, ts.a);
     s.tiles_b = (int32_t)ceil_div(ts.swap ? m : n, ts.b);
     s.k_blocks = (int32_t)kb;
     s.ldp = ts.swap ? s.tiles_a * (int64_t)ts.a : s.tiles_b * (int64_t)ts.b;
-    const double block = t == TILE_256x256 ? 540 : t == TILE_256x128 ? 390 : 260 + ts.b * 2.0;
-    const double wind_down = t == TILE_256x256 ? 4000 : t == TILE_256x128 ? 2500 : 1000 + ts.b * 10.0;
+    const double block = t == TILE_256x256 ? 570 : t == TILE_256x128 ? 340 : 225 + ts.b * 1.5;
+    // The epilogue of a tile, which the next tile's blocks hide if they take
+    // longer; `vec`: the output's rows take whole vectors.
+    const double epilogue = ts.swap ? 400 + 24.0 * std::min<int64_t>(m, ts.b) : (vec ? 20.0 : 55.0) * ts.b;
     for (int64_t want = 1; want <= 32 && want <= std::max<int64_t>(1, kb / 4); ++want) {
       s.split_blocks = (int32_t)ceil_div(kb, want);
       s.splits = (int32_t)ceil_div(kb, s.split_blocks);
       if (s.splits != want) continue;  // the same split as a smaller number's
       const double turns = (double)ceil_div((int64_t)s.tiles_a * s.tiles_b * s.splits, sms / ts.ctas);
-      double cost = turns * (s.split_blocks * block + 300.0) + wind_down + 6000.0;
-      s.partial_bytes = s.splits > 1 ? s.splits * m * s.ldp * 4 : 0;
-      if (s.splits > 1) cost += 5000.0 + (double)s.partial_bytes / 1500.0;
+      const double busy = turns * std::max(s.split_blocks * block + 300.0, epilogue);
+      const double dram = (double)(m + n) * k * 2.0 / 3500.0;
+      // Neither hides the other altogether; a last turn of few CTAs draws less.
+      const double idle = 1.0 - (double)s.tiles_a * s.tiles_b * s.splits / (turns * (sms / ts.ctas));
+      double cost = std::max(busy, dram * (1.0 + 0.3 * idle)) + 0.25 * std::min(busy, dram) + epilogue + 6000.0;
+      s.partial_bytes = s.splits > 1 ? s.splits * (ts.swap ? m : ceil_div(m, 32) * 32) * s.ldp * 4 : 0;
+      if (s.splits > 1) cost += 2500.0 + (double)s.partial_bytes / 900.0;
       if (cost < best_cost) best = s, best_cost = cost;
     }
   }
@@ -109,33 +113,78 @@ int64_t product_workspace(int64_t m, int64_t n, int64_t k, bool a_mn, bool pack_
   if (m <= 0 || n <= 0 || k <= 0) return 0;
   const int sms = std::max(2, ops_num_sms());
   return (pack_a ? packed_bytes(a_rows, a_cols) : 0) + (pack_b ? packed_bytes(b_rows, b_cols) : 0) +
-         pick_plan(m, n, k, a_mn, sms).partial_bytes;
+         std::max(pick_plan(m, n, k, a_mn, false, sms).partial_bytes, pick_plan(m, n, k, a_mn, true, sms).partial_bytes);
 }
 
-// Rows of any alignment to rows of packed_ld(cols), eight elements a thread.
-// (What lies between a row's end and the next row is not read by the product.)
-__global__ void __launch_bounds__(256) pack_kernel(int64_t rows, int64_t cols, const bf16* __restrict__ x, int64_t ldx,
-                                                   bf16* __restrict__ out, int64_t ldo) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int64_t per_row = ldo / 8;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t row = i / per_row, col = (i - row * per_row) * 8;
-  if (row >= rows) return;
+// Rows of any alignment to rows of packed_ld(cols), eight elements a thread,
+// for up to two operands.  (What lies between a row's end and the next row is
+// not read by the product.)
+struct PackArgs {
+  const bf16* x;
+  bf16* out;
+  int64_t rows, cols, ldx, ldo;
+};
+
+__device__ __forceinline__ void pack_eight(const PackArgs& a, int64_t i) {
+  const int64_t per_row = a.ldo / 8;
+  const int64_t row = ((i | per_row) >> 32) ? i / per_row : (uint32_t)i / (uint32_t)per_row;
+  if (row >= a.rows) return;
+  const int64_t col = (i - row * per_row) * 8;
+  const bf16* x = a.x + row * a.ldx + col;
   float v[8];
+  if (col + 8 <= a.cols) {
+    load_any8(x, v);
+  } else {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) v[k] = col + k < cols ? __bfloat162float(x[row * ldx + col + k]) : 0.0f;
-  store_vec<8>(out + row * ldo + col, v);
+    for (int k = 0; k < 8; ++k) v[k] = col + k < a.cols ? __bfloat162float(x[k]) : 0.0f;
+  }
+  store_vec<8>(a.out + row * a.ldo + col, v);
 }
 
-tide_status pack(Operand* o, unsigned char** at, cudaStream_t stream) {
-  const int64_t ld = packed_ld(o->cols);
-  const int64_t grid = ceil_div(o->rows * (ld / 8), 256);
-  if (grid > INT32_MAX) return fail(TIDE_ERR_UNIMPLEMENTED, "linear: operand too large to lay out anew");
-  pack_kernel<<<(unsigned)grid, 256, 0, stream>>>(o->rows, o->cols, o->p, o->ld, (bf16*)*at, ld);
-  o->p = (const bf16*)*at;
-  o->ld = ld;
-  *at += packed_bytes(o->rows, o->cols);
-  return cuda_status(cudaGetLastError(), "laying out an operand");
+__global__ void __launch_bounds__(256) pack_kernel(const PackArgs a, const PackArgs b, int64_t blocks_a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (blockIdx.x < blocks_a)
+    pack_eight(a, (int64_t)blockIdx.x * 256 + threadIdx.x);
+  else
+    pack_eight(b, (blockIdx.x - blocks_a) * 256 + threadIdx.x);
+}
+
+// A launch that may begin before the stream's last kernel, this call's, ends
+// (the kernel waits for it before it reads anything).
+struct LaunchAfter {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  LaunchAfter(int64_t grid, int threads, bool after, cudaStream_t stream) {
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = after ? 1 : 0;
+  }
+};
+
+// Lays out anew, at *at, those of the operands that TMA cannot read.
+tide_status pack(Operand* const (&which)[2], unsigned char** at, bool* after, cudaStream_t stream) {
+  PackArgs a[2] = {};
+  int64_t blocks[2] = {0, 0};
+  int count = 0;
+  for (Operand* o : which) {
+    if (readable(o->p, o->rows, o->ld)) continue;
+    const int64_t ld = packed_ld(o->cols);
+    a[count] = {o->p, (bf16*)*at, o->rows, o->cols, o->ld, ld};
+    blocks[count++] = ceil_div(o->rows * (ld / 8), 256);
+    o->p = (const bf16*)*at;
+    o->ld = ld;
+    *at += packed_bytes(o->rows, o->cols);
+  }
+  if (count == 0) return TIDE_OK;
+  if (blocks[0] + blocks[1] > INT32_MAX) return fail(TIDE_ERR_UNIMPLEMENTED, "linear: operands too large to lay out anew");
+  const LaunchAfter l(blocks[0] + blocks[1], 256, *after, stream);
+  *after = true;
+  return cuda_status(cudaLaunchKernelEx(&l.cfg, pack_kernel, a[0], a[1], blocks[0]), "laying out operands");
 }
 
 using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
@@ -177,14 +226,12 @@ tide_status product(int64_t m, int64_t n, int64_t k, Operand a, bool a_mn, Opera
   TIDE_TRY(check_extent(m, n, k));
   e.rows = m, e.cols = n;
   int splits = 0;
+  bool swapped = true;
   if (k > 0) {
-    const Plan s = pick_plan(m, n, k, a_mn, sms);
+    const Plan s = pick_plan(m, n, k, a_mn, e.vec, sms);
     const TcTileShape ts = tile_shape(s.tile, a_mn);
-    for (Operand* o : {&a, &b}) {
-      if (readable(o->p, o->rows, o->ld)) continue;
-      TIDE_TRY(pack(o, &workspace, stream));
-      after = true;
-    }
+    Operand* const both[2] = {&a, &b};
+    TIDE_TRY(pack(both, &workspace, &after, stream));
     if (ts.swap) std::swap(a, b), std::swap(a_mn, b_mn);
     TcArgs p{};
     TIDE_TRY(make_map(&p.a, a, a_mn ? kTcK : 128));
@@ -201,20 +248,15 @@ tide_status product(int64_t m, int64_t n, int64_t k, Operand a, bool a_mn, Opera
     TIDE_TRY(cuda_status(launch(p, s.tile, grid, after, stream), "linear product"));
     if (s.splits == 1) return TIDE_OK;
     splits = s.splits;
+    swapped = ts.swap;
     after = true;
   }
-  const int64_t grid = ceil_div(m * ceil_div(n, 32), 8);
+  const int64_t warps = (swapped ? m : ceil_div(m, 32)) * ceil_div(n, 32), grid = ceil_div(warps * 32, kJoinThreads);
   if (grid > INT32_MAX) return fail(TIDE_ERR_UNIMPLEMENTED, "linear: too many elements for one launch");
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = after ? 1 : 0;
-  return cuda_status(cudaLaunchKernelEx(&cfg, epilogue_kernel<EPI>, e, splits), "linear epilogue");
+  const LaunchAfter l(grid, kJoinThreads, after, stream);
+  return cuda_status(swapped ? cudaLaunchKernelEx(&l.cfg, join_kernel<EPI, true>, e, splits)
+                             : cudaLaunchKernelEx(&l.cfg, join_kernel<EPI, false>, e, splits),
+                     "linear epilogue");
 }
 
 // db: column sums.  A thread sums V neighbouring columns over its block's rows

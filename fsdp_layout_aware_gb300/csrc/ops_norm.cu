@@ -241,112 +241,139 @@ inline int ring_slot_bytes(int threads, int nv, int elem, bool kept, bool dres) 
 // shared memory and reads nothing else from it, so the copies need no barrier
 // and cost no registers.  What is in flight then is DEPTH - 1 rows a block,
 // whatever the one barrier of a row costs.
-template <typename T, int NV, int DEPTH, bool KEPT, int THREADS>
-__global__ void __launch_bounds__(THREADS) norm_grad_ring_kernel(const NormGradArgs a) {
+template <typename T, int NV, int DEPTH, bool KEPT, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_ring_kernel(const NormGradArgs a) {
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ float scratch[2][32];
-  constexpr int kWords = sizeof(T) / 2;                        // 16-byte words of a vector
+  constexpr int kWords = sizeof(T) / 2;  // 16-byte words of a vector
+  constexpr int kPer = 16 / sizeof(T);   // elements of a word
   const int threads = blockDim.x * blockDim.y, tid = threadIdx.y * blockDim.x + threadIdx.x;
-  const int h_bytes = KEPT ? 8 : 16 * kWords;
-  const uint32_t slot = (uint32_t)(threads * NV * (h_bytes + 16 * kWords * (a.dres ? 2 : 1)));
-  const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring);
+  const bool has_dres = a.dres != nullptr;
   // Within a slot: dy, dres, h; within each, word by word over the threads, so
   // neighbouring threads use neighbouring banks.
   const uint32_t vec_bytes = (uint32_t)threads * 16;
-  const uint32_t off_dres = NV * kWords * vec_bytes, off_h = off_dres * (a.dres ? 2 : 1);
+  const uint32_t off_dres = NV * kWords * vec_bytes, off_h = off_dres * (has_dres ? 2 : 1);
+  const uint32_t slot = off_h + NV * (KEPT ? vec_bytes / 2 : kWords * vec_bytes);
+  const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring);
+  const int apart = blockDim.x * 8;  // columns from one of a thread's vectors to the next
+  const int col0 = threadIdx.x * 8;
 
   int turn = 0;
-  float acc[NV][8] = {}, w[NV][8] = {};
+  float acc[NV][8] = {};
+  T w[NV][8];
+  bool in[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int col = (i * blockDim.x + threadIdx.x) * 8;
-    if (col < a.cols) load_vec<8>((const T*)a.weight + col, w[i]);
+    in[i] = col0 + i * apart < a.cols;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[i][k] = in[i] ? ((const T*)a.weight)[col0 + i * apart + k] : T(0.0f);
   }
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
-  const int64_t first = (int64_t)blockIdx.x * blockDim.y;
+  int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
 
-  auto fetch = [&](int64_t row, uint32_t at) {
-    if (row < a.rows) {
+  // The next row to fetch, and where its vectors are.
+  int64_t ahead = row;
+  const T* dy = (const T*)a.dy + row * a.lddy + col0;
+  const T* dres = has_dres ? (const T*)a.dres + row * a.ldres + col0 : nullptr;
+  const T* h = KEPT ? nullptr : (const T*)a.h + row * a.ldh + col0;
+  const uint8_t* codes = KEPT ? a.codes + row * a.ldc + col0 : nullptr;
+  T* dx = (T*)a.dx + row * a.lddx + col0;
+  auto fetch = [&](uint32_t at) {
+    if (ahead < a.rows) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int col = (i * blockDim.x + threadIdx.x) * 8;
-        if (col >= a.cols) continue;
-        const T* dy = (const T*)a.dy + row * a.lddy + col;
+        if (!in[i]) continue;
 #pragma unroll
         for (int q = 0; q < kWords; ++q) {
           const uint32_t o = at + (i * kWords + q) * vec_bytes + tid * 16;
-          copy_async16(o, dy + q * (16 / sizeof(T)));
-          if (a.dres) copy_async16(o + off_dres, (const T*)a.dres + row * a.ldres + col + q * (16 / sizeof(T)));
-          if (!KEPT) copy_async16(o + off_h, (const T*)a.h + row * a.ldh + col + q * (16 / sizeof(T)));
+          copy_async16(o, dy + i * apart + q * kPer);
+          if (has_dres) copy_async16(o + off_dres, dres + i * apart + q * kPer);
+          if constexpr (!KEPT) copy_async16(o + off_h, h + i * apart + q * kPer);
         }
-        if (KEPT) copy_async8(at + off_h + (i * threads + tid) * 8, a.codes + row * a.ldc + col);
+        if constexpr (KEPT) copy_async8(at + off_h + (i * threads + tid) * 8, codes + i * apart);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
+    ahead += step;
+    dy += step * a.lddy;
+    if (has_dres) dres += step * a.ldres;
+    if constexpr (KEPT)
+      codes += step * a.ldc;
+    else
+      h += step * a.ldh;
+  };
+  auto word = [&](const unsigned char* s, float* v) {  // a 16-byte word of T
+    if constexpr (kWords == 1) {
+      load_vec<8>(reinterpret_cast<const T*>(s), *reinterpret_cast<float(*)[8]>(v));
+    } else {
+      const float4 x = *reinterpret_cast<const float4*>(s);
+      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    }
   };
   // rstd and the scales of a row, one row ahead.
   float rstd = 0.0f;
   uint8_t scale[NV] = {};
-  auto fetch_small = [&](int64_t row) {
-    if (row >= a.rows) return;
-    rstd = a.rstd[row];
+  auto fetch_small = [&](int64_t r) {
+    if (r >= a.rows) return;
+    rstd = a.rstd[r];
     if constexpr (KEPT) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int col = (i * blockDim.x + threadIdx.x) * 8;
-        if (col < a.cols) scale[i] = a.scales[row * a.lds + col / kMxBlock];
-      }
+      for (int i = 0; i < NV; ++i)
+        if (in[i]) scale[i] = a.scales[r * a.lds + (col0 + i * apart) / kMxBlock];
     }
-  };
-  auto word = [&](uint32_t o, float (&v)[8]) {  // a vector of T at ring offset o
-    load_vec<8>(reinterpret_cast<const T*>(ring + o), v);
   };
 
 #pragma unroll
-  for (int d = 0; d < DEPTH - 1; ++d) fetch(first + threadIdx.y + d * step, base + d * slot);
-  fetch_small(first + threadIdx.y);
+  for (int d = 0; d < DEPTH - 1; ++d) fetch(base + d * slot);
+  fetch_small(row);
   int at = 0;
-  for (int64_t r0 = first; r0 < a.rows; r0 += step) {
-    const int64_t row = r0 + threadIdx.y;
+  // Every group of a block makes the same number of turns (row_sum's barrier).
+  for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < a.rows; r0 += step, row += step, dx += step * a.lddx) {
     const bool here = row < a.rows;
     int next = at + DEPTH - 1;
     if (next >= DEPTH) next -= DEPTH;
-    fetch(row + (DEPTH - 1) * step, base + next * slot);
-    const float row_rstd = here ? rstd : 0.0f;
-    uint8_t row_scale[NV];
+    fetch(base + next * slot);
+    const float r = here ? rstd : 0.0f;
+    float to_n[NV];  // what turns a kept value into n
 #pragma unroll
-    for (int i = 0; i < NV; ++i) row_scale[i] = scale[i];
+    for (int i = 0; i < NV; ++i) to_n[i] = KEPT ? scale_value(scale[i]) * r : r;
     fetch_small(row + step);
     asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
-    float n[NV][8] = {}, g[NV][8] = {}, dres[NV][8] = {};
+    const unsigned char* s = ring + at * slot + tid * 16;
+    float n[NV][8] = {}, g[NV][8] = {};
+    float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = (i * blockDim.x + threadIdx.x) * 8;
-      if (!here || col >= a.cols) continue;
-      const unsigned char* s = ring + at * slot;
-      if constexpr (kWords == 1) {
-        word(at * slot + i * vec_bytes + tid * 16, g[i]);
-        if (a.dres) word(at * slot + off_dres + i * vec_bytes + tid * 16, dres[i]);
-        if (!KEPT) word(at * slot + off_h + i * vec_bytes + tid * 16, n[i]);
-      } else {
+      if (!here || !in[i]) continue;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const uint32_t o = (i * 2 + q) * vec_bytes + tid * 16;
-          const float4 x = *reinterpret_cast<const float4*>(s + o);
-          g[i][4 * q] = x.x, g[i][4 * q + 1] = x.y, g[i][4 * q + 2] = x.z, g[i][4 * q + 3] = x.w;
-          if (a.dres) {
-            const float4 y = *reinterpret_cast<const float4*>(s + off_dres + o);
-            dres[i][4 * q] = y.x, dres[i][4 * q + 1] = y.y, dres[i][4 * q + 2] = y.z, dres[i][4 * q + 3] = y.w;
-          }
-          if (!KEPT) {
-            const float4 z = *reinterpret_cast<const float4*>(s + off_h + o);
-            n[i][4 * q] = z.x, n[i][4 * q + 1] = z.y, n[i][4 * q + 2] = z.z, n[i][4 * q + 3] = z.w;
-          }
-        }
+      for (int q = 0; q < kWords; ++q) {
+        word(s + (i * kWords + q) * vec_bytes, g[i] + q * kPer);
+        if constexpr (!KEPT) word(s + off_h + (i * kWords + q) * vec_bytes, n[i] + q * kPer);
       }
-      if (KEPT) decode8(*reinterpret_cast<const uint2*>(s + off_h + (i * threads + tid) * 8), scale_value(row_scale[i]), n[i]);
+      if constexpr (KEPT) decode8(*reinterpret_cast<const uint2*>(ring + at * slot + off_h + (i * threads + tid) * 8), to_n[i], n[i]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if constexpr (!KEPT) n[i][k] *= to_n[i];
+        acc[i][k] = fmaf(g[i][k], n[i][k], acc[i][k]);
+        g[i][k] *= (float)w[i][k];
+        sum = fmaf(g[i][k], n[i][k], sum);
+      }
     }
-    grad_row<T, 8, NV>(a, row, here, row_rstd, n, g, w, acc, scratch, turn, dres);
+    if (a.dx) {
+      const float mean = row_sum(sum, scratch, turn) / (float)a.cols;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (!here || !in[i]) continue;
+        float d[8] = {};
+        if (has_dres) {
+#pragma unroll
+          for (int q = 0; q < kWords; ++q) word(s + off_dres + (i * kWords + q) * vec_bytes, d + q * kPer);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) d[k] = fmaf(r, fmaf(-n[i][k], mean, g[i][k]), d[k]);
+        store_vec<8>(dx + i * apart, d);
+      }
+    }
     if (++at == DEPTH) at = 0;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
@@ -469,13 +496,23 @@ tide_status norm_grad(NormGradArgs a, void* dweight, cudaStream_t stream) {
           }
           st = cuda_status(err, "rms norm backward");
         };
-        constexpr int kT = threads();
-        if (depth == 4) {
-          a.h ? ring(norm_grad_ring_kernel<T, nv(), 4, false, kT>) : ring(norm_grad_ring_kernel<T, nv(), 4, true, kT>);
-          return;
-        }
-        if (depth == 2) {
-          a.h ? ring(norm_grad_ring_kernel<T, nv(), 2, false, kT>) : ring(norm_grad_ring_kernel<T, nv(), 2, true, kT>);
+        // Registers for two blocks an SM where the block is small enough, for
+        // one otherwise (with one, 5120 columns took 79 us where two take 57).
+        auto pick = [&](auto most, auto min_blocks) {
+          constexpr int kT = most(), kB = min_blocks();
+          if (depth == 4)
+            a.h ? ring(norm_grad_ring_kernel<T, nv(), 4, false, kT, kB>) : ring(norm_grad_ring_kernel<T, nv(), 4, true, kT, kB>);
+          else
+            a.h ? ring(norm_grad_ring_kernel<T, nv(), 2, false, kT, kB>) : ring(norm_grad_ring_kernel<T, nv(), 2, true, kT, kB>);
+        };
+        if (depth) {
+          if constexpr (nv() == 1) {
+            pick(Int<256>(), Int<3>());
+          } else if constexpr (nv() == 2) {
+            s.threads <= 320 ? pick(Int<320>(), Int<2>()) : pick(Int<512>(), Int<1>());
+          } else {
+            pick(Int<512>(), Int<1>());
+          }
           return;
         }
       }
