@@ -17,6 +17,8 @@
 // word, and the CTA drains its copies, frees its tensor memory and returns.
 #pragma once
 
+#include <atomic>
+
 #include "ops_common.cuh"
 #include "tc_ptx.cuh"
 
@@ -66,6 +68,7 @@ struct TcArgs {
   int32_t splits;
   int32_t* status;
   uint64_t wait_limit_ns;
+  bool beside;             // runs beside the kernel before it, whose results it does not read
   int64_t test_drop;       // k block (counted per CTA) whose loads are withheld (tests); -1: none
 };
 
@@ -337,7 +340,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_con
   const uint32_t tmem = *tmem_slot;
   // Only now is anything read that an earlier kernel of the call wrote; what
   // follows may be launched while this runs (it waits likewise).
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!p.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const int tiles = p.tiles_a * p.tiles_b;
@@ -500,6 +503,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_con
       }
     }
   }
+  // This kernel is not done before the one beside it is.
+  if (p.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!ok && lane == 0) atomicOr(p.status, TIDE_DEVICE_TIMEOUT);
   __syncwarp();
   tc_fence_before();
@@ -581,8 +586,15 @@ template <int CG, int BN, bool A_MN, bool B_MN, int EPI, bool SWAP>
 cudaError_t launch_tc(const TcArgs& p, int grid, bool after, cudaStream_t stream) {
   auto kernel = gemm_tc_kernel<CG, BN, A_MN, B_MN, EPI, SWAP>;
   constexpr int smem = TcShape<CG, BN>::smem_bytes;
-  const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> ready{0};  // devices (bits) whose limit has been raised
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
+  if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess) return err;
+    if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kTcThreads);

@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <functional>
 #include <utility>
 
 #include "gemm_tc.cuh"
@@ -64,7 +65,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // joining of splits.  Clocks of a block of 64 of the sum, measured with every SM
 // at work (alone, the first two run at the tensor cores' rate, 512 and 256):
 // 570 on 256 x 256, 340 on 256 x 128, and 275 to 420 on the single CTA's tiles.
-Plan pick_plan(int64_t m, int64_t n, int64_t k, bool a_mn, bool vec, int sms) {
+Plan choose_plan(int64_t m, int64_t n, int64_t k, bool a_mn, bool vec, int sms) {
   Plan best;
   double best_cost = 1e300;
   const int64_t kb = ceil_div(k, kTcK);
@@ -97,6 +98,26 @@ Plan pick_plan(int64_t m, int64_t n, int64_t k, bool a_mn, bool vec, int sms) {
     }
   }
   return best;
+}
+
+// choose_plan, remembering the sizes a thread asked for last (a pure function of
+// them; it costs a microsecond or two, and a call and its workspace query ask
+// for the same).
+Plan pick_plan(int64_t m, int64_t n, int64_t k, bool a_mn, bool vec, int sms) {
+  struct Known {
+    int64_t m = -1, n = -1, k = -1;
+    int sms = 0;
+    bool a_mn = false, vec = false;
+    Plan plan;
+  };
+  static thread_local Known known[64];
+  const uint64_t mix = ((uint64_t)m * 0x9E3779B97F4A7C15ull ^ (uint64_t)n * 0xC2B2AE3D27D4EB4Full ^
+                        (uint64_t)k * 0x165667B19E3779F9ull ^ (uint64_t)(a_mn * 2 + vec)) *
+                       0x9E3779B97F4A7C15ull;
+  Known& e = known[mix >> 58];
+  if (e.m != m || e.n != n || e.k != k || e.sms != sms || e.a_mn != a_mn || e.vec != vec)
+    e = Known{m, n, k, sms, a_mn, vec, choose_plan(m, n, k, a_mn, vec, sms)};
+  return e.plan;
 }
 
 tide_status check_extent(int64_t m, int64_t n, int64_t k) {
@@ -217,10 +238,12 @@ using Launch = cudaError_t (*)(const TcArgs&, TcTile, int, bool, cudaStream_t);
 
 // out [m, n] = epilogue(sum over k); a_mn / b_mn: the operand's rows run along
 // k (its contiguous axis is m or n).  `after`: the stream's last kernel is this
-// call's.
+// call's; `beside`, if not null, is called once the operands are laid out, to
+// launch a kernel that the product may overlap.
 template <int EPI>
 tide_status product(int64_t m, int64_t n, int64_t k, Operand a, bool a_mn, Operand b, bool b_mn, EpilogueArgs e,
-                    Launch launch, unsigned char* workspace, bool after, cudaStream_t stream) {
+                    Launch launch, unsigned char* workspace, bool after, cudaStream_t stream,
+                    const std::function<tide_status()>* beside = nullptr) {
   const int sms = ops_num_sms();
   if (sms <= 0) return fail(TIDE_ERR_CUDA, "the current device could not be queried");
   TIDE_TRY(check_extent(m, n, k));
@@ -234,6 +257,10 @@ tide_status product(int64_t m, int64_t n, int64_t k, Operand a, bool a_mn, Opera
     TIDE_TRY(pack(both, &workspace, &after, stream));
     if (ts.swap) std::swap(a, b), std::swap(a_mn, b_mn);
     TcArgs p{};
+    if (beside) {
+      TIDE_TRY((*beside)());
+      p.beside = after = true;
+    }
     TIDE_TRY(make_map(&p.a, a, a_mn ? kTcK : 128));
     TIDE_TRY(make_map(&p.b, b, b_mn ? kTcK : ts.b / ts.ctas));
     if (s.splits > 1) e.partial = (float*)workspace, e.ldp = s.ldp;
@@ -259,33 +286,37 @@ tide_status product(int64_t m, int64_t n, int64_t k, Operand a, bool a_mn, Opera
                      "linear epilogue");
 }
 
-// db: column sums.  A thread sums V neighbouring columns over its block's rows
-// (one in four of them), and the block's four are joined in shared memory;
-// block row y gives partial[y], summed by launch_sum_groups.
+// db: column sums.  A thread sums V neighbouring columns over every other one
+// of its block's rows, and the block's two are joined in shared memory; block
+// row y gives partial[y], summed by launch_sum_groups.  It runs beside the
+// product: its blocks are few and small enough that a product's CTA fits on the
+// SM with them, and it lets the product start as soon as they are all there.
 constexpr int kSumLanes = 64;
 
 template <int V>
-__global__ void __launch_bounds__(256) column_sum_kernel(int64_t rows, int64_t cols, const bf16* __restrict__ x,
-                                                         int64_t ldx, int64_t rows_per_block,
-                                                         float* __restrict__ partial) {
-  __shared__ float s[4][kSumLanes * V];
+__global__ void __launch_bounds__(2 * kSumLanes) column_sum_kernel(int64_t rows, int64_t cols,
+                                                                   const bf16* __restrict__ x, int64_t ldx,
+                                                                   int64_t rows_per_block,
+                                                                   float* __restrict__ partial) {
+  __shared__ float s[2][kSumLanes * V];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x % kSumLanes, part = threadIdx.x / kSumLanes;
   const int64_t col = ((int64_t)blockIdx.x * kSumLanes + lane) * V;
   const int64_t r0 = blockIdx.y * rows_per_block, r1 = min(rows, r0 + rows_per_block);
   float v[V] = {};
   if (col < cols) {
     int64_t r = r0 + part;
-    constexpr int kAhead = V == 8 ? 4 : 8;
-    for (; r + 4 * (kAhead - 1) < r1; r += 4 * kAhead) {
+    constexpr int kAhead = V == 8 ? 8 : 16;
+    for (; r + 2 * (kAhead - 1) < r1; r += 2 * kAhead) {
       float t[kAhead][V];
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) load_vec<V>(x + (r + 4 * j) * ldx + col, t[j]);
+      for (int j = 0; j < kAhead; ++j) load_vec<V>(x + (r + 2 * j) * ldx + col, t[j]);
 #pragma unroll
       for (int j = 0; j < kAhead; ++j)
 #pragma unroll
         for (int k = 0; k < V; ++k) v[k] += t[j][k];
     }
-    for (; r < r1; r += 4) {
+    for (; r < r1; r += 2) {
       float t[V];
       load_vec<V>(x + r * ldx + col, t);
 #pragma unroll
@@ -295,39 +326,36 @@ __global__ void __launch_bounds__(256) column_sum_kernel(int64_t rows, int64_t c
 #pragma unroll
   for (int k = 0; k < V; ++k) s[part][lane * V + k] = v[k];
   __syncthreads();
-  for (int i = threadIdx.x; i < kSumLanes * V; i += 256) {
+  for (int i = threadIdx.x; i < kSumLanes * V; i += 2 * kSumLanes) {
     const int64_t c = (int64_t)blockIdx.x * kSumLanes * V + i;
-    if (c < cols) partial[blockIdx.y * cols + c] = s[0][i] + s[1][i] + s[2][i] + s[3][i];
+    if (c < cols) partial[blockIdx.y * cols + c] = s[0][i] + s[1][i];
   }
 }
 
-// Rows of blocks that column sums take: enough blocks to fill the GPU, of at
-// least 64 rows.
-int64_t sum_groups(int64_t rows, int64_t cols, bool vec, int sms) {
-  const int64_t across = ceil_div(cols, kSumLanes * (vec ? 8 : 1));
-  return std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(ceil_div(rows, 64), ceil_div(sms * 8, across)), 1024));
+// Columns a thread sums, and the row groups of the partial sums: two blocks an
+// SM in all, groups of at least 32 rows.
+int sum_vector(int64_t rows, int64_t cols, const void* x, int64_t ldx) {
+  return cols % 8 == 0 && rows_aligned(x, ldx, 2, rows) ? 8 : 1;
+}
+int64_t sum_groups(int64_t rows, int64_t cols, int v, int sms) {
+  const int64_t across = ceil_div(cols, kSumLanes * v);
+  const int64_t groups = std::max<int64_t>(1, std::min(ceil_div(rows, 32), ceil_div(2 * sms, across)));
+  return ceil_div(rows, ceil_div(rows, groups));  // groups that have rows
 }
 
-bool sums_by_vector(int64_t rows, int64_t cols, const void* x, int64_t ldx) {
-  return cols % 8 == 0 && rows_aligned(x, ldx, 2, rows);
+int64_t sum_bytes(int64_t rows, int64_t cols, int v, int sms) {
+  return ceil_div(sum_groups(rows, cols, v, sms) * cols * 4, 256) * 256;
 }
 
-tide_status column_sums(int64_t rows, int64_t cols, const bf16* x, int64_t ldx, float* partial, bf16* out, int sms,
+tide_status column_sums(int64_t rows, int64_t cols, const bf16* x, int64_t ldx, int v, int64_t groups, float* partial,
                         cudaStream_t stream) {
-  int64_t groups = 0;
-  if (rows > 0) {
-    const bool vec = sums_by_vector(rows, cols, x, ldx);
-    groups = sum_groups(rows, cols, vec, sms);
-    const int64_t per = ceil_div(rows, groups);
-    groups = ceil_div(rows, per);
-    const dim3 grid((unsigned)ceil_div(cols, kSumLanes * (vec ? 8 : 1)), (unsigned)groups);
-    if (vec)
-      column_sum_kernel<8><<<grid, 256, 0, stream>>>(rows, cols, x, ldx, per, partial);
-    else
-      column_sum_kernel<1><<<grid, 256, 0, stream>>>(rows, cols, x, ldx, per, partial);
-    TIDE_TRY(cuda_status(cudaGetLastError(), "bias gradient"));
-  }
-  return launch_sum_groups(partial, groups, cols, TIDE_BF16, out, groups > 0, stream);
+  const dim3 grid((unsigned)ceil_div(cols, kSumLanes * v), (unsigned)groups);
+  const int64_t per = ceil_div(rows, groups);
+  if (v == 8)
+    column_sum_kernel<8><<<grid, 2 * kSumLanes, 0, stream>>>(rows, cols, x, ldx, per, partial);
+  else
+    column_sum_kernel<1><<<grid, 2 * kSumLanes, 0, stream>>>(rows, cols, x, ldx, per, partial);
+  return cuda_status(cudaGetLastError(), "bias gradient");
 }
 
 tide_status check_product(int64_t rows, int64_t inner, int64_t outer) {
@@ -425,13 +453,13 @@ tide_status tide_linear_grad_input(int64_t rows, int64_t inner, int64_t outer, c
 }
 
 int64_t tide_linear_grad_weight_workspace(int64_t rows, int64_t inner, int64_t outer, const void* dy, int64_t lddy,
-                                          const void* x, int64_t ldx) {
+                                          const void* x, int64_t ldx, int32_t with_db) {
   const int sms = std::max(2, ops_num_sms());
   if (rows <= 0 || outer <= 0) return 0;
-  // The product's, and the bias gradient's partial sums in the same place after it.
-  const int64_t sums = sum_groups(rows, outer, sums_by_vector(rows, outer, dy, lddy), sms) * outer * 4;
-  return std::max(sums, product_workspace(outer, inner, rows, true, !readable(dy, rows, lddy), rows, outer,
-                                          !x || !readable(x, rows, ldx), rows, inner));
+  // The bias gradient's partial sums, then the product's.
+  return (with_db ? sum_bytes(rows, outer, sum_vector(rows, outer, dy, lddy), sms) : 0) +
+         product_workspace(outer, inner, rows, true, !readable(dy, rows, lddy), rows, outer,
+                           !x || !readable(x, rows, ldx), rows, inner);
 }
 
 tide_status tide_linear_grad_weight(int64_t rows, int64_t inner, int64_t outer, const void* dy, int64_t lddy,
@@ -454,9 +482,17 @@ tide_status tide_linear_grad_weight(int64_t rows, int64_t inner, int64_t outer, 
   TIDE_TRY(check_matrix(dw, outer, inner, lddw, 2, "dw"));
   if (db) TIDE_TRY(check_matrix(db, 1, outer, outer, 2, "db"));
   TIDE_TRY(check_workspace(workspace, workspace_bytes,
-                           tide_linear_grad_weight_workspace(rows, inner, outer, dy, lddy, x, ldx)));
+                           tide_linear_grad_weight_workspace(rows, inner, outer, dy, lddy, x, ldx, db != nullptr)));
+  const int sms = std::max(2, ops_num_sms());
+  const int v = sum_vector(rows, outer, dy, lddy);
+  const int64_t groups = db && rows > 0 ? sum_groups(rows, outer, v, sms) : 0;
+  float* partial = (float*)workspace;
+  const std::function<tide_status()> sums = [&] {
+    return column_sums(rows, outer, (const bf16*)dy, lddy, v, groups, partial, stream);
+  };
+  bool summed = false;
   if (inner > 0) {
-    unsigned char* at = (unsigned char*)workspace;
+    unsigned char* at = (unsigned char*)workspace + (groups > 0 ? sum_bytes(rows, outer, v, sms) : 0);
     Operand b{(const bf16*)x, rows, inner, ldx};
     if (!x && rows > 0) {
       TIDE_TRY(launch_checkpoint_load_bf16(rows, inner, codes, ld_codes, scales, ld_scales, act, at, packed_ld(inner),
@@ -467,12 +503,13 @@ tide_status tide_linear_grad_weight(int64_t rows, int64_t inner, int64_t outer, 
     EpilogueArgs e{};
     e.out = (bf16*)dw, e.ldo = lddw;
     e.vec = rows_aligned(dw, lddw, 2, outer);
+    summed = groups > 0;
     TIDE_TRY(product<EPI_PLAIN>(outer, inner, rows, {(const bf16*)dy, rows, outer, lddy}, true, b, true, e,
-                                launch_grad_weight, at, !x && rows > 0, stream));
+                                launch_grad_weight, at, !x && rows > 0, stream, summed ? &sums : nullptr));
   }
-  if (db)
-    TIDE_TRY(column_sums(rows, outer, (const bf16*)dy, lddy, (float*)workspace, (bf16*)db, ops_num_sms(), stream));
-  return TIDE_OK;
+  if (!db) return TIDE_OK;
+  if (groups > 0 && !summed) TIDE_TRY(sums());
+  return launch_sum_groups(partial, groups, outer, TIDE_BF16, db, groups > 0, stream);
 }
 
 tide_status tide_ops_check(void) {

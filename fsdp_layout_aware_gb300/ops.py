@@ -42,7 +42,7 @@ def _declare():
         "tide_linear": (_i32, 3 * [_i64] + 2 * _MAT + [_vp, _i32] + 5 * _MAT + [_vp, _i64, _vp]),
         "tide_linear_grad_input_workspace": (_i64, 3 * [_i64] + 2 * _MAT),
         "tide_linear_grad_input": (_i32, 3 * [_i64] + 2 * _MAT + [_i32] + 4 * _MAT + [_vp, _i64, _vp]),
-        "tide_linear_grad_weight_workspace": (_i64, 3 * [_i64] + 2 * _MAT),
+        "tide_linear_grad_weight_workspace": (_i64, 3 * [_i64] + 2 * _MAT + [_i32]),
         "tide_linear_grad_weight": (_i32, 3 * [_i64] + 4 * _MAT + [_i32] + _MAT + [_vp, _vp, _i64, _vp]),
     }
     for name, (res, args) in sig.items():
@@ -276,5 +276,6 @@ def tide_linear_grad_weight(dy, x, dw, db=None, act=TIDE_ACT_NONE, workspace=Non
     size = (rows, inner, outer)
     a, kept = _mat(dy, "dy", rows, outer, bf, dev), _plain_or_kept(x, "x", rows, inner, bf, dev)
     args = (_act(act), *_mat(dw, "dw", outer, inner, bf, dev), _optv(db, "db", outer, bf, dev))
-    keep, ws, ws_bytes = _workspace(workspace, _lib.tide_linear_grad_weight_workspace(*size, *a, *kept[:2]), stream, dev)
+    need = _lib.tide_linear_grad_weight_workspace(*size, *a, *kept[:2], db is not None)
+    keep, ws, ws_bytes = _workspace(workspace, need, stream, dev)
     _check(_lib.tide_linear_grad_weight(*size, *a, *kept, *args, ws, ws_bytes, _stream(stream)))

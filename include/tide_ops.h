@@ -148,9 +148,10 @@ tide_status tide_linear_grad_input(int64_t rows, int64_t inner, int64_t outer, c
  * dw [outer, inner], db [outer].  X [rows, inner] is x in bf16, or, with x
  * NULL, f(value) of an 8-bit checkpoint rounded to bf16, as the forward pass
  * rounded it (exact for TIDE_ACT_NONE).  With x given, act must be
- * TIDE_ACT_NONE.  No rows: dw and db are zero. */
+ * TIDE_ACT_NONE.  No rows: dw and db are zero.  with_db: whether db is asked
+ * for. */
 int64_t tide_linear_grad_weight_workspace(int64_t rows, int64_t inner, int64_t outer, const void* dy, int64_t lddy,
-                                          const void* x, int64_t ldx);
+                                          const void* x, int64_t ldx, int32_t with_db);
 tide_status tide_linear_grad_weight(int64_t rows, int64_t inner, int64_t outer, const void* dy, int64_t lddy,
                                     const void* x, int64_t ldx, const uint8_t* codes, int64_t ld_codes,
                                     const uint8_t* scales, int64_t ld_scales, int32_t act, void* dw, int64_t lddw,

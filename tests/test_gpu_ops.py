@@ -625,12 +625,41 @@ def test_refusals():
 
 # ---------------------------------------------------------------- the pair-of-CTAs product, and bounded waits
 
-BIG = [(2100, 200, 3100), (4096, 520, 2304), (2049, 1030, 2570), (3333, 72, 4100)]  # rows, inner, outer
+# rows, inner, outer.  On 152 SMs the forward and input-gradient products of the first four take tiles of 256 x 256;
+# then 256 x 128 and 256 x 128 in splits; 256 x 256, 256 x 256 in splits; 128 weight rows by 128 tokens, and in splits;
+# each with output rows that start on 16-byte boundaries and that do not.
+BIG = [(2100, 200, 3100), (4096, 520, 2304), (2049, 1030, 2570), (3333, 72, 4100),
+       (2631, 8, 672), (3562, 3017, 191), (2546, 3468, 64), (2511, 9352, 137),
+       (648, 1334, 3256), (413, 4204, 4927), (136, 8384, 5392), (145, 14426, 4894),
+       (1174, 8, 3607), (523, 272, 3576), (2756, 4663, 13), (68, 4624, 2256)]
+# The same for the weight gradient, whose sum runs over the rows.
+BIG_SUMS = [(10, 152, 4912), (3314, 292, 3534), (2633, 4832, 64), (9352, 137, 2511), (3910, 2725, 841), (1300, 736, 3280),
+            (8384, 5392, 136), (14426, 4894, 145), (8, 3790, 2253), (453, 4896, 384), (3799, 3353, 68), (4978, 3336, 72),
+            (750, 11, 9), (710, 8, 9), (16384, 520, 512)]
+
+
+@pytest.mark.parametrize("rows,inner,outer", BIG_SUMS)
+def test_large_weight_gradients(rows, inner, outer):
+    dy, x = rand((rows, outer), BF, 1).to(DEV), rand((rows, inner), BF, 2).to(DEV)
+    ck = tide.Checkpoint8.empty(rows, inner)
+    tide.tide_checkpoint_store(x, ck)
+    kept = torch.empty(rows, inner, device=DEV)
+    tide.tide_checkpoint_load(ck, kept)
+    yd, db = dy.double(), torch.empty(outer, dtype=BF, device=DEV)
+    for operand, xd in ((x, x.double()), (ck, kept.double())):
+        dw = torch.empty(outer, inner, dtype=BF, device=DEV)
+        tide.tide_linear_grad_weight(dy, operand, dw, db=db)
+        want, size = yd.t() @ xd, yd.abs().t() @ xd.abs()
+        over = (dw.double() - want).abs() - R.BF16 * want.abs() - ((rows / 16 + 16) * R.FP32) * size
+        assert over.max().item() <= 0
+    want, size = yd.sum(0), yd.abs().sum(0)
+    assert ((db.double() - want).abs() - R.BF16 * want.abs() - ((rows / 16 + 96) * R.FP32) * size).max().item() <= 0
+    tide.tide_ops_check()
 
 
 @pytest.mark.parametrize("rows,inner,outer", BIG)
 def test_large_products(rows, inner, outer):
-    """Sizes that take 256 x 256 tiles, whole and ragged, against fp64 on the GPU."""
+    """Every tile the products are built of, whole and ragged, against fp64 on the GPU."""
     x, w = rand((rows, inner), BF, 1).to(DEV), rand((outer, inner), BF, 2, scale=inner ** -0.5).to(DEV)
     b, r = rand((outer,), BF, 3).to(DEV), rand((rows, outer), BF, 4).to(DEV)
     xd, wd = x.double(), w.double()
