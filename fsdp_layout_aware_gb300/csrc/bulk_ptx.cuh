@@ -97,4 +97,20 @@ __device__ __forceinline__ uint64_t global_ns() {
   return t;
 }
 
+// Waits for the phase with the given parity to complete, at most limit_ns;
+// false when that ran out.  The clock is only read once try_wait has come back
+// empty a number of times.
+__device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  if (mbar_try_wait(bar, parity)) return true;
+  uint64_t start = 0;
+  for (uint32_t n = 1;; ++n) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (n % 64 == 0) {
+      const uint64_t now = global_ns();
+      if (start == 0) start = now;
+      if (now - start > limit_ns) return false;
+    }
+  }
+}
+
 }  // namespace tide

@@ -74,9 +74,7 @@ __global__ void __launch_bounds__(kThreads) store_vec_kernel(const StoreArgs a) 
 }
 
 // Any alignment: a warp takes 256 columns of a row, a lane eight of them as
-// above.  Codes are stored as aligned 8-byte words: with the row's codes `p`
-// bytes past a boundary, a lane's word is the last p codes of the lane before
-// and its own first 8 - p.
+// above.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) store_any_kernel(const StoreArgs a) {
   const uint32_t i = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
@@ -85,40 +83,13 @@ __global__ void __launch_bounds__(kThreads) store_any_kernel(const StoreArgs a) 
   const int64_t row = a.per_row.quotient(i);
   const int64_t col = (int64_t)(i - (uint32_t)row * a.per_row.d) * 256 + lane * 8;
   const int n = (int)max((int64_t)0, min((int64_t)8, a.cols - col));  // columns that exist
-  const T* x = (const T*)a.x + row * a.ldx + col;
   float v[8];
-  if (n == 8) {
-    load_any8(x, v);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      float t[1] = {0.0f};
-      if (k < n) load_vec<1>(x + k, t);
-      v[k] = t[0];
-    }
-  }
+  load_any8((const T*)a.x + row * a.ldx + col, n, v);
   const int byte = scale_byte(block_magnitude<4>(v));
   uint32_t w[2];
   encode(v, byte, w);
   if (n > 0 && lane % 4 == 0) a.scales[row * a.lds + col / kMxBlock] = (uint8_t)byte;
-
-  uint8_t* c = a.codes + row * a.ldc + col;
-  const int p = (int)((uintptr_t)c & 7);  // the same for every lane
-  const uint64_t cur = (uint64_t)w[1] << 32 | w[0];
-  const uint64_t before = __shfl_up_sync(0xffffffffu, cur, 1);
-  int n_before = __shfl_up_sync(0xffffffffu, n, 1);
-  if (lane == 0) n_before = 0;
-  const uint64_t word = p ? cur << (8 * p) | before >> (64 - 8 * p) : cur;
-  // Byte j of the word is column j - p; valid from `lo` to below `hi`.
-  const int lo = lane == 0 ? p : 0;
-  const int hi = n > 0 ? min(8, p + n) : n_before - (8 - p);
-  if (lo == 0 && hi == 8) {
-    *reinterpret_cast<uint64_t*>(c - p) = word;
-  } else {
-    for (int j = lo; j < hi; ++j) (c - p)[j] = (uint8_t)(word >> (8 * j));
-  }
-  if (lane == 31)
-    for (int k = 8 - p; k < n; ++k) c[k] = (uint8_t)(cur >> (8 * k));
+  store_codes_any(a.codes + row * a.ldc + col, n, w);
 }
 
 // fp32 outputs take the accurate exponential and division.
@@ -181,12 +152,7 @@ __global__ void __launch_bounds__(kThreads) load_any_kernel(const LoadArgs a) {
     const uint2 c = load_any_bytes(codes + col);
     const float s0 = scale_value(scales[col / kMxBlock]), s1 = scale_value(scales[(col + 7) / kMxBlock]);
     const int first = kMxBlock - (int)(col % kMxBlock);  // columns of the first block
-    if (GRAD) {
-      if ((uintptr_t)(grad + col) % 16 == 0)
-        load_vec<8>(grad + col, g);
-      else
-        load_any8(grad + col, g);
-    }
+    if (GRAD) load_any8(grad + col, 8, g);
     decode8(c, 1.0f, v);
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] *= k < first ? s0 : s1;

@@ -71,6 +71,11 @@ inline bool rows_aligned(const void* p, int64_t ld, int64_t elem, int64_t rows) 
 tide_status launch_sum_groups(const float* partial, int64_t groups, int64_t cols, int32_t dtype, void* out, bool after,
                               cudaStream_t stream);
 
+// The current device's status word (TIDE_DEVICE_TIMEOUT: a wait ran out; read by
+// tide_ops_check) and the bound on every wait.
+tide_status ops_status_word(int32_t** word);
+uint64_t ops_wait_limit_ns();
+
 // SMs of the current device (asked once per device); 0 if the query failed.
 int ops_num_sms();
 
@@ -184,6 +189,20 @@ __device__ __forceinline__ void load_any8(const float* p, float (&v)[8]) {
   for (int j = 0; j < 8; ++j) v[j] = p[j];
 }
 
+// The first n of eight elements at any alignment, zeros for the rest.
+template <typename T>
+__device__ __forceinline__ void load_any8(const T* p, int n, float (&v)[8]) {
+  if (n == 8) {
+    if ((uintptr_t)p % 16 == 0)
+      load_vec<8>(p, v);
+    else
+      load_any8(p, v);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = k < n ? (float)p[k] : 0.0f;
+  }
+}
+
 // Eight bytes at any alignment.
 __device__ __forceinline__ uint2 load_any_bytes(const uint8_t* p) {
   const uint32_t phase = (uint32_t)(uintptr_t)p & 3u;
@@ -279,6 +298,30 @@ __device__ __forceinline__ uint8_t encode_one(float v, int byte) {
 __device__ __forceinline__ float2 e4m3_values(uint32_t pair) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)pair, __NV_E4M3);
   return __half22float2(__half2(h));
+}
+
+// A whole warp stores 256 neighbouring codes at any alignment, lane l the first
+// n of eight (w) at c; only the last lanes have fewer than eight.  With the
+// row's codes `p` bytes past an 8-byte boundary, a lane's aligned word is the
+// last p codes of the lane before and its own first 8 - p.
+__device__ __forceinline__ void store_codes_any(uint8_t* c, int n, const uint32_t (&w)[2]) {
+  const int lane = threadIdx.x % 32;
+  const int p = (int)((uintptr_t)c & 7);  // the same for every lane
+  const uint64_t cur = (uint64_t)w[1] << 32 | w[0];
+  const uint64_t before = __shfl_up_sync(0xffffffffu, cur, 1);
+  int n_before = __shfl_up_sync(0xffffffffu, n, 1);
+  if (lane == 0) n_before = 0;
+  const uint64_t word = p ? cur << (8 * p) | before >> (64 - 8 * p) : cur;
+  // Byte j of the word is column j - p; valid from `lo` to below `hi`.
+  const int lo = lane == 0 ? p : 0;
+  const int hi = n > 0 ? min(8, p + n) : n_before - (8 - p);
+  if (lo == 0 && hi == 8) {
+    *reinterpret_cast<uint64_t*>(c - p) = word;
+  } else {
+    for (int j = lo; j < hi; ++j) (c - p)[j] = (uint8_t)(word >> (8 * j));
+  }
+  if (lane == 31)
+    for (int k = 8 - p; k < n; ++k) c[k] = (uint8_t)(cur >> (8 * k));
 }
 
 // Eight values from two words of codes.

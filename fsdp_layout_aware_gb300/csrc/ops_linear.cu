@@ -22,18 +22,6 @@ __device__ int32_t g_status;
 std::atomic<int64_t> g_wait_limit_ns{2000000000};
 std::atomic<int64_t> g_test_drop{-1};
 
-tide_status ops_status_word(int32_t** word) {
-  static std::atomic<int32_t*> known[64];
-  int dev = -1;
-  TIDE_TRY(cuda_status(cudaGetDevice(&dev), "cudaGetDevice"));
-  if (dev < 64 && (*word = known[dev].load(std::memory_order_relaxed))) return TIDE_OK;
-  void* p = nullptr;
-  TIDE_TRY(cuda_status(cudaGetSymbolAddress(&p, g_status), "cudaGetSymbolAddress"));
-  *word = (int32_t*)p;
-  if (dev < 64) known[dev].store(*word, std::memory_order_relaxed);
-  return TIDE_OK;
-}
-
 // One operand: `rows` rows of `cols` contiguous elements.
 struct Operand {
   const bf16* p;
@@ -268,7 +256,7 @@ tide_status product(int64_t m, int64_t n, int64_t k, Operand a, bool a_mn, Opera
     p.tiles_a = s.tiles_a, p.tiles_b = s.tiles_b;
     p.k_blocks = s.k_blocks, p.split_blocks = s.split_blocks, p.splits = s.splits;
     TIDE_TRY(ops_status_word(&p.status));
-    p.wait_limit_ns = (uint64_t)g_wait_limit_ns.load(std::memory_order_relaxed);
+    p.wait_limit_ns = ops_wait_limit_ns();
     p.test_drop = g_test_drop.load(std::memory_order_relaxed);
     const int64_t units = (int64_t)s.tiles_a * s.tiles_b * s.splits;
     const int grid = (int)std::min<int64_t>(units * ts.ctas, sms / ts.ctas * ts.ctas);
@@ -371,6 +359,21 @@ tide_status check_workspace(const void* workspace, int64_t bytes, int64_t need) 
 }
 
 }  // namespace
+
+tide_status ops_status_word(int32_t** word) {
+  static std::atomic<int32_t*> known[64];
+  int dev = -1;
+  TIDE_TRY(cuda_status(cudaGetDevice(&dev), "cudaGetDevice"));
+  if (dev < 64 && (*word = known[dev].load(std::memory_order_relaxed))) return TIDE_OK;
+  void* p = nullptr;
+  TIDE_TRY(cuda_status(cudaGetSymbolAddress(&p, g_status), "cudaGetSymbolAddress"));
+  *word = (int32_t*)p;
+  if (dev < 64) known[dev].store(*word, std::memory_order_relaxed);
+  return TIDE_OK;
+}
+
+uint64_t ops_wait_limit_ns() { return (uint64_t)g_wait_limit_ns.load(std::memory_order_relaxed); }
+
 }  // namespace tide
 
 using namespace tide;

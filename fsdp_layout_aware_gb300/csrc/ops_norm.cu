@@ -8,6 +8,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "bulk_ptx.cuh"
 #include "ops_common.cuh"
 
 namespace tide {
@@ -50,334 +51,514 @@ struct NormGradArgs {
   int64_t ldres;
   void* dx;
   int64_t lddx;
-  float* partial;  // [row groups][cols]: each one's sum of dy * n; NULL: not wanted
+  float* partial;  // [blocks][cols]: each one's sum of dy * n; NULL: not wanted
 };
 
-// Sum of v over the threads of a row (blockDim.x, a multiple of 32; threadIdx.y
-// is the row).  One barrier: `turn` alternates the scratch floats, one per
-// warp, so a sum is read before its place is written again.  The order is
-// fixed.
-__device__ __forceinline__ float row_sum(float v, float (&scratch)[2][32], int& turn) {
+// The threads that share a row: per_row of them (a multiple of 32), this one the
+// x-th, of the y-th row of the block; `all` threads work on rows.  Barriers are
+// named, so that a warp beside them can do something else.
+struct RowThread {
+  int per_row, x, y, all;
+  __device__ __forceinline__ void sync() const {
+    if (per_row > 32)
+      asm volatile("bar.sync 1, %0;" ::"r"(all) : "memory");
+    else
+      __syncwarp();
+  }
+};
+// In a block of (per_row, rows) threads.
+__device__ __forceinline__ RowThread row_thread() {
+  return {(int)blockDim.x, (int)threadIdx.x, (int)threadIdx.y, (int)(blockDim.x * blockDim.y)};
+}
+
+// Sum of v over the threads of a row.  One barrier: `turn` alternates the
+// scratch floats, one per warp, so a sum is read before its place is written
+// again.  The order is fixed.
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  const int warps = blockDim.x / 32;
+  return v;
+}
+__device__ __forceinline__ float row_sum(float v, const RowThread& t, float (&scratch)[2][32], int& turn) {
+  v = warp_sum(v);
+  const int warps = t.per_row / 32;
   if (warps > 1) {
-    const int first = threadIdx.y * warps;
+    const int first = t.y * warps, lane = threadIdx.x % 32;
     float* s = scratch[turn];
     turn ^= 1;
-    if (threadIdx.x % 32 == 0) s[first + threadIdx.x / 32] = v;
-    __syncthreads();
-    v = 0.0f;
-    for (int w = 0; w < warps; ++w) v += s[first + w];
+    if (lane == 0) s[first + t.x / 32] = v;
+    t.sync();
+    v = warp_sum(lane < warps ? s[first + lane] : 0.0f);
   }
   return v;
 }
 
-// A row takes blockDim.x threads, each NV vectors of V columns; a block holds
-// blockDim.y rows.
-template <typename T, int V, int NV, int THREADS>
+// Eight codes of a kept row at any alignment, the first n; the rest as zeros.
+__device__ __forceinline__ uint2 load_codes_any(const uint8_t* c, int n) {
+  if (n == 8) return (uintptr_t)c % 8 == 0 ? *reinterpret_cast<const uint2*>(c) : load_any_bytes(c);
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (k < n) w[k / 4] |= (uint32_t)c[k] << (8 * (k % 4));
+  return make_uint2(w[0], w[1]);
+}
+
+// Rows of any alignment leave through shared memory: threads put their vectors
+// down whole, and the row is stored with neighbouring threads on neighbouring
+// elements, so in whole sectors.  (Staged at its phase and stored in words of 16
+// bytes it was slower: the vectors then go down piece by piece.  So were pairs
+// of bf16.)
+template <typename T>
+__device__ __forceinline__ void store_staged(T* out, const T* staged, int cols, const RowThread& t) {
+  for (int c = t.x; c < cols; c += t.per_row) out[c] = staged[c];
+}
+// Shared memory of a staged row: whole vectors.
+__host__ __device__ inline int stage_room(int64_t cols, int elem) { return (int)((cols + 7) / 8 * 8 * elem); }
+
+// A row takes blockDim.x threads, each NV vectors of eight columns; a block
+// holds blockDim.y rows.  ANY: rows of any alignment; h and y then leave through shared
+// memory.
+template <typename T, int NV, bool ANY, int THREADS>
 __global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a) {
+  extern __shared__ __align__(16) unsigned char stage[];
   __shared__ float scratch[2][32];
   int turn = 0;
-  const int lane = threadIdx.x;
-  const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const RowThread t = row_thread();
+  const int64_t row = (int64_t)blockIdx.x * blockDim.y + t.y;
   const bool here = row < a.rows;
-  float s[NV][V];
+  const int cols = (int)a.cols;
+  T* const h_out = (T*)a.h + row * a.ldh;
+  T* const y_out = (T*)a.y + row * a.ldy;
+  const int room = stage_room(cols, sizeof(T));
+  T* const h_stage = reinterpret_cast<T*>(stage + t.y * 2 * room);
+  T* const y_stage = reinterpret_cast<T*>(stage + t.y * 2 * room + room);
+  float s[NV][8];
   float sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int col = (i * blockDim.x + lane) * V;
+    const int col = ((int)i * (int) blockDim.x + t.x) * 8;
 #pragma unroll
-    for (int k = 0; k < V; ++k) s[i][k] = 0.0f;
-    if (here && col < a.cols) {
-      load_vec<V>((const T*)a.x + row * a.ldx + col, s[i]);
+    for (int k = 0; k < 8; ++k) s[i][k] = 0.0f;
+    if (here && col < cols) {
+      const int n = min(8, cols - col);
+      const T* x = (const T*)a.x + row * a.ldx + col;
+      if constexpr (ANY)
+        load_any8(x, n, s[i]);
+      else
+        load_vec<8>(x, s[i]);
       if (a.residual) {
-        float r[V];
-        load_vec<V>((const T*)a.residual + row * a.ldr + col, r);
+        const T* q = (const T*)a.residual + row * a.ldr + col;
+        float r[8];
+        if constexpr (ANY)
+          load_any8(q, n, r);
+        else
+          load_vec<8>(q, r);
 #pragma unroll
-        for (int k = 0; k < V; ++k) s[i][k] += r[k];
+        for (int k = 0; k < 8; ++k) s[i][k] += r[k];
       }
     }
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int k = 0; k < V; ++k) sum = fmaf(s[i][k], s[i][k], sum);
-  sum = row_sum(sum, scratch, turn);
-  const float rstd = 1.0f / sqrtf(sum / (float)a.cols + a.eps);
-  if (here && lane == 0 && a.rstd) a.rstd[row] = rstd;
+    for (int k = 0; k < 8; ++k) sum = fmaf(s[i][k], s[i][k], sum);
+  sum = row_sum(sum, t, scratch, turn);
+  const float rstd = 1.0f / sqrtf(sum / (float)cols + a.eps);
+  if (here && t.x == 0 && a.rstd) a.rstd[row] = rstd;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int col = (i * blockDim.x + lane) * V;
-    const bool in = here && col < a.cols;
-    float y[V];
+    const int col = ((int)i * (int) blockDim.x + t.x) * 8;
+    const int n = here ? max(0, min(8, cols - col)) : 0;
+    float y[8];
 #pragma unroll
-    for (int k = 0; k < V; ++k) y[k] = 0.0f;
-    if (in) {
-      if (a.h) store_vec<V>((T*)a.h + row * a.ldh + col, s[i]);
-      load_vec<V>((const T*)a.weight + col, y);
+    for (int k = 0; k < 8; ++k) y[k] = 0.0f;
+    if (n > 0) {
+      const T* w = (const T*)a.weight + col;
+      if constexpr (ANY)
+        load_any8(w, n, y);
+      else
+        load_vec<8>(w, y);
 #pragma unroll
-      for (int k = 0; k < V; ++k) y[k] *= s[i][k] * rstd;
-      if (a.y) store_vec<V>((T*)a.y + row * a.ldy + col, y);
-    }
-    if (a.codes) {
-      // 32 / V neighbouring lanes hold a block of 32 columns.
-      const int byte = scale_byte(block_magnitude<kMxBlock / V>(y));
-      if (in) {
-        uint8_t* c = a.codes + row * a.ldc + col;
-        if constexpr (V == 8) {
-          uint32_t w[2];
-          encode(y, byte, w);
-          *reinterpret_cast<uint2*>(c) = make_uint2(w[0], w[1]);
-        } else {
-          *c = encode_one(y[0], byte);
-        }
-        if (col % kMxBlock == 0) a.scales[row * a.lds + col / kMxBlock] = (uint8_t)byte;
+      for (int k = 0; k < 8; ++k) y[k] *= s[i][k] * rstd;
+      if constexpr (ANY) {
+        store_vec<8>(h_stage + col, s[i]);
+        store_vec<8>(y_stage + col, y);
+      } else {
+        if (a.h) store_vec<8>(h_out + col, s[i]);
+        if (a.y) store_vec<8>(y_out + col, y);
       }
     }
+    if (a.codes) {
+      const int byte = scale_byte(block_magnitude<4>(y));
+      uint32_t w[2];
+      encode(y, byte, w);
+      uint8_t* c = a.codes + row * a.ldc + col;
+      if constexpr (ANY)
+        store_codes_any(c, n, w);
+      else if (n > 0)
+        *reinterpret_cast<uint2*>(c) = make_uint2(w[0], w[1]);
+      if (n > 0 && col % kMxBlock == 0) a.scales[row * a.lds + col / kMxBlock] = (uint8_t)byte;
+    }
+  }
+  if constexpr (ANY) {
+    t.sync();
+    if (!here) return;
+    if (a.h) store_staged(h_out, h_stage, cols, t);
+    if (a.y) store_staged(y_out, y_stage, cols, t);
   }
 }
 
 // ---- backward
+//
+// Row groups (per_row threads) walk the rows with a fixed stride, so a thread
+// keeps its columns' weights and their share of dweight in registers.  Within a
+// row each thread has NV vectors of eight columns.
 
-// dx of one row's columns and their share of dweight, once n = h (still without
-// rstd) and g = dy are in registers.
-template <typename T, int V, int NV>
-__device__ __forceinline__ void grad_row(const NormGradArgs& a, int64_t row, bool here, float rstd, float (&n)[NV][V],
-                                         float (&g)[NV][V], const float (&w)[NV][V], float (&acc)[NV][V],
-                                         float (&scratch)[2][32], int& turn, const float (&dres)[NV][V]) {
-  float sum = 0.0f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      n[i][k] *= rstd;
-      acc[i][k] = fmaf(g[i][k], n[i][k], acc[i][k]);
-      g[i][k] *= w[i][k];
-      sum = fmaf(g[i][k], n[i][k], sum);
-    }
-  if (!a.dx) return;
-  const float mean = row_sum(sum, scratch, turn) / (float)a.cols;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int col = (i * blockDim.x + threadIdx.x) * V;
-    if (here && col < a.cols) {
-      float d[V];
-#pragma unroll
-      for (int k = 0; k < V; ++k) d[k] = fmaf(rstd, fmaf(-n[i][k], mean, g[i][k]), dres[i][k]);
-      store_vec<V>((T*)a.dx + row * a.lddx + col, d);
-    }
-  }
-}
-
-template <int V, int NV>
-__device__ __forceinline__ void store_partial(const NormGradArgs& a, const float (&acc)[NV][V]) {
-  if (!a.partial) return;
-  float* p = a.partial + ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * a.cols;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int col = (i * blockDim.x + threadIdx.x) * V;
-    if (col < a.cols) store_vec<V>(p + col, acc[i]);
-  }
-}
-
-// Row groups (blockDim.x threads) walk the rows with a fixed stride, so a
-// thread keeps its columns' weights and their share of dweight in registers.
-// Any alignment (V = 1), and rows too long for the ring below.
-template <typename T, int V, int NV, int THREADS>
-__global__ void __launch_bounds__(THREADS) norm_grad_kernel(const NormGradArgs a) {
-  __shared__ float scratch[2][32];
-  int turn = 0;
-  float acc[NV][V] = {}, w[NV][V] = {};
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int col = (i * blockDim.x + threadIdx.x) * V;
-    if (col < a.cols) load_vec<V>((const T*)a.weight + col, w[i]);
-  }
-  // Every group of a block makes the same number of turns (row_sum's barrier).
-  for (int64_t first = (int64_t)blockIdx.x * blockDim.y; first < a.rows; first += (int64_t)gridDim.x * blockDim.y) {
-    const int64_t row = first + threadIdx.y;
-    const bool here = row < a.rows;
-    const float rstd = here ? a.rstd[row] : 0.0f;
-    float n[NV][V] = {}, g[NV][V] = {}, dres[NV][V] = {};
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int col = (i * blockDim.x + threadIdx.x) * V;
-      if (here && col < a.cols) {
-        if (a.h) {
-          load_vec<V>((const T*)a.h + row * a.ldh + col, n[i]);
-        } else {
-          const float scale = scale_value(a.scales[row * a.lds + col / kMxBlock]);
-          const uint8_t* c = a.codes + row * a.ldc + col;
-          if constexpr (V == 8)
-            decode8(*reinterpret_cast<const uint2*>(c), scale, n[i]);
-          else
-            n[i][0] = e4m3_values(*c).x * scale;
-        }
-        load_vec<V>((const T*)a.dy + row * a.lddy + col, g[i]);
-        if (a.dres) load_vec<V>((const T*)a.dres + row * a.ldres + col, dres[i]);
-      }
-    }
-    grad_row<T, V, NV>(a, row, here, rstd, n, g, w, acc, scratch, turn, dres);
-  }
-  store_partial<V, NV>(a, acc);
-}
-
-__device__ __forceinline__ void copy_async16(uint32_t smem, const void* gmem) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
-}
-__device__ __forceinline__ void copy_async8(uint32_t smem, const void* gmem) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem), "l"(gmem) : "memory");
-}
-
-// Shared memory a ring slot (one row of the block) takes: for every thread and
-// vector, its h (or codes), dy and dres.
-inline int ring_slot_bytes(int threads, int nv, int elem, bool kept, bool dres) {
-  return threads * nv * ((kept ? 8 : 8 * elem) + 8 * elem * (dres ? 2 : 1));
-}
-
-// As above with aligned rows, eight columns a vector, DEPTH rows of a group in
-// flight: each thread copies its own columns of the rows to come into a ring in
-// shared memory and reads nothing else from it, so the copies need no barrier
-// and cost no registers.  What is in flight then is DEPTH - 1 rows a block,
-// whatever the one barrier of a row costs.
-template <typename T, int NV, int DEPTH, bool KEPT, int THREADS, int BLOCKS>
-__global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_ring_kernel(const NormGradArgs a) {
-  extern __shared__ __align__(16) unsigned char ring[];
-  __shared__ float scratch[2][32];
-  constexpr int kWords = sizeof(T) / 2;  // 16-byte words of a vector
-  constexpr int kPer = 16 / sizeof(T);   // elements of a word
-  const int threads = blockDim.x * blockDim.y, tid = threadIdx.y * blockDim.x + threadIdx.x;
-  const bool has_dres = a.dres != nullptr;
-  // Within a slot: dy, dres, h; within each, word by word over the threads, so
-  // neighbouring threads use neighbouring banks.
-  const uint32_t vec_bytes = (uint32_t)threads * 16;
-  const uint32_t off_dres = NV * kWords * vec_bytes, off_h = off_dres * (has_dres ? 2 : 1);
-  const uint32_t slot = off_h + NV * (KEPT ? vec_bytes / 2 : kWords * vec_bytes);
-  const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring);
-  const int apart = blockDim.x * 8;  // columns from one of a thread's vectors to the next
-  const int col0 = threadIdx.x * 8;
-
-  int turn = 0;
-  float acc[NV][8] = {};
-  T w[NV][8];
-  bool in[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    in[i] = col0 + i * apart < a.cols;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) w[i][k] = in[i] ? ((const T*)a.weight)[col0 + i * apart + k] : T(0.0f);
-  }
-  const int64_t step = (int64_t)gridDim.x * blockDim.y;
-  int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-
-  // The next row to fetch, and where its vectors are.
-  int64_t ahead = row;
-  const T* dy = (const T*)a.dy + row * a.lddy + col0;
-  const T* dres = has_dres ? (const T*)a.dres + row * a.ldres + col0 : nullptr;
-  const T* h = KEPT ? nullptr : (const T*)a.h + row * a.ldh + col0;
-  const uint8_t* codes = KEPT ? a.codes + row * a.ldc + col0 : nullptr;
-  T* dx = (T*)a.dx + row * a.lddx + col0;
-  auto fetch = [&](uint32_t at) {
-    if (ahead < a.rows) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        if (!in[i]) continue;
-#pragma unroll
-        for (int q = 0; q < kWords; ++q) {
-          const uint32_t o = at + (i * kWords + q) * vec_bytes + tid * 16;
-          copy_async16(o, dy + i * apart + q * kPer);
-          if (has_dres) copy_async16(o + off_dres, dres + i * apart + q * kPer);
-          if constexpr (!KEPT) copy_async16(o + off_h, h + i * apart + q * kPer);
-        }
-        if constexpr (KEPT) copy_async8(at + off_h + (i * threads + tid) * 8, codes + i * apart);
-      }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    ahead += step;
-    dy += step * a.lddy;
-    if (has_dres) dres += step * a.ldres;
-    if constexpr (KEPT)
-      codes += step * a.ldc;
+// Eight elements of T as they lie in memory.
+template <typename T>
+struct Kept8 {
+  uint32_t w[2 * sizeof(T)];
+  __device__ __forceinline__ float value(int k) const {
+    if constexpr (sizeof(T) == 2)
+      return __uint_as_float(k % 2 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
     else
-      h += step * a.ldh;
-  };
-  auto word = [&](const unsigned char* s, float* v) {  // a 16-byte word of T
-    if constexpr (kWords == 1) {
-      load_vec<8>(reinterpret_cast<const T*>(s), *reinterpret_cast<float(*)[8]>(v));
-    } else {
-      const float4 x = *reinterpret_cast<const float4*>(s);
-      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-    }
-  };
-  // rstd and the scales of a row, one row ahead.
-  float rstd = 0.0f;
-  uint8_t scale[NV] = {};
-  auto fetch_small = [&](int64_t r) {
-    if (r >= a.rows) return;
-    rstd = a.rstd[r];
-    if constexpr (KEPT) {
+      return __uint_as_float(w[k]);
+  }
+  // The first n at p, one by one; zeros for the rest.
+  __device__ __forceinline__ void load(const T* p, int n) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (in[i]) scale[i] = a.scales[r * a.lds + (col0 + i * apart) / kMxBlock];
+    for (int k = 0; k < 2 * (int)sizeof(T); ++k) w[k] = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (k >= n) continue;
+      if constexpr (sizeof(T) == 2)
+        w[k / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[k] << (16 * (k % 2));
+      else
+        w[k] = reinterpret_cast<const uint32_t*>(p)[k];
     }
-  };
+  }
+};
 
+// The block's share of dweight to its row of `partial`; with several rows a block
+// they are joined in `joined`, [rows][cols], first.
+template <int NV>
+__device__ __forceinline__ void store_partial(const NormGradArgs& a, const RowThread& t, int rows,
+                                              const float (&acc)[NV][8], float* joined) {
+  if (!a.partial) return;
+  const int cols = (int)a.cols;
+  float* out = a.partial + (int64_t)blockIdx.x * cols;
+  if (rows > 1) asm volatile("bar.sync 1, %0;" ::"r"(t.all) : "memory");  // what was there has been read
+  float* p = rows > 1 ? joined + t.y * cols : out;
 #pragma unroll
-  for (int d = 0; d < DEPTH - 1; ++d) fetch(base + d * slot);
-  fetch_small(row);
-  int at = 0;
-  // Every group of a block makes the same number of turns (row_sum's barrier).
-  for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < a.rows; r0 += step, row += step, dx += step * a.lddx) {
-    const bool here = row < a.rows;
-    int next = at + DEPTH - 1;
-    if (next >= DEPTH) next -= DEPTH;
-    fetch(base + next * slot);
-    const float r = here ? rstd : 0.0f;
-    float to_n[NV];  // what turns a kept value into n
+  for (int i = 0; i < NV; ++i) {
+    const int col = (i * t.per_row + t.x) * 8;
+    if (cols % 4 == 0 && col + 8 <= cols) {
+      store_vec<8>(p + col, acc[i]);
+    } else {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) to_n[i] = KEPT ? scale_value(scale[i]) * r : r;
-    fetch_small(row + step);
-    asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
-    const unsigned char* s = ring + at * slot + tid * 16;
+      for (int k = 0; k < 8; ++k)
+        if (col + k < cols) p[col + k] = acc[i][k];
+    }
+  }
+  if (rows == 1) return;
+  asm volatile("bar.sync 1, %0;" ::"r"(t.all) : "memory");
+  for (int c = t.y * t.per_row + t.x; c < cols; c += t.all) {
+    float v = 0.0f;
+    for (int y = 0; y < rows; ++y) v += joined[y * cols + c];
+    out[c] = v;
+  }
+}
+
+// Before the row's mean is known: n (from h times to_n), dweight's share,
+// g = dy * weight and this thread's part of the sum of g * n.
+template <typename T>
+__device__ __forceinline__ float grad_vector(float (&n)[8], float (&g)[8], float to_n, const Kept8<T>& w,
+                                             float (&acc)[8], float sum) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    n[k] *= to_n;
+    acc[k] = fmaf(g[k], n[k], acc[k]);
+    g[k] *= w.value(k);
+    sum = fmaf(g[k], n[k], sum);
+  }
+  return sum;
+}
+
+// Rows too long for the ring below, of any alignment, a block each (of several
+// warps); dx leaves through shared memory.
+template <typename T, int NV, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_any_kernel(const NormGradArgs a) {
+  extern __shared__ __align__(16) unsigned char stage[];
+  __shared__ float scratch[2][32];
+  int turn = 0;
+  const RowThread t = row_thread();
+  const int cols = (int)a.cols;
+  const float inv_cols = 1.0f / (float)cols;
+  float acc[NV][8] = {};
+  Kept8<T> w[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int col = (i * t.per_row + t.x) * 8;
+    w[i].load((const T*)a.weight + col, min(8, cols - col));
+  }
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const float rstd = a.rstd[row];
     float n[NV][8] = {}, g[NV][8] = {};
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (!here || !in[i]) continue;
-#pragma unroll
-      for (int q = 0; q < kWords; ++q) {
-        word(s + (i * kWords + q) * vec_bytes, g[i] + q * kPer);
-        if constexpr (!KEPT) word(s + off_h + (i * kWords + q) * vec_bytes, n[i] + q * kPer);
-      }
-      if constexpr (KEPT) decode8(*reinterpret_cast<const uint2*>(ring + at * slot + off_h + (i * threads + tid) * 8), to_n[i], n[i]);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if constexpr (!KEPT) n[i][k] *= to_n[i];
-        acc[i][k] = fmaf(g[i][k], n[i][k], acc[i][k]);
-        g[i][k] *= (float)w[i][k];
-        sum = fmaf(g[i][k], n[i][k], sum);
+      const int col = (i * t.per_row + t.x) * 8;
+      if (col < cols) {
+        const int m = min(8, cols - col);
+        float to_n = rstd;
+        if (a.h) {
+          load_any8((const T*)a.h + row * a.ldh + col, m, n[i]);
+        } else {
+          decode8(load_codes_any(a.codes + row * a.ldc + col, m), 1.0f, n[i]);
+          to_n *= scale_value(a.scales[row * a.lds + col / kMxBlock]);
+        }
+        load_any8((const T*)a.dy + row * a.lddy + col, m, g[i]);
+        sum = grad_vector(n[i], g[i], to_n, w[i], acc[i], sum);
       }
     }
+    if (!a.dx) continue;
+    const float mean = row_sum(sum, t, scratch, turn) * inv_cols;
+    T* const out = (T*)a.dx + row * a.lddx;
+    T* const staged = reinterpret_cast<T*>(stage);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int col = (i * t.per_row + t.x) * 8;
+      if (col < cols) {
+        const int m = min(8, cols - col);
+        float d[8] = {};
+        if (a.dres) load_any8((const T*)a.dres + row * a.ldres + col, m, d);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) d[k] = fmaf(rstd, fmaf(-n[i][k], mean, g[i][k]), d[k]);
+        store_vec<8>(staged + col, d);
+      }
+    }
+    t.sync();
+    store_staged(out, staged, cols, t);
+  }
+  store_partial(a, t, 1, acc, nullptr);
+}
+
+// ---- the backward pass through a ring of rows
+//
+// DEPTH rows of every group lie in shared memory, copied there whole (dy, dres,
+// h or its codes and scales, rstd) by bulk copies, so that a row costs the
+// threads that compute its one barrier and no memory latency, and no address
+// arithmetic.  A warp of its own issues them, lane y for the block's y-th row,
+// once every warp has said that it is done with the slot.
+
+// The part of a row of `bytes` at `from` that whole granules of 16 bytes cover:
+// `skip` bytes after from's granule, the returned number of bytes.  Granules
+// reach up to 15 bytes past the row on either side; one that would begin before
+// the matrix's first byte or end after its last is left out.
+__device__ __forceinline__ uint32_t row_span(const unsigned char* from, int64_t bytes, const unsigned char* first,
+                                             const unsigned char* last, uint32_t& skip) {
+  const uintptr_t f = (uintptr_t)from, lo = f & ~(uintptr_t)15, hi = (f + bytes + 15) & ~(uintptr_t)15;
+  const uintptr_t l = lo < (uintptr_t)first ? lo + 16 : lo, h = hi > (uintptr_t)last ? hi - 16 : hi;
+  skip = (uint32_t)(l - lo);
+  return h > l ? (uint32_t)(h - l) : 0u;
+}
+
+// Copies a row of a matrix (`at`, of cols * elem bytes) to `to` plus its phase
+// within 16 bytes; returns the bytes that will count on `bar`.  What no granule
+// covers goes byte by byte.
+__device__ __forceinline__ uint32_t copy_row(unsigned char* to, const unsigned char* at, const void* base, int64_t rows,
+                                             int64_t cols, int64_t ld, int elem, uint64_t* bar) {
+  const unsigned char* first = (const unsigned char*)base;
+  const unsigned char* end = at + cols * elem;
+  uint32_t skip;
+  const uint32_t n = row_span(at, cols * elem, first, first + ((rows - 1) * ld + cols) * elem, skip);
+  const unsigned char* lo = (const unsigned char*)((uintptr_t)at & ~(uintptr_t)15);
+  if (n) bulk_load(to + skip, lo + skip, n, bar);
+  for (const unsigned char* q = at; q < lo + skip && q < end; ++q) to[q - lo] = *q;
+  for (const unsigned char* q = at < lo + skip + n ? lo + skip + n : at; q < end; ++q) to[q - lo] = *q;
+  return n;
+}
+
+struct RingArgs {
+  NormGradArgs g;
+  int32_t per_row, rows;
+  int32_t* status;
+  uint64_t wait_limit_ns;
+};
+
+// A row in the ring, with room for its phase within 16 bytes.
+__host__ __device__ inline int ring_room(int64_t cols, int elem) { return (int)((cols * elem + 15) / 16 * 16) + 16; }
+
+// A row's part of a slot: where each of the others lies in it, with its phase
+// (five words), then dy, dres, h or codes, scales and rstd.
+enum RingPart { AT_DY, AT_DRES, AT_H, AT_SCALES, AT_RSTD };
+struct RingRow {
+  int dy, dres, h, scales, rstd, bytes;
+  __host__ __device__ RingRow(int64_t cols, int elem, bool kept, bool has_dres) {
+    const int full = ring_room(cols, elem);
+    dy = 32;
+    dres = dy + full;
+    h = dres + (has_dres ? full : 0);
+    scales = h + (kept ? ring_room(cols, 1) : full);
+    rstd = scales + (kept ? ring_room((cols + kMxBlock - 1) / kMxBlock, 1) : 0);
+    bytes = rstd + 32;
+  }
+};
+
+template <typename T, int NV, int DEPTH, bool KEPT, bool ANY, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_ring_kernel(const RingArgs p) {
+  extern __shared__ __align__(16) unsigned char ring[];
+  __shared__ float scratch[2][32];
+  __shared__ uint64_t full[DEPTH], empty[DEPTH];
+  const NormGradArgs& a = p.g;
+  constexpr int kElem = sizeof(T);
+  const bool has_dres = a.dres != nullptr;
+  const int cols = (int)a.cols, rows = p.rows, workers = p.per_row * rows;
+  const RingRow part(cols, kElem, KEPT, has_dres);
+  const int slot_bytes = rows * part.bytes;
+  const int64_t step = (int64_t)gridDim.x * rows, first_row = (int64_t)blockIdx.x * rows;
+
+  if (threadIdx.x == 0) {
+    for (int d = 0; d < DEPTH; ++d) {
+      mbar_init(full + d, rows);
+      mbar_init(empty + d, workers / 32);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+
+  // Copies the block's y-th row of a turn (`row`) into a slot.
+  auto issue = [&](int y, int64_t row, int slot) {
+    uint32_t bytes = 0;
+    if (row < a.rows) {
+      unsigned char* to = ring + slot * slot_bytes + y * part.bytes;
+      uint64_t* bar = full + slot;
+      fence_proxy_async_smem();
+      auto one = [&](RingPart which, const void* base, int64_t n, int64_t ld, int elem, int where) {
+        const unsigned char* at = (const unsigned char*)base + row * ld * elem;
+        reinterpret_cast<int*>(to)[which] = where + (int)((uintptr_t)at & 15);
+        bytes += copy_row(to + where, at, base, a.rows, n, ld, elem, bar);
+      };
+      one(AT_DY, a.dy, cols, a.lddy, kElem, part.dy);
+      if (has_dres) one(AT_DRES, a.dres, cols, a.ldres, kElem, part.dres);
+      if constexpr (KEPT) {
+        one(AT_H, a.codes, cols, a.ldc, 1, part.h);
+        one(AT_SCALES, a.scales, (cols + kMxBlock - 1) / kMxBlock, a.lds, 1, part.scales);
+      } else {
+        one(AT_H, a.h, cols, a.ldh, kElem, part.h);
+      }
+      one(AT_RSTD, a.rstd, 1, 1, 4, part.rstd);
+    }
+    // After the bytes moved one by one; the counted ones may land before they
+    // are expected.
+    mbar_arrive_expect_tx(full + slot, bytes);
+  };
+
+  const int turns = (int)((a.rows - first_row + step - 1) / step);
+  if ((int)threadIdx.x >= workers) {
+    const int y = (int)threadIdx.x - workers;
+    if (y >= rows) return;
+    bool ok = true;
+    int slot = 0, k = 0;
+    for (; k < turns; ++k) {
+      if (k >= DEPTH && !(ok = mbar_wait_bounded(empty + slot, (uint32_t)(k / DEPTH - 1) & 1, p.wait_limit_ns))) break;
+      issue(y, first_row + y + k * step, slot);
+      if (++slot == DEPTH) slot = 0;
+    }
+    if (!ok) {  // the copies in flight land before the block leaves
+      atomicOr(p.status, TIDE_DEVICE_TIMEOUT);
+      for (int d = 0; d < DEPTH && d < k; ++d)
+        mbar_wait_bounded(full + d, (uint32_t)((k - d + DEPTH - 1) / DEPTH - 1) & 1, p.wait_limit_ns);
+    }
+    return;
+  }
+
+  const int t_y = (int)threadIdx.x / p.per_row;
+  const RowThread t{p.per_row, (int)threadIdx.x - t_y * p.per_row, t_y, workers};
+  const int col0 = t.x * 8, apart = p.per_row * 8;
+  const float inv_cols = 1.0f / (float)cols;
+  float acc[NV][8] = {};
+  Kept8<T> w[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) w[i].load((const T*)a.weight + col0 + i * apart, min(8, cols - (col0 + i * apart)));
+  // Every group of a block makes the same number of turns (the row's barriers);
+  // this one has rows in the first `mine`.
+  const int mine = (int)((a.rows - (first_row + t.y) + step - 1) / step);
+  T* dx = (T*)a.dx + (first_row + t.y) * a.lddx;
+  T* const staged = reinterpret_cast<T*>(ring + DEPTH * slot_bytes + t.y * stage_room(cols, kElem));  // ANY: dx
+  int turn = 0, slot = 0;
+  uint32_t phase = 0;
+  bool late = false;
+  for (int k = 0; k < turns; ++k) {
+    const bool here = k < mine;
+    const unsigned char* from = ring + slot * slot_bytes + t.y * part.bytes;
+    const int* at = reinterpret_cast<const int*>(from);
+    if (!late && !mbar_wait_bounded(full + slot, phase, p.wait_limit_ns)) late = true;
+    float n[NV][8], g[NV][8];
+    float sum = 0.0f, rstd = 0.0f;
+    if (here) rstd = *reinterpret_cast<const float*>(from + at[AT_RSTD]);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) n[i][j] = g[i][j] = 0.0f;
+      const int col = col0 + i * apart;
+      if (!here || col >= cols) continue;
+      const T* dy = reinterpret_cast<const T*>(from + (ANY ? at[AT_DY] : part.dy)) + col;
+      const unsigned char* h = from + (ANY || KEPT ? at[AT_H] : part.h) + col * (KEPT ? 1 : kElem);
+      float to_n = rstd;  // what turns a value of h into n
+      if constexpr (KEPT) to_n *= scale_value(from[at[AT_SCALES] + col / kMxBlock]);
+      if constexpr (ANY) {
+        const int m = min(8, cols - col);
+        load_any8(dy, m, g[i]);
+        if constexpr (KEPT)
+          decode8(load_codes_any(h, m), 1.0f, n[i]);
+        else
+          load_any8(reinterpret_cast<const T*>(h), m, n[i]);
+      } else {
+        load_vec<8>(dy, g[i]);
+        if constexpr (KEPT)
+          decode8(*reinterpret_cast<const uint2*>(h), 1.0f, n[i]);
+        else
+          load_vec<8>(reinterpret_cast<const T*>(h), n[i]);
+      }
+      sum = grad_vector(n[i], g[i], to_n, w[i], acc[i], sum);
+    }
+    const float mean = row_sum(sum, t, scratch, turn) * inv_cols;
     if (a.dx) {
-      const float mean = row_sum(sum, scratch, turn) / (float)a.cols;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        if (!here || !in[i]) continue;
+        const int col = col0 + i * apart;
+        if (!here || col >= cols) continue;
         float d[8] = {};
         if (has_dres) {
-#pragma unroll
-          for (int q = 0; q < kWords; ++q) word(s + off_dres + (i * kWords + q) * vec_bytes, d + q * kPer);
+          const T* q = reinterpret_cast<const T*>(from + (ANY ? at[AT_DRES] : part.dres)) + col;
+          if constexpr (ANY)
+            load_any8(q, min(8, cols - col), d);
+          else
+            load_vec<8>(q, d);
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) d[k] = fmaf(r, fmaf(-n[i][k], mean, g[i][k]), d[k]);
-        store_vec<8>(dx + i * apart, d);
+        for (int j = 0; j < 8; ++j) d[j] = fmaf(rstd, fmaf(-n[i][j], mean, g[i][j]), d[j]);
+        if constexpr (ANY)
+          store_vec<8>(staged + col, d);
+        else
+          store_vec<8>(dx + col, d);
       }
     }
-    if (++at == DEPTH) at = 0;
+    __syncwarp();
+    if (threadIdx.x % 32 == 0) mbar_arrive(empty + slot);
+    if constexpr (ANY) {
+      if (a.dx) {
+        t.sync();
+        if (here) store_staged(dx, staged, cols, t);
+        if (p.per_row == 32) __syncwarp();  // row_sum has no barrier then
+      }
+    }
+    dx += step * a.lddx;
+    if (++slot == DEPTH) slot = 0, phase ^= 1;
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  store_partial<8, NV>(a, acc);
+  if (late) atomicOr(p.status, TIDE_DEVICE_TIMEOUT);
+  store_partial(a, t, rows, acc, reinterpret_cast<float*>(ring));
 }
 
 // A block takes 32 columns; warp w adds partials w, w + 32, ...
@@ -412,34 +593,65 @@ __global__ void __launch_bounds__(1024) sum_groups_kernel(const float* __restric
   }
 }
 
-// How a row is spread: V columns a vector, NV vectors a thread, `threads`
-// threads a row, `rows` rows a block.  NV grows with the row so that a block
-// stays at 512 threads or fewer where it can (several blocks an SM).
+// How a row is spread: NV vectors of eight columns a thread, `threads` threads a
+// row, `rows` rows a block, and, in the backward pass, the blocks an SM that its
+// registers are bounded to.
 struct RowShape {
-  int nv, threads, rows;
+  int nv, threads, rows, per_sm;
 };
-RowShape row_shape(bool vec, int64_t cols) {
-  RowShape s{};
-  if (vec)
-    s.nv = cols <= 2048 ? 1 : cols <= 8192 ? 2 : 4;
-  else
-    s.nv = cols <= 1024 ? 4 : cols <= 4096 ? 8 : 16;
-  const int64_t each = (int64_t)s.nv * (vec ? 8 : 1);
-  s.threads = (int)((cols + each * 32 - 1) / (each * 32) * 32);
-  s.rows = std::max(1, 256 / s.threads);
+RowShape spread(int64_t cols, int nv) {
+  const int64_t each = (int64_t)nv * 8 * 32;
+  const int threads = (int)((cols + each - 1) / each * 32);
+  return {nv, threads, std::max(1, 256 / threads), 1};
+}
+// Forward: NV grows with the row so that a block stays at 512 threads or fewer
+// (several blocks an SM).
+RowShape forward_shape(int64_t cols) { return spread(cols, cols <= 2048 ? 1 : cols <= 8192 ? 2 : 4); }
+// Backward: the row's barrier and the latencies around it bind, so few threads
+// with much independent work each: four vectors beat two from 2048 columns on
+// (8192 x 5120 from a checkpoint 50 us against 63, 8192 x 8192 88 against 96).
+RowShape backward_shape(int64_t cols) {
+  RowShape s = spread(cols, cols <= 512 ? 1 : cols <= 2048 ? 2 : 4);
+  if (s.nv == 4) s.rows = 1;
+  s.per_sm = s.nv == 1 ? 3 : s.nv == 2 || s.threads <= 160 ? 2 : 1;
   return s;
 }
 
 template <int N>
 using Int = std::integral_constant<int, N>;
 
-// f(V, NV, most threads of a block), as constants.
+// f(NV, most threads of a block that work on rows, blocks an SM), as constants.
 template <typename F>
-void with_shape(bool vec, const RowShape& s, F&& f) {
-  if (vec)
-    s.nv == 1 ? f(Int<8>(), Int<1>(), Int<256>()) : s.nv == 2 ? f(Int<8>(), Int<2>(), Int<512>()) : f(Int<8>(), Int<4>(), Int<512>());
+void with_forward_shape(const RowShape& s, F&& f) {
+  if (s.nv == 1)
+    f(Int<1>(), Int<256>());
+  else if (s.nv == 2)
+    f(Int<2>(), Int<512>());
   else
-    s.nv == 4 ? f(Int<1>(), Int<4>(), Int<256>()) : s.nv == 8 ? f(Int<1>(), Int<8>(), Int<512>()) : f(Int<1>(), Int<16>(), Int<1024>());
+    f(Int<4>(), Int<512>());
+}
+template <typename F>
+void with_backward_shape(const RowShape& s, F&& f) {
+  if (s.nv == 1)
+    f(Int<1>(), Int<256>(), Int<3>());
+  else if (s.nv == 2)
+    f(Int<2>(), Int<256>(), Int<2>());
+  else if (s.threads <= 160)
+    f(Int<4>(), Int<160>(), Int<2>());
+  else if (s.threads <= 256)
+    f(Int<4>(), Int<256>(), Int<1>());
+  else
+    f(Int<4>(), Int<512>(), Int<1>());
+}
+
+// Launches with `smem` bytes of dynamic shared memory.
+template <typename... Params, typename... Args>
+tide_status launch(void (*kernel)(Params...), int64_t grid, dim3 threads, int smem, cudaStream_t stream, const char* what,
+                   const Args&... args) {
+  if (smem > 32 * 1024)  // beyond the 48 KB, static shared memory included, that need no leave
+    TIDE_TRY(cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem), what));
+  kernel<<<(unsigned)grid, threads, smem, stream>>>(args...);
+  return cuda_status(cudaGetLastError(), what);
 }
 
 template <typename T>
@@ -448,23 +660,26 @@ tide_status norm(const NormArgs& a, cudaStream_t stream) {
                    rows_aligned(a.residual, a.ldr, sizeof(T), a.rows) && rows_aligned(a.h, a.ldh, sizeof(T), a.rows) &&
                    rows_aligned(a.y, a.ldy, sizeof(T), a.rows) && (uintptr_t)a.weight % 16 == 0 &&
                    (uintptr_t)a.codes % 8 == 0 && (!a.codes || a.rows <= 1 || a.ldc % 8 == 0);
-  const RowShape s = row_shape(vec, a.cols);
+  const RowShape s = forward_shape(a.cols);
   const int64_t grid = (a.rows + s.rows - 1) / s.rows;
   if (grid > INT32_MAX) return fail(TIDE_ERR_UNIMPLEMENTED, "too many rows for one launch");
-  with_shape(vec, s, [&](auto v, auto nv, auto threads) {
-    norm_kernel<T, v(), nv(), threads()><<<(unsigned)grid, dim3(s.threads, s.rows), 0, stream>>>(a);
+  const dim3 block(s.threads, s.rows);
+  const int stage = s.rows * 2 * stage_room(a.cols, sizeof(T));
+  tide_status st = TIDE_OK;
+  with_forward_shape(s, [&](auto nv, auto threads) {
+    st = vec ? launch(norm_kernel<T, nv(), false, threads()>, grid, block, 0, stream, "rms norm", a)
+             : launch(norm_kernel<T, nv(), true, threads()>, grid, block, stage, stream, "rms norm", a);
   });
-  return cuda_status(cudaGetLastError(), "rms norm");
+  return st;
 }
 
-// Blocks of the backward pass: up to `per_sm` an SM, but past 64 row groups at
-// least four rows a group, so that the partial sums stay few.
+// Blocks of the backward pass: up to `per_sm` an SM, but past 64 at least four
+// turns a block, so that the partial sums stay few.
 int64_t grad_blocks(int64_t rows, const RowShape& s, int per_sm, int sms) {
   const int64_t most = (rows + s.rows - 1) / s.rows;
-  const int64_t few = std::max<int64_t>(64 / s.rows, (rows + 4 * s.rows - 1) / (4 * s.rows));
+  const int64_t few = std::max<int64_t>(64, (rows + 4 * s.rows - 1) / (4 * s.rows));
   return std::min(std::min(most, few), (int64_t)sms * per_sm);
 }
-int most_per_sm(const RowShape& s) { return std::max(1, 1024 / (s.threads * s.rows)); }
 
 template <typename T>
 tide_status norm_grad(NormGradArgs a, void* dweight, cudaStream_t stream) {
@@ -472,52 +687,42 @@ tide_status norm_grad(NormGradArgs a, void* dweight, cudaStream_t stream) {
   if (sms <= 0) return fail(TIDE_ERR_CUDA, "the current device could not be queried");
   const bool vec = a.cols % 8 == 0 && rows_aligned(a.dy, a.lddy, sizeof(T), a.rows) &&
                    rows_aligned(a.h, a.ldh, sizeof(T), a.rows) && rows_aligned(a.dres, a.ldres, sizeof(T), a.rows) &&
-                   rows_aligned(a.dx, a.lddx, sizeof(T), a.rows) && (uintptr_t)a.weight % 16 == 0 &&
-                   (uintptr_t)a.codes % 8 == 0 && (a.h || a.rows <= 1 || a.ldc % 8 == 0);
+                   rows_aligned(a.dx, a.lddx, sizeof(T), a.rows) && (uintptr_t)a.codes % 8 == 0 &&
+                   (a.h || a.rows <= 1 || a.ldc % 8 == 0);
   tide_status st = TIDE_OK;
   int64_t groups = 0;
   if (a.rows > 0) {
-    const RowShape s = row_shape(vec, a.cols);
-    const dim3 block(s.threads, s.rows);
-    const int slot = ring_slot_bytes(s.threads * s.rows, s.nv, sizeof(T), !a.h, a.dres != nullptr);
-    constexpr int kRoom = 200 * 1024;  // shared memory of an SM that rings may take
-    const int depth = 4 * slot <= kRoom ? 4 : 2 * slot <= kRoom ? 2 : 0;
-    const int per_sm = vec && depth ? std::min(most_per_sm(s), kRoom / (depth * slot)) : most_per_sm(s);
-    const int64_t blocks = grad_blocks(a.rows, s, per_sm, sms);
-    groups = blocks * s.rows;
-    with_shape(vec, s, [&](auto v, auto nv, auto threads) {
-      if constexpr (v() == 8) {
-        auto ring = [&](auto kernel) {
-          const int smem = depth * slot;
-          cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-          if (err == cudaSuccess) {
-            kernel<<<(unsigned)blocks, block, smem, stream>>>(a);
-            err = cudaGetLastError();
-          }
-          st = cuda_status(err, "rms norm backward");
-        };
-        // Registers for two blocks an SM where the block is small enough, for
-        // one otherwise (with one, 5120 columns took 79 us where two take 57).
-        auto pick = [&](auto most, auto min_blocks) {
-          constexpr int kT = most(), kB = min_blocks();
-          if (depth == 4)
-            a.h ? ring(norm_grad_ring_kernel<T, nv(), 4, false, kT, kB>) : ring(norm_grad_ring_kernel<T, nv(), 4, true, kT, kB>);
-          else
-            a.h ? ring(norm_grad_ring_kernel<T, nv(), 2, false, kT, kB>) : ring(norm_grad_ring_kernel<T, nv(), 2, true, kT, kB>);
-        };
-        if (depth) {
-          if constexpr (nv() == 1) {
-            pick(Int<256>(), Int<3>());
-          } else if constexpr (nv() == 2) {
-            s.threads <= 320 ? pick(Int<320>(), Int<2>()) : pick(Int<512>(), Int<1>());
-          } else {
-            pick(Int<512>(), Int<1>());
-          }
-          return;
-        }
-      }
-      norm_grad_kernel<T, v(), nv(), threads()><<<(unsigned)blocks, block, 0, stream>>>(a);
-      st = cuda_status(cudaGetLastError(), "rms norm backward");
+    const RowShape s = backward_shape(a.cols);
+    const char* what = "rms norm backward";
+    constexpr int kRoom = 208 * 1024;  // shared memory of an SM that rings may take
+    const bool kept = !a.h;
+    const int stage = s.rows * stage_room(a.cols, sizeof(T));  // dx, where rows are not aligned
+    const int slot = s.rows * RingRow(a.cols, sizeof(T), kept, a.dres != nullptr).bytes, beside = vec ? 0 : stage;
+    // Four rows, or else two; a block that cannot have two goes without the
+    // ring.
+    const int depth = s.threads <= 256 && s.per_sm * (4 * slot + beside) <= kRoom ? 4 : 2 * slot + beside <= kRoom ? 2 : 0;
+    const int smem = depth ? depth * slot + beside : stage;
+    const int64_t blocks = grad_blocks(a.rows, s, std::max(1, std::min(s.per_sm, kRoom / smem)), sms);
+    const int block = s.threads * s.rows;
+    groups = blocks;
+    RingArgs r{a, s.threads, s.rows, nullptr, ops_wait_limit_ns()};
+    if (depth) TIDE_TRY(ops_status_word(&r.status));
+    with_backward_shape(s, [&](auto nv, auto threads, auto per_sm) {
+      constexpr int kB = per_sm();
+      auto go = [&](auto d, auto any) {
+        constexpr int kD = threads() == 512 ? 2 : d();
+        constexpr bool kAny = any();
+        constexpr int kT = threads() + 32;
+        const int with_copies = block + 32;
+        st = kept ? launch(norm_grad_ring_kernel<T, nv(), kD, true, kAny, kT, kB>, blocks, with_copies, smem, stream, what, r)
+                  : launch(norm_grad_ring_kernel<T, nv(), kD, false, kAny, kT, kB>, blocks, with_copies, smem, stream, what, r);
+      };
+      if (depth == 0)
+        st = launch(norm_grad_any_kernel<T, nv(), threads(), kB>, blocks, s.threads, smem, stream, what, a);
+      else if (vec)
+        depth == 4 ? go(Int<4>(), std::false_type()) : go(Int<2>(), std::false_type());
+      else
+        depth == 4 ? go(Int<4>(), std::true_type()) : go(Int<2>(), std::true_type());
     });
   }
   if (st == TIDE_OK && dweight)
@@ -590,12 +795,8 @@ tide_status tide_rms_norm(int64_t rows, int64_t cols, int32_t dtype, const void*
 int64_t tide_rms_norm_backward_workspace(int64_t rows, int64_t cols) {
   if (rows <= 0 || cols <= 0 || cols > kMaxCols) return 0;
   const int sms = ops_num_sms();
-  int64_t most = 0;  // whichever the alignment of the call's rows selects
-  for (const bool vec : {true, false}) {
-    const RowShape s = row_shape(vec, cols);
-    most = std::max(most, grad_blocks(rows, s, most_per_sm(s), sms) * s.rows);
-  }
-  return most * cols * 4;
+  const RowShape s = backward_shape(cols);
+  return grad_blocks(rows, s, s.per_sm, sms) * cols * 4;
 }
 
 tide_status tide_rms_norm_backward(int64_t rows, int64_t cols, int32_t dtype, const void* dy, int64_t lddy,
