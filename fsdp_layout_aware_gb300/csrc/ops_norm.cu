@@ -7,6 +7,8 @@
 
 #include <algorithm>
 #include <type_traits>
+#include <utility>
+#include <vector>
 
 #include "bulk_ptx.cuh"
 #include "ops_common.cuh"
@@ -644,12 +646,28 @@ void with_backward_shape(const RowShape& s, F&& f) {
     f(Int<4>(), Int<512>(), Int<1>());
 }
 
+// Raises a kernel's dynamic shared memory limit as far as it goes, once for each
+// thread, kernel and device.
+tide_status allow_smem(const void* kernel, const char* what) {
+  static thread_local std::vector<std::pair<const void*, int>> done;
+  int dev = 0, most = 0;
+  TIDE_TRY(cuda_status(cudaGetDevice(&dev), what));
+  for (const auto& d : done)
+    if (d.first == kernel && d.second == dev) return TIDE_OK;
+  cudaFuncAttributes attr;
+  TIDE_TRY(cuda_status(cudaFuncGetAttributes(&attr, kernel), what));
+  TIDE_TRY(cuda_status(cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev), what));
+  TIDE_TRY(cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            most - (int)attr.sharedSizeBytes), what));
+  done.emplace_back(kernel, dev);
+  return TIDE_OK;
+}
+
 // Launches with `smem` bytes of dynamic shared memory.
 template <typename... Params, typename... Args>
 tide_status launch(void (*kernel)(Params...), int64_t grid, dim3 threads, int smem, cudaStream_t stream, const char* what,
                    const Args&... args) {
-  if (smem > 32 * 1024)  // beyond the 48 KB, static shared memory included, that need no leave
-    TIDE_TRY(cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem), what));
+  if (smem > 32 * 1024) TIDE_TRY(allow_smem((const void*)kernel, what));  // 48 KB, static included, need no leave
   kernel<<<(unsigned)grid, threads, smem, stream>>>(args...);
   return cuda_status(cudaGetLastError(), what);
 }
