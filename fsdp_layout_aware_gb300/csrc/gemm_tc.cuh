@@ -92,22 +92,6 @@ struct TcShape {
 
 // ---- epilogues
 
-template <int ACT>
-struct ActTag {
-  static constexpr int value = ACT;
-};
-// f called with the activation as a constant.
-template <typename F>
-__device__ __forceinline__ void with_act(int act, F&& f) {
-  switch (act) {
-    case TIDE_ACT_RELU: f(ActTag<TIDE_ACT_RELU>()); break;
-    case TIDE_ACT_GELU: f(ActTag<TIDE_ACT_GELU>()); break;
-    case TIDE_ACT_GELU_ERF: f(ActTag<TIDE_ACT_GELU_ERF>()); break;
-    case TIDE_ACT_SILU: f(ActTag<TIDE_ACT_SILU>()); break;
-    default: break;
-  }
-}
-
 __device__ __forceinline__ void load32(const bf16* p, float (&v)[32]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {

@@ -92,12 +92,25 @@ __global__ void __launch_bounds__(kThreads) store_any_kernel(const StoreArgs a) 
   store_codes_any(a.codes + row * a.ldc + col, n, w);
 }
 
-// fp32 outputs take the accurate exponential and division.
+// f(v), or g * f'(v).  fp32 outputs take the accurate exponential and division.
 template <typename T, int N>
 __device__ __forceinline__ void loaded(float (&v)[N], int act, bool has_grad, const float (&g)[N]) {
   constexpr bool fast = sizeof(T) == 2;
+  if (has_grad) {
+    with_act(act, [&](auto a) {
 #pragma unroll
-  for (int k = 0; k < N; ++k) v[k] = has_grad ? g[k] * act_grad<fast>(act, v[k]) : act_value<fast>(act, v[k]);
+      for (int k = 0; k < N; ++k) v[k] = g[k] * act_grad<fast>(a.value, v[k]);
+    });
+    if (act == TIDE_ACT_NONE) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] = g[k];
+    }
+  } else {
+    with_act(act, [&](auto a) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] = act_value<fast>(a.value, v[k]);
+    });
+  }
 }
 
 // Eight neighbouring columns a thread and item; rows on 16-byte (out, grad)

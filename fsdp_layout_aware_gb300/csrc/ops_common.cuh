@@ -341,12 +341,16 @@ constexpr float kGeluB = 0.044715f;
 constexpr float kInvSqrt2 = 0.7071067811865475f;
 constexpr float kInvSqrt2Pi = 0.3989422804014327f;
 
-// FAST: the approximate exponential and division, good to a few units in the
-// last place of fp32 over the range that matters, for results that are then
-// rounded to bf16 or 8 bits.  fp32 results take the accurate ones.
+// FAST: exp(t) = 2^(t log2 e) and the reciprocal by the approximate instructions
+// that flush subnormal numbers (a result below 2^-126 becomes 0), good to a few
+// units in the last place of fp32 over the range that matters, for results that
+// are then rounded to bf16 or 8 bits.  fp32 results take the accurate functions.
 template <bool FAST>
 __device__ __forceinline__ float exp_of(float t) {
-  return FAST ? __expf(t) : expf(t);
+  if constexpr (!FAST) return expf(t);
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t * 1.4426950408889634f));
+  return r;
 }
 
 // 1 / (1 + exp(-t)): 0 at -inf (and where the exponential overflows), 1 at
@@ -354,7 +358,10 @@ __device__ __forceinline__ float exp_of(float t) {
 template <bool FAST>
 __device__ __forceinline__ float sigmoid(float t) {
   const float d = 1.0f + exp_of<FAST>(-t);
-  return FAST ? __fdividef(1.0f, d) : 1.0f / d;
+  if constexpr (!FAST) return 1.0f / d;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+  return r;
 }
 
 // GELU, GELU_ERF and SILU are z * p(z) with p from 0 to 1; where p has come
@@ -391,6 +398,23 @@ __device__ __forceinline__ float act_grad(int act, float z) {
       d = p * (1.0f - p);
       return d == 0.0f ? p : p + z * d;
     default: return 1.0f;
+  }
+}
+
+template <int ACT>
+struct ActTag {
+  static constexpr int value = ACT;
+};
+// f called with the activation as a constant (not at all for none): one branch for
+// many elements.
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F&& f) {
+  switch (act) {
+    case TIDE_ACT_RELU: f(ActTag<TIDE_ACT_RELU>()); break;
+    case TIDE_ACT_GELU: f(ActTag<TIDE_ACT_GELU>()); break;
+    case TIDE_ACT_GELU_ERF: f(ActTag<TIDE_ACT_GELU_ERF>()); break;
+    case TIDE_ACT_SILU: f(ActTag<TIDE_ACT_SILU>()); break;
+    default: break;
   }
 }
 
