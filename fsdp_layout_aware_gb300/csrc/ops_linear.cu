@@ -17,7 +17,7 @@ tide_status launch_checkpoint_load_bf16(int64_t rows, int64_t cols, const uint8_
 
 namespace {
 
-// Set where a product's kernel gave up a wait (tide_ops_check).
+// Set where an operator's kernel gave up a wait (tide_ops_check).
 __device__ int32_t g_status;
 std::atomic<int64_t> g_wait_limit_ns{2000000000};
 std::atomic<int64_t> g_test_drop{-1};
@@ -298,7 +298,7 @@ tide_status product(int64_t m, int64_t n, int64_t k, Operand a, bool a_mn, Opera
     p.k_blocks = s.k_blocks, p.split_blocks = s.split_blocks, p.splits = s.splits;
     TIDE_TRY(ops_status_word(&p.status));
     p.wait_limit_ns = ops_wait_limit_ns();
-    p.test_drop = g_test_drop.load(std::memory_order_relaxed);
+    p.test_drop = ops_test_drop();
     const int64_t units = (int64_t)s.tiles_a * s.tiles_b * s.splits;
     const int grid = (int)std::min<int64_t>(units * ts.ctas, sms / ts.ctas * ts.ctas);
     TIDE_TRY(cuda_status(launch(p, s.tile, grid, after, stream), "linear product"));
@@ -414,6 +414,7 @@ tide_status ops_status_word(int32_t** word) {
 }
 
 uint64_t ops_wait_limit_ns() { return (uint64_t)g_wait_limit_ns.load(std::memory_order_relaxed); }
+int64_t ops_test_drop() { return g_test_drop.load(std::memory_order_relaxed); }
 
 }  // namespace tide
 

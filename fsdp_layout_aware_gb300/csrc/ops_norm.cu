@@ -367,15 +367,15 @@ __device__ __forceinline__ uint32_t row_span(const unsigned char* from, int64_t 
 
 // Copies a row of a matrix (`at`, of cols * elem bytes) to `to` plus its phase
 // within 16 bytes; returns the bytes that will count on `bar`.  What no granule
-// covers goes byte by byte.
+// covers goes byte by byte.  withheld (tests): the counted bytes never come.
 __device__ __forceinline__ uint32_t copy_row(unsigned char* to, const unsigned char* at, const void* base, int64_t rows,
-                                             int64_t cols, int64_t ld, int elem, uint64_t* bar) {
+                                             int64_t cols, int64_t ld, int elem, bool withheld, uint64_t* bar) {
   const unsigned char* first = (const unsigned char*)base;
   const unsigned char* end = at + cols * elem;
   uint32_t skip;
   const uint32_t n = row_span(at, cols * elem, first, first + ((rows - 1) * ld + cols) * elem, skip);
   const unsigned char* lo = (const unsigned char*)((uintptr_t)at & ~(uintptr_t)15);
-  if (n) bulk_load(to + skip, lo + skip, n, bar);
+  if (n && !withheld) bulk_load(to + skip, lo + skip, n, bar);
   for (const unsigned char* q = at; q < lo + skip && q < end; ++q) to[q - lo] = *q;
   for (const unsigned char* q = at < lo + skip + n ? lo + skip + n : at; q < end; ++q) to[q - lo] = *q;
   return n;
@@ -386,6 +386,7 @@ struct RingArgs {
   int32_t per_row, rows;
   int32_t* status;
   uint64_t wait_limit_ns;
+  int64_t test_drop;  // turn (counted per block) whose copies are withheld (tests); -1: none
 };
 
 // A row in the ring, with room for its phase within 16 bytes.
@@ -430,7 +431,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_ring_kernel(const R
   __syncthreads();
 
   // Copies the block's y-th row of a turn (`row`) into a slot.
-  auto issue = [&](int y, int64_t row, int slot) {
+  auto issue = [&](int y, int64_t row, int slot, bool withheld) {
     uint32_t bytes = 0;
     if (row < a.rows) {
       unsigned char* to = ring + slot * slot_bytes + y * part.bytes;
@@ -439,7 +440,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_ring_kernel(const R
       auto one = [&](RingPart which, const void* base, int64_t n, int64_t ld, int elem, int where) {
         const unsigned char* at = (const unsigned char*)base + row * ld * elem;
         reinterpret_cast<int*>(to)[which] = where + (int)((uintptr_t)at & 15);
-        bytes += copy_row(to + where, at, base, a.rows, n, ld, elem, bar);
+        bytes += copy_row(to + where, at, base, a.rows, n, ld, elem, withheld, bar);
       };
       one(AT_DY, a.dy, cols, a.lddy, kElem, part.dy);
       if (has_dres) one(AT_DRES, a.dres, cols, a.ldres, kElem, part.dres);
@@ -464,7 +465,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_ring_kernel(const R
     int slot = 0, k = 0;
     for (; k < turns; ++k) {
       if (k >= DEPTH && !(ok = mbar_wait_bounded(empty + slot, (uint32_t)(k / DEPTH - 1) & 1, p.wait_limit_ns))) break;
-      issue(y, first_row + y + k * step, slot);
+      issue(y, first_row + y + k * step, slot, k == p.test_drop);
       if (++slot == DEPTH) slot = 0;
     }
     if (!ok) {  // the copies in flight land before the block leaves
@@ -492,10 +493,10 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_ring_kernel(const R
   uint32_t phase = 0;
   bool late = false;
   for (int k = 0; k < turns; ++k) {
-    const bool here = k < mine;
     const unsigned char* from = ring + slot * slot_bytes + t.y * part.bytes;
     const int* at = reinterpret_cast<const int*>(from);
     if (!late && !mbar_wait_bounded(full + slot, phase, p.wait_limit_ns)) late = true;
+    const bool here = !late && k < mine;  // nothing of a slot is read that did not come
     float n[NV][8], g[NV][8];
     float sum = 0.0f, rstd = 0.0f;
     if (here) rstd = *reinterpret_cast<const float*>(from + at[AT_RSTD]);
@@ -548,7 +549,8 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_ring_kernel(const R
       }
     }
     __syncwarp();
-    if (threadIdx.x % 32 == 0) mbar_arrive(empty + slot);
+    // After a wait that ran out no slot is handed back, so the copies end too.
+    if (!late && threadIdx.x % 32 == 0) mbar_arrive(empty + slot);
     if constexpr (ANY) {
       if (a.dx) {
         t.sync();
@@ -723,7 +725,7 @@ tide_status norm_grad(NormGradArgs a, void* dweight, cudaStream_t stream) {
     const int64_t blocks = grad_blocks(a.rows, s, std::max(1, std::min(s.per_sm, kRoom / smem)), sms);
     const int block = s.threads * s.rows;
     groups = blocks;
-    RingArgs r{a, s.threads, s.rows, nullptr, ops_wait_limit_ns()};
+    RingArgs r{a, s.threads, s.rows, nullptr, ops_wait_limit_ns(), ops_test_drop()};
     if (depth) TIDE_TRY(ops_status_word(&r.status));
     with_backward_shape(s, [&](auto nv, auto threads, auto per_sm) {
       constexpr int kB = per_sm();

@@ -55,19 +55,20 @@ typedef enum tide_act {
   TIDE_ACT_SILU = 4
 } tide_act;
 
-/* Synchronise the current device and report whether a kernel of the linear
- * layer gave up a bounded wait there since the last check (TIDE_ERR_TIMEOUT;
- * the flag is then cleared).  Such a call's outputs are undefined.  Errors:
- * CUDA. */
+/* Synchronise the current device and report whether a kernel of these operators
+ * gave up a bounded wait there since the last check (TIDE_ERR_TIMEOUT; the flag
+ * is then cleared).  Such a call's outputs are undefined.  Errors: CUDA. */
 tide_status tide_ops_check(void);
 
 /* Process-wide options.
  *   TIDE_OPS_OPT_WAIT_LIMIT_NS   bound, in nanoseconds, on every wait inside
- *                                the linear layer's kernels (default 2e9)
+ *                                the operators' kernels (default 2e9)
  *   TIDE_OPS_OPT_TEST_DROP_LOAD  test hook: a product's CTAs withhold the
  *                                loads of the given block of 64 of the summed
- *                                axis (counted per CTA from 0), so a bounded
- *                                wait runs out; -1 (default) disables
+ *                                axis, and the norm's backward pass the
+ *                                copies of the given turn of rows (counted per
+ *                                CTA from 0), so a bounded wait runs out; -1
+ *                                (default) disables
  * Errors: INVALID_ARG. */
 typedef enum tide_ops_option { TIDE_OPS_OPT_WAIT_LIMIT_NS = 1, TIDE_OPS_OPT_TEST_DROP_LOAD = 2 } tide_ops_option;
 tide_status tide_ops_set_option(int32_t option, int64_t value);

@@ -723,3 +723,30 @@ def test_a_wait_that_runs_out_is_reported(rows, inner, outer):
     tide.tide_linear(x, w, y)
     tide.tide_ops_check()
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("rows,cols,kept", [(4000, 1024, False), (3000, 2048, True), (2000, 333, True)])
+def test_a_copy_that_does_not_come_is_reported(rows, cols, kept):
+    """The same for the norm's backward pass, whose rows are copied ahead."""
+    h, dy = rand((rows, cols), BF, 1).to(DEV), rand((rows, cols), BF, 2).to(DEV)
+    w, rstd = torch.ones(cols, dtype=BF, device=DEV), torch.ones(rows, device=DEV)
+    if kept:
+        ck = tide.Checkpoint8.empty(rows, cols)
+        tide.tide_checkpoint_store(h, ck)
+        h = ck
+    out = [[torch.empty(rows, cols, dtype=BF, device=DEV), torch.empty(cols, dtype=BF, device=DEV)] for _ in range(2)]
+    tide.tide_rms_norm_backward(dy, h, w, rstd, out[0][0], dweight=out[0][1])
+    tide.tide_ops_check()
+    tide.tide_ops_set_option(tide.TIDE_OPS_OPT_WAIT_LIMIT_NS, 20_000_000)
+    tide.tide_ops_set_option(tide.TIDE_OPS_OPT_TEST_DROP_LOAD, 1)
+    try:
+        tide.tide_rms_norm_backward(dy, h, w, rstd, out[1][0], dweight=out[1][1])
+        with pytest.raises(tide.TideError) as e:
+            tide.tide_ops_check()
+        assert e.value.status == 8
+    finally:
+        tide.tide_ops_set_option(tide.TIDE_OPS_OPT_TEST_DROP_LOAD, -1)
+        tide.tide_ops_set_option(tide.TIDE_OPS_OPT_WAIT_LIMIT_NS, 2_000_000_000)
+    tide.tide_rms_norm_backward(dy, h, w, rstd, out[1][0], dweight=out[1][1])
+    tide.tide_ops_check()
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
