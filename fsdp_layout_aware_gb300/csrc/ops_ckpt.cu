@@ -3,6 +3,9 @@
 // Both directions are one pass over the matrix, a few operations per element,
 // so they are bound by memory traffic: store reads s bytes and writes 1 + 1/32
 // per element, load reads 1 + 1/32 (and s for a gradient) and writes s.
+//   8192 x 13824 bf16 (343 MB each way): store 57 us, load 49 us, 6.0 and 7.0 TB/s
+//   4093 x 4095 bf16, rows of odd alignment, times a gradient through SiLU'
+//   (84 MB): 22 us, 3.8 TB/s; 31 instructions a value bind it there
 
 #include <algorithm>
 
