@@ -4,7 +4,6 @@
 
 #include <algorithm>
 #include <atomic>
-#include <functional>
 #include <utility>
 
 #include "gemm_tc.cuh"
@@ -74,6 +73,7 @@ Plan choose_plan(int64_t m, int64_t n, int64_t k, bool a_mn, bool vec, int sms) 
       s.split_blocks = (int32_t)ceil_div(kb, want);
       s.splits = (int32_t)ceil_div(kb, s.split_blocks);
       if (s.splits != want) continue;  // the same split as a smaller number's
+      if ((int64_t)s.tiles_a * s.tiles_b * s.splits > INT32_MAX / 2) continue;  // counted in 32 bits
       const double turns = (double)ceil_div((int64_t)s.tiles_a * s.tiles_b * s.splits, sms / ts.ctas);
       const double busy = turns * std::max(s.split_blocks * block + 300.0, epilogue);
       const double dram = (double)(m + n) * k * 2.0 / 3500.0;
@@ -269,12 +269,17 @@ using Launch = cudaError_t (*)(const TcArgs&, TcTile, int, bool, cudaStream_t);
 // k (its contiguous axis is m or n).  `after`: the stream's last kernel is this
 // call's; `beside`, if not null, is called once the operands are laid out, to
 // launch a kernel that the product may overlap.
-template <int EPI>
+struct Nothing {
+  tide_status operator()() const { return TIDE_OK; }
+};
+template <int EPI, typename Beside = Nothing>
 tide_status product(int64_t m, int64_t n, int64_t k, Operand a, bool a_mn, Operand b, bool b_mn, EpilogueArgs e,
                     Launch launch, unsigned char* workspace, bool after, cudaStream_t stream,
-                    const std::function<tide_status()>* beside = nullptr) {
+                    const Beside* beside = nullptr) {
   const int sms = ops_num_sms();
   if (sms <= 0) return fail(TIDE_ERR_CUDA, "the current device could not be queried");
+  int32_t* status = nullptr;
+  TIDE_TRY(ops_status_word(&status));
   TIDE_TRY(check_extent(m, n, k));
   e.rows = m, e.cols = n;
   int splits = 0;
@@ -296,7 +301,7 @@ tide_status product(int64_t m, int64_t n, int64_t k, Operand a, bool a_mn, Opera
     p.e = e;
     p.tiles_a = s.tiles_a, p.tiles_b = s.tiles_b;
     p.k_blocks = s.k_blocks, p.split_blocks = s.split_blocks, p.splits = s.splits;
-    TIDE_TRY(ops_status_word(&p.status));
+    p.status = status;
     p.wait_limit_ns = ops_wait_limit_ns();
     p.test_drop = ops_test_drop();
     const int64_t units = (int64_t)s.tiles_a * s.tiles_b * s.splits;
@@ -532,7 +537,7 @@ tide_status tide_linear_grad_weight(int64_t rows, int64_t inner, int64_t outer, 
   const int v = sum_vector(rows, outer, dy, lddy);
   const int64_t groups = db && rows > 0 ? sum_groups(rows, outer, v, sms) : 0;
   float* partial = (float*)workspace;
-  const std::function<tide_status()> sums = [&] {
+  const auto sums = [&] {
     return column_sums(rows, outer, (const bf16*)dy, lddy, v, groups, partial, stream);
   };
   bool summed = false;

@@ -12,9 +12,8 @@
 //   4999 x 4095 bf16, rows of odd alignment (164 and 144 MB): 56 and 68 us
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
-#include <utility>
-#include <vector>
 
 #include "bulk_ptx.cuh"
 #include "ops_common.cuh"
@@ -657,17 +656,22 @@ void with_backward_shape(const RowShape& s, F&& f) {
 // Raises a kernel's dynamic shared memory limit as far as it goes, once for each
 // thread, kernel and device.
 tide_status allow_smem(const void* kernel, const char* what) {
-  static thread_local std::vector<std::pair<const void*, int>> done;
+  struct Done {
+    const void* kernel;
+    int dev;
+  };
+  static thread_local Done done[128];
+  static thread_local int count = 0;
   int dev = 0, most = 0;
   TIDE_TRY(cuda_status(cudaGetDevice(&dev), what));
-  for (const auto& d : done)
-    if (d.first == kernel && d.second == dev) return TIDE_OK;
+  for (int i = 0; i < count; ++i)
+    if (done[i].kernel == kernel && done[i].dev == dev) return TIDE_OK;
   cudaFuncAttributes attr;
   TIDE_TRY(cuda_status(cudaFuncGetAttributes(&attr, kernel), what));
   TIDE_TRY(cuda_status(cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev), what));
   TIDE_TRY(cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                             most - (int)attr.sharedSizeBytes), what));
-  done.emplace_back(kernel, dev);
+  if (count < 128) done[count++] = {kernel, dev};
   return TIDE_OK;
 }
 
@@ -780,13 +784,13 @@ tide_status launch_sum_groups(const float* partial, int64_t groups, int64_t cols
 }
 
 int ops_num_sms() {
-  static int known[64];
+  static std::atomic<int> known[64];
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
-  if (dev < 64 && known[dev] > 0) return known[dev];
+  if (dev < 64 && known[dev].load(std::memory_order_relaxed) > 0) return known[dev].load(std::memory_order_relaxed);
   int n = 0;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  if (dev < 64) known[dev] = n;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
