@@ -11,7 +11,7 @@
 //
 // One persistent CTA per SM.  Warp 0 streams 64-deep blocks of A and B into a
 // ring of shared-memory stages with TMA; warp 1 (of the first CTA of a pair)
-// issues the matrix instructions; warps 4-7 take a finished accumulator out of
+// issues the matrix instructions; warps 4-11 take a finished accumulator out of
 // tensor memory and run the epilogue while the next tile accumulates in the
 // other half.  Every wait is bounded: a wait that runs out sets the status
 // word, and the CTA drains its copies, frees its tensor memory and returns.
@@ -81,18 +81,24 @@ struct TcArgs {
   int64_t test_drop;       // k block (counted per CTA) whose loads are withheld (tests); -1: none
 };
 
-constexpr int kTcThreads = 256;
+constexpr int kTcThreads = 384;    // four warps as above, and eight for the epilogue
 constexpr int kTcK = 64;           // values of k a stage holds: 128 bytes, one swizzle row
 constexpr int kTcGroup = 8;        // tile rows walked together, for reuse of B in L2
-constexpr int kTcRoom = 224 * 1024;  // shared memory a CTA may take
+constexpr int kTcRoom = 227 * 1024;  // shared memory a CTA may take
 
-template <int CG, int BN>
+// A 32 x 32 block per epilogue warp, to be turned: fp32 (rows of 33), or, where
+// the values are only rounded and stored, pairs of bf16 (rows of 17), which
+// leaves the bias gradient's blocks room beside the weight gradient's.
+template <int EPI, bool SWAP>
+constexpr int kTurnBytes = EPI == EPI_PLAIN && !SWAP ? 32 * 17 * 4 : 32 * 33 * 4;
+
+template <int CG, int BN, int EPI, bool SWAP>
 struct TcShape {
   static constexpr int a_bytes = 128 * kTcK * 2;
   static constexpr int b_rows = BN / CG;
   static constexpr int b_bytes = b_rows * kTcK * 2;
   static constexpr int stage_bytes = a_bytes + b_bytes;
-  static constexpr int transpose_bytes = 4 * 32 * 33 * 4;  // a [32][33] fp32 block per epilogue warp
+  static constexpr int transpose_bytes = 8 * kTurnBytes<EPI, SWAP>;
   static constexpr int columns = 2 * BN;                   // two accumulators
   static constexpr int fixed_bytes = 1024 + transpose_bytes + 512;
   static constexpr int stages = (kTcRoom - fixed_bytes) / stage_bytes < 12 ? (kTcRoom - fixed_bytes) / stage_bytes : 12;
@@ -187,10 +193,13 @@ __device__ __forceinline__ float4* partial_block(const EpilogueArgs& e, int spli
 
 // N rows from `row` (the first n of them exist), a whole warp on one block of 32
 // columns of each, an element a lane; any alignment.  `in`: the column exists.
-// The rows' steps are independent, which keeps a lone warp busy.
+// The rows' steps are independent, and what they load is loaded whether or not it
+// exists (from the nearest place that does): behind a branch each load would be
+// waited for by itself.
 template <int EPI, int N>
 __device__ __forceinline__ void epilogue_columns(const EpilogueArgs& e, int64_t row, int n, int64_t col, bool in,
                                                  float (&v)[N], float bias) {
+  const int64_t c = in ? col : e.cols - 1;  // where to load from
   if constexpr (EPI == EPI_FORWARD) {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += bias;
@@ -214,8 +223,7 @@ __device__ __forceinline__ void epilogue_columns(const EpilogueArgs& e, int64_t 
     float r[N] = {};
     if (e.residual) {
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (in && i < n) r[i] = __bfloat162float(e.residual[(row + i) * e.ldr + col]);
+      for (int i = 0; i < N; ++i) r[i] = __bfloat162float(e.residual[(row + min(i, n - 1)) * e.ldr + c]);
     }
     with_act(e.act, [&](auto a) {
 #pragma unroll
@@ -231,13 +239,16 @@ __device__ __forceinline__ void epilogue_columns(const EpilogueArgs& e, int64_t 
       float z[N] = {};
       if (e.zin) {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-          if (in && i < n) z[i] = __bfloat162float(e.zin[(row + i) * e.ldzin + col]);
+        for (int i = 0; i < N; ++i) z[i] = __bfloat162float(e.zin[(row + min(i, n - 1)) * e.ldzin + c]);
       } else {
+        uint8_t code[N], scale[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-          if (in && i < n)
-            z[i] = e4m3_values(e.cin[(row + i) * e.ldcin + col]).x * scale_value(e.sin[(row + i) * e.ldsin + col / kMxBlock]);
+        for (int i = 0; i < N; ++i) {
+          code[i] = e.cin[(row + min(i, n - 1)) * e.ldcin + c];
+          scale[i] = e.sin[(row + min(i, n - 1)) * e.ldsin + c / kMxBlock];
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) z[i] = e4m3_values(code[i]).x * scale_value(scale[i]);
       }
       with_act(e.act, [&](auto a) {
 #pragma unroll
@@ -260,18 +271,49 @@ __device__ __forceinline__ void epilogue_block(const EpilogueArgs& e, int64_t ro
     if (row + lane < e.rows) epilogue_row<EPI>(e, row + lane, col, v);
     return;
   }
-#pragma unroll
-  for (int i = 0; i < 32; ++i) block[lane * 33 + i] = v[i];
-  __syncwarp();
   const bool in = col + lane < e.cols;
-  float bias = 0.0f;
-  if (EPI == EPI_FORWARD && e.bias && in) bias = __bfloat162float(e.bias[col + lane]);
   const int n = (int)min((int64_t)32, e.rows - row);
-  for (int r = 0; r < n; r += 8) {
-    float t[8];
+  if constexpr (EPI == EPI_PLAIN) {
+    uint32_t* words = reinterpret_cast<uint32_t*>(block);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = block[(r + i) * 33 + lane];
-    epilogue_columns<EPI>(e, row + r, n - r, col + lane, in, t, bias);
+    for (int i = 0; i < 16; ++i) words[lane * 17 + i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+    __syncwarp();
+    const bf16* b = reinterpret_cast<const bf16*>(block);
+    bf16* out = e.out + row * e.ldo + col + lane;
+#pragma unroll 8
+    for (int r = 0; r < n; ++r)
+      if (in) out[r * e.ldo] = b[r * 34 + lane];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) block[lane * 33 + i] = v[i];
+    __syncwarp();
+    float bias = 0.0f;
+    if (EPI == EPI_FORWARD && e.bias && in) bias = __bfloat162float(e.bias[col + lane]);
+    for (int r = 0; r < n; r += 8) {
+      float t[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[i] = block[(r + i) * 33 + lane];
+      epilogue_columns<EPI>(e, row + r, n - r, col + lane, in, t, bias);
+    }
+  }
+}
+
+// Brings into L2 what the epilogue of a lane's row (n columns from col) will
+// read.
+template <int EPI>
+__device__ __forceinline__ void prefetch_row(const EpilogueArgs& e, int64_t row, int64_t col, int n) {
+  if (row >= e.rows) return;
+  auto lines = [&](const void* from, int64_t bytes) {
+    for (int64_t b = 0; b < bytes; b += 128)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"((const unsigned char*)from + b));
+  };
+  const int64_t m = min((int64_t)n, e.cols - col);
+  if (EPI == EPI_FORWARD && e.residual) lines(e.residual + row * e.ldr + col, m * 2);
+  if (EPI == EPI_GRAD_INPUT && e.act != TIDE_ACT_NONE) {
+    if (e.zin)
+      lines(e.zin + row * e.ldzin + col, m * 2);
+    else
+      lines(e.cin + row * e.ldcin + col, m);
   }
 }
 
@@ -292,7 +334,7 @@ __device__ __forceinline__ TileAt tile_at(const TcArgs& p, int t) {
 
 template <int CG, int BN, bool A_MN, bool B_MN, int EPI, bool SWAP>
 __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_constant__ TcArgs p) {
-  using Shape = TcShape<CG, BN>;
+  using Shape = TcShape<CG, BN, EPI, SWAP>;
   constexpr int kStages = Shape::stages;
   static_assert((2 * kStages + 5) * 8 + 4 <= 512, "barriers");
   extern __shared__ unsigned char raw[];
@@ -316,7 +358,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_con
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(acc_full + i, 1);
-      mbar_init(acc_empty + i, 4 * CG);
+      mbar_init(acc_empty + i, 8 * CG);
     }
     mbar_init(drained, 1);
     fence_mbar_init_cluster();
@@ -429,38 +471,43 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_con
     }
   } else if (warp >= 4) {
     // Epilogue: warp w reads lanes 32 (w mod 4) onwards, one row of the tile a
-    // lane, 32 columns at a time.
-    const int quad = warp - 4;
-    float* block = reinterpret_cast<float*>(transpose) + quad * 32 * 33;
+    // lane; warps 4-7 take every other 32 columns, warps 8-11 the rest.
+    const int quad = warp % 4, half = warp / 4 - 1;
+    float* block = reinterpret_cast<float*>(transpose + (warp - 4) * kTurnBytes<EPI, SWAP>);
     int turn = 0;
     for (int u = first; u < units; u += step, ++turn) {
       const TileAt at = tile_at(p, u % tiles);
       const int split = u / tiles;
       const int acc = turn & 1;
+      const int64_t a_row = (int64_t)(at.a * CG + (int)rank) * 128 + quad * 32;  // lane 0's row of A
+      const EpilogueArgs& e = p.e;
+      if constexpr (!SWAP) {
+        if (half == 0 && (int64_t)at.b * BN < e.cols) prefetch_row<EPI>(e, a_row + lane, (int64_t)at.b * BN, BN);
+      }
       ok = warp_wait_bounded(acc_full + acc, (turn >> 1) & 1, p.wait_limit_ns);
       if (!ok) break;
       tc_fence_after();
-      const int64_t a_row = (int64_t)(at.a * CG + (int)rank) * 128 + quad * 32;  // lane 0's row of A
-      const EpilogueArgs& e = p.e;
       const uint32_t from = tmem + acc * BN + ((uint32_t)(quad * 32) << 16);
       float lane_bias = 0.0f;
       if (SWAP && EPI == EPI_FORWARD && e.bias && a_row + lane < e.cols) lane_bias = __bfloat162float(e.bias[a_row + lane]);
+      auto hand_back = [&] {  // this warp has read its share: the accumulator may be written again
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG == 2)
+            mbar_arrive_cluster(mapped_addr(smem_addr(acc_empty + acc), 0));
+          else
+            mbar_arrive(acc_empty + acc);
+        }
+      };
+      if (half * 32 >= BN) hand_back();
 #pragma unroll 1
-      for (int c = 0; c < BN; c += 32) {
+      for (int c = half * 32; c < BN; c += 64) {
         const int64_t b_row = (int64_t)at.b * BN + c;  // the first of 32 rows of B
         float v[32];
         __syncwarp();
         tmem_load32(from + c, v);
-        if (c + 32 == BN) {  // the accumulator may be written again
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if constexpr (CG == 2)
-              mbar_arrive_cluster(mapped_addr(smem_addr(acc_empty + acc), 0));
-            else
-              mbar_arrive(acc_empty + acc);
-          }
-        }
+        if (c + 64 >= BN) hand_back();
         if constexpr (SWAP) {
           // Lane l has column a_row + l of the output in 32 rows: neighbouring
           // lanes on neighbouring elements.
@@ -578,7 +625,7 @@ cudaError_t launch_grad_weight(const TcArgs& p, TcTile t, int grid, bool after, 
 template <int CG, int BN, bool A_MN, bool B_MN, int EPI, bool SWAP>
 cudaError_t launch_tc(const TcArgs& p, int grid, bool after, cudaStream_t stream) {
   auto kernel = gemm_tc_kernel<CG, BN, A_MN, B_MN, EPI, SWAP>;
-  constexpr int smem = TcShape<CG, BN>::smem_bytes;
+  constexpr int smem = TcShape<CG, BN, EPI, SWAP>::smem_bytes;
   static std::atomic<uint64_t> ready{0};  // devices (bits) whose limit has been raised
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);

@@ -68,7 +68,7 @@ Plan choose_plan(int64_t m, int64_t n, int64_t k, bool a_mn, bool vec, int sms) 
     const double block = t == TILE_256x256 ? 570 : t == TILE_256x128 ? 340 : 225 + ts.b * 1.5;
     // The epilogue of a tile, which the next tile's blocks hide if they take
     // longer; `vec`: the output's rows take whole vectors.
-    const double epilogue = ts.swap ? 400 + 24.0 * std::min<int64_t>(m, ts.b) : (vec ? 20.0 : 55.0) * ts.b;
+    const double epilogue = ts.swap ? 300 + 16.0 * std::min<int64_t>(m, ts.b) : (vec ? 10.0 : 30.0) * ts.b;
     for (int64_t want = 1; want <= 32 && want <= std::max<int64_t>(1, kb / 4); ++want) {
       s.split_blocks = (int32_t)ceil_div(kb, want);
       s.splits = (int32_t)ceil_div(kb, s.split_blocks);
