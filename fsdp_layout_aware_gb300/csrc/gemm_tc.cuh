@@ -43,7 +43,7 @@ enum Epilogue { EPI_FORWARD, EPI_GRAD_INPUT, EPI_PLAIN, EPI_PARTIAL };
 struct EpilogueArgs {
   int64_t rows, cols;
   int32_t act;
-  bool vec;  // every matrix below has 16-byte aligned rows (cols may still be odd)
+  bool vec;  // every bf16 matrix below has 16-byte aligned rows, codes 8-byte aligned ones (cols may still be odd)
   const bf16* bias;
   const bf16* residual;
   int64_t ldr;
@@ -87,10 +87,10 @@ constexpr int kTcGroup = 8;        // tile rows walked together, for reuse of B 
 constexpr int kTcRoom = 227 * 1024;  // shared memory a CTA may take
 
 // A 32 x 32 block per epilogue warp, to be turned: fp32 (rows of 33), or, where
-// the values are only rounded and stored, pairs of bf16 (rows of 17), which
-// leaves the bias gradient's blocks room beside the weight gradient's.
+// the values are only rounded and stored, bf16 (rows of 80 bytes), which leaves
+// the bias gradient's blocks room beside the weight gradient's.
 template <int EPI, bool SWAP>
-constexpr int kTurnBytes = EPI == EPI_PLAIN && !SWAP ? 32 * 17 * 4 : 32 * 33 * 4;
+constexpr int kTurnBytes = EPI == EPI_PLAIN && !SWAP ? 32 * 80 : 32 * 33 * 4;
 
 template <int CG, int BN, int EPI, bool SWAP>
 struct TcShape {
@@ -107,54 +107,114 @@ struct TcShape {
 
 // ---- epilogues
 
-__device__ __forceinline__ void load32(const bf16* p, float (&v)[32]) {
+// A warp moves 32 x 32 blocks of a matrix with aligned rows through shared memory
+// (its `block`), so that a lane can hold a whole row of the block while global
+// memory sees neighbouring lanes on neighbouring words: 64 bytes (bf16) or 32
+// (codes) of a row by four or two lanes.  (A lane storing its own row touches 32
+// lines an instruction; 1788 x 13760 with a sum of 64 took 30 us that way.)
+// Staged rows are 80 and 48 bytes apart, which keeps both sides free of bank
+// conflicts.  Rows from `rows` on do not exist.
+
+// Words of 16 bytes: `lanes` of a row by neighbouring lanes, row r at r * kRow.
+template <int LANES, int ROW, typename F>
+__device__ __forceinline__ void by_words(int lane, int rows, F&& f) {
+#pragma unroll
+  for (int i = 0; i < LANES; ++i) {
+    const int r = i * (32 / LANES) + lane / LANES, q = lane % LANES;
+    if (r < rows) f(r, q, r * ROW + q * 16);
+  }
+}
+
+__device__ __forceinline__ void load_tile(const bf16* p, int64_t ld, int lane, int rows, unsigned char* block,
+                                          float (&v)[32]) {
+  by_words<4, 80>(lane, rows, [&](int r, int q, int at) {
+    *reinterpret_cast<uint4*>(block + at) = *reinterpret_cast<const uint4*>(p + r * ld + q * 8);
+  });
+  __syncwarp();
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float t[8];
-    load_vec<8>(p + 8 * i, t);
+    load_vec<8>(reinterpret_cast<const bf16*>(block + lane * 80) + 8 * i, t);
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[8 * i + k] = t[k];
   }
+  __syncwarp();
 }
-__device__ __forceinline__ void store32(bf16* p, const float (&v)[32]) {
+
+__device__ __forceinline__ void store_tile(bf16* p, int64_t ld, int lane, int rows, unsigned char* block,
+                                           const float (&v)[32]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float t[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) t[k] = v[8 * i + k];
-    store_vec<8>(p + 8 * i, t);
+    store_vec<8>(reinterpret_cast<bf16*>(block + lane * 80) + 8 * i, t);
   }
+  __syncwarp();
+  by_words<4, 80>(lane, rows, [&](int r, int q, int at) {
+    *reinterpret_cast<uint4*>(p + r * ld + q * 8) = *reinterpret_cast<const uint4*>(block + at);
+  });
+  __syncwarp();
 }
 
-// 32 neighbouring columns of one row, held by one thread; every matrix's rows
-// are 16-byte aligned and col is a multiple of 32.
+// Codes, whose rows are aligned to 8 bytes.
+__device__ __forceinline__ void load_codes(const uint8_t* p, int64_t ld, int lane, int rows, unsigned char* block,
+                                           uint32_t (&w)[8]) {
+  by_words<2, 48>(lane, rows, [&](int r, int q, int at) {
+    const uint2* x = reinterpret_cast<const uint2*>(p + r * ld + q * 16);
+    const uint2 a = x[0], b = x[1];
+    *reinterpret_cast<uint4*>(block + at) = make_uint4(a.x, a.y, b.x, b.y);
+  });
+  __syncwarp();
+  const uint4* x = reinterpret_cast<const uint4*>(block + lane * 48);
+  const uint4 a = x[0], b = x[1];
+  w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+  __syncwarp();
+}
+
+__device__ __forceinline__ void store_codes(uint8_t* p, int64_t ld, int lane, int rows, unsigned char* block,
+                                            const uint32_t (&w)[8]) {
+  uint4* x = reinterpret_cast<uint4*>(block + lane * 48);
+  x[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  x[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  __syncwarp();
+  by_words<2, 48>(lane, rows, [&](int r, int q, int at) {
+    const uint4 t = *reinterpret_cast<const uint4*>(block + at);
+    uint2* y = reinterpret_cast<uint2*>(p + r * ld + q * 16);
+    y[0] = make_uint2(t.x, t.y);
+    y[1] = make_uint2(t.z, t.w);
+  });
+  __syncwarp();
+}
+
+// The 32 x 32 block of the output at (row, col), lane l holding its l-th row
+// (`rows` of them exist), a whole warp; every matrix's rows take whole vectors.
 template <int EPI>
-__device__ __forceinline__ void epilogue_row(const EpilogueArgs& e, int64_t row, int64_t col, float (&v)[32]) {
+__device__ __forceinline__ void epilogue_tile(const EpilogueArgs& e, int64_t row, int64_t col, int lane, int rows,
+                                              unsigned char* block, float (&v)[32]) {
   float t[32];
   if constexpr (EPI == EPI_FORWARD) {
     if (e.bias) {
-      load32(e.bias + col, t);
+      const float mine = __bfloat162float(e.bias[col + lane]);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] += t[i];
+      for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, mine, i);
     }
-    if (e.z) store32(e.z + row * e.ldz + col, v);
+    if (e.z) store_tile(e.z + row * e.ldz + col, e.ldz, lane, rows, block, v);
     if (e.codes) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) t[i] = v[i];
       const int byte = scale_byte(block_magnitude<1>(t));
       uint32_t w[8];
       encode(t, byte, w);
-      uint4* c = reinterpret_cast<uint4*>(e.codes + row * e.ldc + col);
-      c[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      c[1] = make_uint4(w[4], w[5], w[6], w[7]);
-      e.scales[row * e.lds + col / kMxBlock] = (uint8_t)byte;
+      store_codes(e.codes + row * e.ldc + col, e.ldc, lane, rows, block, w);
+      if (lane < rows) e.scales[(row + lane) * e.lds + col / kMxBlock] = (uint8_t)byte;
     }
     with_act(e.act, [&](auto a) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = act_value<true>(a.value, v[i]);
     });
     if (e.residual) {
-      load32(e.residual + row * e.ldr + col, t);
+      load_tile(e.residual + row * e.ldr + col, e.ldr, lane, rows, block, t);
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] += t[i];
     }
@@ -162,12 +222,11 @@ __device__ __forceinline__ void epilogue_row(const EpilogueArgs& e, int64_t row,
   if constexpr (EPI == EPI_GRAD_INPUT) {
     if (e.act != TIDE_ACT_NONE) {
       if (e.zin) {
-        load32(e.zin + row * e.ldzin + col, t);
+        load_tile(e.zin + row * e.ldzin + col, e.ldzin, lane, rows, block, t);
       } else {
-        const uint4* c = reinterpret_cast<const uint4*>(e.cin + row * e.ldcin + col);
-        const uint4 c0 = c[0], c1 = c[1];
-        const float s = scale_value(e.sin[row * e.ldsin + col / kMxBlock]);
-        const uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+        uint32_t w[8];
+        load_codes(e.cin + row * e.ldcin + col, e.ldcin, lane, rows, block, w);
+        const float s = scale_value(e.sin[(row + min(lane, rows - 1)) * e.ldsin + col / kMxBlock]);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const float2 q = e4m3_values((w[i / 2] >> (16 * (i % 2))) & 0xffffu);
@@ -181,7 +240,7 @@ __device__ __forceinline__ void epilogue_row(const EpilogueArgs& e, int64_t row,
       });
     }
   }
-  store32(e.out + row * e.ldo + col, v);
+  store_tile(e.out + row * e.ldo + col, e.ldo, lane, rows, block, v);
 }
 
 // Where lane `lane`'s row of the 32 x 32 block at (row, col) keeps its partial
@@ -267,12 +326,12 @@ __device__ __forceinline__ void epilogue_columns(const EpilogueArgs& e, int64_t 
 template <int EPI>
 __device__ __forceinline__ void epilogue_block(const EpilogueArgs& e, int64_t row, int64_t col, int lane, float (&v)[32],
                                                float* block) {
+  const int n = (int)min((int64_t)32, e.rows - row);
   if (e.vec && col + 32 <= e.cols) {
-    if (row + lane < e.rows) epilogue_row<EPI>(e, row + lane, col, v);
+    epilogue_tile<EPI>(e, row, col, lane, n, reinterpret_cast<unsigned char*>(block), v);
     return;
   }
   const bool in = col + lane < e.cols;
-  const int n = (int)min((int64_t)32, e.rows - row);
   if constexpr (EPI == EPI_PLAIN) {
     uint32_t* words = reinterpret_cast<uint32_t*>(block);
 #pragma unroll
@@ -582,7 +641,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const EpilogueArgs e
     if (EPI == EPI_FORWARD && e.bias && in) bias = __bfloat162float(e.bias[col]);
     epilogue_columns<EPI>(e, row, 1, col, in, v, bias);
   } else {
-    __shared__ float blocks[kJoinThreads / 32][32 * 33];
+    __shared__ __align__(16) float blocks[kJoinThreads / 32][32 * 33];
     const int64_t row = i / across * 32, col = i % across * 32;
     if (row >= e.rows) return;
     float v[32] = {};

@@ -366,14 +366,20 @@ __device__ __forceinline__ float sigmoid(float t) {
 }
 
 // GELU, GELU_ERF and SILU are z * p(z) with p from 0 to 1; where p has come
-// down to 0 the product is 0 (not -inf * 0).
+// down to 0 the product is 0 (not -inf * 0).  FAST takes the normal distribution
+// from erf, exact to 2^-24 of 1, which is below bf16's step of z * p until z < -4
+// (where z * p is under 2^-12).
+template <bool FAST>
+__device__ __forceinline__ float normal_cdf(float z) {
+  return FAST ? fmaf(0.5f, erff(kInvSqrt2 * z), 0.5f) : 0.5f * erfcf(-kInvSqrt2 * z);
+}
 template <bool FAST>
 __device__ __forceinline__ float act_value(int act, float z) {
   float p;
   switch (act) {
     case TIDE_ACT_RELU: return z < 0.0f ? 0.0f : z;
     case TIDE_ACT_GELU: p = sigmoid<FAST>(2.0f * kGeluA * (z + kGeluB * z * z * z)); break;
-    case TIDE_ACT_GELU_ERF: p = 0.5f * erfcf(-kInvSqrt2 * z); break;
+    case TIDE_ACT_GELU_ERF: p = normal_cdf<FAST>(z); break;
     case TIDE_ACT_SILU: p = sigmoid<FAST>(z); break;
     default: return z;
   }
@@ -391,7 +397,7 @@ __device__ __forceinline__ float act_grad(int act, float z) {
       d = p * (1.0f - p);
       return d == 0.0f ? p : p + z * d * (2.0f * kGeluA * (1.0f + 3.0f * kGeluB * z * z));
     case TIDE_ACT_GELU_ERF:
-      p = 0.5f * erfcf(-kInvSqrt2 * z);
+      p = normal_cdf<FAST>(z);
       d = exp_of<FAST>(-0.5f * z * z);
       return d == 0.0f ? p : p + z * d * kInvSqrt2Pi;
     case TIDE_ACT_SILU:

@@ -392,6 +392,10 @@ tide_status column_sums(int64_t rows, int64_t cols, const bf16* x, int64_t ldx, 
   return cuda_status(cudaGetLastError(), "bias gradient");
 }
 
+bool codes_aligned(const uint8_t* codes, int64_t ld, int64_t rows) {
+  return (uintptr_t)codes % 8 == 0 && (rows <= 1 || ld % 8 == 0);
+}
+
 tide_status check_product(int64_t rows, int64_t inner, int64_t outer) {
   if (rows < 0 || inner < 0 || outer < 0) return fail(TIDE_ERR_INVALID_ARG, "linear: negative size");
   return TIDE_OK;
@@ -456,8 +460,8 @@ tide_status tide_linear(int64_t rows, int64_t inner, int64_t outer, const void* 
   e.out = (bf16*)y, e.ldo = ldy;
   e.z = (bf16*)z, e.ldz = ldz;
   e.codes = codes, e.ldc = ld_codes, e.scales = scales, e.lds = ld_scales;
-  e.vec = (uintptr_t)bias % 16 == 0 && rows_aligned(residual, ldr, 2, rows) && rows_aligned(y, ldy, 2, rows) &&
-          rows_aligned(z, ldz, 2, rows) && rows_aligned(codes, ld_codes, 1, rows);
+  e.vec = rows_aligned(residual, ldr, 2, rows) && rows_aligned(y, ldy, 2, rows) &&
+          rows_aligned(z, ldz, 2, rows) && codes_aligned(codes, ld_codes, rows);
   return product<EPI_FORWARD>(rows, outer, inner, {(const bf16*)x, rows, inner, ldx}, false,
                               {(const bf16*)w, outer, inner, ldw}, false, e, launch_forward, (unsigned char*)workspace, false,
                               (cudaStream_t)stream);
@@ -496,7 +500,7 @@ tide_status tide_linear_grad_input(int64_t rows, int64_t inner, int64_t outer, c
   e.cin = codes, e.ldcin = ld_codes, e.sin = scales, e.ldsin = ld_scales;
   e.out = (bf16*)dx, e.ldo = lddx;
   e.vec = rows_aligned(dx, lddx, 2, rows) &&
-          (act == TIDE_ACT_NONE || (z ? rows_aligned(z, ldz, 2, rows) : rows_aligned(codes, ld_codes, 1, rows)));
+          (act == TIDE_ACT_NONE || (z ? rows_aligned(z, ldz, 2, rows) : codes_aligned(codes, ld_codes, rows)));
   return product<EPI_GRAD_INPUT>(rows, inner, outer, {(const bf16*)dy, rows, outer, lddy}, false,
                                  {(const bf16*)w, outer, inner, ldw}, true, e, launch_grad_input,
                                  (unsigned char*)workspace, false, (cudaStream_t)stream);
