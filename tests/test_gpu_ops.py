@@ -625,17 +625,19 @@ def test_refusals():
 
 # ---------------------------------------------------------------- the pair-of-CTAs product, and bounded waits
 
-# rows, inner, outer.  On 152 SMs the forward and input-gradient products of the first four take tiles of 256 x 256;
-# then 256 x 128 and 256 x 128 in splits; 256 x 256, 256 x 256 in splits; 128 weight rows by 128 tokens, and in splits;
-# each with output rows that start on 16-byte boundaries and that do not.
+# rows, inner, outer.  On 152 SMs these, and BIG_SUMS, take every tile in each of the three products: whole and in
+# splits, with output rows that start on 16-byte boundaries and that do not.
 BIG = [(2100, 200, 3100), (4096, 520, 2304), (2049, 1030, 2570), (3333, 72, 4100),
        (2631, 8, 672), (3562, 3017, 191), (2546, 3468, 64), (2511, 9352, 137),
        (648, 1334, 3256), (413, 4204, 4927), (136, 8384, 5392), (145, 14426, 4894),
-       (1174, 8, 3607), (523, 272, 3576), (2756, 4663, 13), (68, 4624, 2256)]
+       (1174, 8, 3607), (523, 272, 3576), (2756, 4663, 13), (68, 4624, 2256), (1820, 1313, 687), (260, 1787, 5936),
+       (37, 509, 5413), (36, 5574, 504), (143, 994, 8), (141, 5416, 4683), (396, 2529, 4447), (309, 5816, 1236),
+       (210, 357, 24), (1, 425, 4715), (6, 622, 538), (10, 410, 488),
+       (163, 5343, 4824), (163, 5344, 4824)]
 # The same for the weight gradient, whose sum runs over the rows.
 BIG_SUMS = [(10, 152, 4912), (3314, 292, 3534), (2633, 4832, 64), (9352, 137, 2511), (3910, 2725, 841), (1300, 736, 3280),
             (8384, 5392, 136), (14426, 4894, 145), (8, 3790, 2253), (453, 4896, 384), (3799, 3353, 68), (4978, 3336, 72),
-            (750, 11, 9), (710, 8, 9), (16384, 520, 512)]
+            (750, 11, 9), (710, 8, 9), (16384, 520, 512), (1, 5255, 792), (143, 994, 8)]
 
 
 @pytest.mark.parametrize("rows,inner,outer", BIG_SUMS)
