@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_con
         __syncwarp();
         if (lane == 0) {
           if constexpr (CG == 2)
-            mbar_arrive_cluster(mapped_addr(smem_addr(acc_empty + acc), 0));
+            mbar_arrive_cluster_relaxed(mapped_addr(smem_addr(acc_empty + acc), 0));
           else
             mbar_arrive(acc_empty + acc);
         }

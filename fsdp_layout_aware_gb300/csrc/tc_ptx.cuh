@@ -30,8 +30,12 @@ __device__ __forceinline__ uint32_t mapped_addr(uint32_t addr, uint32_t rank) {
   return r;
 }
 
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+// Says that tensor memory has been read (tcgen05.wait::ld and the fence before a
+// thread's synchronisation come first, which order those reads).  Nothing else is
+// handed over, so it is relaxed: a release at this scope would wait until the
+// thread's stores to global memory have been seen, 1000 clocks and more a tile.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
 __device__ __forceinline__ void fence_mbar_init_cluster() {
