@@ -43,7 +43,9 @@ enum Epilogue { EPI_FORWARD, EPI_GRAD_INPUT, EPI_PLAIN, EPI_PARTIAL };
 struct EpilogueArgs {
   int64_t rows, cols;
   int32_t act;
-  bool vec;  // every bf16 matrix below has 16-byte aligned rows, codes 8-byte aligned ones (cols may still be odd)
+  // Bytes that every bf16 matrix's (16, 4 or 2) and checkpoint's (8, 4 or 1) rows
+  // are aligned to; cols may be odd all the same.
+  int32_t unit, code_unit;
   const bf16* bias;
   const bf16* residual;
   int64_t ldr;
@@ -86,11 +88,10 @@ constexpr int kTcK = 64;           // values of k a stage holds: 128 bytes, one 
 constexpr int kTcGroup = 8;        // tile rows walked together, for reuse of B in L2
 constexpr int kTcRoom = 227 * 1024;  // shared memory a CTA may take
 
-// A 32 x 32 block per epilogue warp, to be turned: fp32 (rows of 33), or, where
-// the values are only rounded and stored, bf16 (rows of 80 bytes), which leaves
-// the bias gradient's blocks room beside the weight gradient's.
-template <int EPI, bool SWAP>
-constexpr int kTurnBytes = EPI == EPI_PLAIN && !SWAP ? 32 * 80 : 32 * 33 * 4;
+// A 32 x 32 block per epilogue warp: bf16 to pass through, or, swapped, fp32 to be
+// turned (rows of 33).
+template <bool SWAP>
+constexpr int kBlockBytes = SWAP ? 32 * 33 * 4 : 32 * 64;
 
 template <int CG, int BN, int EPI, bool SWAP>
 struct TcShape {
@@ -98,7 +99,7 @@ struct TcShape {
   static constexpr int b_rows = BN / CG;
   static constexpr int b_bytes = b_rows * kTcK * 2;
   static constexpr int stage_bytes = a_bytes + b_bytes;
-  static constexpr int transpose_bytes = 8 * kTurnBytes<EPI, SWAP>;
+  static constexpr int transpose_bytes = 8 * kBlockBytes<SWAP>;
   static constexpr int columns = 2 * BN;                   // two accumulators
   static constexpr int fixed_bytes = 1024 + transpose_bytes + 512;
   static constexpr int stages = (kTcRoom - fixed_bytes) / stage_bytes < 12 ? (kTcRoom - fixed_bytes) / stage_bytes : 12;
@@ -107,106 +108,152 @@ struct TcShape {
 
 // ---- epilogues
 
-// A warp moves 32 x 32 blocks of a matrix with aligned rows through shared memory
-// (its `block`), so that a lane can hold a whole row of the block while global
-// memory sees neighbouring lanes on neighbouring words: 64 bytes (bf16) or 32
-// (codes) of a row by four or two lanes.  (A lane storing its own row touches 32
-// lines an instruction; 1788 x 13760 with a sum of 64 took 30 us that way.)
-// Staged rows are 80 and 48 bytes apart, which keeps both sides free of bank
-// conflicts.  Rows from `rows` on do not exist.
+// A warp moves 32 x 32 blocks of a matrix through shared memory (its `block`), so
+// that a lane can hold a whole row of the block while global memory sees
+// neighbouring lanes on neighbouring words: W bytes a lane, the ROW bytes of a
+// block's row by ROW / W lanes.  (A lane storing its own row touches 32 lines an
+// instruction: 1788 x 13760 with a sum of 64 took 30 us longer that way.)  The
+// staged rows' 16-byte words are permuted so that both sides are free of bank
+// conflicts.  Only the first `rows` rows and `bytes` bytes of each exist.
+template <int ROW>
+__device__ __forceinline__ int staged(int r, int b) {
+  return r * ROW + (b ^ ((r * ROW / 128 % (ROW / 16)) << 4));
+}
+template <int W>
+struct UnitOf;
+template <> struct UnitOf<16> { using type = uint4; };
+template <> struct UnitOf<8> { using type = uint2; };
+template <> struct UnitOf<4> { using type = uint32_t; };
+template <> struct UnitOf<2> { using type = uint16_t; };
+template <> struct UnitOf<1> { using type = uint8_t; };
 
-// Words of 16 bytes: `lanes` of a row by neighbouring lanes, row r at r * kRow.
-template <int LANES, int ROW, typename F>
-__device__ __forceinline__ void by_words(int lane, int rows, F&& f) {
+template <int ROW, int W>
+__device__ __forceinline__ void load_units(const unsigned char* p, int64_t ld, int lane, int rows, int bytes,
+                                           unsigned char* block) {
+  using Unit = typename UnitOf<W>::type;
+  constexpr int kLanes = ROW / W, kBatch = kLanes < 16 ? kLanes : 16;
+  const int b = lane % kLanes * W;
 #pragma unroll
-  for (int i = 0; i < LANES; ++i) {
-    const int r = i * (32 / LANES) + lane / LANES, q = lane % LANES;
-    if (r < rows) f(r, q, r * ROW + q * 16);
+  for (int j = 0; j < kLanes; j += kBatch) {
+    Unit u[kBatch];  // all on their way before the first is waited for
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int r = (j + i) * (32 / kLanes) + lane / kLanes;
+      u[i] = b < bytes && r < rows ? *reinterpret_cast<const Unit*>(p + r * ld + b) : Unit{};
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      *reinterpret_cast<Unit*>(block + staged<ROW>((j + i) * (32 / kLanes) + lane / kLanes, b)) = u[i];
   }
+  __syncwarp();
 }
 
-__device__ __forceinline__ void load_tile(const bf16* p, int64_t ld, int lane, int rows, unsigned char* block,
-                                          float (&v)[32]) {
-  by_words<4, 80>(lane, rows, [&](int r, int q, int at) {
-    *reinterpret_cast<uint4*>(block + at) = *reinterpret_cast<const uint4*>(p + r * ld + q * 8);
-  });
+template <int ROW, int W>
+__device__ __forceinline__ void store_units(unsigned char* p, int64_t ld, int lane, int rows, int bytes,
+                                            const unsigned char* block) {
+  using Unit = typename UnitOf<W>::type;
+  constexpr int kLanes = ROW / W;
+  const int b = lane % kLanes * W;
   __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kLanes; ++i) {
+    const int r = i * (32 / kLanes) + lane / kLanes;
+    const Unit u = *reinterpret_cast<const Unit*>(block + staged<ROW>(r, b));
+    if (b < bytes && r < rows) *reinterpret_cast<Unit*>(p + r * ld + b) = u;
+  }
+  __syncwarp();
+}
+
+// A 32 x 32 block of a bf16 matrix whose rows take units of `unit` bytes, `cols` of
+// its columns existing; lane l has row l.
+__device__ __forceinline__ void load_tile(const bf16* p, int64_t ld, int unit, int lane, int rows, int cols,
+                                          unsigned char* block, float (&v)[32]) {
+  const unsigned char* x = reinterpret_cast<const unsigned char*>(p);
+  if (unit == 16)
+    load_units<64, 16>(x, ld * 2, lane, rows, 64, block);
+  else if (unit == 4)
+    load_units<64, 4>(x, ld * 2, lane, rows, 64, block);
+  else
+    load_units<64, 2>(x, ld * 2, lane, rows, cols * 2, block);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float t[8];
-    load_vec<8>(reinterpret_cast<const bf16*>(block + lane * 80) + 8 * i, t);
+    load_vec<8>(reinterpret_cast<const bf16*>(block + staged<64>(lane, 16 * i)), t);
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[8 * i + k] = t[k];
   }
   __syncwarp();
 }
 
-__device__ __forceinline__ void store_tile(bf16* p, int64_t ld, int lane, int rows, unsigned char* block,
-                                           const float (&v)[32]) {
+__device__ __forceinline__ void store_tile(bf16* p, int64_t ld, int unit, int lane, int rows, int cols,
+                                           unsigned char* block, const float (&v)[32]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float t[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) t[k] = v[8 * i + k];
-    store_vec<8>(reinterpret_cast<bf16*>(block + lane * 80) + 8 * i, t);
+    store_vec<8>(reinterpret_cast<bf16*>(block + staged<64>(lane, 16 * i)), t);
   }
-  __syncwarp();
-  by_words<4, 80>(lane, rows, [&](int r, int q, int at) {
-    *reinterpret_cast<uint4*>(p + r * ld + q * 8) = *reinterpret_cast<const uint4*>(block + at);
-  });
-  __syncwarp();
+  unsigned char* x = reinterpret_cast<unsigned char*>(p);
+  if (unit == 16)
+    store_units<64, 16>(x, ld * 2, lane, rows, 64, block);
+  else if (unit == 4)
+    store_units<64, 4>(x, ld * 2, lane, rows, 64, block);
+  else
+    store_units<64, 2>(x, ld * 2, lane, rows, cols * 2, block);
 }
 
-// Codes, whose rows are aligned to 8 bytes.
-__device__ __forceinline__ void load_codes(const uint8_t* p, int64_t ld, int lane, int rows, unsigned char* block,
-                                           uint32_t (&w)[8]) {
-  by_words<2, 48>(lane, rows, [&](int r, int q, int at) {
-    const uint2* x = reinterpret_cast<const uint2*>(p + r * ld + q * 16);
-    const uint2 a = x[0], b = x[1];
-    *reinterpret_cast<uint4*>(block + at) = make_uint4(a.x, a.y, b.x, b.y);
-  });
-  __syncwarp();
-  const uint4* x = reinterpret_cast<const uint4*>(block + lane * 48);
-  const uint4 a = x[0], b = x[1];
+// The same for codes.
+__device__ __forceinline__ void load_codes(const uint8_t* p, int64_t ld, int unit, int lane, int rows, int cols,
+                                           unsigned char* block, uint32_t (&w)[8]) {
+  if (unit == 8)
+    load_units<32, 8>(p, ld, lane, rows, 32, block);
+  else if (unit == 4)
+    load_units<32, 4>(p, ld, lane, rows, 32, block);
+  else
+    load_units<32, 1>(p, ld, lane, rows, cols, block);
+  const uint4 a = *reinterpret_cast<const uint4*>(block + staged<32>(lane, 0));
+  const uint4 b = *reinterpret_cast<const uint4*>(block + staged<32>(lane, 16));
   w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
   __syncwarp();
 }
 
-__device__ __forceinline__ void store_codes(uint8_t* p, int64_t ld, int lane, int rows, unsigned char* block,
-                                            const uint32_t (&w)[8]) {
-  uint4* x = reinterpret_cast<uint4*>(block + lane * 48);
-  x[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  x[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  __syncwarp();
-  by_words<2, 48>(lane, rows, [&](int r, int q, int at) {
-    const uint4 t = *reinterpret_cast<const uint4*>(block + at);
-    uint2* y = reinterpret_cast<uint2*>(p + r * ld + q * 16);
-    y[0] = make_uint2(t.x, t.y);
-    y[1] = make_uint2(t.z, t.w);
-  });
-  __syncwarp();
+__device__ __forceinline__ void store_codes(uint8_t* p, int64_t ld, int unit, int lane, int rows, int cols,
+                                            unsigned char* block, const uint32_t (&w)[8]) {
+  *reinterpret_cast<uint4*>(block + staged<32>(lane, 0)) = make_uint4(w[0], w[1], w[2], w[3]);
+  *reinterpret_cast<uint4*>(block + staged<32>(lane, 16)) = make_uint4(w[4], w[5], w[6], w[7]);
+  if (unit == 8)
+    store_units<32, 8>(p, ld, lane, rows, 32, block);
+  else if (unit == 4)
+    store_units<32, 4>(p, ld, lane, rows, 32, block);
+  else
+    store_units<32, 1>(p, ld, lane, rows, cols, block);
 }
 
-// The 32 x 32 block of the output at (row, col), lane l holding its l-th row
-// (`rows` of them exist), a whole warp; every matrix's rows take whole vectors.
+// The 32 x 32 block of the output at (row, col), lane l holding its l-th row, a
+// whole warp; any alignment.
 template <int EPI>
-__device__ __forceinline__ void epilogue_tile(const EpilogueArgs& e, int64_t row, int64_t col, int lane, int rows,
+__device__ __forceinline__ void epilogue_tile(const EpilogueArgs& e, int64_t row, int64_t col, int lane,
                                               unsigned char* block, float (&v)[32]) {
+  const int rows = (int)min((int64_t)32, e.rows - row), cols = (int)min((int64_t)32, e.cols - col);
+  const int unit = cols == 32 ? e.unit : 2, code_unit = cols == 32 ? e.code_unit : 1;
   float t[32];
   if constexpr (EPI == EPI_FORWARD) {
     if (e.bias) {
-      const float mine = __bfloat162float(e.bias[col + lane]);
+      const float mine = lane < cols ? __bfloat162float(e.bias[col + lane]) : 0.0f;
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, mine, i);
     }
-    if (e.z) store_tile(e.z + row * e.ldz + col, e.ldz, lane, rows, block, v);
+    if (e.z) store_tile(e.z + row * e.ldz + col, e.ldz, unit, lane, rows, cols, block, v);
     if (e.codes) {
+      // Columns that do not exist are sums of zeros (or NaN, of a row with an
+      // infinity): neither counts for the scale.
 #pragma unroll
       for (int i = 0; i < 32; ++i) t[i] = v[i];
       const int byte = scale_byte(block_magnitude<1>(t));
       uint32_t w[8];
       encode(t, byte, w);
-      store_codes(e.codes + row * e.ldc + col, e.ldc, lane, rows, block, w);
+      store_codes(e.codes + row * e.ldc + col, e.ldc, code_unit, lane, rows, cols, block, w);
       if (lane < rows) e.scales[(row + lane) * e.lds + col / kMxBlock] = (uint8_t)byte;
     }
     with_act(e.act, [&](auto a) {
@@ -214,7 +261,7 @@ __device__ __forceinline__ void epilogue_tile(const EpilogueArgs& e, int64_t row
       for (int i = 0; i < 32; ++i) v[i] = act_value<true>(a.value, v[i]);
     });
     if (e.residual) {
-      load_tile(e.residual + row * e.ldr + col, e.ldr, lane, rows, block, t);
+      load_tile(e.residual + row * e.ldr + col, e.ldr, unit, lane, rows, cols, block, t);
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] += t[i];
     }
@@ -222,10 +269,10 @@ __device__ __forceinline__ void epilogue_tile(const EpilogueArgs& e, int64_t row
   if constexpr (EPI == EPI_GRAD_INPUT) {
     if (e.act != TIDE_ACT_NONE) {
       if (e.zin) {
-        load_tile(e.zin + row * e.ldzin + col, e.ldzin, lane, rows, block, t);
+        load_tile(e.zin + row * e.ldzin + col, e.ldzin, unit, lane, rows, cols, block, t);
       } else {
         uint32_t w[8];
-        load_codes(e.cin + row * e.ldcin + col, e.ldcin, lane, rows, block, w);
+        load_codes(e.cin + row * e.ldcin + col, e.ldcin, code_unit, lane, rows, cols, block, w);
         const float s = scale_value(e.sin[(row + min(lane, rows - 1)) * e.ldsin + col / kMxBlock]);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -240,7 +287,7 @@ __device__ __forceinline__ void epilogue_tile(const EpilogueArgs& e, int64_t row
       });
     }
   }
-  store_tile(e.out + row * e.ldo + col, e.ldo, lane, rows, block, v);
+  store_tile(e.out + row * e.ldo + col, e.ldo, unit, lane, rows, cols, block, v);
 }
 
 // Where lane `lane`'s row of the 32 x 32 block at (row, col) keeps its partial
@@ -318,43 +365,6 @@ __device__ __forceinline__ void epilogue_columns(const EpilogueArgs& e, int64_t 
 #pragma unroll
   for (int i = 0; i < N; ++i)
     if (in && i < n) e.out[(row + i) * e.ldo + col] = __float2bfloat16_rn(v[i]);
-}
-
-// A 32 x 32 block of the output at (row, col), lane l holding row l; any
-// alignment.  Where a row cannot take whole vectors it is turned in `block`
-// ([32][33], this warp's): lane l then has column l of each row.
-template <int EPI>
-__device__ __forceinline__ void epilogue_block(const EpilogueArgs& e, int64_t row, int64_t col, int lane, float (&v)[32],
-                                               float* block) {
-  const int n = (int)min((int64_t)32, e.rows - row);
-  if (e.vec && col + 32 <= e.cols) {
-    epilogue_tile<EPI>(e, row, col, lane, n, reinterpret_cast<unsigned char*>(block), v);
-    return;
-  }
-  const bool in = col + lane < e.cols;
-  if constexpr (EPI == EPI_PLAIN) {
-    uint32_t* words = reinterpret_cast<uint32_t*>(block);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) words[lane * 17 + i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-    __syncwarp();
-    const bf16* b = reinterpret_cast<const bf16*>(block);
-    bf16* out = e.out + row * e.ldo + col + lane;
-#pragma unroll 8
-    for (int r = 0; r < n; ++r)
-      if (in) out[r * e.ldo] = b[r * 34 + lane];
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) block[lane * 33 + i] = v[i];
-    __syncwarp();
-    float bias = 0.0f;
-    if (EPI == EPI_FORWARD && e.bias && in) bias = __bfloat162float(e.bias[col + lane]);
-    for (int r = 0; r < n; r += 8) {
-      float t[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] = block[(r + i) * 33 + lane];
-      epilogue_columns<EPI>(e, row + r, n - r, col + lane, in, t, bias);
-    }
-  }
 }
 
 // Brings into L2 what the epilogue of a lane's row (n columns from col) will
@@ -532,7 +542,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_con
     // Epilogue: warp w reads lanes 32 (w mod 4) onwards, one row of the tile a
     // lane; warps 4-7 take every other 32 columns, warps 8-11 the rest.
     const int quad = warp % 4, half = warp / 4 - 1;
-    float* block = reinterpret_cast<float*>(transpose + (warp - 4) * kTurnBytes<EPI, SWAP>);
+    unsigned char* block = transpose + (warp - 4) * kBlockBytes<SWAP>;
     int turn = 0;
     for (int u = first; u < units; u += step, ++turn) {
       const TileAt at = tile_at(p, u % tiles);
@@ -571,15 +581,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_con
           // Lane l has column a_row + l of the output in 32 rows: neighbouring
           // lanes on neighbouring elements.
           if (a_row >= e.cols || b_row >= e.rows) continue;
+          float* turned = reinterpret_cast<float*>(block);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) block[lane * 33 + i] = v[i];
+          for (int i = 0; i < 32; ++i) turned[lane * 33 + i] = v[i];
           __syncwarp();
           const int n = (int)min((int64_t)32, e.rows - b_row);
           const bool in = a_row + lane < e.cols;
           for (int r = 0; r < n; r += 8) {
             float t[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) t[i] = block[lane * 33 + r + i];
+            for (int i = 0; i < 8; ++i) t[i] = turned[lane * 33 + r + i];
             if constexpr (EPI == EPI_PARTIAL) {
               float* q = e.partial + (split * e.rows + b_row + r) * e.ldp + a_row + lane;
 #pragma unroll
@@ -596,7 +607,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_con
 #pragma unroll
             for (int i = 0; i < 8; ++i) q[32 * i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           } else {
-            epilogue_block<EPI>(e, a_row, b_row, lane, v, block);
+            epilogue_tile<EPI>(e, a_row, b_row, lane, block, v);
           }
         }
       }
@@ -641,7 +652,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const EpilogueArgs e
     if (EPI == EPI_FORWARD && e.bias && in) bias = __bfloat162float(e.bias[col]);
     epilogue_columns<EPI>(e, row, 1, col, in, v, bias);
   } else {
-    __shared__ __align__(16) float blocks[kJoinThreads / 32][32 * 33];
+    __shared__ __align__(128) unsigned char blocks[kJoinThreads / 32][kBlockBytes<false>];
     const int64_t row = i / across * 32, col = i % across * 32;
     if (row >= e.rows) return;
     float v[32] = {};
@@ -653,7 +664,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const EpilogueArgs e
         v[4 * k] += t.x, v[4 * k + 1] += t.y, v[4 * k + 2] += t.z, v[4 * k + 3] += t.w;
       }
     }
-    epilogue_block<EPI>(e, row, col, lane, v, blocks[threadIdx.x / 32]);
+    epilogue_tile<EPI>(e, row, col, lane, blocks[threadIdx.x / 32], v);
   }
 }
 

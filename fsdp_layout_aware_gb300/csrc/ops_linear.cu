@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <initializer_list>
 #include <utility>
 
 #include "gemm_tc.cuh"
@@ -292,7 +293,7 @@ tide_status product(int64_t m, int64_t n, int64_t k, Operand a, bool a_mn, Opera
   int splits = 0;
   bool swapped = true;
   if (k > 0) {
-    const Plan s = pick_plan(m, n, k, a_mn, e.vec, sms);
+    const Plan s = pick_plan(m, n, k, a_mn, e.unit == 16, sms);
     const TcTileShape ts = tile_shape(s.tile, a_mn);
     Operand* const both[2] = {&a, &b};
     TIDE_TRY(pack(both, &workspace, &after, stream));
@@ -399,8 +400,21 @@ tide_status column_sums(int64_t rows, int64_t cols, const bf16* x, int64_t ldx, 
   return cuda_status(cudaGetLastError(), "bias gradient");
 }
 
-bool codes_aligned(const uint8_t* codes, int64_t ld, int64_t rows) {
-  return (uintptr_t)codes % 8 == 0 && (rows <= 1 || ld % 8 == 0);
+// EpilogueArgs::unit of bf16 matrices (base, row stride; absent ones null), and
+// code_unit of a checkpoint's codes.
+struct Rows {
+  const void* p;
+  int64_t ld;
+};
+int32_t row_unit(std::initializer_list<Rows> matrices, int64_t rows) {
+  uintptr_t bits = 0;
+  for (const Rows& x : matrices)
+    if (x.p) bits |= (uintptr_t)x.p | (rows > 1 ? (uintptr_t)x.ld * 2 : 0);
+  return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
+}
+int32_t code_unit(const uint8_t* codes, int64_t ld, int64_t rows) {
+  const uintptr_t bits = (uintptr_t)codes | (rows > 1 ? (uintptr_t)ld : 0);
+  return bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : 1;
 }
 
 tide_status check_product(int64_t rows, int64_t inner, int64_t outer) {
@@ -467,8 +481,8 @@ tide_status tide_linear(int64_t rows, int64_t inner, int64_t outer, const void* 
   e.out = (bf16*)y, e.ldo = ldy;
   e.z = (bf16*)z, e.ldz = ldz;
   e.codes = codes, e.ldc = ld_codes, e.scales = scales, e.lds = ld_scales;
-  e.vec = rows_aligned(residual, ldr, 2, rows) && rows_aligned(y, ldy, 2, rows) &&
-          rows_aligned(z, ldz, 2, rows) && codes_aligned(codes, ld_codes, rows);
+  e.unit = row_unit({{residual, ldr}, {y, ldy}, {z, ldz}}, rows);
+  e.code_unit = code_unit(codes, ld_codes, rows);
   return product<EPI_FORWARD>(rows, outer, inner, {(const bf16*)x, rows, inner, ldx}, false,
                               {(const bf16*)w, outer, inner, ldw}, false, e, launch_forward, (unsigned char*)workspace, false,
                               (cudaStream_t)stream);
@@ -506,8 +520,8 @@ tide_status tide_linear_grad_input(int64_t rows, int64_t inner, int64_t outer, c
   e.zin = (const bf16*)z, e.ldzin = ldz;
   e.cin = codes, e.ldcin = ld_codes, e.sin = scales, e.ldsin = ld_scales;
   e.out = (bf16*)dx, e.ldo = lddx;
-  e.vec = rows_aligned(dx, lddx, 2, rows) &&
-          (act == TIDE_ACT_NONE || (z ? rows_aligned(z, ldz, 2, rows) : codes_aligned(codes, ld_codes, rows)));
+  e.unit = row_unit({{dx, lddx}, {act == TIDE_ACT_NONE ? nullptr : z, ldz}}, rows);
+  e.code_unit = code_unit(codes, ld_codes, rows);
   return product<EPI_GRAD_INPUT>(rows, inner, outer, {(const bf16*)dy, rows, outer, lddy}, false,
                                  {(const bf16*)w, outer, inner, ldw}, true, e, launch_grad_input,
                                  (unsigned char*)workspace, false, (cudaStream_t)stream);
@@ -563,7 +577,7 @@ tide_status tide_linear_grad_weight(int64_t rows, int64_t inner, int64_t outer, 
     }
     EpilogueArgs e{};
     e.out = (bf16*)dw, e.ldo = lddw;
-    e.vec = rows_aligned(dw, lddw, 2, outer);
+    e.unit = row_unit({{dw, lddw}}, outer);
     summed = groups > 0;
     TIDE_TRY(product<EPI_PLAIN>(outer, inner, rows, {(const bf16*)dy, rows, outer, lddy}, true, b, true, e,
                                 launch_grad_weight, at, !x && rows > 0, stream, summed ? &sums : nullptr));
