@@ -53,9 +53,9 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // joining of splits.  Clocks of a block of 64 of the sum, measured with every SM
 // at work (alone, the first two run at the tensor cores' rate, 512 and 256):
 // 570 on 256 x 256, 340 on 256 x 128, and 275 to 420 on the single CTA's tiles.
-// The epilogues' clocks are fitted to the times of 107 products of 1 to 8700 rows,
-// each with every tile and up to 16 splits; the plan they lead to took 3% longer
-// than the quickest one on average, at worst 1.5 times (11.6 us instead of 7.6).
+// The epilogues' clocks are fitted to the times of 84 products of 1 to 6000 rows,
+// each with every tile and up to 16 splits; the plan they lead to took 2% longer
+// than the quickest one on average, at worst 19% (16.6 us instead of 14.0).
 Plan choose_plan(int64_t m, int64_t n, int64_t k, bool a_mn, bool vec, int sms) {
   Plan best;
   double best_cost = 1e300;
@@ -74,22 +74,22 @@ Plan choose_plan(int64_t m, int64_t n, int64_t k, bool a_mn, bool vec, int sms) 
     // longer; `vec`: the output's rows take whole vectors.
     // A plain one (the weight gradient's) loads nothing and needs no activation.
     const int64_t rows = std::min<int64_t>(ceil_div(m, 8) * 8, ts.b);  // of a swapped tile
-    const double whole = a_mn ? 1900 + (ts.swap ? 11.0 * rows : (vec ? 7.0 : 8.0) * ts.b)
-                              : 2500 + (ts.swap ? 30.0 * rows : (vec ? 9.0 : 31.0) * ts.b);
+    const double whole = a_mn ? 550 + (ts.swap ? 18.0 * rows : (vec ? 7.0 : 11.0) * ts.b)
+                              : 1800 + (ts.swap ? 73.0 * rows : (vec ? 14.5 : 17.0) * ts.b);
     for (int64_t want = 1; want <= 32 && want <= std::max<int64_t>(1, kb / 4); ++want) {
       s.split_blocks = (int32_t)ceil_div(kb, want);
       s.splits = (int32_t)ceil_div(kb, s.split_blocks);
       if (s.splits != want) continue;  // the same split as a smaller number's
       if ((int64_t)s.tiles_a * s.tiles_b * s.splits > INT32_MAX / 2) continue;  // counted in 32 bits
       const double turns = (double)ceil_div((int64_t)s.tiles_a * s.tiles_b * s.splits, sms / ts.ctas);
-      const double epilogue = s.splits > 1 ? 8.0 * (ts.swap ? rows : ts.b) : whole;
+      const double epilogue = s.splits > 1 ? 5.0 * (ts.swap ? rows : ts.b) : whole;
       const double busy = turns * std::max(s.split_blocks * block + 300.0, epilogue);
       const double dram = (double)(m + n) * k * 2.0 / 3500.0;
       // Neither hides the other altogether; a last turn of few CTAs draws less.
       const double idle = 1.0 - (double)s.tiles_a * s.tiles_b * s.splits / (turns * (sms / ts.ctas));
       double cost = std::max(busy, dram * (1.0 + 0.3 * idle)) + 0.25 * std::min(busy, dram) + epilogue;
       s.partial_bytes = s.splits > 1 ? s.splits * (ts.swap ? m : ceil_div(m, 32) * 32) * s.ldp * 4 : 0;
-      if (s.splits > 1) cost += 2000.0 + (double)s.partial_bytes / 1000.0;
+      if (s.splits > 1) cost += 5000.0 + (double)s.partial_bytes / 2300.0;
       if (cost < best_cost) best = s, best_cost = cost;
     }
   }

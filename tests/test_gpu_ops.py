@@ -633,7 +633,7 @@ BIG = [(2100, 200, 3100), (4096, 520, 2304), (2049, 1030, 2570), (3333, 72, 4100
        (1174, 8, 3607), (523, 272, 3576), (2756, 4663, 13), (68, 4624, 2256), (1820, 1313, 687), (260, 1787, 5936),
        (37, 509, 5413), (36, 5574, 504), (143, 994, 8), (141, 5416, 4683), (396, 2529, 4447), (309, 5816, 1236),
        (210, 357, 24), (1, 425, 4715), (6, 622, 538), (10, 410, 488),
-       (163, 5343, 4824), (163, 5344, 4824)]
+       (163, 5343, 4824), (163, 5344, 4824), (806, 2688, 5240), (2930, 2726, 1587), (13, 4688, 33), (516, 3762, 2195)]
 # The same for the weight gradient, whose sum runs over the rows.
 BIG_SUMS = [(10, 152, 4912), (3314, 292, 3534), (2633, 4832, 64), (9352, 137, 2511), (3910, 2725, 841), (1300, 736, 3280),
             (8384, 5392, 136), (14426, 4894, 145), (8, 3790, 2253), (453, 4896, 384), (3799, 3353, 68), (4978, 3336, 72),
