@@ -40,6 +40,7 @@ struct NormArgs {
   int64_t ldc;
   uint8_t* scales;
   int64_t lds;
+  int64_t ahead;  // a row's threads ask for the row so many rows on; 0: for none
 };
 
 struct NormGradArgs {
@@ -122,6 +123,18 @@ __device__ __forceinline__ void store_staged(T* out, const T* staged, int cols, 
 // Shared memory of a staged row: whole vectors.
 __host__ __device__ inline int stage_room(int64_t cols, int elem) { return (int)((cols + 7) / 8 * 8 * elem); }
 
+// Asks for a row of x and of the residual to be brought to L2.
+template <typename T>
+__device__ __forceinline__ void prefetch_row(const NormArgs& a, int64_t row) {
+  auto span = [&](const void* matrix, int64_t ld) {
+    const T* p = (const T*)matrix + row * ld;
+    const uintptr_t from = ((uintptr_t)p + 15) / 16 * 16, end = (uintptr_t)(p + a.cols) / 16 * 16;
+    if (from < end) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"((uint32_t)(end - from)));
+  };
+  span(a.x, a.ldx);
+  if (a.residual) span(a.residual, a.ldr);
+}
+
 // A row takes blockDim.x threads, each NV vectors of eight columns; a block
 // holds blockDim.y rows.  ANY: rows of any alignment; h and y then leave through shared
 // memory.
@@ -139,6 +152,7 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a) {
   const int room = stage_room(cols, sizeof(T));
   T* const h_stage = reinterpret_cast<T*>(stage + t.y * 2 * room);
   T* const y_stage = reinterpret_cast<T*>(stage + t.y * 2 * room + room);
+  if (a.ahead && t.x == 0 && row < a.rows - a.ahead) prefetch_row<T>(a, row + a.ahead);
   float s[NV][8];
   float sum = 0.0f;
 #pragma unroll
@@ -685,7 +699,7 @@ tide_status launch(void (*kernel)(Params...), int64_t grid, dim3 threads, int sm
 }
 
 template <typename T>
-tide_status norm(const NormArgs& a, cudaStream_t stream) {
+tide_status norm(NormArgs a, cudaStream_t stream) {
   const bool vec = a.cols % 8 == 0 && rows_aligned(a.x, a.ldx, sizeof(T), a.rows) &&
                    rows_aligned(a.residual, a.ldr, sizeof(T), a.rows) && rows_aligned(a.h, a.ldh, sizeof(T), a.rows) &&
                    rows_aligned(a.y, a.ldy, sizeof(T), a.rows) && (uintptr_t)a.weight % 16 == 0 &&
@@ -695,6 +709,15 @@ tide_status norm(const NormArgs& a, cudaStream_t stream) {
   if (grid > INT32_MAX) return fail(TIDE_ERR_UNIMPLEMENTED, "too many rows for one launch");
   const dim3 block(s.threads, s.rows);
   const int stage = s.rows * 2 * stage_room(a.cols, sizeof(T));
+  // Rows are asked for kAheadBytes early: registers hold few rows, and those of
+  // bf16 are less than DRAM's latency asks for (8192 x 8192 62 us without, 50 with; with
+  // the residual and codes 101 and 91).  Where that is no further than the rows at
+  // work, or there are few rows, it does not help, and L2 does not hold 20 MB of rows
+  // to come beside the outputs (168 us became 185 for fp32 with the residual).
+  constexpr int64_t kAheadBytes = 10 << 20;
+  const int64_t at_work = (int64_t)ops_num_sms() * std::max(1, 1024 / (s.threads * s.rows)) * s.rows;
+  a.ahead = kAheadBytes / (a.cols * (int64_t)sizeof(T) * (a.residual ? 2 : 1));
+  if (a.ahead < at_work || a.rows < 4 * a.ahead) a.ahead = 0;
   tide_status st = TIDE_OK;
   with_forward_shape(s, [&](auto nv, auto threads) {
     st = vec ? launch(norm_kernel<T, nv(), false, threads()>, grid, block, 0, stream, "rms norm", a)
@@ -817,8 +840,8 @@ tide_status tide_rms_norm(int64_t rows, int64_t cols, int32_t dtype, const void*
   if (y) TIDE_TRY(check_matrix(y, rows, cols, ldy, e, "y"));
   if (rstd) TIDE_TRY(check_matrix(rstd, 1, rows, rows, 4, "rstd"));
   if (codes || scales) TIDE_TRY(check_checkpoint(codes, ld_codes, scales, ld_scales, rows, cols));
-  const NormArgs a{rows, cols, x,   ldx,  residual, ldr,      weight, eps,      h,
-                   ldh,  y,    ldy, rstd, codes,    ld_codes, scales, ld_scales};
+  const NormArgs a{rows, cols, x,   ldx,  residual, ldr,      weight, eps,       h,
+                   ldh,  y,    ldy, rstd, codes,    ld_codes, scales, ld_scales, 0};
   return dtype == TIDE_BF16 ? norm<bf16>(a, (cudaStream_t)stream) : norm<float>(a, (cudaStream_t)stream);
 }
 
