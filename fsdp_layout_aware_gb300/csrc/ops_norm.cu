@@ -5,11 +5,13 @@
 // operations per element, so they are bound by memory traffic; a row stays in
 // registers (forward) or in shared memory (backward) between its sum and its
 // outputs.
-//   forward, 16384 x 8192 bf16, residual added, y also in 8 bits (1.21 GB): 193 us,
-//   6.2 TB/s
+//   forward, 16384 x 8192 bf16, residual added, y also in 8 bits (1.21 GB): 180 us,
+//   6.7 TB/s
 //   backward, 8192 x 5120 bf16 from a checkpoint, dres added (294 MB): 46 us, 6.3
-//   TB/s, and 5 us to join dweight's partial sums; 4096 x 8192 fp32 70 us, 6.3 TB/s
-//   4999 x 4095 bf16, rows of odd alignment (164 and 144 MB): 56 and 68 us
+//   TB/s, and 5 us to join dweight's partial sums; 4096 x 8192 fp32 70 us, 6.3 TB/s;
+//   8192 x 14336 bf16 120 us, 5.9 TB/s
+//   4999 x 4095 bf16, rows of odd alignment (185 and 144 MB): 65 and 68 us, bound by
+//   their instructions
 
 #include <algorithm>
 #include <atomic>
@@ -123,16 +125,11 @@ __device__ __forceinline__ void store_staged(T* out, const T* staged, int cols, 
 // Shared memory of a staged row: whole vectors.
 __host__ __device__ inline int stage_room(int64_t cols, int elem) { return (int)((cols + 7) / 8 * 8 * elem); }
 
-// Asks for a row of x and of the residual to be brought to L2.
+// Asks for a row to be brought to L2.
 template <typename T>
-__device__ __forceinline__ void prefetch_row(const NormArgs& a, int64_t row) {
-  auto span = [&](const void* matrix, int64_t ld) {
-    const T* p = (const T*)matrix + row * ld;
-    const uintptr_t from = ((uintptr_t)p + 15) / 16 * 16, end = (uintptr_t)(p + a.cols) / 16 * 16;
-    if (from < end) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"((uint32_t)(end - from)));
-  };
-  span(a.x, a.ldx);
-  if (a.residual) span(a.residual, a.ldr);
+__device__ __forceinline__ void prefetch_l2(const T* row, int64_t cols) {
+  const uintptr_t from = ((uintptr_t)row + 15) / 16 * 16, end = (uintptr_t)(row + cols) / 16 * 16;
+  if (from < end) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"((uint32_t)(end - from)));
 }
 
 // A row takes blockDim.x threads, each NV vectors of eight columns; a block
@@ -152,7 +149,10 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a) {
   const int room = stage_room(cols, sizeof(T));
   T* const h_stage = reinterpret_cast<T*>(stage + t.y * 2 * room);
   T* const y_stage = reinterpret_cast<T*>(stage + t.y * 2 * room + room);
-  if (a.ahead && t.x == 0 && row < a.rows - a.ahead) prefetch_row<T>(a, row + a.ahead);
+  if (a.ahead && t.x == 0 && row < a.rows - a.ahead) {
+    prefetch_l2((const T*)a.x + (row + a.ahead) * a.ldx, cols);
+    if (a.residual) prefetch_l2((const T*)a.residual + (row + a.ahead) * a.ldr, cols);
+  }
   float s[NV][8];
   float sum = 0.0f;
 #pragma unroll
@@ -305,65 +305,6 @@ __device__ __forceinline__ float grad_vector(float (&n)[8], float (&g)[8], float
   return sum;
 }
 
-// Rows too long for the ring below, of any alignment, a block each (of several
-// warps); dx leaves through shared memory.
-template <typename T, int NV, int THREADS, int BLOCKS>
-__global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_any_kernel(const NormGradArgs a) {
-  extern __shared__ __align__(16) unsigned char stage[];
-  __shared__ float scratch[2][32];
-  int turn = 0;
-  const RowThread t = row_thread();
-  const int cols = (int)a.cols;
-  const float inv_cols = 1.0f / (float)cols;
-  float acc[NV][8] = {};
-  Kept8<T> w[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int col = (i * t.per_row + t.x) * 8;
-    w[i].load((const T*)a.weight + col, min(8, cols - col));
-  }
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const float rstd = a.rstd[row];
-    float n[NV][8] = {}, g[NV][8] = {};
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int col = (i * t.per_row + t.x) * 8;
-      if (col < cols) {
-        const int m = min(8, cols - col);
-        float to_n = rstd;
-        if (a.h) {
-          load_any8((const T*)a.h + row * a.ldh + col, m, n[i]);
-        } else {
-          decode8(load_codes_any(a.codes + row * a.ldc + col, m), 1.0f, n[i]);
-          to_n *= scale_value(a.scales[row * a.lds + col / kMxBlock]);
-        }
-        load_any8((const T*)a.dy + row * a.lddy + col, m, g[i]);
-        sum = grad_vector(n[i], g[i], to_n, w[i], acc[i], sum);
-      }
-    }
-    if (!a.dx) continue;
-    const float mean = row_sum(sum, t, scratch, turn) * inv_cols;
-    T* const out = (T*)a.dx + row * a.lddx;
-    T* const staged = reinterpret_cast<T*>(stage);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int col = (i * t.per_row + t.x) * 8;
-      if (col < cols) {
-        const int m = min(8, cols - col);
-        float d[8] = {};
-        if (a.dres) load_any8((const T*)a.dres + row * a.ldres + col, m, d);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) d[k] = fmaf(rstd, fmaf(-n[i][k], mean, g[i][k]), d[k]);
-        store_vec<8>(staged + col, d);
-      }
-    }
-    t.sync();
-    store_staged(out, staged, cols, t);
-  }
-  store_partial(a, t, 1, acc, nullptr);
-}
-
 // ---- the backward pass through a ring of rows
 //
 // DEPTH rows of every group lie in shared memory, copied there whole (dy, dres,
@@ -403,6 +344,7 @@ __device__ __forceinline__ uint32_t copy_row(unsigned char* to, const unsigned c
 struct RingArgs {
   NormGradArgs g;
   int32_t per_row, rows;
+  int32_t dres_passes;  // dres is read from where it is
   int32_t* status;
   uint64_t wait_limit_ns;
   int64_t test_drop;  // turn (counted per block) whose copies are withheld (tests); -1: none
@@ -434,9 +376,14 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_ring_kernel(const R
   __shared__ uint64_t full[DEPTH], empty[DEPTH];
   const NormGradArgs& a = p.g;
   constexpr int kElem = sizeof(T);
-  const bool has_dres = a.dres != nullptr;
+  // With so many threads registers are few: the row is read from its slot again when
+  // its mean is known (8192 x 14336 bf16 174 us without, 118 with).
+  constexpr bool kReload = THREADS > 288;
+  // Rows so long that dres may have no room in the ring.
+  constexpr bool kMayPass = kReload || (NV == 4 && ANY && !KEPT && kElem == 4);
+  const bool has_dres = a.dres != nullptr, ring_dres = has_dres && !(kMayPass && p.dres_passes);
   const int cols = (int)a.cols, rows = p.rows, workers = p.per_row * rows;
-  const RingRow part(cols, kElem, KEPT, has_dres);
+  const RingRow part(cols, kElem, KEPT, ring_dres);
   const int slot_bytes = rows * part.bytes;
   const int64_t step = (int64_t)gridDim.x * rows, first_row = (int64_t)blockIdx.x * rows;
 
@@ -462,7 +409,10 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_ring_kernel(const R
         bytes += copy_row(to + where, at, base, a.rows, n, ld, elem, withheld, bar);
       };
       one(AT_DY, a.dy, cols, a.lddy, kElem, part.dy);
-      if (has_dres) one(AT_DRES, a.dres, cols, a.ldres, kElem, part.dres);
+      if (ring_dres)
+        one(AT_DRES, a.dres, cols, a.ldres, kElem, part.dres);
+      else if (has_dres)
+        prefetch_l2((const T*)a.dres + row * a.ldres, cols);
       if constexpr (KEPT) {
         one(AT_H, a.codes, cols, a.ldc, 1, part.h);
         one(AT_SCALES, a.scales, (cols + kMxBlock - 1) / kMxBlock, a.lds, 1, part.scales);
@@ -507,6 +457,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_ring_kernel(const R
   // this one has rows in the first `mine`.
   const int mine = (int)((a.rows - (first_row + t.y) + step - 1) / step);
   T* dx = (T*)a.dx + (first_row + t.y) * a.lddx;
+  const T* dres = (const T*)a.dres + (first_row + t.y) * a.ldres;
   T* const staged = reinterpret_cast<T*>(ring + DEPTH * slot_bytes + t.y * stage_room(cols, kElem));  // ANY: dx
   int turn = 0, slot = 0;
   uint32_t phase = 0;
@@ -516,34 +467,41 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_ring_kernel(const R
     const int* at = reinterpret_cast<const int*>(from);
     if (!late && !mbar_wait_bounded(full + slot, phase, p.wait_limit_ns)) late = true;
     const bool here = !late && k < mine;  // nothing of a slot is read that did not come
-    float n[NV][8], g[NV][8];
+    float n[kReload ? 1 : NV][8], g[kReload ? 1 : NV][8];
     float sum = 0.0f, rstd = 0.0f;
     if (here) rstd = *reinterpret_cast<const float*>(from + at[AT_RSTD]);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) n[i][j] = g[i][j] = 0.0f;
-      const int col = col0 + i * apart;
-      if (!here || col >= cols) continue;
+    // h and dy of vector i, and what turns a value of h into n.
+    auto fetch = [&](int col, float (&n)[8], float (&g)[8]) {
       const T* dy = reinterpret_cast<const T*>(from + (ANY ? at[AT_DY] : part.dy)) + col;
       const unsigned char* h = from + (ANY || KEPT ? at[AT_H] : part.h) + col * (KEPT ? 1 : kElem);
-      float to_n = rstd;  // what turns a value of h into n
+      float to_n = rstd;
       if constexpr (KEPT) to_n *= scale_value(from[at[AT_SCALES] + col / kMxBlock]);
       if constexpr (ANY) {
         const int m = min(8, cols - col);
-        load_any8(dy, m, g[i]);
+        load_any8(dy, m, g);
         if constexpr (KEPT)
-          decode8(load_codes_any(h, m), 1.0f, n[i]);
+          decode8(load_codes_any(h, m), 1.0f, n);
         else
-          load_any8(reinterpret_cast<const T*>(h), m, n[i]);
+          load_any8(reinterpret_cast<const T*>(h), m, n);
       } else {
-        load_vec<8>(dy, g[i]);
+        load_vec<8>(dy, g);
         if constexpr (KEPT)
-          decode8(*reinterpret_cast<const uint2*>(h), 1.0f, n[i]);
+          decode8(*reinterpret_cast<const uint2*>(h), 1.0f, n);
         else
-          load_vec<8>(reinterpret_cast<const T*>(h), n[i]);
+          load_vec<8>(reinterpret_cast<const T*>(h), n);
       }
-      sum = grad_vector(n[i], g[i], to_n, w[i], acc[i], sum);
+      return to_n;
+    };
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float (&ni)[8] = n[kReload ? 0 : i];
+      float (&gi)[8] = g[kReload ? 0 : i];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ni[j] = gi[j] = 0.0f;
+      const int col = col0 + i * apart;
+      if (!here || col >= cols) continue;
+      const float to_n = fetch(col, ni, gi);
+      sum = grad_vector(ni, gi, to_n, w[i], acc[i], sum);
     }
     const float mean = row_sum(sum, t, scratch, turn) * inv_cols;
     if (a.dx) {
@@ -551,16 +509,29 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_ring_kernel(const R
       for (int i = 0; i < NV; ++i) {
         const int col = col0 + i * apart;
         if (!here || col >= cols) continue;
+        float (&ni)[8] = n[kReload ? 0 : i];
+        float (&gi)[8] = g[kReload ? 0 : i];
+        if constexpr (kReload) {
+          const float to_n = fetch(col, ni, gi);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) ni[j] *= to_n, gi[j] *= w[i].value(j);
+        }
         float d[8] = {};
-        if (has_dres) {
+        if (ring_dres) {
           const T* q = reinterpret_cast<const T*>(from + (ANY ? at[AT_DRES] : part.dres)) + col;
+          if constexpr (ANY)
+            load_any8(q, min(8, cols - col), d);
+          else
+            load_vec<8>(q, d);
+        } else if (kMayPass && has_dres) {
+          const T* q = dres + col;
           if constexpr (ANY)
             load_any8(q, min(8, cols - col), d);
           else
             load_vec<8>(q, d);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] = fmaf(rstd, fmaf(-n[i][j], mean, g[i][j]), d[j]);
+        for (int j = 0; j < 8; ++j) d[j] = fmaf(rstd, fmaf(-ni[j], mean, gi[j]), d[j]);
         if constexpr (ANY)
           store_vec<8>(staged + col, d);
         else
@@ -578,6 +549,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_ring_kernel(const R
       }
     }
     dx += step * a.lddx;
+    dres += step * a.ldres;
     if (++slot == DEPTH) slot = 0, phase ^= 1;
   }
   if (late) atomicOr(p.status, TIDE_DEVICE_TIMEOUT);
@@ -632,11 +604,14 @@ RowShape spread(int64_t cols, int nv) {
 RowShape forward_shape(int64_t cols) { return spread(cols, cols <= 2048 ? 1 : cols <= 8192 ? 2 : 4); }
 // Backward: the row's barrier and the latencies around it bind, so few threads
 // with much independent work each: four vectors beat two from 2048 columns on
-// (8192 x 5120 from a checkpoint 50 us against 63, 8192 x 8192 88 against 96).
+// (8192 x 5120 from a checkpoint 50 us against 63, 8192 x 8192 88 against 96).  More
+// than 16 warps, the copying one among them, leave a thread 96 registers, 16 leave it
+// 128 (8192 x 10240 bf16 96 us with 10 to 15 working warps, 130 in a kernel bounded
+// to 16); hence five vectors for the longest rows.
 RowShape backward_shape(int64_t cols) {
-  RowShape s = spread(cols, cols <= 512 ? 1 : cols <= 2048 ? 2 : 4);
-  if (s.nv == 4) s.rows = 1;
-  s.per_sm = s.nv == 1 ? 3 : s.nv == 2 || s.threads <= 160 ? 2 : 1;
+  RowShape s = spread(cols, cols <= 512 ? 1 : cols <= 2048 ? 2 : cols <= 480 * 32 ? 4 : 5);
+  if (s.nv >= 4) s.rows = 1;
+  s.per_sm = s.nv == 1 ? 3 : s.nv == 2 || (s.nv == 4 && s.threads <= 160) ? 2 : 1;
   return s;
 }
 
@@ -659,12 +634,14 @@ void with_backward_shape(const RowShape& s, F&& f) {
     f(Int<1>(), Int<256>(), Int<3>());
   else if (s.nv == 2)
     f(Int<2>(), Int<256>(), Int<2>());
+  else if (s.nv == 5)
+    f(Int<5>(), Int<416>(), Int<1>());
   else if (s.threads <= 160)
     f(Int<4>(), Int<160>(), Int<2>());
   else if (s.threads <= 256)
     f(Int<4>(), Int<256>(), Int<1>());
   else
-    f(Int<4>(), Int<512>(), Int<1>());
+    f(Int<4>(), Int<480>(), Int<1>());
 }
 
 // Raises a kernel's dynamic shared memory limit as far as it goes, once for each
@@ -749,33 +726,47 @@ tide_status norm_grad(NormGradArgs a, void* dweight, cudaStream_t stream) {
     const char* what = "rms norm backward";
     constexpr int kRoom = 208 * 1024;  // shared memory of an SM that rings may take
     const bool kept = !a.h;
-    const int stage = s.rows * stage_room(a.cols, sizeof(T));  // dx, where rows are not aligned
-    const int slot = s.rows * RingRow(a.cols, sizeof(T), kept, a.dres != nullptr).bytes, beside = vec ? 0 : stage;
-    // Four rows, or else two; a block that cannot have two goes without the
-    // ring.
-    const int depth = s.threads <= 256 && s.per_sm * (4 * slot + beside) <= kRoom ? 4 : 2 * slot + beside <= kRoom ? 2 : 0;
-    const int smem = depth ? depth * slot + beside : stage;
+    const int beside = vec ? 0 : s.rows * stage_room(a.cols, sizeof(T));  // dx, where rows are not aligned
+    auto fits = [&](int depth, bool with_dres) {
+      const int slot = s.rows * RingRow(a.cols, sizeof(T), kept, with_dres && a.dres).bytes;
+      const int smem = depth * slot + beside;
+      return smem * (depth == 4 ? s.per_sm : 1) <= kRoom ? smem : 0;
+    };
+    // Four rows in the ring, or two; without dres where two do not fit with it; one
+    // of fp32 rows that are too long for that (more than 13000 columns, h plain).
+    int depth = 4, smem = s.threads <= 256 ? fits(4, true) : 0;
+    if (!smem) depth = 2, smem = fits(2, true);
+    const bool passes = !smem;
+    if (!smem) smem = fits(2, false);
+    if (!smem) depth = 1, smem = fits(1, false);
     const int64_t blocks = grad_blocks(a.rows, s, std::max(1, std::min(s.per_sm, kRoom / smem)), sms);
     const int block = s.threads * s.rows;
     groups = blocks;
-    RingArgs r{a, s.threads, s.rows, nullptr, ops_wait_limit_ns(), ops_test_drop()};
-    if (depth) TIDE_TRY(ops_status_word(&r.status));
+    RingArgs r{a, s.threads, s.rows, passes, nullptr, ops_wait_limit_ns(), ops_test_drop()};
+    TIDE_TRY(ops_status_word(&r.status));
     with_backward_shape(s, [&](auto nv, auto threads, auto per_sm) {
       constexpr int kB = per_sm();
+      constexpr int kDeep = threads() > 256 ? 2 : 4;
       auto go = [&](auto d, auto any) {
-        constexpr int kD = threads() == 512 ? 2 : d();
+        constexpr int kD = d();
         constexpr bool kAny = any();
         constexpr int kT = threads() + 32;
         const int with_copies = block + 32;
-        st = kept ? launch(norm_grad_ring_kernel<T, nv(), kD, true, kAny, kT, kB>, blocks, with_copies, smem, stream, what, r)
-                  : launch(norm_grad_ring_kernel<T, nv(), kD, false, kAny, kT, kB>, blocks, with_copies, smem, stream, what, r);
+        if constexpr (kD > 1 || kAny) {  // two aligned rows with codes always fit
+          if (kept) {
+            st = launch(norm_grad_ring_kernel<T, nv(), kD, true, kAny, kT, kB>, blocks, with_copies, smem, stream, what, r);
+            return;
+          }
+        }
+        st = launch(norm_grad_ring_kernel<T, nv(), kD, false, kAny, kT, kB>, blocks, with_copies, smem, stream, what, r);
       };
-      if (depth == 0)
-        st = launch(norm_grad_any_kernel<T, nv(), threads(), kB>, blocks, s.threads, smem, stream, what, a);
-      else if (vec)
-        depth == 4 ? go(Int<4>(), std::false_type()) : go(Int<2>(), std::false_type());
-      else
-        depth == 4 ? go(Int<4>(), std::true_type()) : go(Int<2>(), std::true_type());
+      auto with_depth = [&](auto any) {
+        if constexpr (kDeep == 4 || sizeof(T) == 4) {  // two rows of bf16 always fit
+          if (depth < kDeep) return go(Int<kDeep / 2>(), any);
+        }
+        go(Int<kDeep>(), any);
+      };
+      vec ? with_depth(std::false_type()) : with_depth(std::true_type());
     });
   }
   if (st == TIDE_OK && dweight)

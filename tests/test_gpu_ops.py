@@ -230,7 +230,8 @@ def test_norm_keeps_bad_rows_to_themselves(cols):
 @pytest.mark.parametrize("dtype", [BF, FP])
 @pytest.mark.parametrize("kept", [False, True])
 @pytest.mark.parametrize("lead,extra", [(0, 0), (1, 3)])
-@pytest.mark.parametrize("rows,cols", NORM_SHAPES + [(2000, 96), (700, 1536)])
+@pytest.mark.parametrize("rows,cols", NORM_SHAPES + [(2000, 96), (700, 1536), (400, 8200), (310, 10239), (309, 14336),
+                                                         (305, 15361), (400, 16384)])
 def test_norm_backward(rows, cols, lead, extra, kept, dtype):
     h, dy, dres = rand((rows, cols), dtype, 1), rand((rows, cols), dtype, 2), rand((rows, cols), dtype, 3)
     w = 1 + 0.2 * rand((cols,), dtype, 4)
@@ -727,7 +728,8 @@ def test_a_wait_that_runs_out_is_reported(rows, inner, outer):
     assert torch.equal(y, want)
 
 
-@pytest.mark.parametrize("rows,cols,kept", [(4000, 1024, False), (3000, 2048, True), (2000, 333, True)])
+@pytest.mark.parametrize("rows,cols,kept", [(4000, 1024, False), (3000, 2048, True), (2000, 333, True), (900, 9000, False),
+                                            (900, 16383, True)])
 def test_a_copy_that_does_not_come_is_reported(rows, cols, kept):
     """The same for the norm's backward pass, whose rows are copied ahead."""
     h, dy = rand((rows, cols), BF, 1).to(DEV), rand((rows, cols), BF, 2).to(DEV)
