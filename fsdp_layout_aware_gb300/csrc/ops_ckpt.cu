@@ -5,7 +5,7 @@
 // per element, load reads 1 + 1/32 (and s for a gradient) and writes s.
 //   8192 x 13824 bf16 (343 MB each way): store 57 us, load 49 us, 6.0 and 7.0 TB/s
 //   4093 x 4095 bf16, rows of odd alignment, times a gradient through SiLU'
-//   (84 MB): 22 us, 3.8 TB/s; 31 instructions a value bind it there
+//   (84 MB): 21 us, 4.0 TB/s; 31 instructions a value bind it there
 
 #include <algorithm>
 
@@ -118,8 +118,9 @@ __device__ __forceinline__ void loaded(float (&v)[N], int act, bool has_grad, co
 
 // Eight neighbouring columns a thread and item; rows on 16-byte (out, grad)
 // and 8-byte (codes) boundaries.
+// Registers are bounded: one more than 48 costs a block an SM (60 us for 58).
 template <typename T, bool GRAD>
-__global__ void __launch_bounds__(kThreads) load_vec_kernel(const LoadArgs a) {
+__global__ void __launch_bounds__(kThreads, GRAD ? 3 : 5) load_vec_kernel(const LoadArgs a) {
   uint2 c[kItems];
   uint8_t s[kItems];
   float g[kItems][8];
@@ -150,9 +151,10 @@ __global__ void __launch_bounds__(kThreads) load_vec_kernel(const LoadArgs a) {
 
 // Any alignment: a thread takes the eight columns of an aligned word of out
 // (the row's first and last words may be partial), so that out is stored whole,
-// and grad read whole where it lies as out does.
+// and grad read whole where it lies as out does.  Full occupancy pays: 32 registers
+// 21 us, 34 22.5 (the ragged case above).
 template <typename T, bool GRAD>
-__global__ void __launch_bounds__(kThreads) load_any_kernel(const LoadArgs a) {
+__global__ void __launch_bounds__(kThreads, GRAD && sizeof(T) == 4 ? 6 : 8) load_any_kernel(const LoadArgs a) {
   const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
   if (i >= a.items) return;
   const int64_t row = a.per_row.quotient(i);
