@@ -17,13 +17,15 @@
 // word, and the CTA drains its copies, frees its tensor memory and returns.
 //
 // What binds it, measured:
-//   8192 x 5120 x 13824 with bias, GELU and an 8-bit z: 608 us from a cold start
-//   (1.91 PFLOP/s, tensor pipe 97% active), 690 us (1.68) in a long loop, where the
-//   power limit holds the clock near 1450 MHz; the input gradient 606 and 694 us,
-//   8192 x 28672 x 8192's weight gradient 2.0 and 2.2 ms
+//   8192 x 5120 x 13824 with bias, GELU and an 8-bit z: 600 to 609 us from a cold
+//   start, by the GPU (1.9 PFLOP/s, tensor pipe 97% active), 690 us (1.68) in a long
+//   loop, where the power limit holds the clock near 1450 MHz; the input gradient 598
+//   to 614 and 694 us, 8192 x 28672 x 8192's weight gradient 1.8 to 1.9 and 2.2 ms
 //   one token, 8192 -> 28672: 71 us, 6.6 TB/s of weights (DRAM)
+//   short sums, by their output: 24832 x 64 -> 10304 in 104 us, 4.9 TB/s (plain, a
+//   weight gradient's, 96 us, 5.3); rows of odd alignment 2.2 to 3.6 TB/s
 //   a block of 64 of the sum takes a pair 512 clocks on 256 x 256 and 260 on 256 x
-//   128 alone, 570 and 340 with all SMs drawing on L2; a single CTA 270 to 290
+//   128 alone, 570 and 340 with all SMs drawing on L2; a single CTA 270 to 420
 #pragma once
 
 #include <atomic>
@@ -83,7 +85,7 @@ struct TcArgs {
   int64_t test_drop;       // k block (counted per CTA) whose loads are withheld (tests); -1: none
 };
 
-constexpr int kTcThreads = 384;    // four warps as above, and eight for the epilogue
+constexpr int kTcThreads = 384;    // warps 0 to 3 as above, and eight for the epilogue
 constexpr int kTcK = 64;           // values of k a stage holds: 128 bytes, one swizzle row
 constexpr int kTcGroup = 8;        // tile rows walked together, for reuse of B in L2
 constexpr int kTcRoom = 227 * 1024;  // shared memory a CTA may take
@@ -112,7 +114,7 @@ struct TcShape {
 // that a lane can hold a whole row of the block while global memory sees
 // neighbouring lanes on neighbouring words: W bytes a lane, the ROW bytes of a
 // block's row by ROW / W lanes.  (A lane storing its own row touches 32 lines an
-// instruction: 1788 x 13760 with a sum of 64 took 30 us longer that way.)  The
+// instruction: 2235 x 2632 with a sum of 64 took 50 us that way, 19 this way.)  The
 // staged rows' 16-byte words are permuted so that both sides are free of bank
 // conflicts.  Only the first `rows` rows and `bytes` bytes of each exist.
 template <int ROW>

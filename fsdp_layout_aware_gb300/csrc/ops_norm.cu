@@ -5,8 +5,8 @@
 // operations per element, so they are bound by memory traffic; a row stays in
 // registers (forward) or in shared memory (backward) between its sum and its
 // outputs.
-//   forward, 16384 x 8192 bf16, residual added, y also in 8 bits (1.21 GB): 180 us,
-//   6.7 TB/s
+//   forward, 16384 x 8192 bf16, residual added, y also in 8 bits (1.21 GB): 175 us,
+//   6.9 TB/s
 //   backward, 8192 x 5120 bf16 from a checkpoint, dres added (294 MB): 46 us, 6.3
 //   TB/s, and 5 us to join dweight's partial sums; 4096 x 8192 fp32 70 us, 6.3 TB/s;
 //   8192 x 14336 bf16 120 us, 5.9 TB/s
