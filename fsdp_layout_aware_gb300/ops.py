@@ -172,6 +172,15 @@ def _act(act):
     return code
 
 
+def _torch_stream(stream, dev):
+    """The torch stream of a stream argument."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = _stream_of(stream)
+    # 0 and 1 name the legacy default stream, which no external stream can.
+    return torch.cuda.ExternalStream(handle, dev) if handle > 1 else torch.cuda.default_stream(dev)
+
+
 def _workspace(given, need, stream, dev):
     """(tensor that keeps it alive, address, bytes)."""
     if given is not None:
@@ -180,10 +189,13 @@ def _workspace(given, need, stream, dev):
         return given, given.data_ptr(), given.numel() * given.element_size()
     if need == 0:
         return None, None, 0
-    ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    if stream is not None:
-        # The block must not go to another call of the allocating stream while this one still uses it.
-        ws.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream))
+    if stream is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        # A block of the call's own stream.  One of the current stream's may have been freed while kernels queued there
+        # still use it, and nothing would make the given stream wait for those.
+        with torch.cuda.stream(_torch_stream(stream, dev)):
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
     return ws, ws.data_ptr(), need
 
 
