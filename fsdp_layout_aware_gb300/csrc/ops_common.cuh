@@ -354,32 +354,51 @@ __device__ __forceinline__ float exp_of(float t) {
   return r;
 }
 
-// 1 / (1 + exp(-t)): 0 at -inf (and where the exponential overflows), 1 at
-// +inf, NaN at NaN.
-template <bool FAST>
-__device__ __forceinline__ float sigmoid(float t) {
-  const float d = 1.0f + exp_of<FAST>(-t);
-  if constexpr (!FAST) return 1.0f / d;
+__device__ __forceinline__ float reciprocal_ftz(float d) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
   return r;
 }
 
-// GELU, GELU_ERF and SILU are z * p(z) with p from 0 to 1; where p has come
-// down to 0 the product is 0 (not -inf * 0).  FAST takes the normal distribution
-// from erf, exact to 2^-24 of 1, which is below bf16's step of z * p until z < -4
-// (where z * p is under 2^-12).
+// 1 / (1 + exp(-t)): 0 at -inf (and where the exponential overflows), 1 at
+// +inf, NaN at NaN.
 template <bool FAST>
-__device__ __forceinline__ float normal_cdf(float z) {
-  return FAST ? fmaf(0.5f, erff(kInvSqrt2 * z), 0.5f) : 0.5f * erfcf(-kInvSqrt2 * z);
+__device__ __forceinline__ float sigmoid(float t) {
+  const float d = 1.0f + exp_of<FAST>(-t);
+  return FAST ? reciprocal_ftz(d) : 1.0f / d;
 }
+
+// The normal distribution's p(z), and e = exp(-z^2 / 2).  FAST: for x = |z| and
+// t = 1 / (1 + 0.324 x) the ratio p(-x) / e is smooth in t and goes as 1 / x, so it is
+// t times a polynomial in t, here the one of degree 7 with the least largest error
+// relative to the ratio over all x >= 0 (found by linear programming): 2^-20.6, with
+// fp32's roundings below 2^-19.  Relative, because p alone, of z < 0, is what z * p
+// is made of: 0.5 + 0.5 erf(z / sqrt(2)) cancels there and has nothing left at -5.6.
+template <bool FAST>
+__device__ __forceinline__ float normal_cdf(float z, float& e) {
+  e = exp_of<FAST>(-0.5f * z * z);
+  if constexpr (!FAST) return 0.5f * erfcf(-kInvSqrt2 * z);
+  const float t = reciprocal_ftz(fmaf(0.324f, fabsf(z), 1.0f));
+  float q = fmaf(0.0340613537f, t, -0.11560633f);
+  q = fmaf(q, t, 0.0897367969f);
+  q = fmaf(q, t, 0.0238828231f);
+  q = fmaf(q, t, 0.0942828283f);
+  q = fmaf(q, t, 0.115103588f);
+  q = fmaf(q, t, 0.129282221f);
+  q = fmaf(q, t, 0.129257008f);
+  q *= t * e;
+  return z < 0.0f ? q : 1.0f - q;
+}
+
+// GELU, GELU_ERF and SILU are z * p(z) with p from 0 to 1; where p has come
+// down to 0 the product is 0 (not -inf * 0).
 template <bool FAST>
 __device__ __forceinline__ float act_value(int act, float z) {
-  float p;
+  float p, e;
   switch (act) {
     case TIDE_ACT_RELU: return z < 0.0f ? 0.0f : z;
     case TIDE_ACT_GELU: p = sigmoid<FAST>(2.0f * kGeluA * (z + kGeluB * z * z * z)); break;
-    case TIDE_ACT_GELU_ERF: p = normal_cdf<FAST>(z); break;
+    case TIDE_ACT_GELU_ERF: p = normal_cdf<FAST>(z, e); break;
     case TIDE_ACT_SILU: p = sigmoid<FAST>(z); break;
     default: return z;
   }
@@ -397,8 +416,7 @@ __device__ __forceinline__ float act_grad(int act, float z) {
       d = p * (1.0f - p);
       return d == 0.0f ? p : p + z * d * (2.0f * kGeluA * (1.0f + 3.0f * kGeluB * z * z));
     case TIDE_ACT_GELU_ERF:
-      p = normal_cdf<FAST>(z);
-      d = exp_of<FAST>(-0.5f * z * z);
+      p = normal_cdf<FAST>(z, d);
       return d == 0.0f ? p : p + z * d * kInvSqrt2Pi;
     case TIDE_ACT_SILU:
       p = sigmoid<FAST>(z);
@@ -413,15 +431,19 @@ struct ActTag {
   static constexpr int value = ACT;
 };
 // f called with the activation as a constant (not at all for none): one branch for
-// many elements.
+// many elements.  In this order, with GELU and ReLU expected, the bodies lie so that
+// none pays for another's: 1788 x 64 -> 13760 takes 21.1 us with ReLU, 26.7 with GELU,
+// 35.1 with its erf form and 25.5 with SiLU; from a switch 22.2, 29.1, 34.6 and 26.3.
 template <typename F>
 __device__ __forceinline__ void with_act(int act, F&& f) {
-  switch (act) {
-    case TIDE_ACT_RELU: f(ActTag<TIDE_ACT_RELU>()); break;
-    case TIDE_ACT_GELU: f(ActTag<TIDE_ACT_GELU>()); break;
-    case TIDE_ACT_GELU_ERF: f(ActTag<TIDE_ACT_GELU_ERF>()); break;
-    case TIDE_ACT_SILU: f(ActTag<TIDE_ACT_SILU>()); break;
-    default: break;
+  if (__builtin_expect(act == TIDE_ACT_GELU, 1)) {
+    f(ActTag<TIDE_ACT_GELU>());
+  } else if (__builtin_expect(act == TIDE_ACT_RELU, 1)) {
+    f(ActTag<TIDE_ACT_RELU>());
+  } else if (__builtin_expect(act == TIDE_ACT_GELU_ERF, 0)) {
+    f(ActTag<TIDE_ACT_GELU_ERF>());
+  } else if (__builtin_expect(act == TIDE_ACT_SILU, 0)) {
+    f(ActTag<TIDE_ACT_SILU>());
   }
 }
 

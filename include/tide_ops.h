@@ -46,7 +46,8 @@ typedef enum tide_dtype { TIDE_BF16 = 0, TIDE_F32 = 1 } tide_dtype;
  *   GELU_ERF  z * (1 + erf(z / sqrt(2))) / 2
  *   SILU      z / (1 + exp(-z))
  * At -inf the last three and their derivatives give 0, at +inf z and 1; NaN
- * stays NaN. */
+ * stays NaN.  Values and derivatives below 2^-119 in magnitude, where the
+ * exponentials leave fp32, may come out as 0. */
 typedef enum tide_act {
   TIDE_ACT_NONE = 0,
   TIDE_ACT_RELU = 1,
