@@ -341,6 +341,10 @@ __device__ __forceinline__ uint32_t copy_row(unsigned char* to, const unsigned c
   return n;
 }
 
+// Copies in flight are waited for so long, however short the limit on waits: a
+// millisecond is ample for them.
+constexpr uint64_t kDrainNs = 1000000;
+
 struct RingArgs {
   NormGradArgs g;
   int32_t per_row, rows;
@@ -437,11 +441,12 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_ring_kernel(const R
       issue(y, first_row + y + k * step, slot, k == p.test_drop);
       if (++slot == DEPTH) slot = 0;
     }
-    if (!ok) {  // the copies in flight land before the block leaves
-      atomicOr(p.status, TIDE_DEVICE_TIMEOUT);
-      for (int d = 0; d < DEPTH && d < k; ++d)
-        mbar_wait_bounded(full + d, (uint32_t)((k - d + DEPTH - 1) / DEPTH - 1) & 1, p.wait_limit_ns);
-    }
+    if (!ok) atomicOr(p.status, TIDE_DEVICE_TIMEOUT);
+    // What was asked for lands before the block, and its shared memory, is gone: also
+    // where the threads that compute have given up and wait for nothing more.
+    const uint64_t limit = p.wait_limit_ns > kDrainNs ? p.wait_limit_ns : kDrainNs;
+    for (int d = 0; d < DEPTH && d < k; ++d)
+      mbar_wait_bounded(full + d, (uint32_t)((k - d + DEPTH - 1) / DEPTH - 1) & 1, limit);
     return;
   }
 
