@@ -13,8 +13,8 @@
 // ring of shared-memory stages with TMA; warp 1 (of the first CTA of a pair)
 // issues the matrix instructions; warps 4-11 take a finished accumulator out of
 // tensor memory and run the epilogue while the next tile accumulates in the
-// other half.  Every wait is bounded: a wait that runs out sets the status
-// word, and the CTA drains its copies, frees its tensor memory and returns.
+// other half.  Every wait is bounded: a wait that runs out is
+// counted, and the CTA drains its copies, frees its tensor memory and returns.
 //
 // What binds it, measured:
 //   8192 x 5120 x 13824 with bias, GELU and an 8-bit z: 600 to 609 us from a cold
@@ -79,7 +79,7 @@ struct TcArgs {
   int32_t k_blocks;        // of 64, over the whole sum
   int32_t split_blocks;    // k blocks of one split (all of them without splitting)
   int32_t splits;
-  int32_t* status;
+  uint32_t* timeouts;
   uint64_t wait_limit_ns;
   bool beside;             // runs beside the kernel before it, whose results it does not read
   int64_t test_drop;       // k block (counted per CTA) whose loads are withheld (tests); -1: none
@@ -617,7 +617,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_con
   }
   // This kernel is not done before the one beside it is.
   if (p.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!ok && lane == 0) atomicOr(p.status, TIDE_DEVICE_TIMEOUT);
+  if (!ok && lane == 0) atomicAdd(p.timeouts, 1u);
   __syncwarp();
   tc_fence_before();
   if constexpr (CG == 2)

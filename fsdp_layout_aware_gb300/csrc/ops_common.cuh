@@ -71,9 +71,9 @@ inline bool rows_aligned(const void* p, int64_t ld, int64_t elem, int64_t rows) 
 tide_status launch_sum_groups(const float* partial, int64_t groups, int64_t cols, int32_t dtype, void* out, bool after,
                               cudaStream_t stream);
 
-// The current device's status word (TIDE_DEVICE_TIMEOUT: a wait ran out; read by
-// tide_ops_check) and the bound on every wait.
-tide_status ops_status_word(int32_t** word);
+// The current device's count of waits that ran out (read by tide_ops_check) and the
+// bound on every wait.
+tide_status ops_timeouts(uint32_t** word);
 uint64_t ops_wait_limit_ns();
 int64_t ops_test_drop();  // TIDE_OPS_OPT_TEST_DROP_LOAD
 

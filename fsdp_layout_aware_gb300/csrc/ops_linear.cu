@@ -17,8 +17,9 @@ tide_status launch_checkpoint_load_bf16(int64_t rows, int64_t cols, const uint8_
 
 namespace {
 
-// Set where an operator's kernel gave up a wait (tide_ops_check).
-__device__ int32_t g_status;
+// Raised where an operator's kernel gives up a wait.  It only grows, so that no
+// check takes a report from another: each remembers what it saw (tide_ops_check).
+__device__ uint32_t g_timeouts;
 std::atomic<int64_t> g_wait_limit_ns{2000000000};
 std::atomic<int64_t> g_test_drop{-1};
 
@@ -286,8 +287,8 @@ tide_status product(int64_t m, int64_t n, int64_t k, Operand a, bool a_mn, Opera
                     const Beside* beside = nullptr) {
   const int sms = ops_num_sms();
   if (sms <= 0) return fail(TIDE_ERR_CUDA, "the current device could not be queried");
-  int32_t* status = nullptr;
-  TIDE_TRY(ops_status_word(&status));
+  uint32_t* timeouts = nullptr;
+  TIDE_TRY(ops_timeouts(&timeouts));
   TIDE_TRY(check_extent(m, n, k));
   e.rows = m, e.cols = n;
   int splits = 0;
@@ -309,7 +310,7 @@ tide_status product(int64_t m, int64_t n, int64_t k, Operand a, bool a_mn, Opera
     p.e = e;
     p.tiles_a = s.tiles_a, p.tiles_b = s.tiles_b;
     p.k_blocks = s.k_blocks, p.split_blocks = s.split_blocks, p.splits = s.splits;
-    p.status = status;
+    p.timeouts = timeouts;
     p.wait_limit_ns = ops_wait_limit_ns();
     p.test_drop = ops_test_drop();
     const int64_t units = (int64_t)s.tiles_a * s.tiles_b * s.splits;
@@ -431,14 +432,14 @@ tide_status check_workspace(const void* workspace, int64_t bytes, int64_t need) 
 
 }  // namespace
 
-tide_status ops_status_word(int32_t** word) {
-  static std::atomic<int32_t*> known[64];
+tide_status ops_timeouts(uint32_t** word) {
+  static std::atomic<uint32_t*> known[64];
   int dev = -1;
   TIDE_TRY(cuda_status(cudaGetDevice(&dev), "cudaGetDevice"));
   if (dev < 64 && (*word = known[dev].load(std::memory_order_relaxed))) return TIDE_OK;
   void* p = nullptr;
-  TIDE_TRY(cuda_status(cudaGetSymbolAddress(&p, g_status), "cudaGetSymbolAddress"));
-  *word = (int32_t*)p;
+  TIDE_TRY(cuda_status(cudaGetSymbolAddress(&p, g_timeouts), "cudaGetSymbolAddress"));
+  *word = (uint32_t*)p;
   if (dev < 64) known[dev].store(*word, std::memory_order_relaxed);
   return TIDE_OK;
 }
@@ -589,16 +590,19 @@ tide_status tide_linear_grad_weight(int64_t rows, int64_t inner, int64_t outer, 
 
 tide_status tide_ops_check(void) {
   clear_error();
-  int32_t* word = nullptr;
-  TIDE_TRY(ops_status_word(&word));
-  cudaError_t err = cudaDeviceSynchronize();
-  int32_t got = 0;
-  if (err == cudaSuccess) err = cudaMemcpy(&got, word, sizeof got, cudaMemcpyDeviceToHost);
-  if (err == cudaSuccess && got) err = cudaMemset(word, 0, sizeof got);
-  TIDE_TRY(cuda_status(err, "reading the operators' status word"));
-  if (got & TIDE_DEVICE_TIMEOUT)
-    return fail(TIDE_ERR_TIMEOUT, "an operator's kernel gave up a bounded wait; its outputs are undefined");
-  return TIDE_OK;
+  static thread_local uint32_t seen[64];
+  int dev = 0;
+  uint32_t* word = nullptr;
+  TIDE_TRY(ops_timeouts(&word));
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err == cudaSuccess) err = cudaDeviceSynchronize();
+  uint32_t count = 0;
+  if (err == cudaSuccess) err = cudaMemcpy(&count, word, sizeof count, cudaMemcpyDeviceToHost);
+  TIDE_TRY(cuda_status(err, "reading the operators' count of timeouts"));
+  uint32_t& last = seen[std::min(dev, 63)];
+  if (count == last) return TIDE_OK;
+  last = count;
+  return fail(TIDE_ERR_TIMEOUT, "an operator's kernel gave up a bounded wait; its outputs are undefined");
 }
 
 tide_status tide_ops_set_option(int32_t option, int64_t value) {

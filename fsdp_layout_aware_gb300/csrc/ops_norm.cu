@@ -349,7 +349,7 @@ struct RingArgs {
   NormGradArgs g;
   int32_t per_row, rows;
   int32_t dres_passes;  // dres is read from where it is
-  int32_t* status;
+  uint32_t* timeouts;
   uint64_t wait_limit_ns;
   int64_t test_drop;  // turn (counted per block) whose copies are withheld (tests); -1: none
 };
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_ring_kernel(const R
       issue(y, first_row + y + k * step, slot, k == p.test_drop);
       if (++slot == DEPTH) slot = 0;
     }
-    if (!ok) atomicOr(p.status, TIDE_DEVICE_TIMEOUT);
+    if (!ok) atomicAdd(p.timeouts, 1u);
     // What was asked for lands before the block, and its shared memory, is gone: also
     // where the threads that compute have given up and wait for nothing more.
     const uint64_t limit = p.wait_limit_ns > kDrainNs ? p.wait_limit_ns : kDrainNs;
@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_ring_kernel(const R
     dres += step * a.ldres;
     if (++slot == DEPTH) slot = 0, phase ^= 1;
   }
-  if (late) atomicOr(p.status, TIDE_DEVICE_TIMEOUT);
+  if (late) atomicAdd(p.timeouts, 1u);
   store_partial(a, t, rows, acc, reinterpret_cast<float*>(ring));
 }
 
@@ -748,7 +748,7 @@ tide_status norm_grad(NormGradArgs a, void* dweight, cudaStream_t stream) {
     const int block = s.threads * s.rows;
     groups = blocks;
     RingArgs r{a, s.threads, s.rows, passes, nullptr, ops_wait_limit_ns(), ops_test_drop()};
-    TIDE_TRY(ops_status_word(&r.status));
+    TIDE_TRY(ops_timeouts(&r.timeouts));
     with_backward_shape(s, [&](auto nv, auto threads, auto per_sm) {
       constexpr int kB = per_sm();
       constexpr int kDeep = threads() > 256 ? 2 : 4;

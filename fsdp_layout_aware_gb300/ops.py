@@ -200,7 +200,8 @@ def _workspace(given, need, stream, dev):
 
 
 def tide_ops_check():
-    """Synchronise and raise TideError(TIDE_ERR_TIMEOUT) if an operator's kernel gave up a wait on this device."""
+    """Synchronise and raise TideError(TIDE_ERR_TIMEOUT) if an operator's kernel gave up a wait on this device since this
+    thread's last check of it."""
     _check(_lib.tide_ops_check())
 
 

@@ -57,8 +57,10 @@ typedef enum tide_act {
 } tide_act;
 
 /* Synchronise the current device and report whether a kernel of these operators
- * gave up a bounded wait there since the last check (TIDE_ERR_TIMEOUT; the flag
- * is then cleared).  Such a call's outputs are undefined.  Errors: CUDA. */
+ * gave up a bounded wait there (TIDE_ERR_TIMEOUT) since the calling thread's last
+ * check of that device, or since the library was loaded if this is its first.
+ * Every thread that checks learns of it, whichever thread made the call.  Such a
+ * call's outputs are undefined.  Errors: CUDA. */
 tide_status tide_ops_check(void);
 
 /* Process-wide options.

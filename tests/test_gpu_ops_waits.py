@@ -1,6 +1,8 @@
 """Bounded waits of the training-block operators that run out: what is reported,
 and that the calls after it are right."""
 
+import concurrent.futures
+
 import pytest
 import torch
 
@@ -83,3 +85,41 @@ def test_a_limit_that_no_copy_meets(rows, cols, kept):
         except tide.TideError as e:
             assert e.status == 8
         assert all(torch.equal(t, w) for t, w in zip(outs, want))
+
+
+def product():
+    x, w, y = randn(64, 4096, seed=1), randn(256, 4096, seed=2), torch.empty(64, 256, dtype=BF, device=DEV)
+    return lambda: tide.tide_linear(x, w, y)
+
+
+def status_of(f):
+    try:
+        f()
+    except tide.TideError as e:
+        return e.status
+    return 0
+
+
+@pytest.mark.parametrize("first", ["caller", "other"])
+def test_every_thread_that_checks_learns_of_a_timeout(first):
+    """Whichever checks first, the thread that made the call or another, takes no report from the other."""
+    run = product()
+    with concurrent.futures.ThreadPoolExecutor(1) as pool:
+        def other():
+            return pool.submit(status_of, tide.tide_ops_check).result()
+
+        other(), status_of(tide.tide_ops_check)  # what earlier calls left
+        assert (other(), status_of(tide.tide_ops_check)) == (0, 0)
+        with options(20_000_000, 2):
+            run()
+        if first == "caller":
+            got = [status_of(tide.tide_ops_check), other()]
+        else:
+            got = [other(), status_of(tide.tide_ops_check)]
+        assert got == [8, 8]
+        assert (other(), status_of(tide.tide_ops_check)) == (0, 0)
+        with options(20_000_000, 2):
+            pool.submit(run).result()
+        assert (status_of(tide.tide_ops_check), other()) == (8, 8)
+        run()
+        assert (status_of(tide.tide_ops_check), other()) == (0, 0)
