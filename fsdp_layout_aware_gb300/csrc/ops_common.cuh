@@ -75,7 +75,7 @@ tide_status launch_sum_groups(const float* partial, int64_t groups, int64_t cols
 // bound on every wait.
 tide_status ops_timeouts(uint32_t** word);
 uint64_t ops_wait_limit_ns();
-int64_t ops_test_drop();  // TIDE_OPS_OPT_TEST_DROP_LOAD
+int64_t ops_test_drop();  // the calling thread's TIDE_OPS_OPT_TEST_DROP_LOAD
 
 // SMs of the current device (asked once per device); 0 if the query failed.
 int ops_num_sms();

@@ -21,7 +21,7 @@ namespace {
 // check takes a report from another: each remembers what it saw (tide_ops_check).
 __device__ uint32_t g_timeouts;
 std::atomic<int64_t> g_wait_limit_ns{2000000000};
-std::atomic<int64_t> g_test_drop{-1};
+thread_local int64_t g_test_drop = -1;
 
 // One operand: `rows` rows of `cols` contiguous elements.
 struct Operand {
@@ -445,7 +445,7 @@ tide_status ops_timeouts(uint32_t** word) {
 }
 
 uint64_t ops_wait_limit_ns() { return (uint64_t)g_wait_limit_ns.load(std::memory_order_relaxed); }
-int64_t ops_test_drop() { return g_test_drop.load(std::memory_order_relaxed); }
+int64_t ops_test_drop() { return g_test_drop; }
 
 }  // namespace tide
 
@@ -614,7 +614,7 @@ tide_status tide_ops_set_option(int32_t option, int64_t value) {
       return TIDE_OK;
     case TIDE_OPS_OPT_TEST_DROP_LOAD:
       if (value < -1) return fail(TIDE_ERR_INVALID_ARG, "the load to withhold must be -1 or more");
-      g_test_drop.store(value);
+      g_test_drop = value;
       return TIDE_OK;
     default: return fail(TIDE_ERR_INVALID_ARG, "unknown option");
   }

@@ -63,10 +63,12 @@ typedef enum tide_act {
  * call's outputs are undefined.  Errors: CUDA. */
 tide_status tide_ops_check(void);
 
-/* Process-wide options.
+/* Options.
  *   TIDE_OPS_OPT_WAIT_LIMIT_NS   bound, in nanoseconds, on every wait inside
- *                                the operators' kernels (default 2e9)
- *   TIDE_OPS_OPT_TEST_DROP_LOAD  test hook: a product's CTAs withhold the
+ *                                the operators' kernels (default 2e9), for the
+ *                                whole process
+ *   TIDE_OPS_OPT_TEST_DROP_LOAD  test hook, for the calling thread's own calls
+ *                                alone: a product's CTAs withhold the
  *                                loads of the given block of 64 of the summed
  *                                axis, and the norm's backward pass the
  *                                copies of the given turn of rows (counted per

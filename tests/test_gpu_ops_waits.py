@@ -104,22 +104,39 @@ def status_of(f):
 def test_every_thread_that_checks_learns_of_a_timeout(first):
     """Whichever checks first, the thread that made the call or another, takes no report from the other."""
     run = product()
+
+    def withheld():
+        with options(20_000_000, 2):
+            run()
+
     with concurrent.futures.ThreadPoolExecutor(1) as pool:
         def other():
             return pool.submit(status_of, tide.tide_ops_check).result()
 
         other(), status_of(tide.tide_ops_check)  # what earlier calls left
         assert (other(), status_of(tide.tide_ops_check)) == (0, 0)
-        with options(20_000_000, 2):
-            run()
+        withheld()
         if first == "caller":
             got = [status_of(tide.tide_ops_check), other()]
         else:
             got = [other(), status_of(tide.tide_ops_check)]
         assert got == [8, 8]
         assert (other(), status_of(tide.tide_ops_check)) == (0, 0)
-        with options(20_000_000, 2):
-            pool.submit(run).result()
+        pool.submit(withheld).result()
         assert (status_of(tide.tide_ops_check), other()) == (8, 8)
         run()
         assert (status_of(tide.tide_ops_check), other()) == (0, 0)
+
+
+def test_a_withheld_load_is_the_calling_threads_own():
+    """The test hook set in one thread leaves another thread's products and norms alone."""
+    outs, run = norm_gradient(700, 2048, False)
+    run()
+    product()()
+    status_of(tide.tide_ops_check)
+    with concurrent.futures.ThreadPoolExecutor(1) as pool, options(20_000_000, 1):
+        pool.submit(run).result()
+        pool.submit(product()).result()
+        assert status_of(tide.tide_ops_check) == 0
+        product()()
+        assert status_of(tide.tide_ops_check) == 8
