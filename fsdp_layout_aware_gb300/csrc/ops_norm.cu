@@ -123,7 +123,7 @@ __device__ __forceinline__ void store_staged(T* out, const T* staged, int cols, 
   for (int c = t.x; c < cols; c += t.per_row) out[c] = staged[c];
 }
 // Shared memory of a staged row: whole vectors.
-__host__ __device__ inline int stage_room(int64_t cols, int elem) { return (int)((cols + 7) / 8 * 8 * elem); }
+__host__ __device__ constexpr int stage_room(int64_t cols, int elem) { return (int)((cols + 7) / 8 * 8 * elem); }
 
 // Asks for a row to be brought to L2.
 template <typename T>
@@ -355,22 +355,20 @@ struct RingArgs {
 };
 
 // A row in the ring, with room for its phase within 16 bytes.
-__host__ __device__ inline int ring_room(int64_t cols, int elem) { return (int)((cols * elem + 15) / 16 * 16) + 16; }
+__host__ __device__ constexpr int ring_room(int64_t cols, int elem) { return (int)((cols * elem + 15) / 16 * 16) + 16; }
 
 // A row's part of a slot: where each of the others lies in it, with its phase
 // (five words), then dy, dres, h or codes, scales and rstd.
 enum RingPart { AT_DY, AT_DRES, AT_H, AT_SCALES, AT_RSTD };
 struct RingRow {
   int dy, dres, h, scales, rstd, bytes;
-  __host__ __device__ RingRow(int64_t cols, int elem, bool kept, bool has_dres) {
-    const int full = ring_room(cols, elem);
-    dy = 32;
-    dres = dy + full;
-    h = dres + (has_dres ? full : 0);
-    scales = h + (kept ? ring_room(cols, 1) : full);
-    rstd = scales + (kept ? ring_room((cols + kMxBlock - 1) / kMxBlock, 1) : 0);
-    bytes = rstd + 32;
-  }
+  __host__ __device__ constexpr RingRow(int64_t cols, int elem, bool kept, bool has_dres)
+      : dy(32),
+        dres(dy + ring_room(cols, elem)),
+        h(dres + (has_dres ? ring_room(cols, elem) : 0)),
+        scales(h + ring_room(cols, kept ? 1 : elem)),
+        rstd(scales + (kept ? ring_room((cols + kMxBlock - 1) / kMxBlock, 1) : 0)),
+        bytes(rstd + 32) {}
 };
 
 template <typename T, int NV, int DEPTH, bool KEPT, bool ANY, int THREADS, int BLOCKS>
@@ -599,7 +597,7 @@ __global__ void __launch_bounds__(1024) sum_groups_kernel(const float* __restric
 struct RowShape {
   int nv, threads, rows, per_sm;
 };
-RowShape spread(int64_t cols, int nv) {
+constexpr RowShape spread(int64_t cols, int nv) {
   const int64_t each = (int64_t)nv * 8 * 32;
   const int threads = (int)((cols + each - 1) / each * 32);
   return {nv, threads, std::max(1, 256 / threads), 1};
@@ -613,11 +611,51 @@ RowShape forward_shape(int64_t cols) { return spread(cols, cols <= 2048 ? 1 : co
 // than 16 warps, the copying one among them, leave a thread 96 registers, 16 leave it
 // 128 (8192 x 10240 bf16 96 us with 10 to 15 working warps, 130 in a kernel bounded
 // to 16); hence five vectors for the longest rows.
-RowShape backward_shape(int64_t cols) {
+constexpr RowShape backward_shape(int64_t cols) {
   RowShape s = spread(cols, cols <= 512 ? 1 : cols <= 2048 ? 2 : cols <= 480 * 32 ? 4 : 5);
   if (s.nv >= 4) s.rows = 1;
   s.per_sm = s.nv == 1 ? 3 : s.nv == 2 || (s.nv == 4 && s.threads <= 160) ? 2 : 1;
   return s;
+}
+
+// The ring of a call: its depth and the shared memory it takes, dx's staged rows
+// included; whether dres is left out of it.
+struct Ring {
+  int depth, smem;
+  bool passes;
+};
+constexpr int kRingRoom = 208 * 1024;  // shared memory of an SM that rings may take
+
+// Four rows, or two; without dres where two do not fit with it; one of fp32 rows that
+// are too long for that (h plain: from 13304 columns, or 10641 if rows are not
+// aligned; h from a checkpoint: from 15129 if not aligned).
+constexpr Ring ring_of(const RowShape& s, int64_t cols, int elem, bool kept, bool any, bool has_dres) {
+  const int beside = any ? s.rows * stage_room(cols, elem) : 0;
+  for (int depth = s.threads <= 256 ? 4 : 2; depth > 0; depth /= 2) {
+    for (const bool with_dres : {true, false}) {
+      if (!with_dres && depth == 4) continue;
+      if (with_dres && depth == 1) continue;
+      const int smem = depth * s.rows * RingRow(cols, elem, kept, with_dres && has_dres).bytes + beside;
+      if (smem * (depth == 4 ? s.per_sm : 1) <= kRingRoom) return {depth, smem, has_dres && !with_dres};
+    }
+  }
+  return {0, 0, false};
+}
+
+// Whether some row of NV vectors and more than LEAST, at most MOST threads has a ring
+// of so many rows.  For each number of threads: its shortest row takes the deepest,
+// its longest the shallowest.
+constexpr bool ring_taken(int nv, int least, int most, int elem, bool kept, bool any, int depth) {
+  for (int threads = least + 32; threads <= most; threads += 32) {
+    const int64_t longest = (int64_t)threads * nv * 8 < kMaxCols ? (int64_t)threads * nv * 8 : kMaxCols;
+    const int64_t shortest = (int64_t)(threads - 32) * nv * 8 + (any ? 1 : 8);
+    const RowShape s = backward_shape(longest), t = backward_shape(shortest);
+    if (s.nv != nv || t.nv != nv || s.threads != threads || t.threads != threads) continue;
+    if (ring_of(s, longest, elem, kept, any, true).depth <= depth &&
+        depth <= ring_of(t, shortest, elem, kept, any, false).depth)
+      return true;
+  }
+  return false;
 }
 
 template <int N>
@@ -633,20 +671,21 @@ void with_forward_shape(const RowShape& s, F&& f) {
   else
     f(Int<4>(), Int<512>());
 }
+// Here also the fewest threads a row, less one warp.
 template <typename F>
 void with_backward_shape(const RowShape& s, F&& f) {
   if (s.nv == 1)
-    f(Int<1>(), Int<256>(), Int<3>());
+    f(Int<1>(), Int<0>(), Int<256>(), Int<3>());
   else if (s.nv == 2)
-    f(Int<2>(), Int<256>(), Int<2>());
+    f(Int<2>(), Int<0>(), Int<256>(), Int<2>());
   else if (s.nv == 5)
-    f(Int<5>(), Int<416>(), Int<1>());
+    f(Int<5>(), Int<0>(), Int<416>(), Int<1>());
   else if (s.threads <= 160)
-    f(Int<4>(), Int<160>(), Int<2>());
+    f(Int<4>(), Int<0>(), Int<160>(), Int<2>());
   else if (s.threads <= 256)
-    f(Int<4>(), Int<256>(), Int<1>());
+    f(Int<4>(), Int<160>(), Int<256>(), Int<1>());
   else
-    f(Int<4>(), Int<480>(), Int<1>());
+    f(Int<4>(), Int<256>(), Int<480>(), Int<1>());
 }
 
 // Raises a kernel's dynamic shared memory limit as far as it goes, once for each
@@ -729,50 +768,28 @@ tide_status norm_grad(NormGradArgs a, void* dweight, cudaStream_t stream) {
   if (a.rows > 0) {
     const RowShape s = backward_shape(a.cols);
     const char* what = "rms norm backward";
-    constexpr int kRoom = 208 * 1024;  // shared memory of an SM that rings may take
     const bool kept = !a.h;
-    const int beside = vec ? 0 : s.rows * stage_room(a.cols, sizeof(T));  // dx, where rows are not aligned
-    auto fits = [&](int depth, bool with_dres) {
-      const int slot = s.rows * RingRow(a.cols, sizeof(T), kept, with_dres && a.dres).bytes;
-      const int smem = depth * slot + beside;
-      return smem * (depth == 4 ? s.per_sm : 1) <= kRoom ? smem : 0;
-    };
-    // Four rows in the ring, or two; without dres where two do not fit with it; one
-    // of fp32 rows that are too long for that (more than 13000 columns, h plain).
-    int depth = 4, smem = s.threads <= 256 ? fits(4, true) : 0;
-    if (!smem) depth = 2, smem = fits(2, true);
-    const bool passes = !smem;
-    if (!smem) smem = fits(2, false);
-    if (!smem) depth = 1, smem = fits(1, false);
-    const int64_t blocks = grad_blocks(a.rows, s, std::max(1, std::min(s.per_sm, kRoom / smem)), sms);
-    const int block = s.threads * s.rows;
+    const Ring ring = ring_of(s, a.cols, sizeof(T), kept, !vec, a.dres != nullptr);
+    const int64_t blocks = grad_blocks(a.rows, s, std::max(1, std::min(s.per_sm, kRingRoom / ring.smem)), sms);
+    const int with_copies = s.threads * s.rows + 32;
     groups = blocks;
-    RingArgs r{a, s.threads, s.rows, passes, nullptr, ops_wait_limit_ns(), ops_test_drop()};
+    RingArgs r{a, s.threads, s.rows, ring.passes, nullptr, ops_wait_limit_ns(), ops_test_drop()};
     TIDE_TRY(ops_timeouts(&r.timeouts));
-    with_backward_shape(s, [&](auto nv, auto threads, auto per_sm) {
-      constexpr int kB = per_sm();
-      constexpr int kDeep = threads() > 256 ? 2 : 4;
-      auto go = [&](auto d, auto any) {
-        constexpr int kD = d();
-        constexpr bool kAny = any();
-        constexpr int kT = threads() + 32;
-        const int with_copies = block + 32;
-        if constexpr (kD > 1 || kAny) {  // two aligned rows with codes always fit
-          if (kept) {
-            st = launch(norm_grad_ring_kernel<T, nv(), kD, true, kAny, kT, kB>, blocks, with_copies, smem, stream, what, r);
-            return;
-          }
+    bool built = false;
+    with_backward_shape(s, [&](auto nv, auto least, auto most, auto per_sm) {
+      auto go = [&](auto d, auto k, auto any) {
+        if constexpr (ring_taken(nv(), least(), most(), sizeof(T), k(), any(), d())) {
+          if (ring.depth != d() || kept != k() || vec == any()) return;
+          built = true;
+          st = launch(norm_grad_ring_kernel<T, nv(), d(), k(), any(), most() + 32, per_sm()>, blocks, with_copies, ring.smem,
+                      stream, what, r);
         }
-        st = launch(norm_grad_ring_kernel<T, nv(), kD, false, kAny, kT, kB>, blocks, with_copies, smem, stream, what, r);
       };
-      auto with_depth = [&](auto any) {
-        if constexpr (kDeep == 4 || sizeof(T) == 4) {  // two rows of bf16 always fit
-          if (depth < kDeep) return go(Int<kDeep / 2>(), any);
-        }
-        go(Int<kDeep>(), any);
-      };
-      vec ? with_depth(std::false_type()) : with_depth(std::true_type());
+      auto depths = [&](auto k, auto any) { go(Int<4>(), k, any), go(Int<2>(), k, any), go(Int<1>(), k, any); };
+      depths(std::false_type(), std::false_type()), depths(std::false_type(), std::true_type());
+      depths(std::true_type(), std::false_type()), depths(std::true_type(), std::true_type());
     });
+    if (!built) return fail(TIDE_ERR_UNIMPLEMENTED, "rms norm backward: no kernel for rows of this length");
   }
   if (st == TIDE_OK && dweight)
     st = launch_sum_groups(a.partial, groups, a.cols, sizeof(T) == 2 ? TIDE_BF16 : TIDE_F32, dweight, groups > 0, stream);
