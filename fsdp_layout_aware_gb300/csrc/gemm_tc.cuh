@@ -39,7 +39,7 @@ enum Epilogue { EPI_FORWARD, EPI_GRAD_INPUT, EPI_PLAIN, EPI_PARTIAL };
 
 // What becomes of a sum v at (row, col):
 //   FORWARD      v += bias; z, and its checkpoint, get v; out = f(v) + residual
-//   GRAD_INPUT   out = v * f'(kept z)
+//   GRAD_INPUT   out = v * f'(kept z), or v with no activation
 //   PLAIN        out = v
 //   PARTIAL      v in fp32 to partial[split], for join_kernel
 struct EpilogueArgs {
@@ -234,7 +234,7 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int64_t ld, int unit, in
 
 // The 32 x 32 block of the output at (row, col), lane l holding its l-th row, a
 // whole warp; any alignment.
-template <int EPI>
+template <int EPI, int ACT>
 __device__ __forceinline__ void epilogue_tile(const EpilogueArgs& e, int64_t row, int64_t col, int lane,
                                               unsigned char* block, float (&v)[32]) {
   const int rows = (int)min((int64_t)32, e.rows - row), cols = (int)min((int64_t)32, e.cols - col);
@@ -258,36 +258,30 @@ __device__ __forceinline__ void epilogue_tile(const EpilogueArgs& e, int64_t row
       store_codes(e.codes + row * e.ldc + col, e.ldc, code_unit, lane, rows, cols, block, w);
       if (lane < rows) e.scales[(row + lane) * e.lds + col / kMxBlock] = (uint8_t)byte;
     }
-    with_act(e.act, [&](auto a) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = act_value<true>(a.value, v[i]);
-    });
+    for (int i = 0; i < 32; ++i) v[i] = act_value<true>(ACT, v[i]);
     if (e.residual) {
       load_tile(e.residual + row * e.ldr + col, e.ldr, unit, lane, rows, cols, block, t);
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] += t[i];
     }
   }
-  if constexpr (EPI == EPI_GRAD_INPUT) {
-    if (e.act != TIDE_ACT_NONE) {
-      if (e.zin) {
-        load_tile(e.zin + row * e.ldzin + col, e.ldzin, unit, lane, rows, cols, block, t);
-      } else {
-        uint32_t w[8];
-        load_codes(e.cin + row * e.ldcin + col, e.ldcin, code_unit, lane, rows, cols, block, w);
-        const float s = scale_value(e.sin[(row + min(lane, rows - 1)) * e.ldsin + col / kMxBlock]);
+  if constexpr (EPI == EPI_GRAD_INPUT && ACT != TIDE_ACT_NONE) {
+    if (e.zin) {
+      load_tile(e.zin + row * e.ldzin + col, e.ldzin, unit, lane, rows, cols, block, t);
+    } else {
+      uint32_t w[8];
+      load_codes(e.cin + row * e.ldcin + col, e.ldcin, code_unit, lane, rows, cols, block, w);
+      const float s = scale_value(e.sin[(row + min(lane, rows - 1)) * e.ldsin + col / kMxBlock]);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 q = e4m3_values((w[i / 2] >> (16 * (i % 2))) & 0xffffu);
-          t[2 * i] = q.x * s;
-          t[2 * i + 1] = q.y * s;
-        }
+      for (int i = 0; i < 16; ++i) {
+        const float2 q = e4m3_values((w[i / 2] >> (16 * (i % 2))) & 0xffffu);
+        t[2 * i] = q.x * s;
+        t[2 * i + 1] = q.y * s;
       }
-      with_act(e.act, [&](auto a) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] *= act_grad<true>(a.value, t[i]);
-      });
     }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] *= act_grad<true>(ACT, t[i]);
   }
   store_tile(e.out + row * e.ldo + col, e.ldo, unit, lane, rows, cols, block, v);
 }
@@ -304,7 +298,7 @@ __device__ __forceinline__ float4* partial_block(const EpilogueArgs& e, int spli
 // The rows' steps are independent, and what they load is loaded whether or not it
 // exists (from the nearest place that does): behind a branch each load would be
 // waited for by itself.
-template <int EPI, int N>
+template <int EPI, int ACT, int N>
 __device__ __forceinline__ void epilogue_columns(const EpilogueArgs& e, int64_t row, int n, int64_t col, bool in,
                                                  float (&v)[N], float bias) {
   const int64_t c = in ? col : e.cols - 1;  // where to load from
@@ -333,36 +327,30 @@ __device__ __forceinline__ void epilogue_columns(const EpilogueArgs& e, int64_t 
 #pragma unroll
       for (int i = 0; i < N; ++i) r[i] = __bfloat162float(e.residual[(row + min(i, n - 1)) * e.ldr + c]);
     }
-    with_act(e.act, [&](auto a) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = act_value<true>(a.value, v[i]);
-    });
+    for (int i = 0; i < N; ++i) v[i] = act_value<true>(ACT, v[i]);
     if (e.residual) {
 #pragma unroll
       for (int i = 0; i < N; ++i) v[i] += r[i];
     }
   }
-  if constexpr (EPI == EPI_GRAD_INPUT) {
-    if (e.act != TIDE_ACT_NONE) {
-      float z[N] = {};
-      if (e.zin) {
+  if constexpr (EPI == EPI_GRAD_INPUT && ACT != TIDE_ACT_NONE) {
+    float z[N] = {};
+    if (e.zin) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) z[i] = __bfloat162float(e.zin[(row + min(i, n - 1)) * e.ldzin + c]);
-      } else {
-        uint8_t code[N], scale[N];
+      for (int i = 0; i < N; ++i) z[i] = __bfloat162float(e.zin[(row + min(i, n - 1)) * e.ldzin + c]);
+    } else {
+      uint8_t code[N], scale[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          code[i] = e.cin[(row + min(i, n - 1)) * e.ldcin + c];
-          scale[i] = e.sin[(row + min(i, n - 1)) * e.ldsin + c / kMxBlock];
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) z[i] = e4m3_values(code[i]).x * scale_value(scale[i]);
+      for (int i = 0; i < N; ++i) {
+        code[i] = e.cin[(row + min(i, n - 1)) * e.ldcin + c];
+        scale[i] = e.sin[(row + min(i, n - 1)) * e.ldsin + c / kMxBlock];
       }
-      with_act(e.act, [&](auto a) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] *= act_grad<true>(a.value, z[i]);
-      });
+      for (int i = 0; i < N; ++i) z[i] = e4m3_values(code[i]).x * scale_value(scale[i]);
     }
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] *= act_grad<true>(ACT, z[i]);
   }
 #pragma unroll
   for (int i = 0; i < N; ++i)
@@ -371,7 +359,7 @@ __device__ __forceinline__ void epilogue_columns(const EpilogueArgs& e, int64_t 
 
 // Brings into L2 what the epilogue of a lane's row (n columns from col) will
 // read.
-template <int EPI>
+template <int EPI, int ACT>
 __device__ __forceinline__ void prefetch_row(const EpilogueArgs& e, int64_t row, int64_t col, int n) {
   if (row >= e.rows) return;
   auto lines = [&](const void* from, int64_t bytes) {
@@ -380,7 +368,7 @@ __device__ __forceinline__ void prefetch_row(const EpilogueArgs& e, int64_t row,
   };
   const int64_t m = min((int64_t)n, e.cols - col);
   if (EPI == EPI_FORWARD && e.residual) lines(e.residual + row * e.ldr + col, m * 2);
-  if (EPI == EPI_GRAD_INPUT && e.act != TIDE_ACT_NONE) {
+  if (EPI == EPI_GRAD_INPUT && ACT != TIDE_ACT_NONE) {
     if (e.zin)
       lines(e.zin + row * e.ldzin + col, m * 2);
     else
@@ -403,7 +391,7 @@ __device__ __forceinline__ TileAt tile_at(const TcArgs& p, int t) {
   return {first + i % height, i / height};
 }
 
-template <int CG, int BN, bool A_MN, bool B_MN, int EPI, bool SWAP>
+template <int CG, int BN, bool A_MN, bool B_MN, int EPI, int ACT, bool SWAP>
 __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_constant__ TcArgs p) {
   using Shape = TcShape<CG, BN, EPI, SWAP>;
   constexpr int kStages = Shape::stages;
@@ -553,7 +541,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_con
       const int64_t a_row = (int64_t)(at.a * CG + (int)rank) * 128 + quad * 32;  // lane 0's row of A
       const EpilogueArgs& e = p.e;
       if constexpr (!SWAP) {
-        if (half == 0 && (int64_t)at.b * BN < e.cols) prefetch_row<EPI>(e, a_row + lane, (int64_t)at.b * BN, BN);
+        if (half == 0 && (int64_t)at.b * BN < e.cols) prefetch_row<EPI, ACT>(e, a_row + lane, (int64_t)at.b * BN, BN);
       }
       ok = warp_wait_bounded(acc_full + acc, (turn >> 1) & 1, p.wait_limit_ns);
       if (!ok) break;
@@ -599,7 +587,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_con
               for (int i = 0; i < 8; ++i)
                 if (r + i < n) q[i * e.ldp] = t[i];
             } else {
-              epilogue_columns<EPI>(e, b_row + r, n - r, a_row + lane, in, t, lane_bias);
+              epilogue_columns<EPI, ACT>(e, b_row + r, n - r, a_row + lane, in, t, lane_bias);
             }
           }
         } else {
@@ -609,7 +597,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_con
 #pragma unroll
             for (int i = 0; i < 8; ++i) q[32 * i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           } else {
-            epilogue_tile<EPI>(e, a_row, b_row, lane, block, v);
+            epilogue_tile<EPI, ACT>(e, a_row, b_row, lane, block, v);
           }
         }
       }
@@ -635,7 +623,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemm_tc_kernel(const __grid_con
 // Otherwise a warp takes a block of 32 x 32.
 constexpr int kJoinThreads = 128;
 
-template <int EPI, bool SWAP>
+template <int EPI, int ACT, bool SWAP>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const EpilogueArgs e, int splits) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x % 32;
@@ -652,7 +640,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const EpilogueArgs e
       for (int s = 0; s < splits; ++s) v[0] += q[(int64_t)s * e.rows * e.ldp];
     float bias = 0.0f;
     if (EPI == EPI_FORWARD && e.bias && in) bias = __bfloat162float(e.bias[col]);
-    epilogue_columns<EPI>(e, row, 1, col, in, v, bias);
+    epilogue_columns<EPI, ACT>(e, row, 1, col, in, v, bias);
   } else {
     __shared__ __align__(128) unsigned char blocks[kJoinThreads / 32][kBlockBytes<false>];
     const int64_t row = i / across * 32, col = i % across * 32;
@@ -666,7 +654,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const EpilogueArgs e
         v[4 * k] += t.x, v[4 * k + 1] += t.y, v[4 * k + 2] += t.z, v[4 * k + 3] += t.w;
       }
     }
-    epilogue_tile<EPI>(e, row, col, lane, blocks[threadIdx.x / 32], v);
+    epilogue_tile<EPI, ACT>(e, row, col, lane, blocks[threadIdx.x / 32], v);
   }
 }
 
@@ -694,9 +682,9 @@ cudaError_t launch_forward(const TcArgs& p, TcTile t, int grid, bool after, cuda
 cudaError_t launch_grad_input(const TcArgs& p, TcTile t, int grid, bool after, cudaStream_t stream);
 cudaError_t launch_grad_weight(const TcArgs& p, TcTile t, int grid, bool after, cudaStream_t stream);
 
-template <int CG, int BN, bool A_MN, bool B_MN, int EPI, bool SWAP>
+template <int CG, int BN, bool A_MN, bool B_MN, int EPI, int ACT, bool SWAP>
 cudaError_t launch_tc(const TcArgs& p, int grid, bool after, cudaStream_t stream) {
-  auto kernel = gemm_tc_kernel<CG, BN, A_MN, B_MN, EPI, SWAP>;
+  auto kernel = gemm_tc_kernel<CG, BN, A_MN, B_MN, EPI, ACT, SWAP>;
   constexpr int smem = TcShape<CG, BN, EPI, SWAP>::smem_bytes;
   static std::atomic<uint64_t> ready{0};  // devices (bits) whose limit has been raised
   int dev = 0;
@@ -728,25 +716,27 @@ cudaError_t launch_tc(const TcArgs& p, int grid, bool after, cudaStream_t stream
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-// A_MN, B_MN: the operands' majors unswapped.  Sums of several splits go to
-// p.e.partial.
+// A tile's kernel, of the call's epilogue or, with several splits, of the one that
+// puts their sums to p.e.partial.
+template <int CG, int BN, bool A_MN, bool B_MN, int EPI, bool SWAP>
+cudaError_t launch_tile(const TcArgs& p, int grid, bool after, cudaStream_t stream) {
+  if (p.splits > 1) return launch_tc<CG, BN, A_MN, B_MN, EPI_PARTIAL, TIDE_ACT_NONE, SWAP>(p, grid, after, stream);
+  if constexpr (EPI == EPI_PLAIN)
+    return launch_tc<CG, BN, A_MN, B_MN, EPI, TIDE_ACT_NONE, SWAP>(p, grid, after, stream);
+  else
+    return with_act(p.e.act, [&](auto act) {
+      return launch_tc<CG, BN, A_MN, B_MN, EPI, act.value, SWAP>(p, grid, after, stream);
+    });
+}
+
+// A_MN, B_MN: the operands' majors unswapped.
 template <bool A_MN, bool B_MN, int EPI>
 cudaError_t launch_layout(const TcArgs& p, TcTile t, int grid, bool after, cudaStream_t stream) {
-  const bool partial = p.splits > 1;
-  constexpr int kSmall = small_b(A_MN);
   switch (t) {
-    case TILE_256x256:
-      return partial ? launch_tc<2, 256, A_MN, B_MN, EPI_PARTIAL, false>(p, grid, after, stream)
-                     : launch_tc<2, 256, A_MN, B_MN, EPI, false>(p, grid, after, stream);
-    case TILE_256x128:
-      return partial ? launch_tc<2, 128, A_MN, B_MN, EPI_PARTIAL, false>(p, grid, after, stream)
-                     : launch_tc<2, 128, A_MN, B_MN, EPI, false>(p, grid, after, stream);
-    case TILE_SWAP_128:
-      return partial ? launch_tc<1, 128, B_MN, A_MN, EPI_PARTIAL, true>(p, grid, after, stream)
-                     : launch_tc<1, 128, B_MN, A_MN, EPI, true>(p, grid, after, stream);
-    default:
-      return partial ? launch_tc<1, kSmall, B_MN, A_MN, EPI_PARTIAL, true>(p, grid, after, stream)
-                     : launch_tc<1, kSmall, B_MN, A_MN, EPI, true>(p, grid, after, stream);
+    case TILE_256x256: return launch_tile<2, 256, A_MN, B_MN, EPI, false>(p, grid, after, stream);
+    case TILE_256x128: return launch_tile<2, 128, A_MN, B_MN, EPI, false>(p, grid, after, stream);
+    case TILE_SWAP_128: return launch_tile<1, 128, B_MN, A_MN, EPI, true>(p, grid, after, stream);
+    default: return launch_tile<1, small_b(A_MN), B_MN, A_MN, EPI, true>(p, grid, after, stream);
   }
 }
 

@@ -3,9 +3,12 @@
 // Both directions are one pass over the matrix, a few operations per element,
 // so they are bound by memory traffic: store reads s bytes and writes 1 + 1/32
 // per element, load reads 1 + 1/32 (and s for a gradient) and writes s.
-//   8192 x 13824 bf16 (343 MB each way): store 57 us, load 49 us, 6.0 and 7.0 TB/s
-//   4093 x 4095 bf16, rows of odd alignment, times a gradient through SiLU'
-//   (84 MB): 21 us, 4.0 TB/s; 31 instructions a value bind it there
+//   8192 x 13824 bf16 (343 MB each way): store 57 us, load 50 us, 6.0 and 6.8 TB/s
+// Rows of odd alignment and the costlier activations are bound by issuing
+// instructions instead:
+//   4093 x 4095 bf16 times a gradient through SiLU' (84 MB): 17 us, 4.8 TB/s; 30
+//   instructions a value keep 79% of the issue slots busy, and DRAM 33%
+//   8192 x 13824 bf16 through GELU 65 us, its erf form 97 us
 
 #include <algorithm>
 
@@ -36,7 +39,6 @@ struct LoadArgs {
   int64_t ldc;
   const uint8_t* scales;
   int64_t lds;
-  int act;
   const void* grad;
   int64_t ldg;
   void* out;
@@ -96,30 +98,23 @@ __global__ void __launch_bounds__(kThreads) store_any_kernel(const StoreArgs a) 
 }
 
 // f(v), or g * f'(v).  fp32 outputs take the accurate exponential and division.
-template <typename T, int N>
-__device__ __forceinline__ void loaded(float (&v)[N], int act, bool has_grad, const float (&g)[N]) {
+template <typename T, bool GRAD, int ACT, int N>
+__device__ __forceinline__ void loaded(float (&v)[N], const float (&g)[N]) {
   constexpr bool fast = sizeof(T) == 2;
-  if (has_grad) {
-    with_act(act, [&](auto a) {
 #pragma unroll
-      for (int k = 0; k < N; ++k) v[k] = g[k] * act_grad<fast>(a.value, v[k]);
-    });
-    if (act == TIDE_ACT_NONE) {
-#pragma unroll
-      for (int k = 0; k < N; ++k) v[k] = g[k];
-    }
-  } else {
-    with_act(act, [&](auto a) {
-#pragma unroll
-      for (int k = 0; k < N; ++k) v[k] = act_value<fast>(a.value, v[k]);
-    });
+  for (int k = 0; k < N; ++k) {
+    if constexpr (GRAD)
+      v[k] = ACT == TIDE_ACT_NONE ? g[k] : g[k] * act_grad<fast>(ACT, v[k]);
+    else
+      v[k] = act_value<fast>(ACT, v[k]);
   }
 }
 
 // Eight neighbouring columns a thread and item; rows on 16-byte (out, grad)
 // and 8-byte (codes) boundaries.
-// Registers are bounded: one more than 48 costs a block an SM (60 us for 58).
-template <typename T, bool GRAD>
+// Registers are bounded, to what bf16 asks for: one more than 48 cost a block an SM
+// (58 us became 60).  fp32's erf form alone keeps 4 bytes of a thread in memory for it.
+template <typename T, bool GRAD, int ACT>
 __global__ void __launch_bounds__(kThreads, GRAD ? 3 : 5) load_vec_kernel(const LoadArgs a) {
   uint2 c[kItems];
   uint8_t s[kItems];
@@ -144,16 +139,16 @@ __global__ void __launch_bounds__(kThreads, GRAD ? 3 : 5) load_vec_kernel(const 
     if (!here[j]) continue;
     float v[8];
     decode8(c[j], scale_value(s[j]), v);
-    loaded<T>(v, a.act, GRAD, g[j]);
+    loaded<T, GRAD, ACT>(v, g[j]);
     store_vec<8>((T*)a.out + row[j] * a.ldo + col[j], v);
   }
 }
 
 // Any alignment: a thread takes the eight columns of an aligned word of out
 // (the row's first and last words may be partial), so that out is stored whole,
-// and grad read whole where it lies as out does.  Full occupancy pays: 32 registers
-// 21 us, 34 22.5 (the ragged case above).
-template <typename T, bool GRAD>
+// and grad read whole where it lies as out does.  Full occupancy pays: 34 registers
+// instead of 32 cost 7% (the SiLU' case above).
+template <typename T, bool GRAD, int ACT>
 __global__ void __launch_bounds__(kThreads, GRAD && sizeof(T) == 4 ? 6 : 8) load_any_kernel(const LoadArgs a) {
   const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
   if (i >= a.items) return;
@@ -174,13 +169,13 @@ __global__ void __launch_bounds__(kThreads, GRAD && sizeof(T) == 4 ? 6 : 8) load
     decode8(c, 1.0f, v);
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] *= k < first ? s0 : s1;
-    loaded<T>(v, a.act, GRAD, g);
+    loaded<T, GRAD, ACT>(v, g);
     store_vec<8>(out + col, v);
   } else {
     for (int64_t k = max(col, (int64_t)0); k < min(col + 8, a.cols); ++k) {
       float t[1] = {e4m3_values(codes[k]).x * scale_value(scales[k / kMxBlock])}, u[1] = {0.0f};
       if (GRAD) load_vec<1>(grad + k, u);
-      loaded<T>(t, a.act, GRAD, u);
+      loaded<T, GRAD, ACT>(t, u);
       store_vec<1>(out + k, t);
     }
   }
@@ -220,23 +215,28 @@ tide_status store(int64_t rows, int64_t cols, const void* x, int64_t ldx, uint8_
   });
 }
 
-template <typename T>
-tide_status load(int64_t rows, int64_t cols, const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds,
-                 int32_t act, const void* grad, int64_t ldg, void* out, int64_t ldo, cudaStream_t stream) {
+template <typename T, bool GRAD, int ACT>
+tide_status load_act(int64_t rows, int64_t cols, const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds,
+                     const void* grad, int64_t ldg, void* out, int64_t ldo, cudaStream_t stream) {
   const bool vec = cols % 8 == 0 && rows_aligned(grad, ldg, sizeof(T), rows) &&
                    rows_aligned(out, ldo, sizeof(T), rows) && (uintptr_t)codes % 8 == 0 && (rows <= 1 || ldc % 8 == 0);
   const int64_t per_row = vec ? cols / 8 : (cols + 14) / 8;  // words that any phase of a row touches
   return in_launches(rows, per_row, vec ? kThreads * kItems : kThreads, [&](int64_t r, uint32_t items, unsigned grid) {
-    const LoadArgs a{items, FastDiv((uint32_t)per_row), cols, codes + r * ldc, ldc, scales + r * lds, lds, act,
-                     grad ? (const T*)grad + r * ldg : nullptr, ldg, (T*)out + r * ldo, ldo};
-    if (vec && grad)
-      load_vec_kernel<T, true><<<grid, kThreads, 0, stream>>>(a);
-    else if (vec)
-      load_vec_kernel<T, false><<<grid, kThreads, 0, stream>>>(a);
-    else if (grad)
-      load_any_kernel<T, true><<<grid, kThreads, 0, stream>>>(a);
+    const LoadArgs a{items, FastDiv((uint32_t)per_row), cols, codes + r * ldc, ldc, scales + r * lds, lds,
+                     GRAD ? (const T*)grad + r * ldg : nullptr, ldg, (T*)out + r * ldo, ldo};
+    if (vec)
+      load_vec_kernel<T, GRAD, ACT><<<grid, kThreads, 0, stream>>>(a);
     else
-      load_any_kernel<T, false><<<grid, kThreads, 0, stream>>>(a);
+      load_any_kernel<T, GRAD, ACT><<<grid, kThreads, 0, stream>>>(a);
+  });
+}
+
+template <typename T>
+tide_status load(int64_t rows, int64_t cols, const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds,
+                 int32_t act, const void* grad, int64_t ldg, void* out, int64_t ldo, cudaStream_t stream) {
+  return with_act(act, [&](auto a) {
+    return grad ? load_act<T, true, a.value>(rows, cols, codes, ldc, scales, lds, grad, ldg, out, ldo, stream)
+                : load_act<T, false, a.value>(rows, cols, codes, ldc, scales, lds, nullptr, 0, out, ldo, stream);
   });
 }
 

@@ -60,6 +60,25 @@ inline tide_status check_dtype(int32_t dtype) {
   return dtype != TIDE_BF16 && dtype != TIDE_F32 ? fail(TIDE_ERR_INVALID_ARG, "unknown element type") : TIDE_OK;
 }
 
+// f called with the activation as a constant: kernels are built for each, since one
+// for all of them takes the registers and the order of code that the costliest asks
+// for (24832 x 64 -> 10301 without any 181 us then, 167 alone; 4093 x 4095 bf16 loaded
+// without any 13.0 and 10.9).
+template <int ACT>
+struct ActTag {
+  static constexpr int value = ACT;
+};
+template <typename F>
+auto with_act(int act, F&& f) {
+  switch (act) {
+    case TIDE_ACT_RELU: return f(ActTag<TIDE_ACT_RELU>());
+    case TIDE_ACT_GELU: return f(ActTag<TIDE_ACT_GELU>());
+    case TIDE_ACT_GELU_ERF: return f(ActTag<TIDE_ACT_GELU_ERF>());
+    case TIDE_ACT_SILU: return f(ActTag<TIDE_ACT_SILU>());
+    default: return f(ActTag<TIDE_ACT_NONE>());
+  }
+}
+
 // Whether rows of a matrix start on 16-byte boundaries (NULL counts: it is
 // not touched).
 inline bool rows_aligned(const void* p, int64_t ld, int64_t elem, int64_t rows) {
@@ -423,27 +442,6 @@ __device__ __forceinline__ float act_grad(int act, float z) {
       d = p * (1.0f - p);
       return d == 0.0f ? p : p + z * d;
     default: return 1.0f;
-  }
-}
-
-template <int ACT>
-struct ActTag {
-  static constexpr int value = ACT;
-};
-// f called with the activation as a constant (not at all for none): one branch for
-// many elements.  In this order, with GELU and ReLU expected, the bodies lie so that
-// none pays for another's: 1788 x 64 -> 13760 takes 21.1 us with ReLU, 26.7 with GELU,
-// 35.1 with its erf form and 25.5 with SiLU; from a switch 22.2, 29.1, 34.6 and 26.3.
-template <typename F>
-__device__ __forceinline__ void with_act(int act, F&& f) {
-  if (__builtin_expect(act == TIDE_ACT_GELU, 1)) {
-    f(ActTag<TIDE_ACT_GELU>());
-  } else if (__builtin_expect(act == TIDE_ACT_RELU, 1)) {
-    f(ActTag<TIDE_ACT_RELU>());
-  } else if (__builtin_expect(act == TIDE_ACT_GELU_ERF, 0)) {
-    f(ActTag<TIDE_ACT_GELU_ERF>());
-  } else if (__builtin_expect(act == TIDE_ACT_SILU, 0)) {
-    f(ActTag<TIDE_ACT_SILU>());
   }
 }
 

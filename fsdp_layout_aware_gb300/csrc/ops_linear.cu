@@ -324,8 +324,12 @@ tide_status product(int64_t m, int64_t n, int64_t k, Operand a, bool a_mn, Opera
   const int64_t warps = (swapped ? m : ceil_div(m, 32)) * ceil_div(n, 32), grid = ceil_div(warps * 32, kJoinThreads);
   if (grid > INT32_MAX) return fail(TIDE_ERR_UNIMPLEMENTED, "linear: too many elements for one launch");
   const LaunchAfter l(grid, kJoinThreads, after, stream);
-  return cuda_status(swapped ? cudaLaunchKernelEx(&l.cfg, join_kernel<EPI, true>, e, splits)
-                             : cudaLaunchKernelEx(&l.cfg, join_kernel<EPI, false>, e, splits),
+  return cuda_status(with_act(EPI == EPI_PLAIN ? TIDE_ACT_NONE : e.act,
+                              [&](auto act) {
+                                constexpr int kAct = EPI == EPI_PLAIN ? TIDE_ACT_NONE : act.value;
+                                return swapped ? cudaLaunchKernelEx(&l.cfg, join_kernel<EPI, kAct, true>, e, splits)
+                                               : cudaLaunchKernelEx(&l.cfg, join_kernel<EPI, kAct, false>, e, splits);
+                              }),
                      "linear epilogue");
 }
 
