@@ -17,13 +17,13 @@
 // counted, and the CTA drains its copies, frees its tensor memory and returns.
 //
 // What binds it, measured:
-//   8192 x 5120 x 13824 with bias, GELU and an 8-bit z: 600 to 609 us from a cold
-//   start, by the GPU (1.9 PFLOP/s, tensor pipe 97% active), 690 us (1.68) in a long
+//   8192 x 5120 x 13824 with bias, GELU and an 8-bit z: 600 to 611 us from a cold
+//   start, by the GPU (1.9 PFLOP/s, tensor pipe 97% active), 700 us (1.66) in a long
 //   loop, where the power limit holds the clock near 1450 MHz; the input gradient 598
-//   to 614 and 694 us, 8192 x 28672 x 8192's weight gradient 1.8 to 1.9 and 2.2 ms
-//   one token, 8192 -> 28672: 71 us, 6.6 TB/s of weights (DRAM)
-//   short sums, by their output: 24832 x 64 -> 10304 in 104 us, 4.9 TB/s (plain, a
-//   weight gradient's, 96 us, 5.3); rows of odd alignment 2.2 to 3.6 TB/s
+//   to 614 and 697 us, 8192 x 28672 x 8192's weight gradient 1.8 to 1.9 and 2.2 ms
+//   one token, 8192 -> 28672: 73 us, 6.4 TB/s of weights (DRAM)
+//   short sums, by their output: 24832 x 64 -> 10304 in 103 us, 5.0 TB/s (plain, a
+//   weight gradient's, 98 us, 5.2); rows of odd alignment 2.2 to 3.6 TB/s
 //   a block of 64 of the sum takes a pair 512 clocks on 256 x 256 and 260 on 256 x
 //   128 alone, 570 and 340 with all SMs drawing on L2; a single CTA 270 to 420
 #pragma once

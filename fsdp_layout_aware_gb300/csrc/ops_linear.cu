@@ -336,8 +336,9 @@ tide_status product(int64_t m, int64_t n, int64_t k, Operand a, bool a_mn, Opera
 // db: column sums.  A thread sums V neighbouring columns over every other one
 // of its block's rows, and the block's two are joined in shared memory; block
 // row y gives partial[y], summed by launch_sum_groups.  It runs beside the
-// product: its blocks are few and small enough that a product's CTA fits on the
-// SM with them, and it lets the product start as soon as they are all there.
+// product, which it lets start as soon as its blocks are all there: they are few, and a
+// pair tile's CTA leaves 17 KB of shared memory for their 4.  The swapped tiles of 64
+// and 128 tokens leave half a KB: such a CTA starts once the sums on its SM are done.
 constexpr int kSumLanes = 64;
 
 template <int V>

@@ -8,10 +8,10 @@
 //   forward, 16384 x 8192 bf16, residual added, y also in 8 bits (1.21 GB): 175 us,
 //   6.9 TB/s
 //   backward, 8192 x 5120 bf16 from a checkpoint, dres added (294 MB): 46 us, 6.3
-//   TB/s, and 5 us to join dweight's partial sums; 4096 x 8192 fp32 70 us, 6.3 TB/s;
-//   8192 x 14336 bf16 120 us, 5.9 TB/s
-//   4999 x 4095 bf16, rows of odd alignment (185 and 144 MB): 65 and 68 us, bound by
-//   their instructions
+//   TB/s, 49 with dweight's partial sums joined; without dres 4096 x 8192 fp32 67 us,
+//   6.0 TB/s, 8192 x 14336 bf16 120 us, 5.9 TB/s
+//   4999 x 4095 bf16, rows of odd alignment: forward (82 MB) 31 us, backward (123 MB, 103
+//   from a checkpoint) 57 and 56 us, bound by their instructions
 
 #include <algorithm>
 #include <atomic>

@@ -30,10 +30,12 @@ __device__ __forceinline__ uint32_t mapped_addr(uint32_t addr, uint32_t rank) {
   return r;
 }
 
-// Says that tensor memory has been read (tcgen05.wait::ld and the fence before a
-// thread's synchronisation come first, which order those reads).  Nothing else is
-// handed over, so it is relaxed: a release at this scope would wait until the
-// thread's stores to global memory have been seen, 1000 clocks and more a tile.
+// Says that tensor memory has been read: tcgen05.wait::ld comes first, after which the
+// values are in registers, and the fence before a thread's synchronisation, which orders
+// those reads before this arrive; the other side waits and fences likewise before its
+// next matrix instruction.  Nothing else is handed over, so it is relaxed: a release at
+// this scope would wait until the thread's stores to global memory have been seen, 1000
+// clocks and more a tile.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
