@@ -3,7 +3,9 @@
 ``tide_rs_reduce`` and ``tide_ag_place`` run in hand-written CUDA kernels in
 ``libtide.so`` (C ABI: include/tide.h); this package only binds them.  So do the
 training block's operators that run between the two (include/tide_ops.h): RMS
-norm, linear layer, 8-bit activation checkpoints.
+norm, linear layer, 8-bit activation checkpoints; and those at the two ends of a
+language model's step (include/tide_lm_ops.h): token embedding, log
+probabilities, gradient norm and clipping.
 """
 
 from .tide import (  # noqa: F401
@@ -28,15 +30,24 @@ _OPS = frozenset((
     "tide_ops_check", "tide_ops_set_option", "TIDE_OPS_OPT_WAIT_LIMIT_NS", "TIDE_OPS_OPT_TEST_DROP_LOAD",
     "TIDE_ACT_NONE", "TIDE_ACT_RELU", "TIDE_ACT_GELU", "TIDE_ACT_GELU_ERF", "TIDE_ACT_SILU",
 ))
+_LM_OPS = frozenset((
+    "tide_embedding", "tide_embedding_backward", "tide_log_probs", "tide_log_probs_backward", "tide_grad_norm",
+    "tide_grad_clip", "TensorList", "TIDE_I32", "TIDE_I64",
+))
 
 
 def __getattr__(name):
-    if name not in _OPS:
+    if name in _OPS:
+        from . import ops as module
+        names = _OPS
+    elif name in _LM_OPS:
+        from . import lm_ops as module
+        names = _LM_OPS
+    else:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    from . import ops
-    globals().update({n: getattr(ops, n) for n in _OPS})
+    globals().update({n: getattr(module, n) for n in names})
     return globals()[name]
 
 
 def __dir__():
-    return sorted(set(globals()) | _OPS)
+    return sorted(set(globals()) | _OPS | _LM_OPS)

@@ -2,7 +2,7 @@
 
 ``build_all()`` compiles, with nvcc and in parallel:
   * ``fsdp_layout_aware_gb300/libtide.so``  -- the C-ABI library (include/tide.h,
-                                               include/tide_ops.h)
+                                               include/tide_ops.h, include/tide_lm_ops.h)
   * ``synth/libtide_synth.so``              -- the seeded input generator's
                                                device twin (tests and bench only)
 and, on request (``build_lib("tide_checked")``, ``--checked``):
@@ -42,10 +42,12 @@ CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler",
 TIDE_SRCS = [os.path.join(HERE, "csrc", f) for f in ("plan.cpp", "runtime.cu", "rs_kernel.cu", "rs_bulk.cu",
                                                      "rs_staged.cu", "ag_kernel.cu", "ag_bulk.cu", "rs_noalloc.cu",
                                                      "ops_norm.cu", "ops_ckpt.cu", "ops_linear.cu", "ops_linear_forward.cu",
-                                                     "ops_linear_grad_input.cu", "ops_linear_grad_weight.cu")]
+                                                     "ops_linear_grad_input.cu", "ops_linear_grad_weight.cu",
+                                                     "ops_embed.cu", "ops_logprob.cu", "ops_gradnorm.cu")]
 TIDE_DEPS = [os.path.join(HERE, "csrc", f) for f in ("tide_internal.h", "rs_device.cuh", "bulk_ptx.cuh",
-                                                     "check.cuh", "ops_common.cuh", "gemm_tc.cuh", "tc_ptx.cuh")] + \
-            [os.path.join(ROOT, "include", f) for f in ("tide.h", "tide_ops.h")]
+                                                     "check.cuh", "ops_common.cuh", "gemm_tc.cuh", "tc_ptx.cuh",
+                                                     "cluster_ptx.cuh", "lm_common.cuh")] + \
+            [os.path.join(ROOT, "include", f) for f in ("tide.h", "tide_ops.h", "tide_lm_ops.h")]
 
 LIBS = {
     "tide": {
