@@ -77,20 +77,53 @@ struct Raw8 {
   }
 };
 
+// Eight elements that begin BYTES past a 16-byte boundary, from the granules that hold them.
+template <int BYTES, typename T>
+__device__ __forceinline__ void load_shifted(const T* p, float (&v)[8]) {
+  constexpr int kGranules = (BYTES + 8 * (int)sizeof(T) + 15) / 16, kWord = BYTES / 4;
+  const uint4* g = reinterpret_cast<const uint4*>((uintptr_t)p - BYTES);
+  uint32_t w[4 * kGranules];
+#pragma unroll
+  for (int j = 0; j < kGranules; ++j) {
+    const uint4 u = g[j];
+    w[4 * j] = u.x, w[4 * j + 1] = u.y, w[4 * j + 2] = u.z, w[4 * j + 3] = u.w;
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    if constexpr (sizeof(T) == 2) {
+      const int e = BYTES / 2 + k;
+      v[k] = __uint_as_float(e % 2 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+    } else {
+      v[k] = __uint_as_float(w[kWord + k]);
+    }
+  }
+}
+
 // The columns col .. col + 7 of a row of `cols` that exist, at any alignment of the row;
-// zeros for the rest.
+// zeros for the rest.  Whole granules inside the row where there are any: narrow loads at a
+// stride cost L1 four to eight times as many turns.  A row's vectors all branch alike.
 template <typename T>
 __device__ __forceinline__ void load_columns(const T* row, int64_t col, int64_t cols, float (&v)[8]) {
   const T* p = row + col;
-  if (col >= 0 && col + 8 <= cols) {
-    if ((uintptr_t)p % 16 == 0)
-      load_vec<8>(p, v);
-    else
-      load_any8(p, v);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = col + k >= 0 && col + k < cols ? (float)p[k] : 0.0f;
+  const int phase = (int)((uintptr_t)p & 15), before = phase / (int)sizeof(T);
+  if (col >= before && col - before + (phase ? 16 / (int)sizeof(T) : 0) + 8 <= cols) {
+    switch (phase) {
+      case 0: return load_vec<8>(p, v);
+      case 4: return load_shifted<4>(p, v);
+      case 8: return load_shifted<8>(p, v);
+      case 12: return load_shifted<12>(p, v);
+    }
+    if constexpr (sizeof(T) == 2) {
+      switch (phase) {
+        case 2: return load_shifted<2>(p, v);
+        case 6: return load_shifted<6>(p, v);
+        case 10: return load_shifted<10>(p, v);
+        default: return load_shifted<14>(p, v);
+      }
+    }
   }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = col + k >= 0 && col + k < cols ? (float)p[k] : 0.0f;
 }
 // ... and stored, at a 16-byte boundary where all eight exist.
 template <typename T>

@@ -5,15 +5,15 @@
 // Backward, dweight[v] = scale * sum of dy[t] over the t with token v, is dense: every row
 // of dweight is written once, the rows of dy are read once, and both dwarf the ids.
 //   1. A cluster of blocks sorts the ids, stably, by eight bits at a time (their places
-//      with them), so that a token's rows of dy are a run of places in ascending order: the sum's order
-//      is fixed.
-//   2. Tokens that fill whole tiles of kTile sorted places (padding, separators, articles) have
-//      these tiles' rows summed, a tile a block, so that no block is left with a run of thousands.
-//   3. A block takes kRows rows of dweight by kCols columns, finds its tokens' runs by binary
-//      search, and writes zeros or sums.  A run of more than kLong rows is added up by all of the
-//      block's warps, with the tiles' sums in the place of their rows.
+//      with them), so that a token's rows of dy are a run of sorted places, in ascending order: the
+//      sum's order is fixed.  A second kernel writes the rows that no id names meanwhile.
+//   2. The sorted places are cut into tiles.  A thread takes eight columns and a tile, and
+//      sums and stores the runs that begin in it, reading up to a tile beyond its end for the last.
+//      Where a run is longer than that, every tile leaves its part of it in the workspace.
+//   3. The parts of such runs (padding, separators, articles) are joined, a block at a time.
 
 #include <algorithm>
+#include <type_traits>
 
 #include "cluster_ptx.cuh"
 #include "lm_common.cuh"
@@ -21,7 +21,7 @@
 namespace tide {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 256;
 constexpr int64_t kMaxCols = 1 << 24;
 
 // ---------------------------------------------------------------- forward
@@ -87,8 +87,11 @@ __global__ void __launch_bounds__(kThreads) embed_any_kernel(const EmbedArgs a) 
 
 // ---------------------------------------------------------------- sorting
 
-constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kDigits = 256;
-constexpr int kSortCluster = 8;
+constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32, kSortCluster = 8;
+// A digit: 18 bits, a vocabulary of 262,143, take two passes.
+constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
+constexpr int kRounds = 8;  // places a lane has in registers
+static_assert(kDigits == kSortThreads, "a thread a digit");
 
 struct SortArgs {
   int64_t tokens, vocab;
@@ -97,265 +100,399 @@ struct SortArgs {
   uint32_t *key, *place;    // out, sorted by key; ids outside the vocabulary have key vocab
   uint32_t *key2, *place2;  // scratch
   int passes;
+  int32_t tile;     // places a tile
+  uint32_t* longs;  // number of the runs that are joined from parts, and the tiles that they begin in
 };
 
-// A stable counting sort a digit of eight bits.  The cluster's warps take consecutive parts of
-// the places; a warp walks its part 32 places at a time, and equal digits among those are
-// ranked by lane.
+// One cluster: a stable counting sort a digit at a time.  The cluster's warps take consecutive
+// parts of the places; a warp walks its part 32 places at a time, and equal digits among
+// those are ranked by lane.  16384 ids of 18 bits take 17 us, 4093 of 13 bits 11, nearly all of it
+// latency: of the ids, of a pass's counts on their way between blocks, of its keys.
 __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const SortArgs a) {
   __shared__ uint32_t counts[kSortWarps][kDigits];
   __shared__ uint32_t totals[kDigits];  // the block's
-  __shared__ uint32_t scan[kDigits / 32];
+  __shared__ uint32_t scan[kSortWarps];
+  let_next_kernel_start();
   const uint32_t blocks = cluster_size(), rank = cluster_rank();
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, digit_here = threadIdx.x;
   const uint32_t n = (uint32_t)a.tokens, parts = blocks * kSortWarps;
   const uint32_t part = (uint32_t)(((uint64_t)n + parts * 32 - 1) / (parts * 32) * 32);
   const uint64_t begin = min((uint64_t)(rank * kSortWarps + warp) * part, (uint64_t)n), end = min(begin + part, (uint64_t)n);
+  const bool held = part <= kRounds * 32;  // all of a warp's part in registers
+  if (rank == 0 && threadIdx.x == 0) a.longs[0] = 0;
   for (int pass = 0; pass < a.passes; ++pass) {
     // The last pass ends in key and place.
     const bool to_first = (a.passes - pass) % 2 == 1;
     const uint32_t *key = to_first ? a.key2 : a.key, *place = to_first ? a.place2 : a.place;
     uint32_t *key_out = to_first ? a.key : a.key2, *place_out = to_first ? a.place : a.place2;
-    const int shift = pass * 8;
-    auto key_at = [&](uint64_t i) {
-      if (pass == 0) {
-        const int t = token_at(a.ids, a.index, (int64_t)i, a.vocab);
-        return t >= 0 ? (uint32_t)t : (uint32_t)a.vocab;
+    const int shift = pass * kDigitBits;
+    uint32_t k[kRounds], q[kRounds];
+    auto load = [&](uint64_t i0) {
+#pragma unroll
+      for (int r = 0; r < kRounds; ++r) {
+        const uint64_t i = i0 + r * 32 + lane;
+        k[r] = 0, q[r] = (uint32_t)i;
+        if (i >= end) continue;
+        if (pass == 0) {
+          const int t = token_at(a.ids, a.index, (int64_t)i, a.vocab);
+          k[r] = t >= 0 ? (uint32_t)t : (uint32_t)a.vocab;
+        } else {
+          k[r] = __ldcg(key + i), q[r] = __ldcg(place + i);
+        }
       }
-      return __ldcg(key + i);
     };
     for (int d = lane; d < kDigits; d += 32) counts[warp][d] = 0;
     __syncwarp();
-    for (uint64_t i = begin + lane; i < end; i += 32) atomicAdd(&counts[warp][(key_at(i) >> shift) & 255], 1u);
-    __syncthreads();
-    uint32_t sum = 0;
-    if (threadIdx.x < kDigits) {
-      for (int w = 0; w < kSortWarps; ++w) {
-        const uint32_t c = counts[w][threadIdx.x];
-        counts[w][threadIdx.x] = sum;
-        sum += c;
-      }
-      totals[threadIdx.x] = sum;
-    }
-    cluster_sync();
-    if (threadIdx.x < kDigits) {  // where each digit's keys of this block begin
-      uint32_t before = 0, all = 0;
-      for (uint32_t b = 0; b < blocks; ++b) {
-        const uint32_t c = load_peer_u32(peer_smem(&totals[threadIdx.x], b));
-        if (b < rank) before += c;
-        all += c;
-      }
-      uint32_t up = all;
+    for (uint64_t i0 = begin; i0 < end; i0 += kRounds * 32) {
+      load(i0);
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const uint32_t o = __shfl_up_sync(0xffffffffu, up, d);
-        if (lane >= d) up += o;
-      }
-      if (lane == 31) scan[warp] = up;
-      sum = before + up - all;
+      for (int r = 0; r < kRounds; ++r)
+        if (i0 + r * 32 + lane < end) atomicAdd(&counts[warp][(k[r] >> shift) % kDigits], 1u);
     }
     __syncthreads();
-    if (threadIdx.x < kDigits) {
-      for (int w = 0; w < warp; ++w) sum += scan[w];
-      for (int w = 0; w < kSortWarps; ++w) counts[w][threadIdx.x] += sum;
+    // A digit's places in each warp's part begin behind those in the parts before.
+    uint32_t in_warp[kSortWarps], sum = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) in_warp[w] = counts[w][digit_here];
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) {
+      const uint32_t c = in_warp[w];
+      in_warp[w] = sum;
+      sum += c;
     }
+    totals[digit_here] = sum;
+    cluster_sync();
+    uint32_t before = 0, all = 0, peer[kSortCluster];
+#pragma unroll
+    for (uint32_t b = 0; b < kSortCluster; ++b) peer[b] = b < blocks ? load_peer_u32(peer_smem(&totals[digit_here], b)) : 0;
+#pragma unroll
+    for (uint32_t b = 0; b < kSortCluster; ++b) {
+      if (b < rank) before += peer[b];
+      all += peer[b];
+    }
+    uint32_t up = all;  // ... and behind all of the smaller digits'
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t o = __shfl_up_sync(0xffffffffu, up, d);
+      if (lane >= d) up += o;
+    }
+    if (lane == 31) scan[warp] = up;
     __syncthreads();
-    for (uint64_t i0 = begin; i0 < end; i0 += 32) {
-      const uint64_t i = i0 + lane;
-      const bool here = i < end;
-      const uint32_t k = here ? key_at(i) : 0;
-      const uint32_t digit = here ? (k >> shift) & 255 : kDigits;
-      const uint32_t same = __match_any_sync(0xffffffffu, digit);
-      const uint32_t rank_in = __popc(same & ((1u << lane) - 1));
-      const uint32_t base = here ? counts[warp][digit] : 0;
-      __syncwarp();
-      if (here) {
-        if (rank_in == 0) counts[warp][digit] = base + __popc(same);
-        key_out[base + rank_in] = k;
-        place_out[base + rank_in] = pass == 0 ? (uint32_t)i : __ldcg(place + i);
+    uint32_t base = before + up - all;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w)
+      if (w < warp) base += scan[w];
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) counts[w][digit_here] = base + in_warp[w];
+    __syncthreads();
+    for (uint64_t i0 = begin; i0 < end; i0 += kRounds * 32) {
+      if (!held) load(i0);
+#pragma unroll
+      for (int r = 0; r < kRounds; ++r) {
+        if (i0 + r * 32 >= end) break;  // the same for the warp
+        const bool here = i0 + r * 32 + lane < end;
+        const uint32_t digit = here ? (k[r] >> shift) % kDigits : kDigits;
+        const uint32_t same = __match_any_sync(0xffffffffu, digit);
+        const uint32_t rank_in = __popc(same & ((1u << lane) - 1));
+        const uint32_t at = here ? counts[warp][digit] : 0;
+        __syncwarp();
+        if (here) {
+          if (rank_in == 0) counts[warp][digit] = at + __popc(same);
+          key_out[at + rank_in] = k[r];
+          place_out[at + rank_in] = q[r];
+        }
+        __syncwarp();
       }
-      __syncwarp();
     }
-    __threadfence();
     cluster_sync();
   }
+  // Runs that begin in a tile and go on beyond the next one's end.
+  const int64_t tile = a.tile, tiles = (a.tokens + tile - 1) / tile;
+  for (int64_t t = rank * kSortThreads + threadIdx.x; t + 2 < tiles; t += blocks * kSortThreads) {
+    const uint32_t k = __ldcg(a.key + (t + 1) * tile), last = __ldcg(a.key + (t + 1) * tile - 1),
+                   behind = __ldcg(a.key + (t + 2) * tile), before = t > 0 ? __ldcg(a.key + t * tile - 1) : (uint32_t)a.vocab;
+    if (k < (uint32_t)a.vocab && last == k && behind == k && before != k) a.longs[1 + atomicAdd(a.longs, 1u)] = (uint32_t)t;
+  }
+}
+
+// ---------------------------------------------------------------- rows without a token
+
+constexpr int kZeroThreads = 1024, kZeroWords = 8192;
+
+struct ZeroArgs {
+  int64_t tokens, vocab, cols;
+  int32_t index;
+  const void* ids;
+  void* dweight;
+  int64_t lddw;
+  FastDiv vectors, blocks;
+};
+
+// Zeros for the rows of dweight that no id names.  Block b of B takes rows b, b + B, ... (named
+// ones lie together), a piece at a time, with a bit for each that an id names: it looks at all
+// ids by itself, so that it need not wait for the sort, which runs beside it.
+template <typename T>
+__global__ void __launch_bounds__(kZeroThreads, 1) zero_kernel(const ZeroArgs a) {
+  __shared__ uint32_t named[kZeroWords];
+  let_next_kernel_start();
+  const uint32_t step = gridDim.x;
+  const int64_t all = (a.vocab - blockIdx.x + step - 1) / step;  // rows of this block
+  const int64_t most = min((int64_t)kZeroWords * 32, (int64_t)(1 << 30) / a.vectors.d);
+  for (int64_t first = 0; first < all; first += most) {
+    const uint32_t rows = (uint32_t)min(most, all - first);
+    for (uint32_t i = threadIdx.x; i < (rows + 31) / 32; i += kZeroThreads) named[i] = 0;
+    __syncthreads();
+#pragma unroll 8
+    for (int64_t i = threadIdx.x; i < a.tokens; i += kZeroThreads) {
+      const int token = token_at(a.ids, a.index, i, a.vocab);
+      const uint32_t down = token < 0 ? 0 : a.blocks.quotient((uint32_t)token);
+      const int64_t r = (int64_t)down - first;
+      if (token >= 0 && (uint32_t)token - down * step == blockIdx.x && r >= 0 && r < rows) atomicOr(named + r / 32, 1u << (r % 32));
+    }
+    __syncthreads();
+    const float zeros[8] = {};
+    for (uint32_t i = threadIdx.x; i < rows * a.vectors.d; i += kZeroThreads) {
+      const uint32_t r = a.vectors.quotient(i);
+      if (named[r / 32] >> (r % 32) & 1) continue;
+      T* const out = (T*)a.dweight + ((first + r) * step + blockIdx.x) * a.lddw;
+      const int64_t col = (int64_t)(i - r * a.vectors.d) * 8 - row_phase(out);
+      if (col < a.cols) store_columns(out, col, a.cols, zeros);
+    }
+    __syncthreads();  // the bits are written again
+  }
+  wait_for_kernel_before();  // so that the next kernel, which waits for this one, has waited for the sort too
 }
 
 // ---------------------------------------------------------------- sums
 
-constexpr int kTile = 64;                 // sorted places of a tile
-constexpr int kRows = 32;                 // rows of dweight a block
-constexpr int kSteps = 4;                 // vectors of a row a lane holds
-constexpr int kCols = kSteps * 256;       // columns a block
-constexpr int kLong = 64;                 // rows of a run that one warp adds up
-
 struct SumArgs {
+  uint32_t items;    // threads with work in this launch
+  FastDiv vectors;   // of a row, at any phase; a thread's is the remainder
+  int64_t tile0;     // the launch's first tile
   int64_t tokens, vocab, cols;
-  const uint32_t *key, *place;
+  int32_t tile;
+  const uint32_t *key, *place, *longs;
   const void* dy;
   int64_t lddy;
   float scale;
   void* dweight;
   int64_t lddw;
   int32_t accumulate;
-  float* tiles;    // [whole tiles][ldt]: sums of the tiles of one token; NULL: none are made
-  int64_t ldt;
-  FastDiv slabs;   // blocks beside each other
+  float* parts;  // [tiles][2][vectors * 8]: a tile's part of a long run that began before it, and of one that begins in it
 };
 
-// A lane's columns of a block's: kSteps vectors of eight, a warp's width (256) apart.
-struct Columns {
-  float v[kSteps][8];
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[s][k] = 0.0f;
-  }
-};
-
-// Adds row `p` (of `cols`) from column `col` on.
-template <bool ANY, typename T>
-__device__ __forceinline__ void add_row(Columns& c, const T* p, int64_t col, int64_t cols) {
-#pragma unroll
-  for (int s = 0; s < kSteps; ++s) {
-    const int64_t at = col + s * 256;
-    if (at >= cols) continue;
-    float t[8];
-    if constexpr (ANY)
-      load_columns(p, at, cols, t);
-    else
-      load_vec<8>(p + at, t);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) c.v[s][k] += t[k];
-  }
+__device__ __forceinline__ float* part_of(const SumArgs& a, int64_t tile, int which, uint32_t vector) {
+  return a.parts + ((tile * 2 + which) * a.vectors.d + vector) * 8;
 }
 
-// A block: a tile by kCols columns.  Only tiles of one token; warp w adds rows w, w + 8, ...
+// The column that a vector of a row of dweight starts at.
 template <typename T, bool ANY>
-__global__ void __launch_bounds__(kThreads) tiles_kernel(const SumArgs a) {
-  __shared__ __align__(16) float joined[kWarps][kCols];
-  wait_for_kernel_before();
-  const int64_t first = (int64_t)blockIdx.x * kTile;
-  const uint32_t token = a.key[first];
-  if (token >= (uint32_t)a.vocab || a.key[first + kTile - 1] != token) return;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int64_t col0 = (int64_t)blockIdx.y * kCols, col = col0 + lane * 8;
-  Columns c;
-  c.zero();
-#pragma unroll 2
-  for (int i = warp; i < kTile; i += kWarps)
-    add_row<ANY>(c, (const T*)a.dy + (int64_t)a.place[first + i] * a.lddy, col, a.cols);
-#pragma unroll
-  for (int s = 0; s < kSteps; ++s) store_vec<8>(&joined[warp][s * 256 + lane * 8], c.v[s]);
-  __syncthreads();
-  for (int i = threadIdx.x; i < kCols; i += kThreads) {
-    float v = 0.0f;
-    for (int w = 0; w < kWarps; ++w) v += joined[w][i];
-    if (col0 + i < a.cols) a.tiles[(int64_t)blockIdx.x * a.ldt + col0 + i] = v;
-  }
-}
-
-// First place whose key is not below `key`.
-__device__ __forceinline__ uint32_t lower_bound(const uint32_t* keys, uint32_t n, uint32_t key) {
-  uint32_t lo = 0;
-  while (n > 0) {
-    const uint32_t half = n / 2;
-    if (keys[lo + half] < key)
-      lo += half + 1, n -= half + 1;
-    else
-      n = half;
-  }
-  return lo;
+__device__ __forceinline__ int64_t column(const SumArgs& a, int64_t row, uint32_t vector) {
+  return (int64_t)vector * 8 - (ANY ? row_phase((const T*)a.dweight + row * a.lddw) : 0);
 }
 
 template <typename T, bool ANY>
-__device__ __forceinline__ void store_row(const SumArgs& a, int64_t row, int64_t col, Columns& c) {
+__device__ __forceinline__ void store_sum(const SumArgs& a, int64_t row, uint32_t vector, float (&sum)[8]) {
   T* const out = (T*)a.dweight + row * a.lddw;
+  const int64_t col = column<T, ANY>(a, row, vector);
+  if (col >= a.cols) return;
+  float old[8];
+  if (a.accumulate) load_columns(out, col, a.cols, old);
 #pragma unroll
-  for (int s = 0; s < kSteps; ++s) {
-    const int64_t at = col + s * 256;
-    if (at >= a.cols) continue;
-    float old[8];
-    if (a.accumulate) {
-      if constexpr (ANY)
-        load_columns(out, at, a.cols, old);
-      else
-        load_vec<8>(out + at, old);
+  for (int k = 0; k < 8; ++k) sum[k] = a.accumulate ? fmaf(sum[k], a.scale, old[k]) : sum[k] * a.scale;
+  if constexpr (ANY)
+    store_columns(out, col, a.cols, sum);
+  else
+    store_vec<8>(out + col, sum);
+}
+
+// Rows of dy on their way to a thread, through slots of its own in shared memory by asynchronous
+// copies of 16 bytes, which take no registers: with them eight rows ahead, not four, and four blocks
+// an SM, not two (16384 rows of 8192 bf16 into 131072: 108 us became 64).  Of rows of any alignment (ANY) the granules
+// that hold a vector are copied, one more than a vector fills, and it is cut out when it is added.
+// Granules reach up to 15 bytes past a row, but never past the matrix: what of one that does lies
+// inside goes by itself.
+template <typename T, bool ANY, int kAhead>
+struct Coming {
+  static constexpr int kGranules = (int)sizeof(T) / 2 + ANY;
+  static constexpr int kBytes = kAhead * kGranules * 16 * kThreads;
+  uint4* mine;  // [kAhead][kGranules][kThreads], this thread's
+  uintptr_t first, last;  // the matrix's bytes
+
+  __device__ __forceinline__ Coming(uint4* ring, const void* dy, int64_t rows, int64_t ld, int64_t cols)
+      : mine(ring + threadIdx.x), first((uintptr_t)dy), last((uintptr_t)dy + ((rows - 1) * ld + cols) * sizeof(T)) {}
+  __device__ __forceinline__ void fetch(int slot, const T* p) {
+    const uintptr_t from = (uintptr_t)p & ~(uintptr_t)15;
+#pragma unroll
+    for (int g = 0; g < kGranules; ++g) {
+      uint4* const to = mine + (slot * kGranules + g) * kThreads;
+      const uintptr_t at = from + g * 16;
+      if (!ANY || (at >= first && at + 16 <= last)) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(at) : "memory");
+      } else {
+        for (int e = 0; e < 16; e += (int)sizeof(T))
+          if (at + e >= first && at + e < last)
+            *reinterpret_cast<T*>(reinterpret_cast<unsigned char*>(to) + e) = *reinterpret_cast<const T*>(at + e);
+      }
+    }
+  }
+  __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory"); }
+  template <int BYTES>
+  __device__ __forceinline__ void add_shifted(int slot, float (&sum)[8]) {
+    uint32_t w[4 * kGranules];
+#pragma unroll
+    for (int g = 0; g < kGranules; ++g) {
+      if (16 * g >= BYTES + 8 * (int)sizeof(T)) continue;  // nothing of it
+      const uint4 u = mine[(slot * kGranules + g) * kThreads];
+      w[4 * g] = u.x, w[4 * g + 1] = u.y, w[4 * g + 2] = u.z, w[4 * g + 3] = u.w;
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) c.v[s][k] = a.accumulate ? fmaf(c.v[s][k], a.scale, old[k]) : c.v[s][k] * a.scale;
-    if constexpr (ANY)
-      store_columns(out, at, a.cols, c.v[s]);
-    else
-      store_vec<8>(out + at, c.v[s]);
+    for (int k = 0; k < 8; ++k) {
+      const int at = BYTES + k * (int)sizeof(T);
+      if constexpr (sizeof(T) == 2)
+        sum[k] += __uint_as_float(at % 4 ? w[at / 4] & 0xffff0000u : w[at / 4] << 16);
+      else
+        sum[k] += __uint_as_float(w[at / 4]);
+    }
   }
-}
+  // phase: bytes by which the vector lies past a granule's start; a row's vectors all have the same.
+  __device__ __forceinline__ void add(int slot, int phase, float (&sum)[8]) {
+    if constexpr (!ANY) return add_shifted<0>(slot, sum);
+    switch (phase) {
+      case 0: return add_shifted<0>(slot, sum);
+      case 4: return add_shifted<4>(slot, sum);
+      case 8: return add_shifted<8>(slot, sum);
+      case 12: return add_shifted<12>(slot, sum);
+    }
+    if constexpr (sizeof(T) == 2) {
+      switch (phase) {
+        case 2: return add_shifted<2>(slot, sum);
+        case 6: return add_shifted<6>(slot, sum);
+        case 10: return add_shifted<10>(slot, sum);
+        default: return add_shifted<14>(slot, sum);
+      }
+    }
+  }
+};
 
 // ANY: rows of any alignment; the vectors of a row of dweight start on its 16-byte boundaries.
-template <typename T, bool ANY>
-__global__ void __launch_bounds__(kThreads) sum_kernel(const SumArgs a) {
-  __shared__ uint32_t begins[kRows + 1];
-  __shared__ __align__(16) float joined[kWarps][kCols];
+// kAhead rows of dy are on their way to a thread, and the place of the one behind them.
+template <typename T, bool ANY, int kAhead>
+__global__ void __launch_bounds__(kThreads, 4) runs_kernel(const SumArgs a) {
+  extern __shared__ __align__(16) uint4 ring[];
   wait_for_kernel_before();
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const uint32_t down = a.slabs.quotient(blockIdx.x), slab = blockIdx.x - down * a.slabs.d;
-  const int64_t row0 = (int64_t)down * kRows;
-  const int rows = (int)min((int64_t)kRows, a.vocab - row0);
-  if ((int)threadIdx.x <= rows) begins[threadIdx.x] = lower_bound(a.key, (uint32_t)a.tokens, (uint32_t)(row0 + threadIdx.x));
-  __syncthreads();
-  const int64_t col0 = (int64_t)slab * kCols;
-  Columns c;
-  bool any_long = false;
-  for (int r = warp; r < rows; r += kWarps) {
-    const uint32_t begin = begins[r], end = begins[r + 1];
-    if (end - begin > kLong) continue;
-    if (begin == end && a.accumulate) continue;
-    const int64_t row = row0 + r, col = col0 + lane * 8 - (ANY ? row_phase((T*)a.dweight + row * a.lddw) : 0);
-    c.zero();
-#pragma unroll 2
-    for (uint32_t i = begin; i < end; ++i) add_row<ANY>(c, (const T*)a.dy + (int64_t)a.place[i] * a.lddy, col, a.cols);
-    store_row<T, ANY>(a, row, col, c);
+  const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
+  if (i >= a.items) return;
+  const uint32_t down = a.vectors.quotient(i), vector = i - down * a.vectors.d;
+  const uint32_t n = (uint32_t)a.tokens, tile = (uint32_t)a.tile, none = (uint32_t)a.vocab;
+  const int64_t t = a.tile0 + down;
+  const uint32_t begin = (uint32_t)t * tile, end = min(begin + tile, n), next_end = min(end + tile, n);  // below 2^31 + 2^7
+  // The keys at the tile's ends, beside it, and beside its neighbours.
+  const uint32_t first = a.key[begin], last = a.key[end - 1], before = begin > 0 ? a.key[begin - 1] : none,
+                 two_before = begin > tile ? a.key[begin - tile - 1] : none, behind = end < n ? a.key[end] : none,
+                 two_behind = next_end < n ? a.key[next_end] : none;
+  if (first >= none) return;
+  // The run that has begun before: the tile before sums it, if it begins in that one and ends in
+  // this; else it is left in parts.
+  bool head = before == first;
+  const bool skip = head && two_before != first && behind != first;
+  // The last run goes on to the end of the next tile at most, if it begins in this one.
+  const bool goes_on = behind == last && last < none, further = goes_on && two_behind != last && !(head && first == last);
+  const uint32_t stop = further ? next_end : end;
+  Coming<T, ANY, kAhead> coming(ring, a.dy, n, a.lddy, a.cols);
+  auto source = [&](uint32_t key, uint32_t place) {
+    return (const T*)a.dy + (int64_t)place * a.lddy + column<T, ANY>(a, key, vector);
+  };
+  auto fetch = [&](int slot, uint32_t p, uint32_t key, uint32_t place) {
+    if (p < stop && key < none && !(skip && key == first) && (p < end || key == last)) {
+      coming.fetch(slot, source(key, place));
+    }
+    coming.commit();
+  };
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) {
+    const uint32_t p = min(begin + j, n - 1);
+    fetch(j, begin + j, a.key[p], a.place[p]);
   }
-  for (int r = 0; r < rows; ++r) any_long |= begins[r + 1] - begins[r] > kLong;
-  if (!any_long) return;  // the same for every thread
-  for (int r = 0; r < rows; ++r) {
-    const uint32_t begin = begins[r], end = begins[r + 1];
-    if (end - begin <= kLong) continue;
-    const int64_t row = row0 + r, col = col0 + lane * 8 - (ANY ? row_phase((T*)a.dweight + row * a.lddw) : 0);
-    // Rows before the first whole tile, the whole tiles, rows behind the last.
-    uint32_t head = end, tail = end;
-    if (a.tiles) {
-      head = min(end, (begin + kTile - 1) / kTile * kTile);
-      tail = max(head, end / kTile * kTile);
+  uint32_t key = first, here = first, here_place = a.place[begin];
+  // Of the place that comes kAhead behind.
+  uint32_t far_key = a.key[min(begin + kAhead, n - 1)], far_place = a.place[min(begin + kAhead, n - 1)];
+  float sum[8] = {};
+  auto flush = [&](bool part) {
+    if (part) {
+      if (!skip || !head) store_vec<8>(part_of(a, t, head ? 0 : 1, vector), sum);
+    } else {
+      store_sum<T, ANY>(a, key, vector, sum);
     }
-    c.zero();
-#pragma unroll 2
-    for (uint32_t i = begin + warp; i < head; i += kWarps)
-      add_row<ANY>(c, (const T*)a.dy + (int64_t)a.place[i] * a.lddy, col, a.cols);
-#pragma unroll 2
-    for (uint32_t i = head / kTile + warp; i < tail / kTile; i += kWarps)
-      add_row<ANY>(c, a.tiles + (int64_t)i * a.ldt, col, a.cols);
-#pragma unroll 2
-    for (uint32_t i = tail + warp; i < end; i += kWarps)
-      add_row<ANY>(c, (const T*)a.dy + (int64_t)a.place[i] * a.lddy, col, a.cols);
-    __syncthreads();  // what the last run left has been read
+  };
+  int slot = 0;
+#pragma unroll 1
+  for (uint32_t p = begin; p < stop; ++p) {
+    const uint32_t next = min(p + 1, n - 1), far = min(p + kAhead + 1, n - 1);
+    const uint32_t next_here = a.key[next], next_place = ANY ? a.place[next] : 0, next_far_key = a.key[far], next_far_place = a.place[far];
+    if (here != key) {
+      flush(head);
+      head = false;
+      key = here;
+      if (key >= none || p >= end) break;
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) store_vec<8>(&joined[warp][s * 256 + lane * 8], c.v[s]);
+      for (int c = 0; c < 8; ++c) sum[c] = 0.0f;
+    }
+    coming.wait();
+    if (!(skip && key == first)) coming.add(slot, ANY ? (int)((uintptr_t)source(key, here_place) & 15) : 0, sum);
+    fetch(slot, p + kAhead, far_key, far_place);
+    here = next_here, here_place = next_place, far_key = next_far_key, far_place = next_far_place;
+    if (++slot == kAhead) slot = 0;
+    if (p + 1 == stop) flush(head || (goes_on && !further));
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+constexpr int kJoinThreads = 512;
+
+// Joins a long run's parts for 32 vectors: a thread of each warp a vector, and their sums in order.
+template <typename T, bool ANY>
+__global__ void __launch_bounds__(kJoinThreads, 2) join_kernel(const SumArgs a) {
+  __shared__ __align__(16) float joined[kJoinThreads / 32][32][8];
+  wait_for_kernel_before();
+  const uint32_t chunks = (a.vectors.d + 31) / 32;
+  const int64_t items = (int64_t)a.longs[0] * chunks;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+    const int64_t t = a.longs[1 + i / chunks];
+    const uint32_t vector = (uint32_t)(i % chunks) * 32 + lane, key = a.key[(t + 1) * a.tile];
+    // Tiles behind t that begin with the key: the run's other parts.
+    int64_t more = 0;
+    for (;;) {
+      const int64_t p = (t + 1 + more + threadIdx.x) * a.tile;
+      const int found = __syncthreads_count(p < a.tokens && a.key[p] == key);
+      more += found;
+      if (found < kJoinThreads) break;
+    }
+    float sum[8] = {};
+    if (vector < a.vectors.d) {
+#pragma unroll 4
+      for (int64_t j = warp; j <= more; j += kJoinThreads / 32) {
+        float v[8];
+        load_vec<8>(part_of(a, t + j, j == 0, vector), v);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) sum[c] += v[c];
+      }
+    }
+    store_vec<8>(joined[warp][lane], sum);
     __syncthreads();
-    if (warp == 0) {
-      c.zero();
+    if (warp == 0 && vector < a.vectors.d) {
+#pragma unroll 8
+      for (int w = 1; w < kJoinThreads / 32; ++w) {
+        float v[8];
+        load_vec<8>(joined[w][lane], v);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w)
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-          float t[8];
-          load_vec<8>(&joined[w][s * 256 + lane * 8], t);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) c.v[s][k] += t[k];
-        }
-      store_row<T, ANY>(a, row, col, c);
+        for (int c = 0; c < 8; ++c) sum[c] += v[c];
+      }
+      store_sum<T, ANY>(a, key, vector, sum);
     }
+    __syncthreads();  // the sums are written again
   }
 }
 
@@ -381,47 +518,75 @@ tide_status embed(EmbedArgs a, int64_t tokens, cudaStream_t stream) {
                          });
 }
 
-// The workspace: sorted keys and places, twice, and the whole tiles' sums.
+// Places a tile: few, while that leaves less than two turns of the SMs' threads, since a thread's
+// places follow one another; many, since runs of more than a tile or two go through memory.
+int tile_of(int64_t tokens, int64_t vectors) {
+  const int64_t enough = (int64_t)std::max(ops_num_sms(), 1) * 2048;
+  int tile = 64;
+  while (tile > 8 && tokens / tile * vectors < enough) tile /= 2;
+  return tile;
+}
+
+// The workspace: sorted keys and places, twice; the long runs; their parts.
 struct GradSpace {
-  int64_t list, tiles, ldt, bytes;
+  int64_t list, longs, parts, bytes;
+  int tile;
 };
 GradSpace grad_space(int64_t tokens, int64_t cols) {
   GradSpace g;
+  const int64_t vectors = (cols + 14) / 8;
+  g.tile = tile_of(tokens, vectors);
+  const int64_t tiles = (tokens + g.tile - 1) / g.tile;
   g.list = (tokens * 4 + 15) / 16 * 16;
-  g.tiles = tokens > 4 * kTile ? tokens / kTile : 0;
-  g.ldt = (cols + 3) / 4 * 4;
-  g.bytes = 4 * g.list + g.tiles * g.ldt * 4;
+  g.longs = (4 + tiles * 4 + 15) / 16 * 16;
+  g.parts = tiles > 2 ? tiles * 2 * vectors * 32 : 0;
+  g.bytes = 4 * g.list + g.longs + g.parts;
   return g;
 }
 
 template <typename T>
 tide_status embed_grad(SumArgs a, SortArgs s, cudaStream_t stream) {
+  const char* const what = "embedding gradient";
   const bool vec = a.cols % 8 == 0 && rows_aligned(a.dy, a.lddy, sizeof(T), a.tokens) &&
                    rows_aligned(a.dweight, a.lddw, sizeof(T), a.vocab);
-  // With a phase a row may touch one vector more.
-  const int64_t wide = vec ? a.cols : a.cols + 7;
-  a.slabs = FastDiv((uint32_t)((wide + kCols - 1) / kCols));
-  const int64_t grid = (a.vocab + kRows - 1) / kRows * a.slabs.d;
-  if (grid > INT32_MAX) return fail(TIDE_ERR_UNIMPLEMENTED, "embedding gradient: too many rows for one launch");
+  const int sms = ops_num_sms();
+  if (sms <= 0) return fail(TIDE_ERR_CUDA, "the current device could not be queried");
+  const int64_t vectors = vec ? a.cols / 8 : (a.cols + 14) / 8;
+  a.vectors = FastDiv((uint32_t)vectors);
   int bits = 1;
   while (a.vocab >> bits) ++bits;  // keys are 0 .. vocab
-  s.passes = (bits + 7) / 8;
-  // A block sorts 4096 ids about as fast as a cluster, whose barriers cost more.
-  const int cluster = a.tokens > 4096 ? kSortCluster : 1;
-  const ClusterLaunch sort(cluster, dim3(kSortThreads), cluster, false, 0, stream);
-  TIDE_TRY(cuda_status(cudaLaunchKernelEx(&sort.cfg, sort_kernel, s), "sorting token ids"));
-  const GradSpace g = grad_space(a.tokens, a.cols);
-  if (g.tiles > 0) {
-    ClusterLaunch l(1, dim3(kThreads), 1, true, 0, stream);
-    l.cfg.gridDim = dim3((unsigned)g.tiles, (unsigned)((a.cols + kCols - 1) / kCols));
-    TIDE_TRY(cuda_status(vec ? cudaLaunchKernelEx(&l.cfg, tiles_kernel<T, false>, a)
-                             : cudaLaunchKernelEx(&l.cfg, tiles_kernel<T, true>, a),
-                         "embedding gradient, frequent tokens"));
+  s.passes = (bits + kDigitBits - 1) / kDigitBits;
+  // Few ids: a block's warps have them all in registers.
+  const int cluster = a.tokens > 1024 ? kSortCluster : 1;
+  if (a.tokens > 0) {
+    const ClusterLaunch l(cluster, dim3(kSortThreads), cluster, false, 0, stream);
+    TIDE_TRY(cuda_status(cudaLaunchKernelEx(&l.cfg, sort_kernel, s), what));
   }
-  const ClusterLaunch l(grid, dim3(kThreads), 1, true, 0, stream);
-  return cuda_status(vec ? cudaLaunchKernelEx(&l.cfg, sum_kernel<T, false>, a)
-                         : cudaLaunchKernelEx(&l.cfg, sum_kernel<T, true>, a),
-                     "embedding gradient");
+  if (!a.accumulate) {
+    // The sort's SMs have no room: a block there would be as late as the sort is long.
+    const int grid = (int)std::min<int64_t>(std::max(1, sms - cluster), a.vocab);
+    const ZeroArgs z{a.tokens, a.vocab, a.cols, s.index, s.ids, a.dweight, a.lddw, a.vectors, FastDiv((uint32_t)grid)};
+    const ClusterLaunch l(grid, dim3(kZeroThreads), 1, a.tokens > 0, 0, stream);
+    TIDE_TRY(cuda_status(cudaLaunchKernelEx(&l.cfg, zero_kernel<T>, z), what));
+  }
+  if (a.tokens == 0) return TIDE_OK;
+  const int64_t tiles = (a.tokens + a.tile - 1) / a.tile;
+  cudaError_t err = cudaSuccess;
+  TIDE_TRY(in_row_launches(tiles, vectors, kThreads, what, [&](int64_t t, uint32_t items, unsigned blocks) {
+    a.tile0 = t, a.items = items;
+    // 32 KB of slots a block, or 48.
+    constexpr int kAhead = sizeof(T) == 2 ? 8 : 4, kAnyAhead = sizeof(T) == 2 ? 6 : 4;
+    const int room = vec ? Coming<T, false, kAhead>::kBytes : Coming<T, true, kAnyAhead>::kBytes;
+    const ClusterLaunch l(blocks, dim3(kThreads), 1, true, room, stream);
+    if (err == cudaSuccess)
+      err = vec ? cudaLaunchKernelEx(&l.cfg, runs_kernel<T, false, kAhead>, a)
+                : cudaLaunchKernelEx(&l.cfg, runs_kernel<T, true, kAnyAhead>, a);
+  }));
+  TIDE_TRY(cuda_status(err, what));
+  if (tiles <= 2) return TIDE_OK;  // no run goes on beyond a second tile
+  const ClusterLaunch l(sms * 2, dim3(kJoinThreads), 1, true, 0, stream);
+  return cuda_status(vec ? cudaLaunchKernelEx(&l.cfg, join_kernel<T, false>, a) : cudaLaunchKernelEx(&l.cfg, join_kernel<T, true>, a),
+                     what);
 }
 
 tide_status check_embedding(int64_t tokens, int64_t vocab, int64_t cols, int32_t index, int32_t dtype, const void* ids) {
@@ -473,11 +638,14 @@ tide_status tide_embedding_backward(int64_t tokens, int64_t vocab, int64_t cols,
     return fail(TIDE_ERR_INVALID_ARG, "workspace too small: " + std::to_string(need) + " bytes are needed");
   if ((uintptr_t)workspace % 16) return fail(TIDE_ERR_ALIGNMENT, "workspace is not 16-byte aligned");
   const GradSpace g = grad_space(tokens, cols);
-  uint32_t* const w = (uint32_t*)workspace;
-  const int64_t n = g.list / 4;
-  const SortArgs s{tokens, vocab, index, ids, w, w + n, w + 2 * n, w + 3 * n, 0};
-  const SumArgs a{tokens, vocab, cols, w, w + n, dy, lddy, scale, dweight, lddw, accumulate,
-                  g.tiles > 0 ? (float*)(w + 4 * n) : nullptr, g.ldt, FastDiv()};
+  uint8_t* const w = (uint8_t*)workspace;
+  uint32_t* list[4];
+  for (int i = 0; i < 4; ++i) list[i] = (uint32_t*)(w + i * g.list);
+  uint32_t* const longs = tokens > 0 ? (uint32_t*)(w + 4 * g.list) : nullptr;
+  float* const parts = (float*)(w + 4 * g.list + g.longs);
+  const SortArgs s{tokens, vocab, index, ids, list[0], list[1], list[2], list[3], 0, g.tile, longs};
+  const SumArgs a{0,  FastDiv(), 0,     tokens,  vocab, cols,       g.tile, list[0], list[1], longs,
+                  dy, lddy,      scale, dweight, lddw,  accumulate, parts};
   return dtype == TIDE_BF16 ? embed_grad<bf16>(a, s, (cudaStream_t)stream) : embed_grad<float>(a, s, (cudaStream_t)stream);
 }
 

@@ -7,12 +7,15 @@
 // The threads' (m, S, E) are joined by the same rule, and
 //   lse = scale m + ln S,   entropy = ln S - ln 2 E / S  (no cancellation: E <= 0),
 //   logp = scale (logit - m) - ln S.
-// Alternatives: each thread also keeps the first vector of eight in which its largest
-// logit stood.  The `top` threads with the largest such (logit, vector) pairs are the only ones
-// that can hold any of the `top` largest logits: against a logit of another thread there are
-// `top` larger ones.  So only those threads' logits, 1 / 25 of a row or less, are read again (L2
-// has them), by whole warps that keep a sorted list of 32 in their lanes.
-//
+// Alternatives: the threads' largest logits, joined by lane, are the largest of 32 disjoint parts of the row,
+// and the `top`-th largest of these 32 is one that `top` logits at least reach.  So all alternatives are
+// among the logits that reach it: 31 are expected for 20 alternatives of a row in random order, 112 for 32.
+// A thread also keeps where its largest stood and the largest of its other vectors: where only the first
+// reaches the bound one vector is read again, else all of the thread's (L2 has them), by the whole warp.  The
+// logits that reach the bound are listed in shared memory, and each finds its rank by counting.
+// Where equal logits make the list too long, or NaN the bound too high, the alternatives are found one
+// after the other instead.
+
 // Backward: element by element, one exponential each.
 
 #include <algorithm>
@@ -51,6 +54,29 @@ __device__ __forceinline__ float exp2_of(float d) {
   return r;
 }
 
+// Two fp32 in one register pair, added and multiplied by one instruction.
+struct Pair {
+  uint64_t v;
+  __device__ __forceinline__ Pair(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
+  __device__ __forceinline__ float2 parts() const {
+    float2 p;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(p.x), "=f"(p.y) : "l"(v));
+    return p;
+  }
+};
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
+  return a;
+}
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
+  return a;
+}
+__device__ __forceinline__ Pair fma_pair(Pair a, Pair b, Pair c) {
+  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(a.v) : "l"(b.v), "l"(c.v));
+  return a;
+}
+
 // What a set of logits leaves: the largest, and the sums over it (none: m is the lowest
 // number, S and E are 0).  An infinite or NaN logit makes S NaN.
 struct Sums {
@@ -71,7 +97,7 @@ struct Sums {
   }
 };
 
-// ---- alternatives: keys that order logits, larger first, ties by the lower place
+// ---- alternatives: keys that order logits, larger first, ties by the lower token
 
 __device__ __forceinline__ uint32_t ordered(float v) {
   v = fmaxf(v, -INFINITY) + 0.0f;  // NaN as -inf, -0 as 0
@@ -81,65 +107,45 @@ __device__ __forceinline__ uint32_t ordered(float v) {
 __device__ __forceinline__ float of_ordered(uint32_t u) {
   return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
 }
-__device__ __forceinline__ uint64_t key_of(float v, uint32_t place) { return (uint64_t)ordered(v) << 32 | (uint32_t)~place; }
+__device__ __forceinline__ uint64_t key_of(float v, uint32_t token) { return (uint64_t)ordered(v) << 32 | (uint32_t)~token; }
 
 __device__ __forceinline__ uint64_t larger(uint64_t a, uint64_t b) { return a > b ? a : b; }
-__device__ __forceinline__ uint64_t smaller(uint64_t a, uint64_t b) { return a < b ? a : b; }
-
-// One exchange of a bitonic network over the warp: lanes j apart, the larger key to the lower
-// lane where `down`.
-__device__ __forceinline__ uint64_t exchange(uint64_t key, int j, bool down) {
-  const uint64_t other = __shfl_xor_sync(0xffffffffu, key, j);
-  const bool low = (threadIdx.x & j) == 0;
-  return low == down ? larger(key, other) : smaller(key, other);
+__device__ __forceinline__ uint64_t warp_largest(uint64_t key) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) key = larger(key, __shfl_xor_sync(0xffffffffu, key, d));
+  return key;
 }
-__device__ __forceinline__ uint64_t sort_down(uint64_t key) {
+
+// The top-th largest of the lanes' values, by a bitonic sort.
+__device__ __forceinline__ float warp_nth(float v, int top) {
 #pragma unroll
   for (int k = 2; k <= 32; k <<= 1)
 #pragma unroll
-    for (int j = k >> 1; j > 0; j >>= 1) key = exchange(key, j, (threadIdx.x & k) == 0 || k == 32);
-  return key;
-}
-// The 32 largest of two lists sorted downwards over the lanes, the second one given backwards.
-__device__ __forceinline__ uint64_t merge_down(uint64_t list, uint64_t backwards) {
-  list = larger(list, backwards);
-#pragma unroll
-  for (int j = 16; j > 0; j >>= 1) list = exchange(list, j, true);
-  return list;
-}
-
-// The row's list, in its first warp, from one list a warp.
-template <int WARPS>
-__device__ __forceinline__ uint64_t merge_warps(uint64_t list, uint64_t (&lists)[WARPS][32]) {
-  if constexpr (WARPS > 1) {
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    lists[warp][lane] = list;
-    __syncthreads();
-#pragma unroll
-    for (int step = 1; step < WARPS; step <<= 1) {
-      if (warp % (2 * step) == 0 && warp + step < WARPS) {
-        list = merge_down(list, lists[warp + step][31 - lane]);
-        lists[warp][lane] = list;
-      }
-      __syncthreads();
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      const float o = __shfl_xor_sync(0xffffffffu, v, j);
+      const bool low = (threadIdx.x & j) == 0, down = k == 32 || (threadIdx.x & k) == 0;
+      v = low == down ? fmaxf(v, o) : fminf(v, o);
     }
-  }
-  return list;
+  return __shfl_sync(0xffffffffu, v, top - 1);
 }
 
 // PER_ROW threads share a row (a warp, or a whole block), or those of a cluster of
 // blocks; a block of warps takes eight rows.
 template <typename T, int PER_ROW, bool CLUSTER, bool ENTROPY, bool TOP>
-__global__ void __launch_bounds__(PER_ROW == 32 ? 256 : PER_ROW, PER_ROW == 512 ? 2 : 4)
+__global__ void __launch_bounds__(PER_ROW == 32 ? 256 : PER_ROW, 1024 / (PER_ROW == 32 ? 256 : PER_ROW))
     log_probs_kernel(const LogProbArgs a) {
   constexpr int WARPS = PER_ROW / 32, kAhead = sizeof(T) == 2 ? 4 : 2;
+  constexpr int kRowsHere = PER_ROW == 32 ? 8 : 1, kRoom = 512;
   __shared__ float stat[3][WARPS];
-  __shared__ uint64_t lists[TOP ? WARPS : 1][32];
-  __shared__ uint64_t bound;
+  __shared__ float largest[TOP ? WARPS : 1][32];
+  __shared__ uint64_t listed[TOP ? kRowsHere : 1][TOP ? kRoom : 1];
+  __shared__ uint32_t listed_count[kRowsHere];
+  __shared__ uint8_t who[TOP ? (PER_ROW == 32 ? 8 : WARPS) : 1][32];
+  __shared__ uint64_t found[TOP ? WARPS + 1 : 1];
   const uint32_t blocks = CLUSTER ? cluster_size() : 1, rank = CLUSTER ? cluster_rank() : 0;
   const int64_t row = PER_ROW == 32 ? (int64_t)blockIdx.x * 8 + threadIdx.x / 32 : (int64_t)(blockIdx.x / blocks);
   if (row >= a.rows) return;  // a whole warp, of rows of one
-  const int x = threadIdx.x % PER_ROW, warp = x / 32, lane = x % 32;
+  const int x = threadIdx.x % PER_ROW, warp = x / 32, lane = x % 32, here = PER_ROW == 32 ? threadIdx.x / 32 : 0;
   const int64_t vocab = a.vocab;
   const T* const logits = (const T*)a.logits + row * a.ldl;
   const float k = a.scale * kLog2e;
@@ -147,6 +153,12 @@ __global__ void __launch_bounds__(PER_ROW == 32 ? 256 : PER_ROW, PER_ROW == 512 
   const int phase = row_phase(logits), count = (int)((vocab + phase + 7) / 8);
   const int lo = phase > 0, hi = (int)((vocab + phase) / 8);
   const int64_t stride = (int64_t)PER_ROW * blocks, first = (int64_t)rank * PER_ROW + x;
+  auto sync = [&]() {
+    if constexpr (WARPS > 1)
+      __syncthreads();
+    else
+      __syncwarp();
+  };
 
   int target = -1;
   float target_logit = 0.0f;
@@ -154,10 +166,12 @@ __global__ void __launch_bounds__(PER_ROW == 32 ? 256 : PER_ROW, PER_ROW == 512 
     target = token_at(a.targets, a.index, row, vocab);
     if (target >= 0) target_logit = (float)logits[target];
   }
+  if (TOP && x == 0) listed_count[here] = 0;
+  __syncwarp();  // for rows of a warp; others have a barrier below
 
   Sums sums;
-  float best = -INFINITY;
-  int64_t best_at = first;
+  int64_t best_at = first;    // the vector in which the largest logit stood first
+  float second = -INFINITY;   // the largest of the others
   for (int64_t v = first; v < count; v += kAhead * stride) {
     Raw8<T> r[kAhead];
     if (v >= lo && v + (kAhead - 1) * stride < hi) {
@@ -178,126 +192,219 @@ __global__ void __launch_bounds__(PER_ROW == 32 ? 256 : PER_ROW, PER_ROW == 512 
       float most = r[j].value(0);
 #pragma unroll
       for (int i = 1; i < 8; ++i) most = fmaxf(most, r[j].value(i));
-      if constexpr (TOP) {
-        if (most > best) best = most, best_at = v + j * stride;
+      if (most > sums.m) {
+        if constexpr (TOP) second = sums.m, best_at = v + j * stride;
+        sums.raise(most, k);
+      } else if constexpr (TOP) {
+        second = fmaxf(second, most);
       }
-      if (most > sums.m) sums.raise(most, k);
+      // Pairs take half the issue slots: 2048 x 131072 bf16 with entropy 97.8 us became 92.3 (256 threads a row).
+      Pair s2(sums.s, 0.0f), e2(sums.e, 0.0f);
+      const Pair down(-sums.m, -sums.m), by(k, k);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float d = (r[j].value(i) - sums.m) * k, p = exp2_of(d);
-        sums.s += p;
-        if constexpr (ENTROPY) sums.e = fmaf(p, fmaxf(d, kLeast), sums.e);
+      for (int i = 0; i < 8; i += 2) {
+        const float2 d = ((Pair(r[j].value(i), r[j].value(i + 1)) + down) * by).parts();
+        const Pair p(exp2_of(d.x), exp2_of(d.y));
+        s2 = s2 + p;
+        if constexpr (ENTROPY) e2 = fma_pair(p, Pair(fmaxf(d.x, kLeast), fmaxf(d.y, kLeast)), e2);
       }
+      sums.s = s2.parts().x + s2.parts().y;
+      if constexpr (ENTROPY) sums.e = e2.parts().x + e2.parts().y;
     }
   }
+  // This thread's largest logit: -inf with none (or no other).
+  const float mine = sums.s == 0.0f ? -INFINITY : sums.m;
 
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    Sums o;
-    o.m = __shfl_xor_sync(0xffffffffu, sums.m, d);
-    o.s = __shfl_xor_sync(0xffffffffu, sums.s, d);
-    o.e = __shfl_xor_sync(0xffffffffu, sums.e, d);
-    // Both lanes of a pair add the same two in the same order.
-    Sums& lower = lane & d ? o : sums;
-    Sums& upper = lane & d ? sums : o;
-    lower.join(upper, k);
-    sums = lower;
-  }
+  auto join_lanes = [&](int lanes) {
+    for (int d = lanes / 2; d > 0; d >>= 1) {
+      Sums o;
+      o.m = __shfl_xor_sync(0xffffffffu, sums.m, d);
+      o.s = __shfl_xor_sync(0xffffffffu, sums.s, d);
+      if (ENTROPY) o.e = __shfl_xor_sync(0xffffffffu, sums.e, d);
+      // Both lanes of a pair add the same two in the same order.
+      Sums& lower = lane & d ? o : sums;
+      Sums& upper = lane & d ? sums : o;
+      lower.join(upper, k);
+      sums = lower;
+    }
+  };
+  join_lanes(32);
+  float bound = mine;  // the largest of the row's part that goes by this lane
   if constexpr (WARPS > 1) {
     if (lane == 0) stat[0][warp] = sums.m, stat[1][warp] = sums.s, stat[2][warp] = sums.e;
-  }
-
-  uint64_t key = 0, list = 0;
-  if constexpr (TOP) {
-    key = first < count ? key_of(best, (uint32_t)best_at) : 0;
-    list = merge_warps(sort_down(key), lists);
-    if constexpr (CLUSTER) {
-      cluster_sync();
-      if (warp == 0) {
-        for (uint32_t b = 0; b < blocks; ++b)
-          if (b != rank) list = merge_down(list, load_peer_u64(peer_smem(&lists[0][31 - lane], b)));
-      }
-      cluster_sync();  // the lists are written again below
-    }
-    const uint64_t least = __shfl_sync(0xffffffffu, list, a.top - 1);
-    if constexpr (WARPS > 1) {
-      if (x == 0) bound = least;
-      __syncthreads();
-    } else {
-      bound = 0;  // not used
-    }
-    const uint64_t from = WARPS > 1 ? bound : least;
-    list = 0;
-    for (uint32_t mine = __ballot_sync(0xffffffffu, key != 0 && key >= from); mine; mine &= mine - 1) {
-      const int64_t start = first - lane + (__ffs(mine) - 1);  // that thread's first vector
-      for (int64_t v = start; v < count; v += 32 * stride) {
-        const int64_t at = v + lane * stride;
-        Raw8<T> r;
-        if (at >= lo && at < hi)
-          r.load(logits + at * 8 - phase);
-        else
-          r.load_some(logits, at * 8 - phase, vocab);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int64_t col = at * 8 - phase + i;
-          const float z = r.value(i);
-          uint64_t one = col >= 0 && col < vocab ? key_of(z, (uint32_t)col) : 0;
-          const uint64_t last = __shfl_sync(0xffffffffu, list, a.top - 1);
-          if (key_of(z, (uint32_t)at) < from || one < last) one = 0;
-          if (__any_sync(0xffffffffu, one != 0)) {
-            one = sort_down(one);
-            list = merge_down(list, __shfl_sync(0xffffffffu, one, 31 - lane));
-          }
-        }
-      }
-    }
-    list = merge_warps(list, lists);
-  } else if constexpr (WARPS > 1) {
+    if constexpr (TOP) largest[warp][lane] = mine;
     __syncthreads();
-  }
-
-  // The row's sums, in the first warp.
-  if constexpr (WARPS > 1) {
-    if (warp == 0) {
-      sums = Sums();
-      for (int w = 0; w < WARPS; ++w) {
-        Sums o;
-        o.m = stat[0][w], o.s = stat[1][w], o.e = stat[2][w];
-        sums.join(o, k);
-      }
+    if constexpr (TOP) {
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) bound = fmaxf(bound, largest[w][lane]);
     }
+    // Every warp joins the warps' sums.
+    sums = Sums();
+    if (lane < WARPS) sums.m = stat[0][lane], sums.s = stat[1][lane], sums.e = stat[2][lane];
+    join_lanes(WARPS);
   }
   if constexpr (CLUSTER) {
-    __syncwarp();  // the first warp has read them
-    if (x == 0) stat[0][0] = sums.m, stat[1][0] = sums.s, stat[2][0] = sums.e;
-    cluster_sync();
-    if (warp == 0 && rank == 0) {
-      for (uint32_t b = 1; b < blocks; ++b) {
-        Sums o;
-        o.m = load_peer_f32(peer_smem(&stat[0][0], b));
-        o.s = load_peer_f32(peer_smem(&stat[1][0], b));
-        o.e = load_peer_f32(peer_smem(&stat[2][0], b));
-        sums.join(o, k);
-        if constexpr (TOP) list = merge_down(list, load_peer_u64(peer_smem(&lists[0][31 - lane], b)));
-      }
+    // The blocks' in their turn, all of each.
+    __syncthreads();
+    if (warp == 0) {
+      if (lane == 0) stat[0][0] = sums.m, stat[1][0] = sums.s, stat[2][0] = sums.e;
+      if constexpr (TOP) largest[0][lane] = bound;
     }
-    cluster_sync();  // no block leaves while it is read
+    cluster_sync();
+    Sums all;
+    for (uint32_t b = 0; b < blocks; ++b) {
+      Sums o;
+      o.m = load_peer_f32(peer_smem(&stat[0][0], b));
+      o.s = load_peer_f32(peer_smem(&stat[1][0], b));
+      o.e = load_peer_f32(peer_smem(&stat[2][0], b));
+      all.join(o, k);
+      if constexpr (TOP) bound = fmaxf(bound, load_peer_f32(peer_smem(&largest[0][lane], b)));
+    }
+    sums = all;
+    cluster_sync();  // no block leaves, or writes there again, while it is read
+  } else if constexpr (WARPS > 1) {
+    sums.m = __shfl_sync(0xffffffffu, sums.m, 0);
+    sums.s = __shfl_sync(0xffffffffu, sums.s, 0);
+    sums.e = __shfl_sync(0xffffffffu, sums.e, 0);
   }
-  if (warp != 0 || rank != 0) return;
+
   const bool empty = sums.s == 0.0f;
   const float log_s = logf(sums.s);
-  if (x == 0) {
+  if (x == 0 && rank == 0) {
     if (a.lse) a.lse[row] = empty ? -INFINITY : fmaf(sums.m, a.scale, log_s);
     if (ENTROPY) a.entropy[row] = empty ? 0.0f : log_s - kLn2 * (sums.e / sums.s);
     if (a.logp) a.logp[row] = target < 0 ? 0.0f : empty ? -INFINITY : fmaf(target_logit - sums.m, a.scale, -log_s);
   }
   if constexpr (TOP) {
-    if (lane < a.top) {
+    const int top = a.top;
+    auto put = [&](int at, uint64_t key) {
       if (a.top_logp)
-        a.top_logp[row * a.ld_logp + lane] =
-            empty ? -INFINITY : fmaf(of_ordered((uint32_t)(list >> 32)) - sums.m, a.scale, -log_s);
-      if (a.top_tokens) a.top_tokens[row * a.ld_tokens + lane] = (int32_t)~(uint32_t)list;
+        a.top_logp[row * a.ld_logp + at] =
+            empty ? -INFINITY : fmaf(of_ordered((uint32_t)(key >> 32)) - sums.m, a.scale, -log_s);
+      if (a.top_tokens) a.top_tokens[row * a.ld_tokens + at] = (int32_t)~(uint32_t)key;
+    };
+    auto load = [&](Raw8<T>& r, int64_t at) {
+      if (at >= lo && at < hi)
+        r.load(logits + at * 8 - phase);
+      else
+        r.load_some(logits, at * 8 - phase, vocab);
+    };
+    // Lists those of a vector's logits that reach the bound.
+    auto list = [&](const Raw8<T>& r, int64_t v) {
+      uint32_t hits = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (r.value(i) >= bound) hits |= 1u << i;
+      if (bound == -INFINITY) {  // whatever there is, NaN as -inf; above, what is not there is -inf
+        hits = 0;
+        for (int i = 0; i < 8; ++i) {
+          const int64_t col = v * 8 - phase + i;
+          if (col >= 0 && col < vocab) hits |= 1u << i;
+        }
+      }
+      if (hits == 0) return;
+      uint32_t at = atomicAdd(&listed_count[here], (uint32_t)__popc(hits));
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (hits >> i & 1) {
+          if (at < kRoom) listed[here][at] = key_of(r.value(i), (uint32_t)(v * 8 - phase + i));
+          ++at;
+        }
+    };
+    bound = warp_nth(bound, top);
+    if (mine >= bound && first < count) {
+      Raw8<T> r;
+      load(r, best_at);
+      list(r, best_at);
     }
+    // The warp's threads that may have met more: all their other vectors, spread over the warp.
+    const bool more = mine >= bound && second >= bound && first < count;
+    const uint32_t some = __ballot_sync(0xffffffffu, more);
+    if (some) {
+      if (more) who[threadIdx.x / 32][__popc(some & ((1u << lane) - 1))] = (uint8_t)lane;
+      __syncwarp();
+      const uint32_t each = (uint32_t)((count - (first - lane) + stride - 1) / stride), all = each * __popc(some);
+      for (uint32_t i0 = 0; i0 < all; i0 += 32 * kAhead) {
+        Raw8<T> r[kAhead];
+        int64_t at[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          const uint32_t i = i0 + j * 32 + lane, thread = i < all ? i / each : 0, l = who[threadIdx.x / 32][thread];
+          const int64_t best = __shfl_sync(0xffffffffu, best_at, l);
+          at[j] = first - lane + l + (int64_t)(i - thread * each) * stride;
+          if (i >= all || at[j] >= count || at[j] == best) at[j] = -1;
+          if (at[j] >= 0) load(r[j], at[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+          if (at[j] >= 0) list(r[j], at[j]);
+      }
+    }
+    uint32_t n = 0;
+    if constexpr (CLUSTER) {
+      cluster_sync();
+      for (uint32_t b = 0; b < blocks; ++b) {
+        const uint32_t c = load_peer_u32(peer_smem(&listed_count[0], b));
+        n = c > kRoom || n + c > kRoom ? kRoom + 1 : n + c;
+      }
+    } else {
+      sync();
+      n = listed_count[here];
+    }
+    if (n >= (uint32_t)top && n <= kRoom) {
+      if constexpr (CLUSTER) {
+        // The first block brings the others' lists to its own.
+        if (rank == 0) {
+          uint32_t at = listed_count[0];
+          for (uint32_t b = 1; b < blocks; ++b) {
+            const uint32_t c = load_peer_u32(peer_smem(&listed_count[0], b));
+            if ((uint32_t)x < c) listed[0][at + x] = load_peer_u64(peer_smem(&listed[0][x], b));
+            at += c;
+          }
+          __syncthreads();
+        }
+        if (rank != 0) n = 0;
+      }
+      for (uint32_t i = x; i < n; i += PER_ROW) {
+        const uint64_t key = listed[here][i];
+        int above = 0;
+        for (uint32_t j = 0; j < n; ++j) above += listed[here][j] > key;
+        if (above < top) put(above, key);
+      }
+    } else {
+      // One after the other: the largest key below the last one.
+      uint64_t last = ~0ull;
+      for (int i = 0; i < top; ++i) {
+        uint64_t key = 0;
+        for (int64_t v = first; v < count; v += stride) {
+          Raw8<T> r;
+          load(r, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int64_t col = v * 8 - phase + j;
+            const uint64_t one = key_of(r.value(j), (uint32_t)col);
+            if (col >= 0 && col < vocab && one < last) key = larger(key, one);
+          }
+        }
+        key = warp_largest(key);
+        if constexpr (WARPS > 1) {
+          if (lane == 0) found[warp] = key;
+          __syncthreads();
+          key = warp_largest(lane < WARPS ? found[lane] : 0);
+          if constexpr (CLUSTER) {
+            if (x == 0) found[WARPS] = key;
+            cluster_sync();
+            for (uint32_t b = 0; b < blocks; ++b) key = larger(key, load_peer_u64(peer_smem(&found[WARPS], b)));
+            cluster_sync();
+          } else {
+            __syncthreads();
+          }
+        }
+        if (x == 0 && rank == 0) put(i, key);
+        last = key;
+      }
+    }
+    if constexpr (CLUSTER) cluster_sync();  // no block leaves while its list is read
   }
 }
 
@@ -406,9 +513,16 @@ template <typename T>
 tide_status log_probs(const LogProbArgs& a, cudaStream_t stream) {
   const int sms = ops_num_sms();
   if (sms <= 0) return fail(TIDE_ERR_CUDA, "the current device could not be queried");
-  // A warp for short rows, a block for long ones; where they are too few to fill the GPU,
-  // up to eight blocks share a row, while each thread has a vector or more.
+  // The fewest threads a row that still fill the SMs with the threads their registers hold, since
+  // what is not a thread's own logits costs each of them alike (16384 x 4999 bf16: 39 us with a warp a row, 80
+  // with 128 threads, 112 with 256; 2048 x 131072: 124, 92 and 92).  Alternatives of long rows ask for 128: a warp's
+  // lanes hold too much of such a row to read again (16384 x 8192 with 20: 105 and 114 us, 16384 x 16384
+  // 180 and 154, 4096 x 65536 221 and 113).
   const int64_t vectors = a.vocab / 8;
+  int want = 32;
+  for (const int next : {128, 256, 512})
+    if (vectors >= next && (a.rows * want < (int64_t)sms * 1024 || (a.top > 0 && vectors > 1536 && next == 128))) want = next;
+  // Still too few: up to eight blocks share a row, while each thread has a vector or more.
   int cluster = 1;
   if (vectors > 1024)
     while (cluster < 8 && a.rows * cluster * 2 <= 2 * sms && vectors >= (int64_t)cluster * 2 * 512) cluster *= 2;
@@ -423,9 +537,11 @@ tide_status log_probs(const LogProbArgs& a, cudaStream_t stream) {
       };
       if (cluster > 1)
         go(std::integral_constant<int, 512>(), std::true_type());
-      else if (vectors > 1024)
+      else if (want == 512)
         go(std::integral_constant<int, 512>(), std::false_type());
-      else if (vectors > 128)
+      else if (want == 256)
+        go(std::integral_constant<int, 256>(), std::false_type());
+      else if (want == 128)
         go(std::integral_constant<int, 128>(), std::false_type());
       else
         go(std::integral_constant<int, 32>(), std::false_type());
