@@ -77,7 +77,7 @@ CASES = [
     (embed_grad, dict(vocab=0), OK), (embed_grad, dict(cols=0), OK), (embed_grad, dict(tokens=0, add=1), OK),
     (embed_grad, dict(vocab=(1 << 31) - 1), UNIMPLEMENTED), (embed_grad, dict(dw=P + 1), ALIGNMENT),
     (embed_grad, dict(dtype=2), INVALID), (embed_grad, dict(ids=None), INVALID),
-    (embed_grad, dict(vocab=(1 << 31) - 2, cols=1 << 20, lddy=1 << 20, lddw=1 << 20, wsb=1 << 40), UNIMPLEMENTED),
+    (embed_grad, dict(cols=(1 << 24) + 1, lddy=BIG, lddw=BIG), UNIMPLEMENTED),
     (probs, dict(rows=-1), INVALID), (probs, dict(vocab=-1), INVALID), (probs, dict(dtype=2), INVALID),
     (probs, dict(z=None), INVALID), (probs, dict(ldz=39), INVALID), (probs, dict(z=P + 1), ALIGNMENT),
     (probs, dict(scale=0.0), INVALID), (probs, dict(scale=-1.0), INVALID), (probs, dict(scale=math.inf), INVALID),
