@@ -13,8 +13,9 @@
 // A thread also keeps where its largest stood and the largest of its other vectors: where only the first
 // reaches the bound one vector is read again, else all of the thread's (L2 has them), by the whole warp.  The
 // logits that reach the bound are listed in shared memory, and each finds its rank by counting.
-// Where equal logits make the list too long, or NaN the bound too high, the alternatives are found one
-// after the other instead.
+// Where equal logits make the list too long only those above the bound are listed, and the first of the ones at it.
+// Where all that fails (more than 512 different logits above a bound, NaN that makes it too high) the alternatives
+// are found one after the other.
 
 // Backward: element by element, one exponential each.
 
@@ -40,7 +41,7 @@ struct LogProbArgs {
   float scale;
   int32_t index;
   const void* targets;
-  float *logp, *lse, *entropy;
+  float *logp, *lse, *lse_parts, *entropy;
   int32_t top;
   float* top_logp;
   int64_t ld_logp;
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(PER_ROW == 32 ? 256 : PER_ROW, 1024 / (PER_ROW
   // Vectors of the row that are whole: from `lo` to below `hi`.
   const int phase = row_phase(logits), count = (int)((vocab + phase + 7) / 8);
   const int lo = phase > 0, hi = (int)((vocab + phase) / 8);
-  const int64_t stride = (int64_t)PER_ROW * blocks, first = (int64_t)rank * PER_ROW + x;
+  const int stride = PER_ROW * (int)blocks, first = (int)rank * PER_ROW + x;  // vectors are fewer than 2^28
   auto sync = [&]() {
     if constexpr (WARPS > 1)
       __syncthreads();
@@ -170,46 +171,55 @@ __global__ void __launch_bounds__(PER_ROW == 32 ? 256 : PER_ROW, 1024 / (PER_ROW
   __syncwarp();  // for rows of a warp; others have a barrier below
 
   Sums sums;
-  int64_t best_at = first;    // the vector in which the largest logit stood first
-  float second = -INFINITY;   // the largest of the others
-  for (int64_t v = first; v < count; v += kAhead * stride) {
+  int best_at = first;   // the vector in which the largest logit stood first
+  float second = -INFINITY;  // the largest of the others
+  for (int v = first; v < count; v += kAhead * stride) {
     Raw8<T> r[kAhead];
     if (v >= lo && v + (kAhead - 1) * stride < hi) {
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) r[j].load(logits + (v + j * stride) * 8 - phase);
+      for (int j = 0; j < kAhead; ++j) r[j].load(logits + (int64_t)(v + j * stride) * 8 - phase);
     } else {
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
-        const int64_t at = v + j * stride;
+        const int at = v + j * stride;
         if (at >= lo && at < hi)
-          r[j].load(logits + at * 8 - phase);
+          r[j].load(logits + (int64_t)at * 8 - phase);
         else
-          r[j].load_some(logits, at * 8 - phase, vocab);
+          r[j].load_some(logits, (int64_t)at * 8 - phase, vocab);
       }
     }
+    // Alternatives want each vector's largest logit; else one rise for all of them will do.
+    constexpr int kAtOnce = TOP || !ENTROPY ? 1 : kAhead;
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      float most = r[j].value(0);
+    for (int j = 0; j < kAhead; j += kAtOnce) {
+      auto value = [&](int i) { return r[j + i / 8].value(i % 8); };
+      float most = value(0);
 #pragma unroll
-      for (int i = 1; i < 8; ++i) most = fmaxf(most, r[j].value(i));
+      for (int i = 1; i < 8 * kAtOnce; ++i) most = fmaxf(most, value(i));
       if (most > sums.m) {
         if constexpr (TOP) second = sums.m, best_at = v + j * stride;
         sums.raise(most, k);
       } else if constexpr (TOP) {
         second = fmaxf(second, most);
       }
-      // Pairs take half the issue slots: 2048 x 131072 bf16 with entropy 97.8 us became 92.3 (256 threads a row).
-      Pair s2(sums.s, 0.0f), e2(sums.e, 0.0f);
-      const Pair down(-sums.m, -sums.m), by(k, k);
+      if constexpr (ENTROPY) {
+        // In pairs, which take half the issue slots (4096 x 131072 bf16 172 us became 168; without the entropy they
+        // were slower, 162 against 156).
+        Pair s2(sums.s, 0.0f), e2(sums.e, 0.0f);
+        const Pair down(-sums.m, -sums.m), by(k, k);
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        const float2 d = ((Pair(r[j].value(i), r[j].value(i + 1)) + down) * by).parts();
-        const Pair p(exp2_of(d.x), exp2_of(d.y));
-        s2 = s2 + p;
-        if constexpr (ENTROPY) e2 = fma_pair(p, Pair(fmaxf(d.x, kLeast), fmaxf(d.y, kLeast)), e2);
+        for (int i = 0; i < 8 * kAtOnce; i += 2) {
+          const float2 d = ((Pair(value(i), value(i + 1)) + down) * by).parts();
+          const Pair p(exp2_of(d.x), exp2_of(d.y));
+          s2 = s2 + p;
+          e2 = fma_pair(p, Pair(fmaxf(d.x, kLeast), fmaxf(d.y, kLeast)), e2);
+        }
+        sums.s = s2.parts().x + s2.parts().y;
+        sums.e = e2.parts().x + e2.parts().y;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8 * kAtOnce; ++i) sums.s += exp2_of((value(i) - sums.m) * k);
       }
-      sums.s = s2.parts().x + s2.parts().y;
-      if constexpr (ENTROPY) sums.e = e2.parts().x + e2.parts().y;
     }
   }
   // This thread's largest logit: -inf with none (or no other).
@@ -272,6 +282,7 @@ __global__ void __launch_bounds__(PER_ROW == 32 ? 256 : PER_ROW, 1024 / (PER_ROW
   const float log_s = logf(sums.s);
   if (x == 0 && rank == 0) {
     if (a.lse) a.lse[row] = empty ? -INFINITY : fmaf(sums.m, a.scale, log_s);
+    if (a.lse_parts) a.lse_parts[2 * row] = empty ? -INFINITY : sums.m, a.lse_parts[2 * row + 1] = log_s;
     if (ENTROPY) a.entropy[row] = empty ? 0.0f : log_s - kLn2 * (sums.e / sums.s);
     if (a.logp) a.logp[row] = target < 0 ? 0.0f : empty ? -INFINITY : fmaf(target_logit - sums.m, a.scale, -log_s);
   }
@@ -283,88 +294,132 @@ __global__ void __launch_bounds__(PER_ROW == 32 ? 256 : PER_ROW, 1024 / (PER_ROW
             empty ? -INFINITY : fmaf(of_ordered((uint32_t)(key >> 32)) - sums.m, a.scale, -log_s);
       if (a.top_tokens) a.top_tokens[row * a.ld_tokens + at] = (int32_t)~(uint32_t)key;
     };
-    auto load = [&](Raw8<T>& r, int64_t at) {
+    auto load = [&](Raw8<T>& r, int at) {
       if (at >= lo && at < hi)
-        r.load(logits + at * 8 - phase);
+        r.load(logits + (int64_t)at * 8 - phase);
       else
-        r.load_some(logits, at * 8 - phase, vocab);
+        r.load_some(logits, (int64_t)at * 8 - phase, vocab);
     };
-    // Lists those of a vector's logits that reach the bound.
-    auto list = [&](const Raw8<T>& r, int64_t v) {
+    // Which of a vector's logits reach a finite limit (what is not there is -inf).
+    auto reach = [&](const Raw8<T>& r, float limit) {
       uint32_t hits = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (r.value(i) >= bound) hits |= 1u << i;
-      if (bound == -INFINITY) {  // whatever there is, NaN as -inf; above, what is not there is -inf
-        hits = 0;
-        for (int i = 0; i < 8; ++i) {
-          const int64_t col = v * 8 - phase + i;
-          if (col >= 0 && col < vocab) hits |= 1u << i;
-        }
-      }
+        if (r.value(i) >= limit) hits |= 1u << i;
+      return hits;
+    };
+    auto list = [&](const Raw8<T>& r, int v, uint32_t hits) {
       if (hits == 0) return;
       uint32_t at = atomicAdd(&listed_count[here], (uint32_t)__popc(hits));
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (hits >> i & 1) {
-          if (at < kRoom) listed[here][at] = key_of(r.value(i), (uint32_t)(v * 8 - phase + i));
+          if (at < kRoom) listed[here][at] = key_of(r.value(i), (uint32_t)v * 8 - (uint32_t)(phase - i));
           ++at;
         }
     };
     bound = warp_nth(bound, top);
-    if (mine >= bound && first < count) {
-      Raw8<T> r;
-      load(r, best_at);
-      list(r, best_at);
-    }
-    // The warp's threads that may have met more: all their other vectors, spread over the warp.
-    const bool more = mine >= bound && second >= bound && first < count;
-    const uint32_t some = __ballot_sync(0xffffffffu, more);
-    if (some) {
-      if (more) who[threadIdx.x / 32][__popc(some & ((1u << lane) - 1))] = (uint8_t)lane;
-      __syncwarp();
-      const uint32_t each = (uint32_t)((count - (first - lane) + stride - 1) / stride), all = each * __popc(some);
-      for (uint32_t i0 = 0; i0 < all; i0 += 32 * kAhead) {
-        Raw8<T> r[kAhead];
-        int64_t at[kAhead];
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          const uint32_t i = i0 + j * 32 + lane, thread = i < all ? i / each : 0, l = who[threadIdx.x / 32][thread];
-          const int64_t best = __shfl_sync(0xffffffffu, best_at, l);
-          at[j] = first - lane + l + (int64_t)(i - thread * each) * stride;
-          if (i >= all || at[j] >= count || at[j] == best) at[j] = -1;
-          if (at[j] >= 0) load(r[j], at[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-          if (at[j] >= 0) list(r[j], at[j]);
-      }
-    }
+    // Logits that reach the bound; where too many do (or the bound is that of masked ones), those above
+    // it, and of the ones at it as many as it takes, the lowest tokens, below.
+    bool strict = bound == -INFINITY;
     uint32_t n = 0;
-    if constexpr (CLUSTER) {
-      cluster_sync();
-      for (uint32_t b = 0; b < blocks; ++b) {
-        const uint32_t c = load_peer_u32(peer_smem(&listed_count[0], b));
-        n = c > kRoom || n + c > kRoom ? kRoom + 1 : n + c;
+    for (;;) {
+      const float limit = strict ? nextafterf(bound, INFINITY) : bound;  // of +inf itself; NaN rows alone have that
+      if (mine >= limit && first < count) {
+        Raw8<T> r;
+        load(r, best_at);
+        list(r, best_at, reach(r, limit));
       }
-    } else {
-      sync();
-      n = listed_count[here];
-    }
-    if (n >= (uint32_t)top && n <= kRoom) {
-      if constexpr (CLUSTER) {
-        // The first block brings the others' lists to its own.
-        if (rank == 0) {
-          uint32_t at = listed_count[0];
-          for (uint32_t b = 1; b < blocks; ++b) {
-            const uint32_t c = load_peer_u32(peer_smem(&listed_count[0], b));
-            if ((uint32_t)x < c) listed[0][at + x] = load_peer_u64(peer_smem(&listed[0][x], b));
-            at += c;
+      // The warp's threads that may have met more: all their other vectors, spread over the warp.
+      const bool more = mine >= limit && second >= limit && first < count;
+      const uint32_t some = __ballot_sync(0xffffffffu, more);
+      if (some) {
+        if (more) who[threadIdx.x / 32][__popc(some & ((1u << lane) - 1))] = (uint8_t)lane;
+        __syncwarp();
+        const uint32_t each = (uint32_t)((count - (first - lane) + stride - 1) / stride), all = each * __popc(some);
+        for (uint32_t i0 = 0; i0 < all; i0 += 32 * kAhead) {
+          Raw8<T> r[kAhead];
+          int at[kAhead];
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j) {
+            const uint32_t i = i0 + j * 32 + lane, thread = i < all ? i / each : 0, l = who[threadIdx.x / 32][thread];
+            const int best = __shfl_sync(0xffffffffu, best_at, l);
+            at[j] = first - lane + (int)l + (int)(i - thread * each) * stride;
+            if (i >= all || at[j] >= count || at[j] == best) at[j] = -1;
+            if (at[j] >= 0) load(r[j], at[j]);
           }
-          __syncthreads();
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j)
+            if (at[j] >= 0) list(r[j], at[j], reach(r[j], limit));
         }
-        if (rank != 0) n = 0;
       }
+      if constexpr (CLUSTER) {
+        cluster_sync();
+        n = 0;
+        for (uint32_t b = 0; b < blocks; ++b) {
+          const uint32_t c = load_peer_u32(peer_smem(&listed_count[0], b));
+          n = c > kRoom || n + c > kRoom ? kRoom + 1 : n + c;
+        }
+      } else {
+        sync();
+        n = listed_count[here];
+      }
+      if (strict || n <= kRoom) break;
+      strict = true;
+      if constexpr (CLUSTER)
+        cluster_sync();
+      else
+        sync();
+      if (x == 0) listed_count[here] = 0;
+      sync();
+    }
+    if constexpr (CLUSTER) {
+      // The first block brings the others' lists to its own.
+      if (rank == 0 && n <= kRoom) {
+        uint32_t at = listed_count[0];
+        for (uint32_t b = 1; b < blocks; ++b) {
+          const uint32_t c = load_peer_u32(peer_smem(&listed_count[0], b));
+          if ((uint32_t)x < c) listed[0][at + x] = load_peer_u64(peer_smem(&listed[0][x], b));
+          at += c;
+        }
+        __syncthreads();
+      }
+    }
+    // The ones at the bound, 32 vectors at a time in order, by one warp, until there are enough.
+    constexpr uint32_t kSweep = 256;
+    if (strict && n < (uint32_t)top) {
+      if constexpr (CLUSTER) {
+        cluster_sync();  // all have read the counts
+        if (x == 0 && rank == 0) listed_count[0] = n;
+      }
+      __syncwarp();
+      if (warp == 0 && rank == 0) {
+        for (int v = lane; v - lane < count; v += 32) {
+          if (v < count) {
+            Raw8<T> r;
+            load(r, v);
+            uint32_t hits = 0;
+            for (int i = 0; i < 8; ++i)
+              if (fmaxf(r.value(i), -INFINITY) == bound && (int64_t)v * 8 - phase + i >= 0 && (int64_t)v * 8 - phase + i < vocab) hits |= 1u << i;
+            list(r, v, hits);
+          }
+          __syncwarp();
+          const uint32_t so_far = *(volatile uint32_t*)&listed_count[here];
+          __syncwarp();
+          if (so_far >= (uint32_t)top) break;
+        }
+      }
+      if constexpr (CLUSTER) {
+        cluster_sync();
+        n = load_peer_u32(peer_smem(&listed_count[0], 0));
+      } else {
+        sync();
+        n = listed_count[here];
+      }
+    }
+    static_assert(kMaxTop + kSweep <= kRoom, "fewer than top are listed when a sweep begins");
+    if (n >= (uint32_t)top && n <= kRoom) {
+      if (rank != 0) n = 0;
       for (uint32_t i = x; i < n; i += PER_ROW) {
         const uint64_t key = listed[here][i];
         int above = 0;
@@ -376,12 +431,12 @@ __global__ void __launch_bounds__(PER_ROW == 32 ? 256 : PER_ROW, 1024 / (PER_ROW
       uint64_t last = ~0ull;
       for (int i = 0; i < top; ++i) {
         uint64_t key = 0;
-        for (int64_t v = first; v < count; v += stride) {
+        for (int v = first; v < count; v += stride) {
           Raw8<T> r;
           load(r, v);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const int64_t col = v * 8 - phase + j;
+            const int64_t col = (int64_t)v * 8 - phase + j;
             const uint64_t one = key_of(r.value(j), (uint32_t)col);
             if (col >= 0 && col < vocab && one < last) key = larger(key, one);
           }
@@ -417,7 +472,7 @@ struct GradArgs {
   const void* logits;
   int64_t ldl;
   float scale;
-  const float* lse;
+  const float *lse, *lse_parts;
   int32_t index;
   const void* targets;
   const float *dlogp, *entropy, *dentropy;
@@ -425,14 +480,18 @@ struct GradArgs {
   int64_t ldd;
 };
 
-// A row's gradient: p (a + b ln p), and g more at the target.
+// A row's gradient: p (a + b ln p), and g more at the target, with ln p = (logit - peak) scale - rest.
 struct RowGrad {
-  float lse, a, b, g;
+  float peak, rest, a, b, g;
   int target;
-  __device__ __forceinline__ RowGrad(const GradArgs& p, int64_t row) : g(0.0f), target(-1) {
-    lse = p.lse[row];
-    const bool empty = lse == -INFINITY;
-    if (empty) lse = INFINITY;  // every p is 0
+  __device__ __forceinline__ void load(const GradArgs& p, int64_t row) {
+    peak = 0.0f, g = 0.0f, target = -1;
+    if (p.lse_parts)
+      peak = p.lse_parts[2 * row], rest = p.lse_parts[2 * row + 1];
+    else
+      rest = p.lse[row];
+    const bool empty = rest == -INFINITY;
+    if (empty) peak = 0.0f, rest = INFINITY;  // every p is 0
     float h = 0.0f, entropy = 0.0f;
     if (p.dentropy) h = p.dentropy[row], entropy = p.entropy[row];
     if (p.targets) {
@@ -444,12 +503,24 @@ struct RowGrad {
   }
 };
 
+// The gradient of a vector's logits; at: the target's place in it, if it is there.
 template <typename T, bool ENTROPY>
-__device__ __forceinline__ float grad_of(float z, const RowGrad& r, float scale) {
-  const float d = fmaf(z, scale, -r.lse);
-  const float p = sizeof(T) == 2 ? exp2_of(d * kLog2e) : expf(d);
-  if constexpr (ENTROPY) return p * fmaf(r.b, fmaxf(d, kLeast), r.a);
-  return p * r.a;
+__device__ __forceinline__ void grad_of(float (&z)[8], const RowGrad& r, float scale, int64_t at) {
+  const Pair down(-r.peak, -r.peak), by(scale, scale), rest(-r.rest, -r.rest), a(r.a, r.a), b(r.b, r.b),
+      to_two(kLog2e, kLog2e);
+#pragma unroll
+  for (int k = 0; k < 8; k += 2) {
+    const Pair d2 = fma_pair(Pair(z[k], z[k + 1]) + down, by, rest);
+    const float2 d = d2.parts(), t = (d2 * to_two).parts();
+    const Pair p = sizeof(T) == 2 ? Pair(exp2_of(t.x), exp2_of(t.y)) : Pair(expf(d.x), expf(d.y));
+    const float2 g = (p * (ENTROPY ? fma_pair(b, Pair(fmaxf(d.x, kLeast), fmaxf(d.y, kLeast)), a) : a)).parts();
+    z[k] = g.x, z[k + 1] = g.y;
+  }
+  if (at >= 0 && at < 8) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k == at) z[k] += r.g;
+  }
 }
 
 constexpr int kThreads = 256, kItems = 4;
@@ -468,14 +539,15 @@ __global__ void __launch_bounds__(kThreads) grad_vec_kernel(const GradArgs a) {
     v[j] = i - row[j] * a.per_row.d;
     if (here[j]) r[j].load((const T*)a.logits + (a.row0 + row[j]) * a.ldl + (int64_t)v[j] * 8);
   }
+  RowGrad g;
 #pragma unroll
   for (int j = 0; j < kItems; ++j) {
     if (!here[j]) continue;
-    const RowGrad g(a, a.row0 + row[j]);
+    if (j == 0 || row[j] != row[j - 1]) g.load(a, a.row0 + row[j]);
     float d[8];
-    const int at = g.target - (int)(v[j] * 8);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) d[k] = grad_of<T, ENTROPY>(r[j].value(k), g, a.scale) + (k == at ? g.g : 0.0f);
+    for (int k = 0; k < 8; ++k) d[k] = r[j].value(k);
+    grad_of<T, ENTROPY>(d, g, a.scale, g.target < 0 ? -1 : g.target - (int64_t)v[j] * 8);
     store_vec<8>((T*)a.out + (a.row0 + row[j]) * a.ldd + (int64_t)v[j] * 8, d);
   }
 }
@@ -492,9 +564,9 @@ __global__ void __launch_bounds__(kThreads) grad_any_kernel(const GradArgs a) {
   if (col >= a.vocab) return;
   float d[8];
   load_columns((const T*)a.logits + row * a.ldl, col, a.vocab, d);
-  const RowGrad g(a, row);
-#pragma unroll
-  for (int k = 0; k < 8; ++k) d[k] = grad_of<T, ENTROPY>(d[k], g, a.scale) + (g.target >= 0 && col + k == g.target ? g.g : 0.0f);
+  RowGrad g;
+  g.load(a, row);
+  grad_of<T, ENTROPY>(d, g, a.scale, g.target < 0 ? -1 : g.target - col);
   store_columns(out, col, a.vocab, d);
 }
 
@@ -584,8 +656,8 @@ using namespace tide;
 extern "C" {
 
 tide_status tide_log_probs(int64_t rows, int64_t vocab, int32_t dtype, const void* logits, int64_t ldl, float scale,
-                           int32_t index, const void* targets, float* logp, float* lse, float* entropy, int32_t top,
-                           float* top_logp, int64_t ld_top_logp, int32_t* top_tokens, int64_t ld_top_tokens,
+                           int32_t index, const void* targets, float* logp, float* lse, float* lse_parts,
+                           float* entropy, int32_t top, float* top_logp, int64_t ld_top_logp, int32_t* top_tokens, int64_t ld_top_tokens,
                            void* stream) {
   clear_error();
   TIDE_TRY(check_logits(rows, vocab, dtype, logits, ldl, scale));
@@ -598,26 +670,30 @@ tide_status tide_log_probs(int64_t rows, int64_t vocab, int32_t dtype, const voi
     TIDE_TRY(check_matrix(logp, 1, rows, rows, 4, "logp"));
   }
   if (lse) TIDE_TRY(check_matrix(lse, 1, rows, rows, 4, "lse"));
+  if (lse_parts) TIDE_TRY(check_matrix(lse_parts, rows, 2, 2, 4, "lse_parts"));
   if (entropy) TIDE_TRY(check_matrix(entropy, 1, rows, rows, 4, "entropy"));
   if (top > 0 && top_logp) TIDE_TRY(check_matrix(top_logp, rows, top, ld_top_logp, 4, "top_logp"));
   if (top > 0 && top_tokens) TIDE_TRY(check_matrix(top_tokens, rows, top, ld_top_tokens, 4, "top_tokens"));
   if (!top_logp && !top_tokens) top = 0;
-  if (!logp && !lse && !entropy && top == 0) return TIDE_OK;
-  const LogProbArgs a{rows, vocab,   logits, ldl,      scale,       index,      targets, logp,
-                      lse,  entropy, top,    top_logp, ld_top_logp, top_tokens, ld_top_tokens};
+  if (!logp && !lse && !lse_parts && !entropy && top == 0) return TIDE_OK;
+  const LogProbArgs a{rows,    vocab,   logits, ldl, scale,    index,       targets,    logp,
+                      lse,     lse_parts, entropy, top, top_logp, ld_top_logp, top_tokens, ld_top_tokens};
   return dtype == TIDE_BF16 ? log_probs<bf16>(a, (cudaStream_t)stream) : log_probs<float>(a, (cudaStream_t)stream);
 }
 
 tide_status tide_log_probs_backward(int64_t rows, int64_t vocab, int32_t dtype, const void* logits, int64_t ldl,
-                                    float scale, const float* lse, int32_t index, const void* targets,
-                                    const float* dlogp, const float* entropy, const float* dentropy, void* dlogits,
+                                    float scale, const float* lse, const float* lse_parts, int32_t index,
+                                    const void* targets, const float* dlogp, const float* entropy, const float* dentropy, void* dlogits,
                                     int64_t ldd, void* stream) {
   clear_error();
   TIDE_TRY(check_logits(rows, vocab, dtype, logits, ldl, scale));
   if (rows == 0 || vocab == 0) return TIDE_OK;
   if (!targets != !dlogp) return fail(TIDE_ERR_INVALID_ARG, "targets and dlogp go together");
   if (!entropy != !dentropy) return fail(TIDE_ERR_INVALID_ARG, "entropy and dentropy go together");
-  TIDE_TRY(check_matrix(lse, 1, rows, rows, 4, "lse"));
+  if (lse_parts)
+    TIDE_TRY(check_matrix(lse_parts, rows, 2, 2, 4, "lse_parts"));
+  else
+    TIDE_TRY(check_matrix(lse, 1, rows, rows, 4, "lse"));
   if (targets) {
     TIDE_TRY(check_index(index));
     TIDE_TRY(check_matrix(targets, 1, rows, rows, index_bytes_of(index), "targets"));
@@ -628,8 +704,8 @@ tide_status tide_log_probs_backward(int64_t rows, int64_t vocab, int32_t dtype, 
     TIDE_TRY(check_matrix(dentropy, 1, rows, rows, 4, "dentropy"));
   }
   TIDE_TRY(check_matrix(dlogits, rows, vocab, ldd, elem_bytes_of(dtype), "dlogits"));
-  const GradArgs a{0,       FastDiv(), 0,     vocab,   logits,   ldl,     scale, lse,
-                   index,   targets,   dlogp, entropy, dentropy, dlogits, ldd};
+  const GradArgs a{0,     FastDiv(), 0,     vocab, logits,  ldl,      scale,   lse,
+                   lse_parts, index,   targets, dlogp, entropy, dentropy, dlogits, ldd};
   return dtype == TIDE_BF16 ? log_probs_grad<bf16>(a, rows, (cudaStream_t)stream)
                             : log_probs_grad<float>(a, rows, (cudaStream_t)stream);
 }

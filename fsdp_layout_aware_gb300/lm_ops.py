@@ -25,9 +25,9 @@ def _declare():
         "tide_embedding": (_i32, 3 * [_i64] + [_i32, _vp, _i32] + _MAT + [_f32] + _MAT + [_vp]),
         "tide_embedding_backward_workspace": (_i64, 3 * [_i64]),
         "tide_embedding_backward": (_i32, 3 * [_i64] + [_i32, _vp, _i32] + _MAT + [_f32] + _MAT + [_i32, _vp, _i64, _vp]),
-        "tide_log_probs": (_i32, [_i64, _i64, _i32] + _MAT + [_f32, _i32, _vp, _vp, _vp, _vp, _i32] + 2 * _MAT + [_vp]),
-        "tide_log_probs_backward": (_i32, [_i64, _i64, _i32] + _MAT + [_f32, _vp, _i32, _vp, _vp, _vp, _vp] + _MAT +
-                                    [_vp]),
+        "tide_log_probs": (_i32, [_i64, _i64, _i32] + _MAT + [_f32, _i32] + 5 * [_vp] + [_i32] + 2 * _MAT + [_vp]),
+        "tide_log_probs_backward": (_i32, [_i64, _i64, _i32] + _MAT + [_f32, _vp, _vp, _i32] + 4 * [_vp] +
+                                    _MAT + [_vp]),
         "tide_grad_norm_workspace": (_i64, [_i32, _vp, _vp]),
         "tide_grad_norm": (_i32, lists + [_vp, _vp, _i64, _vp]),
         "tide_grad_clip": (_i32, [_i32, _vp, _vp, _vp, _vp, _vp, _f32, _f32, _vp]),
@@ -77,9 +77,20 @@ def tide_embedding_backward(ids, dy, dweight, scale=1.0, accumulate=False, works
     _check(_lib.tide_embedding_backward(*args, ws, ws_bytes, _stream(stream)))
 
 
-def tide_log_probs(logits, targets=None, logp=None, lse=None, entropy=None, top=None, scale=1.0, stream=None):
-    """For each row of z = scale * logits: logp = log softmax(z)[targets] (0 for a target outside the vocabulary), lse,
-    entropy, and top, a pair (log probabilities, int32 tokens) of (rows, k) tensors for the k likeliest tokens."""
+def _parts(t, rows, dev):
+    """Address of lse's parts, a contiguous (rows, 2) tensor or None."""
+    if t is None:
+        return None
+    at, ld = _mat(t, "lse_parts", rows, 2, torch.float32, dev)
+    if rows > 1 and ld != 2:
+        _refuse("lse_parts is not contiguous")
+    return at
+
+
+def tide_log_probs(logits, targets=None, logp=None, lse=None, entropy=None, top=None, scale=1.0, lse_parts=None, stream=None):
+    """For each row of z = scale * logits: logp = log softmax(z)[targets] (0 for a target outside the vocabulary), lse
+    (and lse_parts, (rows, 2): the largest logit, and the rest of lse), entropy, and top, a pair (log probabilities, int32
+    tokens) of (rows, k) tensors for the k likeliest tokens."""
     dev = _device()
     rows, vocab = _shape2(logits, "logits")
     f32 = torch.float32
@@ -90,18 +101,19 @@ def tide_log_probs(logits, targets=None, logp=None, lse=None, entropy=None, top=
         best = (*_mat(top[0], "top[0]", rows, k, f32, dev), *_mat(top[1], "top[1]", rows, k, torch.int32, dev))
     _check(_lib.tide_log_probs(rows, vocab, _dtype(logits, "logits"), *_mat(logits, "logits", rows, vocab, logits.dtype, dev),
                                scale, index, at, _optv(logp, "logp", rows, f32, dev), _optv(lse, "lse", rows, f32, dev),
-                               _optv(entropy, "entropy", rows, f32, dev), k, *best, _stream(stream)))
+                               _parts(lse_parts, rows, dev), _optv(entropy, "entropy", rows, f32, dev), k, *best, _stream(stream)))
 
 
 def tide_log_probs_backward(logits, lse, dlogits, targets=None, dlogp=None, entropy=None, dentropy=None, scale=1.0,
-                            stream=None):
-    """dlogits of tide_log_probs' logp (dlogp, with targets) and entropy (dentropy, with entropy); may be logits."""
+                            lse_parts=None, stream=None):
+    """dlogits of tide_log_probs' logp (dlogp, with targets) and entropy (dentropy, with entropy); may be logits.  lse_parts
+    takes the place of lse, which may be None then: p is right by it whatever the logits' size."""
     dev = _device()
     rows, vocab = _shape2(logits, "logits")
     t, f32 = logits.dtype, torch.float32
     index, at = (0, None) if targets is None else _ids(targets, "targets", rows, dev)
     _check(_lib.tide_log_probs_backward(rows, vocab, _dtype(logits, "logits"), *_mat(logits, "logits", rows, vocab, t, dev),
-                                        scale, _vec(lse, "lse", rows, f32, dev), index, at,
+                                        scale, _optv(lse, "lse", rows, f32, dev), _parts(lse_parts, rows, dev), index, at,
                                         _optv(dlogp, "dlogp", rows, f32, dev), _optv(entropy, "entropy", rows, f32, dev),
                                         _optv(dentropy, "dentropy", rows, f32, dev),
                                         *_mat(dlogits, "dlogits", rows, vocab, t, dev), _stream(stream)))
@@ -113,7 +125,7 @@ class TensorList:
     The tensors are held, and must stay where they are while the list is in use.
     """
 
-    __slots__ = ("tensors", "count", "device", "addresses", "numels", "dtypes", "room")
+    __slots__ = ("tensors", "count", "device", "addresses", "numels", "dtypes", "room", "_apart")
 
     def __init__(self, tensors):
         self.tensors = tensors = list(tensors)
@@ -121,6 +133,7 @@ class TensorList:
         self.addresses, self.numels, self.dtypes = (_vp * n)(), (_i64 * n)(), (_i32 * n)()
         self.device = tensors[0].get_device() if n else None
         self.room = {}  # workspace bytes by device
+        self._apart = None
         for i, t in enumerate(tensors):
             code = _DTYPES.get(t.dtype)
             if code is None:
@@ -135,6 +148,13 @@ class TensorList:
 
     def __len__(self):
         return self.count
+
+    def apart(self):
+        """Whether no two tensors share memory, as outputs must not (tied weights' gradient listed twice, for one)."""
+        if self._apart is None:
+            spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in self.tensors if t.numel())
+            self._apart = all(a[1] <= b[0] for a, b in zip(spans, spans[1:]))
+        return self._apart
 
 
 def _list(tensors, dev):
@@ -167,5 +187,7 @@ def tide_grad_clip(tensors, norm, max_norm, eps=1e-6, out=None, stream=None):
             _refuse(f"{y.count} outputs for {x.count} tensors")
         if bytes(y.numels) != bytes(x.numels) or bytes(y.dtypes) != bytes(x.dtypes):
             _refuse("an output has another size or type than its tensor")
+    if not y.apart():
+        _refuse("two of the outputs share memory")
     _check(_lib.tide_grad_clip(x.count, x.addresses, y.addresses, x.numels, x.dtypes,
                                _vec(norm, "norm", 1, torch.float32, dev), max_norm, eps, _stream(stream)))

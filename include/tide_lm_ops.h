@@ -50,31 +50,35 @@ tide_status tide_embedding_backward(int64_t tokens, int64_t vocab, int64_t cols,
  * For each row of logits [rows, vocab] (`dtype`), with z = scale * logits
  * (scale positive and finite: 1 / temperature) and p = exp(z - lse):
  *   lse [rows]                log(sum over v of exp(z[v]))
+ *   lse_parts [rows, 2]       the largest logit, and lse less scale times that
  *   logp [rows]               z[targets] - lse; 0 for a target outside 0..vocab-1
  *   entropy [rows]            -sum over v of p[v] log p[v]
  *   top_tokens, top_logp      the `top` largest logits' tokens, the largest first,
  *   [rows, top]               equal ones by the lower token, and their z - lse
- * All but top_tokens (int32) are fp32; each of lse, entropy, top_logp and
- * top_tokens may be NULL, and targets with logp.  top is 0 to 32 and at most vocab.
+ * All but top_tokens (int32) are fp32; each of lse, lse_parts, entropy,
+ * top_logp and top_tokens may be NULL, and targets with logp.  top is 0 to 32 and at most vocab.
  * A logit of -inf is a token of probability 0.  A row without any other (or
- * with vocab 0) has lse -inf, entropy 0, logp -inf (0 for a target outside)
+ * with vocab 0) has lse and both its parts -inf, entropy 0, logp -inf (0 for a target outside)
  * and top_logp -inf.  A row that holds +inf or NaN has NaN throughout but for targets
  * outside; its top_tokens are those of its other values (NaN counts as -inf).
  * vocab below 2^31, rows below 2^31 (UNIMPLEMENTED beyond). */
 tide_status tide_log_probs(int64_t rows, int64_t vocab, int32_t dtype, const void* logits, int64_t ldl, float scale,
-                           int32_t index, const void* targets, float* logp, float* lse, float* entropy, int32_t top,
-                           float* top_logp, int64_t ld_top_logp, int32_t* top_tokens, int64_t ld_top_tokens,
+                           int32_t index, const void* targets, float* logp, float* lse, float* lse_parts,
+                           float* entropy, int32_t top, float* top_logp, int64_t ld_top_logp, int32_t* top_tokens, int64_t ld_top_tokens,
                            void* stream);
 
 /* The gradient, from what the forward call gave: with g = dlogp [rows] (taken as
  * 0 for a target outside 0..vocab-1), h = dentropy [rows] and p = exp(z - lse),
  *   dlogits = scale * (g * ([v == target] - p) - h * p * (log p + entropy)).
  * targets and dlogp are given together or both NULL (g = 0), likewise entropy
- * and dentropy (h = 0).  lse is the forward call's at the same scale; a row with lse -inf has no gradient.
+ * and dentropy (h = 0).  lse is the forward call's at the same scale; a row with
+ * lse -inf has no gradient.  fp32 holds lse to 2^-24 of it, and ln p is off by as much
+ * as lse is; lse_parts, given in lse's place, makes p right whatever the logits' size,
+ * as of a row that a finite mask covers whole (lse is not read then, and may be NULL).
  * dlogits [rows, vocab] is of `dtype` and may be logits. */
 tide_status tide_log_probs_backward(int64_t rows, int64_t vocab, int32_t dtype, const void* logits, int64_t ldl,
-                                    float scale, const float* lse, int32_t index, const void* targets,
-                                    const float* dlogp, const float* entropy, const float* dentropy, void* dlogits,
+                                    float scale, const float* lse, const float* lse_parts, int32_t index,
+                                    const void* targets, const float* dlogp, const float* entropy, const float* dentropy, void* dlogits,
                                     int64_t ldd, void* stream);
 
 /* ---- gradient norm and clipping -------------------------------------------

@@ -87,12 +87,14 @@ def log_probs(logits, targets, scale, top):
     return want, tol
 
 
-def log_probs_grad(logits, lse, targets, dlogp, entropy, dentropy, scale):
-    """(values, tolerance), from the lse and entropy given."""
+def log_probs_grad(logits, lse, targets, dlogp, entropy, dentropy, scale, parts=None):
+    """(values, tolerance), from the lse (or its parts) and entropy given."""
     rows, vocab = logits.shape
-    x, lse = logits.double(), lse.double()
-    empty = lse == -math.inf
-    d = x * scale - torch.where(empty, math.inf, lse)[:, None]
+    x, peak, rest = logits.double(), 0.0, lse.double() if parts is None else parts[:, 1].double()
+    empty = rest == -math.inf
+    if parts is not None:
+        peak = torch.where(empty, 0.0, parts[:, 0].double())[:, None]
+    d = (x - peak) * scale - torch.where(empty, math.inf, rest)[:, None]
     p = torch.exp(d)
     far = torch.clamp(d, min=-200.0)
     g = torch.zeros(rows, dtype=torch.float64)

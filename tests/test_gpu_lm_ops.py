@@ -266,23 +266,37 @@ def test_rows_with_nan_and_infinity(vocab):
     assert torch.equal(got["top_tokens"].cpu().long(), want["top_tokens"])
 
 
+def test_parts_of_empty_rows_and_their_gradient():
+    x = torch.full((3, 50), -math.inf)
+    x[1] = -1e9
+    parts = torch.empty(3, 2, device=DEV)
+    tide.tide_log_probs(x.to(DEV), lse_parts=parts)
+    assert (parts[[0, 2]] == -math.inf).all()
+    t, g, d = torch.tensor([1, 2, 3], device=DEV), torch.ones(3, device=DEV), torch.full((3, 50), 9.0, device=DEV)
+    tide.tide_log_probs_backward(x.to(DEV), None, d, targets=t, dlogp=g, lse_parts=parts)
+    assert (d[[0, 2]] == 0).all() and abs(d[1, 2].item() - 0.98) < 1e-6 and abs(d[1, 0].item() + 0.02) < 1e-6
+
+
 def test_log_probs_of_no_vocabulary():
     got = run_log_probs(torch.empty(3, 0), torch.tensor([0, -1, 5]))
     assert (got["logp"] == 0).all() and (got["lse"] == -math.inf).all() and (got["entropy"] == 0).all()
 
 
 def test_log_probs_outputs_one_by_one():
-    x = logits(5, 3000, BF, 1).to(DEV)
-    t = tokens(5, 3000, 1).to(DEV)
-    full = run_log_probs(x.cpu(), t.cpu(), 1.0, 6)
+    """Which outputs are asked for may change the order of the sums, not what they are within their tolerances."""
+    x, t = logits(5, 3000, BF, 1), tokens(5, 3000, 1)
+    dx, dt = x.to(DEV), t.to(DEV)
+    want, tol = R.log_probs(x, t, 1.0, 6)
     one = {k: torch.empty(5, device=DEV) for k in ("logp", "lse", "entropy")}
     best = torch.empty(5, 6, device=DEV), torch.empty(5, 6, dtype=torch.int32, device=DEV)
-    tide.tide_log_probs(x, t, one["logp"])
-    tide.tide_log_probs(x, lse=one["lse"])
-    tide.tide_log_probs(x, entropy=one["entropy"])
-    tide.tide_log_probs(x, top=best)
-    assert all(torch.equal(one[k], full[k]) for k in one)
-    assert torch.equal(best[0], full["top_logp"]) and torch.equal(best[1], full["top_tokens"])
+    tide.tide_log_probs(dx, dt, one["logp"])
+    tide.tide_log_probs(dx, lse=one["lse"])
+    tide.tide_log_probs(dx, entropy=one["entropy"])
+    tide.tide_log_probs(dx, top=best)
+    for k, v in one.items():
+        R.check(v, want[k], tol[k], k)
+    R.check(best[0], want["top_logp"], tol["top_logp"], "top_logp")
+    assert torch.equal(best[1].cpu().long(), want["top_tokens"])
 
 
 def grad_inputs(rows, vocab, seed, scale):
@@ -338,6 +352,41 @@ def test_log_probs_gradient_in_place_and_of_masked_rows(vocab, dtype):
     keep = [0, 1, 2, 3, 5]
     R.check(d[keep], want[keep], tol[keep], "in place")
     assert (d[0] == 0).all() and d[4].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("scale", [1.0, 0.7])
+@pytest.mark.parametrize("vocab", [40, 4999])
+def test_log_probs_gradient_of_rows_far_from_zero(vocab, scale, dtype):
+    """Rows whose logits are all a mask's value, or lie about one: lse alone has no bits left for the sum."""
+    at = [torch.finfo(dtype).min, -1e9, -3e4, 1e6, 3e4, torch.finfo(dtype).max, -1e30, 0.0]
+    x = torch.stack([torch.full((vocab,), v) for v in at]).to(dtype)
+    x[2:5] += torch.randint(-2, 3, (3, vocab), generator=gen(1)).to(dtype)
+    rows = len(at)
+    t = torch.arange(rows) % vocab
+    parts, entropy = torch.empty(rows, 2, device=DEV), torch.empty(rows, device=DEV)
+    tide.tide_log_probs(x.to(DEV), lse_parts=parts, entropy=entropy, scale=scale)
+    scale = float(torch.tensor(scale))
+    # The largest logit is exact; the sum's logarithm is known as in the reference's tolerance, here for 160 terms a
+    # thread, a range of 4 and a logarithm of 9: 460 U.
+    peak = x.double().amax(1)
+    assert torch.equal(parts[:, 0].cpu().double(), peak)
+    rest = torch.logsumexp((x.double() - peak[:, None]) * scale, 1)
+    assert ((parts[:, 1].cpu().double() - rest).abs() <= 2.0 ** -15).all()
+    g, h = randn((rows,), FP, 3), randn((rows,), FP, 4)
+    d = torch.empty(rows, vocab, dtype=dtype, device=DEV)
+    tide.tide_log_probs_backward(x.to(DEV), None, d, targets=t.to(DEV), dlogp=g.to(DEV), entropy=entropy,
+                                 dentropy=h.to(DEV), scale=scale, lse_parts=parts)
+    want, tol = R.log_probs_grad(x, None, t, g, entropy.cpu(), h, scale, parts.cpu())
+    R.check(d, want, tol, "dlogits")
+    p = torch.exp((x.double() - peak[:, None]) * scale - rest[:, None])
+    alone = torch.empty_like(d)
+    tide.tide_log_probs_backward(x.to(DEV), None, alone, targets=t.to(DEV), dlogp=g.to(DEV), scale=scale, lse_parts=parts)
+    onehot = torch.nn.functional.one_hot(t, vocab).double()
+    exact = scale * g.double()[:, None] * (onehot - p)
+    # p by that, and its own 32 roundings at most.
+    tol = R.half(dtype) * exact.abs() + scale * g.double().abs()[:, None] * (2.0 ** -14 * p + 4 * R.U * onehot)
+    assert ((alone.double().cpu() - exact).abs() <= tol).all()
 
 
 def test_log_probs_gradient_is_the_differences():
@@ -493,10 +542,16 @@ def test_the_binding_refuses():
         lambda: tide.tide_log_probs(x, ids, row, scale=0.0),
         lambda: tide.tide_log_probs_backward(x, row, x.clone(), targets=ids),
         lambda: tide.tide_log_probs_backward(x, row[:3], x.clone()),
+        lambda: tide.tide_log_probs_backward(x, None, x.clone()),
+        lambda: tide.tide_log_probs_backward(x, None, x.clone(), lse_parts=row),
+        lambda: tide.tide_log_probs(x, lse_parts=x[:, :2]),
         lambda: tide.tide_grad_norm([x, x.half()], one),
         lambda: tide.tide_grad_norm([x.t()], one),
         lambda: tide.tide_grad_norm([x], row),
         lambda: tide.tide_grad_clip([x], one, -1.0),
+        lambda: tide.tide_grad_clip([x, x], one, 1.0),
+        lambda: tide.tide_grad_clip([x, x[1:]], one, 1.0),
+        lambda: tide.tide_grad_clip([x, x], one, 1.0, out=[x.clone()] * 2),
         lambda: tide.tide_grad_clip([x], one, 1.0, out=[x, x]),
         lambda: tide.tide_grad_clip([x], one, 1.0, out=[x[:2]]),
         lambda: tide.tide_grad_clip([x], one, 1.0, out=[x.bfloat16()]),

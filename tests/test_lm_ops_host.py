@@ -35,14 +35,14 @@ def embed_grad(tokens=4, vocab=10, cols=8, index=0, ids=P, dtype=0, dy=P, lddy=8
                                          None)
 
 
-def probs(rows=4, vocab=40, dtype=0, z=P, ldz=40, scale=1.0, index=0, t=P, logp=P, lse=None, h=None, top=0, tl=None,
+def probs(rows=4, vocab=40, dtype=0, z=P, ldz=40, scale=1.0, index=0, t=P, logp=P, lse=None, parts=None, h=None, top=0, tl=None,
           ldl=0, tt=None, ldt=0):
-    return lib().tide_log_probs(rows, vocab, dtype, z, ldz, scale, index, t, logp, lse, h, top, tl, ldl, tt, ldt, None)
+    return lib().tide_log_probs(rows, vocab, dtype, z, ldz, scale, index, t, logp, lse, parts, h, top, tl, ldl, tt, ldt, None)
 
 
-def probs_grad(rows=4, vocab=40, dtype=0, z=P, ldz=40, scale=1.0, lse=P, index=0, t=P, dlogp=P, h=None, dh=None, out=P,
+def probs_grad(rows=4, vocab=40, dtype=0, z=P, ldz=40, scale=1.0, lse=P, parts=None, index=0, t=P, dlogp=P, h=None, dh=None, out=P,
                ldo=40):
-    return lib().tide_log_probs_backward(rows, vocab, dtype, z, ldz, scale, lse, index, t, dlogp, h, dh, out, ldo, None)
+    return lib().tide_log_probs_backward(rows, vocab, dtype, z, ldz, scale, lse, parts, index, t, dlogp, h, dh, out, ldo, None)
 
 
 def arrays(addresses, numels, dtypes):
@@ -83,7 +83,8 @@ CASES = [
     (probs, dict(scale=0.0), INVALID), (probs, dict(scale=-1.0), INVALID), (probs, dict(scale=math.inf), INVALID),
     (probs, dict(scale=math.nan), INVALID), (probs, dict(t=None), INVALID), (probs, dict(logp=None), INVALID),
     (probs, dict(index=2), INVALID), (probs, dict(t=P + 2), ALIGNMENT), (probs, dict(lse=P + 2), ALIGNMENT),
-    (probs, dict(h=P + 1), ALIGNMENT), (probs, dict(top=-1), INVALID), (probs, dict(top=33), INVALID),
+    (probs, dict(h=P + 1), ALIGNMENT), (probs, dict(parts=P + 2), ALIGNMENT),
+    (probs_grad, dict(parts=P + 1), ALIGNMENT), (probs_grad, dict(lse=None, parts=P, out=None), INVALID), (probs, dict(top=-1), INVALID), (probs, dict(top=33), INVALID),
     (probs, dict(vocab=4, top=5), INVALID), (probs, dict(top=5, tl=P, ldl=4), INVALID),
     (probs, dict(top=5, tt=P, ldt=4), INVALID), (probs, dict(top=5, tt=P + 2, ldt=5), ALIGNMENT),
     (probs, dict(rows=0, t=None), OK), (probs, dict(t=None, logp=None), OK), (probs, dict(t=None, logp=None, top=3), OK),
