@@ -11,7 +11,7 @@
 // and the `top`-th largest of these 32 is one that `top` logits at least reach.  So all alternatives are
 // among the logits that reach it: 31 are expected for 20 alternatives of a row in random order, 112 for 32.
 // A thread also keeps where its largest stood and the largest of its other vectors: where only the first
-// reaches the bound one vector is read again, else all of the thread's (L2 has them), by the whole warp.  The
+// reaches the bound one vector is read again, else all of the thread's (L2 has them), by all of the row's threads.  The
 // logits that reach the bound are listed in shared memory, and each finds its rank by counting.
 // Where equal logits make the list too long only those above the bound are listed, and the first of the ones at it.
 // Where all that fails (more than 512 different logits above a bound, NaN that makes it too high) the alternatives
@@ -141,7 +141,8 @@ __global__ void __launch_bounds__(PER_ROW == 32 ? 256 : PER_ROW, 1024 / (PER_ROW
   __shared__ float largest[TOP ? WARPS : 1][32];
   __shared__ uint64_t listed[TOP ? kRowsHere : 1][TOP ? kRoom : 1];
   __shared__ uint32_t listed_count[kRowsHere];
-  __shared__ uint8_t who[TOP ? (PER_ROW == 32 ? 8 : WARPS) : 1][32];
+  __shared__ uint32_t again_count[kRowsHere];
+  __shared__ int2 again[TOP ? kRowsHere : 1][TOP ? PER_ROW : 1];
   __shared__ uint64_t found[TOP ? WARPS + 1 : 1];
   const uint32_t blocks = CLUSTER ? cluster_size() : 1, rank = CLUSTER ? cluster_rank() : 0;
   const int64_t row = PER_ROW == 32 ? (int64_t)blockIdx.x * 8 + threadIdx.x / 32 : (int64_t)(blockIdx.x / blocks);
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(PER_ROW == 32 ? 256 : PER_ROW, 1024 / (PER_ROW
     target = token_at(a.targets, a.index, row, vocab);
     if (target >= 0) target_logit = (float)logits[target];
   }
-  if (TOP && x == 0) listed_count[here] = 0;
+  if (TOP && x == 0) listed_count[here] = again_count[here] = 0;
   __syncwarp();  // for rows of a warp; others have a barrier below
 
   Sums sums;
@@ -330,28 +331,29 @@ __global__ void __launch_bounds__(PER_ROW == 32 ? 256 : PER_ROW, 1024 / (PER_ROW
         load(r, best_at);
         list(r, best_at, reach(r, limit));
       }
-      // The warp's threads that may have met more: all their other vectors, spread over the warp.
-      const bool more = mine >= limit && second >= limit && first < count;
-      const uint32_t some = __ballot_sync(0xffffffffu, more);
-      if (some) {
-        if (more) who[threadIdx.x / 32][__popc(some & ((1u << lane) - 1))] = (uint8_t)lane;
-        __syncwarp();
-        const uint32_t each = (uint32_t)((count - (first - lane) + stride - 1) / stride), all = each * __popc(some);
-        for (uint32_t i0 = 0; i0 < all; i0 += 32 * kAhead) {
-          Raw8<T> r[kAhead];
-          int at[kAhead];
+      // Threads that may have met more: all their other vectors, spread over the row's threads here.
+      if (mine >= limit && second >= limit && first < count) {
+        const uint32_t at = atomicAdd(&again_count[here], 1u);
+        again[here][at] = make_int2(first, best_at);
+      }
+      sync();
+      const uint32_t each = (uint32_t)((count + stride - 1) / stride), all = each * again_count[here];
+      for (uint32_t i0 = x; i0 < all; i0 += PER_ROW * kAhead) {
+        Raw8<T> r[kAhead];
+        int at[kAhead];
 #pragma unroll
-          for (int j = 0; j < kAhead; ++j) {
-            const uint32_t i = i0 + j * 32 + lane, thread = i < all ? i / each : 0, l = who[threadIdx.x / 32][thread];
-            const int best = __shfl_sync(0xffffffffu, best_at, l);
-            at[j] = first - lane + (int)l + (int)(i - thread * each) * stride;
-            if (i >= all || at[j] >= count || at[j] == best) at[j] = -1;
-            if (at[j] >= 0) load(r[j], at[j]);
-          }
-#pragma unroll
-          for (int j = 0; j < kAhead; ++j)
-            if (at[j] >= 0) list(r[j], at[j], reach(r[j], limit));
+        for (int j = 0; j < kAhead; ++j) {
+          const uint32_t i = i0 + j * PER_ROW, which = i / each;
+          at[j] = -1;
+          if (i >= all) continue;
+          const int2 of = again[here][which];
+          at[j] = of.x + (int)(i - which * each) * stride;
+          if (at[j] >= count || at[j] == of.y) at[j] = -1;
+          if (at[j] >= 0) load(r[j], at[j]);
         }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+          if (at[j] >= 0) list(r[j], at[j], reach(r[j], limit));
       }
       if constexpr (CLUSTER) {
         cluster_sync();
@@ -370,7 +372,7 @@ __global__ void __launch_bounds__(PER_ROW == 32 ? 256 : PER_ROW, 1024 / (PER_ROW
         cluster_sync();
       else
         sync();
-      if (x == 0) listed_count[here] = 0;
+      if (x == 0) listed_count[here] = again_count[here] = 0;
       sync();
     }
     if constexpr (CLUSTER) {
