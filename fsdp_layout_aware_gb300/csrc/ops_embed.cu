@@ -508,6 +508,148 @@ __global__ void __launch_bounds__(kJoinThreads, 2) join_kernel(const SumArgs a) 
   }
 }
 
+// ---------------------------------------------------------------- few tokens
+
+// One launch and no workspace, for 512 tokens at most and 2^21 elements of dweight: 512 into 1000 x 64 bf16
+// 4.9 us against 14.4 with the sort, 100 into 300 x 101 6.9 against 14.9; 512 into 32000 x 2048 are
+// 36 against 33, and, all of one token, into 1000 x 8192 44 against 16.  A block looks at all ids by itself, lists those of its rows of dweight
+// in the rows' order, and writes kFewVectors vectors of each row.  A run of more than kFewLong rows
+// is added up by all of the block's warps.
+constexpr int kFew = 512, kFewRows = 128, kFewVectors = 128, kFewLong = 16;
+constexpr int64_t kFewElements = 1 << 21, kFewBytes = 16 << 10;
+static_assert(kFew == 2 * kThreads, "two ids a thread");
+
+struct FewArgs {
+  int64_t tokens, vocab, cols;
+  int32_t index;
+  const void* ids;
+  const void* dy;
+  int64_t lddy;
+  float scale;
+  void* dweight;
+  int64_t lddw;
+  int32_t accumulate;
+  int32_t rows;        // of dweight a block
+  FastDiv slabs;       // blocks beside each other
+  FastDiv vectors;     // of a row in a block, the last of them perhaps beyond the row
+};
+
+template <typename T, bool ANY>
+__global__ void __launch_bounds__(kThreads, 4) few_kernel(const FewArgs a) {
+  constexpr int kWarps = kThreads / 32;
+  __shared__ uint16_t row_of[kFew], place_of[kFew], place[kFew];  // by place; by row
+  __shared__ uint16_t begins[kFewRows + 1];
+  __shared__ int warp_count[kWarps];
+  __shared__ __align__(16) float joined[kWarps][kFewVectors][8];
+  const int x = threadIdx.x, warp = x / 32, lane = x % 32;
+  const uint32_t down = a.slabs.quotient(blockIdx.x), slab = blockIdx.x - down * a.slabs.d;
+  const int64_t row0 = (int64_t)down * a.rows;
+  const int rows = (int)min((int64_t)a.rows, a.vocab - row0);
+  int mine[2], count = 0;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int t = 2 * x + j, token = t < a.tokens ? token_at(a.ids, a.index, t, a.vocab) : -1;
+    mine[j] = token >= row0 && token < row0 + rows ? (int)(token - row0) : -1;
+    count += mine[j] >= 0;
+  }
+  int up = count;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, up, d);
+    if (lane >= d) up += o;
+  }
+  if (lane == 31) warp_count[warp] = up;
+  __syncthreads();
+  int at = up - count, n = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) at += warp_count[w];
+    n += warp_count[w];
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (mine[j] >= 0) row_of[at] = (uint16_t)mine[j], place_of[at++] = (uint16_t)(2 * x + j);
+  __syncthreads();
+  for (int i = x; i < n; i += kThreads) {  // behind those of lower rows, and those before of its own
+    const int r = row_of[i];
+    int to = 0;
+    for (int j = 0; j < n; ++j) to += row_of[j] < r || (row_of[j] == r && j < i);
+    place[to] = place_of[i];
+  }
+  for (int r = x; r <= rows; r += kThreads) {
+    int to = 0;
+    for (int j = 0; j < n; ++j) to += row_of[j] < r;
+    begins[r] = (uint16_t)to;
+  }
+  __syncthreads();
+
+  auto column_of = [&](int64_t row, uint32_t v) {
+    return ((int64_t)slab * kFewVectors + v) * 8 - (ANY ? row_phase((const T*)a.dweight + row * a.lddw) : 0);
+  };
+  auto add = [&](float (&sum)[8], int p, int64_t col) {
+    const T* row = (const T*)a.dy + (int64_t)place[p] * a.lddy;
+    float v[8];
+    if constexpr (ANY)
+      load_columns(row, col, a.cols, v);
+    else
+      load_vec<8>(row + col, v);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) sum[c] += v[c];
+  };
+  auto store = [&](float (&sum)[8], int64_t row, int64_t col) {
+    T* const out = (T*)a.dweight + row * a.lddw;
+    float old[8];
+    if (a.accumulate) load_columns(out, col, a.cols, old);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) sum[c] = a.accumulate ? fmaf(sum[c], a.scale, old[c]) : sum[c] * a.scale;
+    if constexpr (ANY)
+      store_columns(out, col, a.cols, sum);
+    else
+      store_vec<8>(out + col, sum);
+  };
+  for (uint32_t i = x; i < rows * a.vectors.d; i += kThreads) {
+    const uint32_t r = a.vectors.quotient(i), v = i - r * a.vectors.d;
+    const int begin = begins[r], end = begins[r + 1];
+    if (end - begin > kFewLong || (begin == end && a.accumulate)) continue;
+    const int64_t row = row0 + r, col = column_of(row, v);
+    if (col >= a.cols) continue;
+    float sum[8] = {};
+#pragma unroll 4
+    for (int p = begin; p < end; ++p) add(sum, p, col);
+    store(sum, row, col);
+  }
+  if (n <= kFewLong) return;
+  for (int r = 0; r < rows; ++r) {
+    const int begin = begins[r], end = begins[r + 1];
+    if (end - begin <= kFewLong) continue;
+    const int64_t row = row0 + r;
+    __syncthreads();  // what the last run left has been read
+    for (uint32_t v = lane; v < a.vectors.d; v += 32) {
+      const int64_t col = column_of(row, v);
+      float sum[8] = {};
+      if (col < a.cols) {
+#pragma unroll 4
+        for (int p = begin + warp; p < end; p += kWarps) add(sum, p, col);
+      }
+      store_vec<8>(joined[warp][v], sum);
+    }
+    __syncthreads();
+    for (uint32_t v = x; v < a.vectors.d; v += kThreads) {
+      const int64_t col = column_of(row, v);
+      if (col >= a.cols) continue;
+      float sum[8] = {};
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        float t[8];
+        load_vec<8>(joined[w][v], t);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) sum[c] += t[c];
+      }
+      store(sum, row, col);
+    }
+  }
+}
+
 // ---------------------------------------------------------------- host side
 
 template <typename T>
@@ -539,13 +681,15 @@ int tile_of(int64_t tokens, int64_t vectors) {
   return tile;
 }
 
-// The workspace: sorted keys and places, twice; the long runs; their parts.
+// The workspace: sorted keys and places, twice; the long runs; their parts.  Few tokens need none.
 struct GradSpace {
-  int64_t list, longs, parts, bytes;
-  int tile;
+  int64_t list = 0, longs = 0, parts = 0, bytes = 0;
+  int tile = 0;
 };
-GradSpace grad_space(int64_t tokens, int64_t cols) {
+bool few(int64_t tokens, int64_t vocab, int64_t cols) { return tokens <= kFew && vocab <= kFewElements / cols; }
+GradSpace grad_space(int64_t tokens, int64_t vocab, int64_t cols) {
   GradSpace g;
+  if (tokens == 0 || few(tokens, vocab, cols)) return g;
   const int64_t vectors = (cols + 14) / 8;
   g.tile = tile_of(tokens, vectors);
   const int64_t tiles = (tokens + g.tile - 1) / g.tile;
@@ -554,6 +698,26 @@ GradSpace grad_space(int64_t tokens, int64_t cols) {
   g.parts = tiles > 2 ? tiles * 2 * vectors * 32 : 0;
   g.bytes = 4 * g.list + g.longs + g.parts;
   return g;
+}
+
+// 16 to 32 KB of dweight a block, where a block's rows are not fewer than the blocks that the GPU holds.
+template <typename T>
+tide_status embed_grad_few(FewArgs a, cudaStream_t stream) {
+  const bool vec = a.cols % 8 == 0 && rows_aligned(a.dy, a.lddy, sizeof(T), a.tokens) &&
+                   rows_aligned(a.dweight, a.lddw, sizeof(T), a.vocab);
+  const int64_t vectors = vec ? a.cols / 8 : (a.cols + 14) / 8, slabs = (vectors + kFewVectors - 1) / kFewVectors;
+  const int64_t here = std::min<int64_t>(vectors, kFewVectors), most = (int64_t)std::max(ops_num_sms(), 1) * 4;
+  a.slabs = FastDiv((uint32_t)slabs), a.vectors = FastDiv((uint32_t)here);
+  a.rows = 1;
+  while (a.rows < kFewRows && a.rows * here * 8 * (int64_t)sizeof(T) < kFewBytes && a.vocab / (2 * a.rows) * slabs >= most)
+    a.rows *= 2;
+  const int64_t grid = (a.vocab + a.rows - 1) / a.rows * slabs;
+  if (grid > INT32_MAX) return fail(TIDE_ERR_UNIMPLEMENTED, "embedding gradient: too many rows for one launch");
+  if (vec)
+    few_kernel<T, false><<<(unsigned)grid, kThreads, 0, stream>>>(a);
+  else
+    few_kernel<T, true><<<(unsigned)grid, kThreads, 0, stream>>>(a);
+  return cuda_status(cudaGetLastError(), "embedding gradient");
 }
 
 template <typename T>
@@ -635,7 +799,7 @@ tide_status tide_embedding(int64_t tokens, int64_t vocab, int64_t cols, int32_t 
 
 int64_t tide_embedding_backward_workspace(int64_t tokens, int64_t vocab, int64_t cols) {
   if (tokens <= 0 || vocab <= 0 || cols <= 0 || tokens > INT32_MAX || cols > kMaxCols) return 0;
-  return grad_space(tokens, cols).bytes;
+  return grad_space(tokens, vocab, cols).bytes;
 }
 
 tide_status tide_embedding_backward(int64_t tokens, int64_t vocab, int64_t cols, int32_t index, const void* ids,
@@ -652,11 +816,15 @@ tide_status tide_embedding_backward(int64_t tokens, int64_t vocab, int64_t cols,
   if (need > 0 && (!workspace || workspace_bytes < need))
     return fail(TIDE_ERR_INVALID_ARG, "workspace too small: " + std::to_string(need) + " bytes are needed");
   if ((uintptr_t)workspace % 16) return fail(TIDE_ERR_ALIGNMENT, "workspace is not 16-byte aligned");
-  const GradSpace g = grad_space(tokens, cols);
+  if (few(tokens, vocab, cols)) {
+    const FewArgs f{tokens, vocab, cols, index, ids, dy, lddy, scale, dweight, lddw, accumulate, 0, FastDiv(), FastDiv()};
+    return dtype == TIDE_BF16 ? embed_grad_few<bf16>(f, (cudaStream_t)stream) : embed_grad_few<float>(f, (cudaStream_t)stream);
+  }
+  const GradSpace g = grad_space(tokens, vocab, cols);
   uint8_t* const w = (uint8_t*)workspace;
   uint32_t* list[4];
   for (int i = 0; i < 4; ++i) list[i] = (uint32_t*)(w + i * g.list);
-  uint32_t* const longs = tokens > 0 ? (uint32_t*)(w + 4 * g.list) : nullptr;
+  uint32_t* const longs = (uint32_t*)(w + 4 * g.list);
   float* const parts = (float*)(w + 4 * g.list + g.longs);
   const SortArgs s{tokens, vocab, index, ids, list[0], list[1], list[2], list[3], 0, g.tile, longs};
   const SumArgs a{0,  FastDiv(), 0,     tokens,  vocab, cols,       g.tile, list[0], list[1], longs,

@@ -72,7 +72,7 @@ CASES = [
     (embed, dict(tokens=1 << 31, ldo=8), UNIMPLEMENTED), (embed, dict(vocab=1 << 31), UNIMPLEMENTED),
     (embed, dict(cols=(1 << 24) + 1, ldw=BIG, ldo=BIG), UNIMPLEMENTED), (embed, dict(vocab=1 << 30, ldw=BIG), OVERFLOW),
     (embed_grad, dict(tokens=-1), INVALID), (embed_grad, dict(dy=None), INVALID), (embed_grad, dict(dw=None), INVALID),
-    (embed_grad, dict(ws=None), INVALID), (embed_grad, dict(wsb=15), INVALID), (embed_grad, dict(ws=P + 8), ALIGNMENT),
+    (embed_grad, dict(tokens=1000, ws=None), INVALID), (embed_grad, dict(tokens=1000, wsb=15), INVALID), (embed_grad, dict(ws=P + 8), ALIGNMENT),
     (embed_grad, dict(lddy=7), INVALID), (embed_grad, dict(lddw=7), INVALID), (embed_grad, dict(index=5), INVALID),
     (embed_grad, dict(vocab=0), OK), (embed_grad, dict(cols=0), OK), (embed_grad, dict(tokens=0, add=1), OK),
     (embed_grad, dict(vocab=(1 << 31) - 1), UNIMPLEMENTED), (embed_grad, dict(dw=P + 1), ALIGNMENT),
@@ -135,7 +135,9 @@ def test_header_is_plain_c(tmp_path):
 def test_workspace_queries():
     q = lib().tide_embedding_backward_workspace
     assert q(0, 10, 8) == q(10, 0, 8) == q(10, 10, 0) == q(-1, 10, 8) == 0
-    assert q(1, 10, 8) >= 16  # four lists of one id
+    assert q(1, 10, 8) == q(512, 10, 8) == q(512, 1 << 18, 8) == 0  # few tokens, few rows: one launch, nothing kept
+    assert q(1, 1 << 19, 8) >= 16
+    assert q(513, 10, 8) >= 4 * 4 * 513  # four lists of ids
     assert q(100000, 10, 8) >= 4 * 400000 + 100000 // 64 * 32
     assert lib().tide_grad_norm_workspace(0, None, None) == 0
     _, n, d = arrays((P, P), (8, 8), (0, 1))
