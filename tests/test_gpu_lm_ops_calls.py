@@ -231,3 +231,30 @@ def test_norm_and_clip_beyond_31_bits():
     tide.tide_grad_clip([x, y], norm, want / 4, eps=0.0)  # a quarter, but for roundings
     assert (x[-2000:].float() - 0.25).abs().max() <= 2.0 ** -10 and (x[:2000].float() - 0.25).abs().max() <= 2.0 ** -10
     assert bool((x == x[0]).all()) and (y - 0.5).abs().max() <= 4 * R.U
+
+
+def test_more_rows_than_one_launch_takes():
+    """Rows of one column, on both sides of the place where the second launch begins."""
+    rows = (1 << 31) - 1
+    at = torch.tensor([0, 1, rows // 2, rows - 300, rows - 257, rows - 256, rows - 255, rows - 2, rows - 1], device=DEV)
+    ids = torch.zeros(rows, dtype=torch.int32, device=DEV)
+    w = torch.tensor([[1.5], [-2.0], [7.0]], dtype=BF, device=DEV)
+    want = torch.tensor([0, 1, 2, 1, 2, 0, 1, 2, 1], dtype=torch.int32, device=DEV)
+    ids[at] = want
+    x = torch.empty(rows, 1, dtype=BF, device=DEV)
+    tide.tide_embedding(ids, w, x)
+    assert torch.equal(x[at], w[want.long()])
+    x[at] = 1.5
+    assert bool((x == 1.5).all())
+    # One logit a row, x, and an lse of x + 1: p = 1 / e, so that the gradient is g (1 - 1 / e), and 0 where the target is
+    # outside.
+    lse = torch.full((rows,), 2.5, device=DEV)
+    g = torch.full((rows,), 1.0, device=DEV)
+    g[at] = torch.arange(1.0, 10.0, device=DEV)
+    tide.tide_log_probs_backward(x, lse, x, targets=ids, dlogp=g)
+    p = 2.718281828459045 ** -1
+    got = x[at].double().cpu()[:, 0]
+    exact = torch.arange(1.0, 10.0, dtype=torch.float64) * torch.where(want.cpu() == 0, 1 - p, 0.0)
+    assert ((got - exact).abs() <= 2.0 ** -8 * 1.01 * exact.abs()).all()
+    x[at] = x[5000].clone()
+    assert bool((x == x[5000]).all()) and abs(x[5000].item() - (1 - p)) <= 2.0 ** -8

@@ -81,7 +81,7 @@ CASES = [
     (probs, dict(rows=-1), INVALID), (probs, dict(vocab=-1), INVALID), (probs, dict(dtype=2), INVALID),
     (probs, dict(z=None), INVALID), (probs, dict(ldz=39), INVALID), (probs, dict(z=P + 1), ALIGNMENT),
     (probs, dict(scale=0.0), INVALID), (probs, dict(scale=-1.0), INVALID), (probs, dict(scale=math.inf), INVALID),
-    (probs, dict(scale=math.nan), INVALID), (probs, dict(t=None), INVALID), (probs, dict(logp=None), INVALID),
+    (probs, dict(scale=math.nan), INVALID), (probs, dict(scale=2.0 ** 65), INVALID), (probs, dict(t=None), INVALID), (probs, dict(logp=None), INVALID),
     (probs, dict(index=2), INVALID), (probs, dict(t=P + 2), ALIGNMENT), (probs, dict(lse=P + 2), ALIGNMENT),
     (probs, dict(h=P + 1), ALIGNMENT), (probs, dict(parts=P + 2), ALIGNMENT),
     (probs_grad, dict(parts=P + 1), ALIGNMENT), (probs_grad, dict(lse=None, parts=P, out=None), INVALID), (probs, dict(top=-1), INVALID), (probs, dict(top=33), INVALID),
