@@ -33,6 +33,7 @@ namespace tide {
 namespace {
 
 constexpr int kMaxTop = 32;
+constexpr uint32_t kMostBlocks = 8;  // of a cluster
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // 2^kLeast is 0 in fp32: exponents are kept from -inf, which times 0 would be NaN.
 constexpr float kLeast = -200.0f;
@@ -266,17 +267,25 @@ __global__ void __launch_bounds__(PER_ROW == 32 ? 256 : PER_ROW, 1024 / (PER_ROW
       if constexpr (TOP) largest[0][lane] = bound;
     }
     cluster_sync();
-    Sums all;
-    for (uint32_t b = 0; b < blocks; ++b) {
-      Sums o;
-      o.m = load_peer_f32(peer_smem(&stat[0][0], b));
-      o.s = load_peer_f32(peer_smem(&stat[1][0], b));
-      o.e = load_peer_f32(peer_smem(&stat[2][0], b));
-      all.join(o, k);
-      if constexpr (TOP) bound = fmaxf(bound, load_peer_f32(peer_smem(&largest[0][lane], b)));
+    sums = Sums();
+    if ((uint32_t)lane < blocks) {
+      sums.m = load_peer_f32(peer_smem(&stat[0][0], lane));
+      sums.s = load_peer_f32(peer_smem(&stat[1][0], lane));
+      sums.e = load_peer_f32(peer_smem(&stat[2][0], lane));
     }
-    sums = all;
-    cluster_sync();  // no block leaves, or writes there again, while it is read
+    if constexpr (TOP) {
+      float theirs[kMostBlocks];  // loads at once: each takes the better part of a microsecond
+#pragma unroll
+      for (uint32_t b = 0; b < kMostBlocks; ++b)
+        theirs[b] = b < blocks ? load_peer_f32(peer_smem(&largest[0][lane], b)) : -INFINITY;
+#pragma unroll
+      for (uint32_t b = 0; b < kMostBlocks; ++b) bound = fmaxf(bound, theirs[b]);
+    }
+    join_lanes(kMostBlocks);
+    sums.m = __shfl_sync(0xffffffffu, sums.m, 0);
+    sums.s = __shfl_sync(0xffffffffu, sums.s, 0);
+    sums.e = __shfl_sync(0xffffffffu, sums.e, 0);
+    if constexpr (!TOP) cluster_sync();  // no block leaves while it is read
   } else if constexpr (WARPS > 1) {
     sums.m = __shfl_sync(0xffffffffu, sums.m, 0);
     sums.s = __shfl_sync(0xffffffffu, sums.s, 0);
@@ -327,7 +336,7 @@ __global__ void __launch_bounds__(PER_ROW == 32 ? 256 : PER_ROW, 1024 / (PER_ROW
     // Logits that reach the bound; where too many do (or the bound is that of masked ones), those above
     // it, and of the ones at it as many as it takes, the lowest tokens, below.
     bool strict = bound == -INFINITY;
-    uint32_t n = 0;
+    uint32_t n = 0, theirs = 0;  // listed, of a cluster also by block `lane`
     for (;;) {
       const float limit = strict ? nextafterf(bound, INFINITY) : bound;  // of +inf itself; NaN rows alone have that
       if (mine >= limit && first < count) {
@@ -361,11 +370,11 @@ __global__ void __launch_bounds__(PER_ROW == 32 ? 256 : PER_ROW, 1024 / (PER_ROW
       }
       if constexpr (CLUSTER) {
         cluster_sync();
-        n = 0;
-        for (uint32_t b = 0; b < blocks; ++b) {
-          const uint32_t c = load_peer_u32(peer_smem(&listed_count[0], b));
-          n = c > kRoom || n + c > kRoom ? kRoom + 1 : n + c;
-        }
+        theirs = (uint32_t)lane < blocks ? min(load_peer_u32(peer_smem(&listed_count[0], lane)), kRoom + 1u) : 0;
+        n = theirs;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
+        n = min(n, kRoom + 1u);
       } else {
         sync();
         n = listed_count[here];
@@ -380,14 +389,17 @@ __global__ void __launch_bounds__(PER_ROW == 32 ? 256 : PER_ROW, 1024 / (PER_ROW
       sync();
     }
     if constexpr (CLUSTER) {
-      // The first block brings the others' lists to its own.
+      // The first block brings the others' lists to its own, behind one another.
       if (rank == 0 && n <= kRoom) {
-        uint32_t at = listed_count[0];
-        for (uint32_t b = 1; b < blocks; ++b) {
-          const uint32_t c = load_peer_u32(peer_smem(&listed_count[0], b));
-          if ((uint32_t)x < c) listed[0][at + x] = load_peer_u64(peer_smem(&listed[0][x], b));
-          at += c;
+        uint32_t from = 0, i = x;
+        bool found = false;
+#pragma unroll
+        for (int b = 0; b < (int)kMostBlocks; ++b) {
+          const uint32_t c = __shfl_sync(0xffffffffu, theirs, b);
+          if (!found && i < c) from = b, found = true;
+          if (!found) i -= c;
         }
+        if (found && from > 0) listed[0][x] = load_peer_u64(peer_smem(&listed[0][i], from));
         __syncthreads();
       }
     }
@@ -603,7 +615,7 @@ tide_status log_probs(const LogProbArgs& a, cudaStream_t stream) {
   // Still too few: up to eight blocks share a row, while each thread has a vector or more.
   int cluster = 1;
   if (vectors > 1024)
-    while (cluster < 8 && a.rows * cluster * 2 <= 2 * sms && vectors >= (int64_t)cluster * 2 * 512) cluster *= 2;
+    while (cluster < (int)kMostBlocks && a.rows * cluster * 2 <= 2 * sms && vectors >= (int64_t)cluster * 2 * 512) cluster *= 2;
   cudaError_t err = cudaSuccess;
   with_bool(a.entropy != nullptr, [&](auto entropy) {
     with_bool(a.top > 0, [&](auto top) {
