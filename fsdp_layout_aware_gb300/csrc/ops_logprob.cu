@@ -603,15 +603,17 @@ template <typename T>
 tide_status log_probs(const LogProbArgs& a, cudaStream_t stream) {
   const int sms = ops_num_sms();
   if (sms <= 0) return fail(TIDE_ERR_CUDA, "the current device could not be queried");
-  // The fewest threads a row that still fill the SMs with the threads their registers hold, since
-  // what is not a thread's own logits costs each of them alike (16384 x 4999 bf16: 39 us with a warp a row, 80
-  // with 128 threads, 112 with 256; 2048 x 131072: 124, 92 and 92).  Alternatives of long rows ask for 128: a warp's
-  // lanes hold too much of such a row to read again (16384 x 8192 with 20: 105 and 114 us, 16384 x 16384
-  // 180 and 154, 4096 x 65536 221 and 113).
-  const int64_t vectors = a.vocab / 8;
+  // The fewest threads a row that still fill the GPU, since what is not a thread's own logits costs each of
+  // them alike (16384 x 4999 bf16: 38 us with a warp a row, 80 with 128 threads, 112 with 256; 2048 x
+  // 131072: 124, 92 and 92).  800 threads an SM fill it where rows are long, fewer where a row's latency
+  // is a launch's (warps against 128 threads: 300 x 4999 6.3 and 5.2 us, 600 x 4999 6.4 and 6.5, 1500 x 16384 18
+  // and 16, 4800 x 16384 31 and 34; 128 against 256: 600 x 50001 18 and 16, 1021 x 50001 24 and 26).  Beyond 32768
+  // logits a warp is slower however many rows there are (4096 x 65536 99 and 90), and with alternatives beyond 12288,
+  // since its lanes hold too much of the row to read again (16384 x 16384 with 20 180 and 154, 16384 x 8192 105 and 114).
+  const int64_t vectors = a.vocab / 8, threads = (int64_t)sms * std::min<int64_t>(800, vectors / 5);
   int want = 32;
   for (const int next : {128, 256, 512})
-    if (vectors >= next && (a.rows * want < (int64_t)sms * 1024 || (a.top > 0 && vectors > 1536 && next == 128))) want = next;
+    if (vectors >= next && (a.rows * want < threads || (next == 128 && vectors > (a.top > 0 ? 1536 : 4096)))) want = next;
   // Still too few: up to eight blocks share a row, while each thread has a vector or more.
   int cluster = 1;
   if (vectors > 1024)
