@@ -704,7 +704,7 @@ GradSpace grad_space(int64_t tokens, int64_t vocab, int64_t cols) {
   return g;
 }
 
-// 16 to 32 KB of dweight a block, where a block's rows are not fewer than the blocks that the GPU holds.
+// Up to 16 KB of dweight a block, less where that would leave the GPU with fewer blocks than it holds.
 template <typename T>
 tide_status embed_grad_few(FewArgs a, cudaStream_t stream) {
   const bool vec = a.cols % 8 == 0 && rows_aligned(a.dy, a.lddy, sizeof(T), a.tokens) &&
