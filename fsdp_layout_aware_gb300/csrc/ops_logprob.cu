@@ -403,7 +403,8 @@ __global__ void __launch_bounds__(PER_ROW == 32 ? 256 : PER_ROW, 1024 / (PER_ROW
         __syncthreads();
       }
     }
-    // The ones at the bound, 32 vectors at a time in order, by one warp, until there are enough.
+    // The ones at the bound in order, eight vectors and then 32 at a time, by one warp, until there are enough (of a
+    // row of equals eight vectors hold them, and ranks cost their number squared).
     constexpr uint32_t kSweep = 256;
     if (strict && n < (uint32_t)top) {
       if constexpr (CLUSTER) {
@@ -412,13 +413,17 @@ __global__ void __launch_bounds__(PER_ROW == 32 ? 256 : PER_ROW, 1024 / (PER_ROW
       }
       __syncwarp();
       if (warp == 0 && rank == 0) {
-        for (int v = lane; v - lane < count; v += 32) {
-          if (v < count) {
+        for (int from = 0, most = 8; from < count; from += most, most = 32) {
+          const int v = from + lane;
+          if (lane < most && v < count) {
             Raw8<T> r;
             load(r, v);
             uint32_t hits = 0;
-            for (int i = 0; i < 8; ++i)
-              if (fmaxf(r.value(i), -INFINITY) == bound && (int64_t)v * 8 - phase + i >= 0 && (int64_t)v * 8 - phase + i < vocab) hits |= 1u << i;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int64_t col = (int64_t)v * 8 - phase + i;
+              if (fmaxf(r.value(i), -INFINITY) == bound && col >= 0 && col < vocab) hits |= 1u << i;  // NaN as -inf
+            }
             list(r, v, hits);
           }
           __syncwarp();
@@ -441,6 +446,7 @@ __global__ void __launch_bounds__(PER_ROW == 32 ? 256 : PER_ROW, 1024 / (PER_ROW
       for (uint32_t i = x; i < n; i += PER_ROW) {
         const uint64_t key = listed[here][i];
         int above = 0;
+#pragma unroll 8
         for (uint32_t j = 0; j < n; ++j) above += listed[here][j] > key;
         if (above < top) put(above, key);
       }
