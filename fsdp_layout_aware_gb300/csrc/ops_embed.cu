@@ -514,13 +514,14 @@ __global__ void __launch_bounds__(kJoinThreads, 2) join_kernel(const SumArgs a) 
 
 // ---------------------------------------------------------------- few tokens
 
-// One launch and no workspace, for 512 tokens at most and 2^21 elements of dweight: 512 into 1000 x 64 bf16
+// One launch and no workspace, for 512 tokens at most and 2^21 elements of dweight, or 64 and 2^24: 512 into 1000 x 64 bf16
 // 4.9 us against 14.4 with the sort, 100 into 300 x 101 6.9 against 14.9; 512 into 32000 x 2048 are
 // 36 against 33, and, all of one token, into 1000 x 8192 44 against 16.  A block looks at all ids by itself, lists those of its rows of dweight
 // in the rows' order, and writes kFewVectors vectors of each row.  A run of more than kFewLong rows
 // is added up by all of the block's warps.
 constexpr int kFew = 512, kFewRows = 128, kFewVectors = 128, kFewLong = 16;
-constexpr int64_t kFewElements = 1 << 21, kFewBytes = 16 << 10;
+constexpr int kVeryFew = 64;
+constexpr int64_t kFewElements = 1 << 21, kVeryFewElements = 1 << 24, kFewBytes = 64 << 10;
 static_assert(kFew == 2 * kThreads, "two ids a thread");
 
 struct FewArgs {
@@ -690,7 +691,9 @@ struct GradSpace {
   int64_t list = 0, longs = 0, parts = 0, bytes = 0;
   int tile = 0;
 };
-bool few(int64_t tokens, int64_t vocab, int64_t cols) { return tokens <= kFew && vocab <= kFewElements / cols; }
+bool few(int64_t tokens, int64_t vocab, int64_t cols) {
+  return tokens <= kFew && vocab <= (tokens <= kVeryFew ? kVeryFewElements : kFewElements) / cols;
+}
 GradSpace grad_space(int64_t tokens, int64_t vocab, int64_t cols) {
   GradSpace g;
   if (tokens == 0 || few(tokens, vocab, cols)) return g;
@@ -704,7 +707,7 @@ GradSpace grad_space(int64_t tokens, int64_t vocab, int64_t cols) {
   return g;
 }
 
-// Up to 16 KB of dweight a block, less where that would leave the GPU with fewer blocks than it holds.
+// Up to 64 KB of dweight a block, less where that would leave the GPU with fewer blocks than it holds.
 template <typename T>
 tide_status embed_grad_few(FewArgs a, cudaStream_t stream) {
   const bool vec = a.cols % 8 == 0 && rows_aligned(a.dy, a.lddy, sizeof(T), a.tokens) &&

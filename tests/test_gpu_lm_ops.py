@@ -82,7 +82,7 @@ def test_embedding_of_no_vocabulary_is_zero():
 
 
 GRADS = [  # tokens, vocab, columns, share of one id
-    (0, 5, 24, 0.0), (512, 700, 48, 0.0), (512, 30, 1040, 0.9), (513, 30, 1040, 0.9), (511, 129, 2047, 0.1), (0, 70000, 33, 0.0), (300, 70000, 40, 0.3), (512, 1030, 2047, 0.9), (3, 40000, 65, 0.0), (1, 1, 1, 0.0), (1, 300, 16, 0.0), (7, 3, 33, 0.0), (64, 9, 64, 0.5), (65, 64, 40, 1.0),
+    (0, 5, 24, 0.0), (512, 700, 48, 0.0), (512, 30, 1040, 0.9), (513, 30, 1040, 0.9), (511, 129, 2047, 0.1), (0, 70000, 33, 0.0), (300, 70000, 40, 0.3), (512, 1030, 2047, 0.9), (3, 40000, 65, 0.0), (64, 20000, 130, 0.5), (65, 20000, 130, 0.5), (1, 1, 1, 0.0), (1, 300, 16, 0.0), (7, 3, 33, 0.0), (64, 9, 64, 0.5), (65, 64, 40, 1.0),
     (257, 100, 100, 1.0), (300, 33, 130, 0.7), (1000, 70000, 24, 0.1), (4096, 300, 56, 0.3), (4097, 257, 72, 0.9),
     (9000, 65536, 17, 0.2), (3000, 300000, 9, 0.1), (400000, 5000, 8, 0.3), (20011, 1000, 31, 0.05), (5000, 40, 1032, 0.6), (4099, 2, 2056, 0.4)]
 
