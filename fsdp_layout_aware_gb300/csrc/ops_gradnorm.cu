@@ -14,7 +14,6 @@
 
 #include <algorithm>
 #include <cmath>
-#include <limits>
 
 #include "cluster_ptx.cuh"
 #include "ops_common.cuh"
@@ -35,11 +34,12 @@ constexpr int kKept = (64 << 20) / (int)kChunk;
 
 // Tensors of a launch, by the room that a kernel's 32,764 bytes of arguments leave;
 // small lists take small tables, since arguments are copied for every launch.
-constexpr int kNormTables[] = {32, 128, 512, 1600}, kClipTables[] = {32, 128, 512, 1150};
+constexpr int kNormTables[] = {32, 256, 512, 1600}, kClipTables[] = {32, 256, 512, 1150};
 
 template <int CAP>
 struct NormTable {
   int32_t count, chunks;
+  float per_chunk;    // tensors
   uint64_t at[CAP];   // address; bit 0: fp32
   int64_t bytes[CAP];
   int32_t end[CAP];   // chunks of the tensors up to this one
@@ -61,13 +61,19 @@ struct ChunkRange {
 
 template <int CAP>
 __device__ __forceinline__ ChunkRange chunk_of(const NormTable<CAP>& t, int chunk) {
-  int lo = 0, hi = t.count - 1;  // the first tensor whose chunks end behind this one
+  // The first tensor whose chunks end behind this one.  Each look at the table costs half a microsecond while it is
+  // not in the SM's constant cache, so the first is at the place where a list of like tensors has it.
+  int lo = 0, hi = t.count - 1;
+  int mid = min((int)((float)chunk * t.per_chunk), hi);
   while (lo < hi) {
-    const int mid = (lo + hi) / 2;
-    if (t.end[mid] > chunk)
-      hi = mid;
+    const int end = t.end[mid], begin = mid > 0 ? t.end[mid - 1] : 0;
+    if (begin <= chunk && chunk < end)
+      lo = hi = mid;
+    else if (chunk < begin)
+      hi = mid - 1;
     else
       lo = mid + 1;
+    mid = (lo + hi) / 2;
   }
   const uint64_t a = t.at[lo] & ~1ull;
   ChunkRange r;
@@ -105,16 +111,16 @@ __device__ __forceinline__ uint4 load_once(const unsigned char* p, uint64_t poli
   return v;
 }
 
-// A thread's granules of a chunk; once: an L2 policy for whole chunks' loads, 0 for none.
-__device__ __forceinline__ void load_chunk(const ChunkRange& r, uint4 (&u)[kGranules], uint64_t once = 0) {
-  const unsigned char* p = r.granule + r.at + threadIdx.x * 16;
+// The granules of a chunk that are the x-th of kThreads threads'; once: an L2 policy for whole chunks' loads, 0 for none.
+__device__ __forceinline__ void load_chunk(const ChunkRange& r, int x, uint4 (&u)[kGranules], uint64_t once = 0) {
+  const unsigned char* p = r.granule + r.at + x * 16;
   if (r.whole()) {
 #pragma unroll
     for (int j = 0; j < kGranules; ++j) u[j] = once ? load_once(p + j * kThreads * 16, once) : *reinterpret_cast<const uint4*>(p + j * kThreads * 16);
   } else {
 #pragma unroll
     for (int j = 0; j < kGranules; ++j) {
-      const int64_t off = r.at + (j * kThreads + (int)threadIdx.x) * 16;
+      const int64_t off = r.at + (j * kThreads + x) * 16;
       u[j] = make_uint4(0, 0, 0, 0);
       if (off >= r.first && off + 16 <= r.last)
         u[j] = *reinterpret_cast<const uint4*>(r.granule + off);
@@ -189,16 +195,16 @@ __device__ __forceinline__ double block_sum(double v) {
   return v;
 }
 
-// JOIN: the grid is one cluster, whose first block joins the others' sums by itself.
-template <int CAP, bool JOIN>
-__global__ void __launch_bounds__(kThreads, kPerSm) norm_kernel(const __grid_constant__ NormTable<CAP> t, double* partial,
-                                                               float* norm) {
+// JOIN: the grid is one cluster, whose first block joins the others' sums by itself.  Blocks take AT_ONCE chunks at a time.
+template <int CAP, bool JOIN, int AT_ONCE>
+__global__ void __launch_bounds__(kThreads * AT_ONCE, AT_ONCE == 1 ? kPerSm : 1)
+    norm_kernel(const __grid_constant__ NormTable<CAP> t, double* partial, float* norm) {
   const uint64_t policy = policy_evict_first();
   double sum = 0.0;
-  for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
+  for (int c = blockIdx.x * AT_ONCE + threadIdx.x / kThreads; c < t.chunks; c += gridDim.x * AT_ONCE) {
     const ChunkRange r = chunk_of(t, c);
     uint4 u[kGranules];
-    load_chunk(r, u, c < t.chunks - kKept ? policy : 0);
+    load_chunk(r, threadIdx.x % kThreads, u, c < t.chunks - kKept ? policy : 0);
     sum += squares(u, r.fp32);
   }
   sum = block_sum(sum);
@@ -238,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) clip_kernel(const __grid_con
     if (by == 1.0f && out == r.granule + r.first) continue;
     if (((uintptr_t)out & 15) == (uintptr_t)r.first) {
       uint4 u[kGranules];
-      load_chunk(r, u);
+      load_chunk(r, threadIdx.x, u);
 #pragma unroll
       for (int j = 0; j < kGranules; ++j) {
         uint32_t w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
@@ -321,16 +327,21 @@ int32_t fill(NormTable<CAP>& t, int32_t i, int32_t count, const void* const* ten
     ++t.count;
   }
   t.chunks = (int32_t)chunks;
+  t.per_chunk = chunks > 0 ? (float)t.count / (float)chunks : 0.0f;
   return i;
 }
 
-// Up to so many chunks a single cluster of kCluster blocks does alone: no partial sums in memory and
-// one launch, which from Python takes 5 us and two take 8 (12 tensors of 16 KB: 5.4 us of the GPU's time, as with two;
-// 48 of one element 10.5 against 6, 400 of 100 40 against 8).
-constexpr int64_t kAlone = 24;
-constexpr int kCluster = 8;
+// Up to so many chunks and bytes a single cluster of kCluster blocks does alone: no partial sums in memory, for which the
+// binding would ask the allocator (7 us), and one launch.  One cluster against two launches, us a call from Python and in a
+// graph: 12 tensors of 32 KB 4.6 and 4.4 against 11.7 and 5.1, 100 of 400 bytes 8.9 and 10.6 against 13.2 and 5.5,
+// 211 of 400 bytes 11.8 and 14.9 against 14.4 and 6.3.  Blocks of kAtOnce chunks at a time take a microsecond longer
+// to begin (12 tensors in a graph 5.7 against 4.4), so those are for the longer lists.
+constexpr int64_t kAlone = 160, kAloneBytes = 2 << 20;
+constexpr int kCluster = 8, kAtOnce = 4;
 bool alone(int32_t count, const int64_t* numels, const int32_t* dtypes) {
-  return count <= kAlone && count + list_bytes(count, numels, dtypes) / kChunk <= kAlone;
+  if (count > kAlone) return false;
+  const int64_t bytes = list_bytes(count, numels, dtypes);
+  return bytes <= kAloneBytes && count + bytes / kChunk <= kAlone;
 }
 
 // Launches of a list of tensors at most: a table full of tensors, or of chunks.
@@ -344,8 +355,11 @@ tide_status norm_list(int32_t count, const void* const* tensors, const int64_t* 
   NormTable<CAP> t;
   if (alone(count, numels, dtypes)) {
     fill(t, 0, count, tensors, numels, dtypes, [](int, int32_t) {});
-    const ClusterLaunch l(kCluster, dim3(kThreads), kCluster, false, 0, stream);
-    return cuda_status(cudaLaunchKernelEx(&l.cfg, norm_kernel<CAP, true>, t, (double*)nullptr, norm), "gradient norm");
+    const bool few = t.chunks <= 3 * kCluster;
+    const ClusterLaunch l(kCluster, dim3(few ? kThreads : kThreads * kAtOnce), kCluster, false, 0, stream);
+    return cuda_status(few ? cudaLaunchKernelEx(&l.cfg, norm_kernel<CAP, true, 1>, t, (double*)nullptr, norm)
+                           : cudaLaunchKernelEx(&l.cfg, norm_kernel<CAP, true, kAtOnce>, t, (double*)nullptr, norm),
+                       "gradient norm");
   }
   const int64_t most = (int64_t)ops_num_sms() * kPerSm;
   int64_t sums = 0;
@@ -354,7 +368,7 @@ tide_status norm_list(int32_t count, const void* const* tensors, const int64_t* 
     if (t.count == 0) continue;
     const int64_t grid = std::min<int64_t>(t.chunks, most);
     if ((sums + grid) * (int64_t)sizeof(double) > room) return fail(TIDE_ERR_INVALID_ARG, "workspace too small");
-    norm_kernel<CAP, false><<<(unsigned)grid, kThreads, 0, stream>>>(t, partial + sums, nullptr);
+    norm_kernel<CAP, false, 1><<<(unsigned)grid, kThreads, 0, stream>>>(t, partial + sums, nullptr);
     TIDE_TRY(cuda_status(cudaGetLastError(), "gradient norm"));
     sums += grid;
   }
