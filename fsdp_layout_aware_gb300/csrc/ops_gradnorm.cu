@@ -5,7 +5,7 @@
 // travels in the kernel's arguments (up to 32 KB of them), so a call copies nothing to the device,
 // and a captured one keeps its list.
 //
-//   64 fp32 tensors of 5.5 million elements (1.4 GB): norm 197 us, 7.1 TB/s; clipping 430 us, 6.5 TB/s of
+//   64 fp32 tensors of 5.5 million elements (1.4 GB): norm 195 to 198 us, 7.1 TB/s; clipping 433 us, 6.5 TB/s of
 //   reads and writes; 391 tensors of all sizes and alignments (60 MB) 17 and 23 us
 //
 // A tensor is walked in chunks of kChunk bytes counted from the 16-byte granule it starts
@@ -199,6 +199,7 @@ __device__ __forceinline__ double block_sum(double v) {
 template <int CAP, bool JOIN, int AT_ONCE>
 __global__ void __launch_bounds__(kThreads * AT_ONCE, AT_ONCE == 1 ? kPerSm : 1)
     norm_kernel(const __grid_constant__ NormTable<CAP> t, double* partial, float* norm) {
+  if constexpr (!JOIN) let_next_kernel_start();  // the join's block waits beside this: 211 tensors of 400 bytes 5.9 us became 5.2
   const uint64_t policy = policy_evict_first();
   double sum = 0.0;
   for (int c = blockIdx.x * AT_ONCE + threadIdx.x / kThreads; c < t.chunks; c += gridDim.x * AT_ONCE) {
@@ -331,17 +332,20 @@ int32_t fill(NormTable<CAP>& t, int32_t i, int32_t count, const void* const* ten
   return i;
 }
 
-// Up to so many chunks and bytes a single cluster of kCluster blocks does alone: no partial sums in memory, for which the
+// Up to so many chunks a single cluster of kCluster blocks does alone: no partial sums in memory, for which the
 // binding would ask the allocator (7 us), and one launch.  One cluster against two launches, us a call from Python and in a
-// graph: 12 tensors of 32 KB 4.6 and 4.4 against 11.7 and 5.1, 100 of 400 bytes 8.9 and 10.6 against 13.2 and 5.5,
-// 211 of 400 bytes 11.8 and 14.9 against 14.4 and 6.3.  Blocks of kAtOnce chunks at a time take a microsecond longer
-// to begin (12 tensors in a graph 5.7 against 4.4), so those are for the longer lists.
-constexpr int64_t kAlone = 160, kAloneBytes = 2 << 20;
+// graph: 12 tensors of 32 KB 4.4 and 4.4 against 13.6 and 4.6, 60 of 32 KB 7.4 and 7.8 against 14.0 and 5.1, one of 2 MB
+// 4.3 and 6.9 against 13.2 and 4.9; 100 of 400 bytes 8.9 and 10.5 against 14.9 and 4.5.  Blocks of kAtOnce chunks at a
+// time take a microsecond longer to begin (12 tensors in a graph 5.7 against 4.4), so those are for the longer lists.
+constexpr int64_t kAlone = 64;
 constexpr int kCluster = 8, kAtOnce = 4;
 bool alone(int32_t count, const int64_t* numels, const int32_t* dtypes) {
-  if (count > kAlone) return false;
-  const int64_t bytes = list_bytes(count, numels, dtypes);
-  return bytes <= kAloneBytes && count + bytes / kChunk <= kAlone;
+  int64_t chunks = 0;  // at most, whatever the addresses
+  for (int32_t i = 0; i < count && chunks <= kAlone; ++i) {
+    const int64_t bytes = std::min<int64_t>(numels[i], (int64_t)1 << 40) * elem_bytes_of(dtypes[i]);
+    chunks += bytes > 0 ? (15 + bytes + kChunk - 1) / kChunk : 0;
+  }
+  return chunks <= kAlone;
 }
 
 // Launches of a list of tensors at most: a table full of tensors, or of chunks.

@@ -511,6 +511,20 @@ def test_norm_of_norms():
     assert abs(norm.item() - want) <= 2 * tol * want
 
 
+@pytest.mark.parametrize("sizes", [
+    [5] * 24, [5] * 25, [5] * 64, [5] * 65, [8192] * 32, [8192] * 33, [8192 * 62], [8192 * 65],
+    [0] * 300 + [9000] * 3 + [0] * 1400 + [1], [0] * 40, [8192 * 40, 0, 3] + [1] * 30,
+])
+@pytest.mark.parametrize("lead", [0, 1])
+def test_norm_of_lists_of_few_chunks(sizes, lead):
+    """Lists at the sizes where one launch, or blocks of another size, take their place."""
+    host, dev, _ = lists(sizes, (FP,), 11, lead)
+    norm = torch.full((1,), -1.0, device=DEV)
+    tide.tide_grad_norm(dev, norm)
+    want, tol = R.norm(host)
+    assert abs(norm.item() - want) <= tol * want
+
+
 def test_norm_is_the_same_every_time():
     _, dev, _ = lists([700000, 12, 300001, 5000000], (FP, BF), 1, 1)
     x = tide.TensorList(dev)
