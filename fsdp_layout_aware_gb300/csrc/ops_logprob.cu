@@ -407,11 +407,14 @@ __global__ void __launch_bounds__(PER_ROW == 32 ? 256 : PER_ROW, 1024 / (PER_ROW
     // row of equals eight vectors hold them, and ranks cost their number squared).
     constexpr uint32_t kSweep = 256;
     if (strict && n < (uint32_t)top) {
+      // All have read the counts, by which they came here, before a count moves.
       if constexpr (CLUSTER) {
-        cluster_sync();  // all have read the counts
+        cluster_sync();
         if (x == 0 && rank == 0) listed_count[0] = n;
+        __syncwarp();
+      } else {
+        sync();
       }
-      __syncwarp();
       if (warp == 0 && rank == 0) {
         for (int from = 0, most = 8; from < count; from += most, most = 32) {
           const int v = from + lane;

@@ -1,0 +1,50 @@
+"""The operators at the ends of a training step on inputs whose results are exact or known in closed form, so that one
+element left out, counted twice or written from a list that is not complete shows."""
+
+import math
+
+import pytest
+import torch
+
+import fsdp_layout_aware_gb300 as tide
+from test_gpu_lm_ops import BF, DEV, FP
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- alternatives
+
+# Rows and vocabularies at which 32, 128, 256 and 512 threads share a row with alternatives, and a cluster of blocks.
+SHARED = [(3000, 1000), (600, 4000), (300, 4000), (64, 4096), (400, 13000), (400, 20000), (200, 32000), (64, 20000), (2, 131072)]
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("rows,vocab", SHARED)
+def test_alternatives_of_few_tokens_every_time(rows, vocab, dtype):
+    """Fewer tokens than alternatives are left, none are, or all are alike: the list is filled up in the tokens' order,
+    the same in each of many calls."""
+    top = 20
+    x = torch.full((rows, vocab), -math.inf)
+    want = torch.arange(top).repeat(rows, 1)
+    left = torch.arange(rows) % 7  # of them: 0 none, 6 all alike
+    for n in range(1, 6):
+        at = torch.tensor([vocab - 1, vocab // 2, 40, vocab // 3, 7 * vocab // 8][:n])
+        some = left == n
+        x[some[:, None] & torch.zeros(vocab, dtype=torch.bool).index_fill(0, at, True)] = 3.0
+        first = torch.sort(at).values
+        rest = torch.tensor([t for t in range(64) if t not in at.tolist()])[:top - n]
+        want[some] = torch.cat([first, rest])
+    x[left == 6] = 0.5
+    count = torch.where(left == 6, vocab, left).double()
+    logp = torch.where(torch.arange(top) < count[:, None], -torch.log(count)[:, None], -math.inf)
+    x, want, logp = x.to(dtype).to(DEV), want.to(DEV), logp.to(DEV)
+    values, names = torch.empty(rows, top, device=DEV), torch.empty(rows, top, dtype=torch.int32, device=DEV)
+    wrong = torch.zeros((), dtype=torch.int64, device=DEV)
+    for _ in range(200 if rows * vocab < 1 << 22 else 60):
+        values.fill_(7.0), names.fill_(-7)
+        tide.tide_log_probs(x, top=(values, names))
+        wrong += (names != want).sum()
+        # ln of a whole number below 2^18: exact sum, ln to 2 steps, the difference from 0 exact.
+        far = (values.double() - logp).abs() > 4 * 2.0 ** -24 * 13
+        wrong += (torch.where(logp.isinf(), values != logp.float(), far)).sum()
+    assert wrong.item() == 0
