@@ -521,6 +521,7 @@ struct RowGrad {
     if (empty) peak = 0.0f, rest = INFINITY;  // every p is 0
     float h = 0.0f, entropy = 0.0f;
     if (p.dentropy) h = p.dentropy[row], entropy = p.entropy[row];
+    if (empty) h = entropy = 0.0f;  // what came back for it may be infinite or NaN, and 0 times that is not 0
     if (p.targets) {
       target = token_at(p.targets, p.index, row, p.vocab);
       if (target >= 0 && !empty) g = p.scale * p.dlogp[row];

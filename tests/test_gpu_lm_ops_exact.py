@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import fsdp_layout_aware_gb300 as tide
-from test_gpu_lm_ops import BF, DEV, FP
+from test_gpu_lm_ops import BF, DEV, FP, logits, put, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +48,35 @@ def test_alternatives_of_few_tokens_every_time(rows, vocab, dtype):
         far = (values.double() - logp).abs() > 4 * 2.0 ** -24 * 13
         wrong += (torch.where(logp.isinf(), values != logp.float(), far)).sum()
     assert wrong.item() == 0
+
+
+# ---------------------------------------------------------------- the gradient
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("parts", [False, True])
+@pytest.mark.parametrize("vocab,lead", [(64, 0), (64, 1), (4999, 0)])
+@pytest.mark.parametrize("given", [math.nan, math.inf, -math.inf])
+def test_rows_without_a_token_have_no_gradient(given, vocab, lead, parts, dtype):
+    """Whatever comes back for their entropy (0) and log probability (-inf); nor does a target outside take dlogp in."""
+    rows = 6
+    x = logits(rows, vocab, dtype, 1)
+    x[[0, 3]] = -math.inf
+    x, _ = put(x, lead, 0)
+    t = torch.tensor([2, 5, vocab, -1, 7, 1], device=DEV)
+    g, h = randn((rows,), FP, 2).to(DEV), randn((rows,), FP, 3).to(DEV)
+    logp, lse, entropy = (torch.empty(rows, device=DEV) for _ in range(3))
+    two = torch.empty(rows, 2, device=DEV)
+    tide.tide_log_probs(x, t, logp, lse=lse, entropy=entropy, lse_parts=two)
+    source = dict(lse=None, lse_parts=two) if parts else dict(lse=lse)
+
+    def grad(g, h):
+        d = torch.full((rows, vocab), 9.0, dtype=dtype, device=DEV)
+        tide.tide_log_probs_backward(x, dlogits=d, targets=t, dlogp=g, entropy=entropy, dentropy=h, **source)
+        return d
+
+    want = grad(g, h)
+    assert want.isfinite().all() and (want[[0, 3]] == 0).all()
+    odd_g, odd_h = g.clone(), h.clone()
+    odd_g[[0, 2, 3]] = given  # rows without a token, or with a target outside
+    odd_h[[0, 3]] = given
+    assert torch.equal(grad(odd_g, odd_h), want)
