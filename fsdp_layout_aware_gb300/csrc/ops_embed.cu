@@ -83,9 +83,11 @@ __global__ void __launch_bounds__(kThreads) embed_any_kernel(const EmbedArgs a) 
   if (col >= a.cols) return;
   const int token = token_at(a.ids, a.index, row, a.vocab);
   float v[8] = {};
-  if (token >= 0) load_columns((const T*)a.weight + token * a.ldw, col, a.cols, v);
+  if (token >= 0) {
+    load_columns((const T*)a.weight + token * a.ldw, col, a.cols, v);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) v[k] *= a.scale;
+    for (int k = 0; k < 8; ++k) v[k] *= a.scale;
+  }
   store_columns(out, col, a.cols, v);
 }
 
@@ -601,12 +603,13 @@ __global__ void __launch_bounds__(kThreads, 4) few_kernel(const FewArgs a) {
 #pragma unroll
     for (int c = 0; c < 8; ++c) sum[c] += v[c];
   };
-  auto store = [&](float (&sum)[8], int64_t row, int64_t col) {
+  // by: the scale, but 0 of a row that no id names: its zeros have a sign, or are NaN, by some scales.
+  auto store = [&](float (&sum)[8], int64_t row, int64_t col, float by) {
     T* const out = (T*)a.dweight + row * a.lddw;
     float old[8];
     if (a.accumulate) load_columns(out, col, a.cols, old);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) sum[c] = a.accumulate ? fmaf(sum[c], a.scale, old[c]) : sum[c] * a.scale;
+    for (int c = 0; c < 8; ++c) sum[c] = a.accumulate ? fmaf(sum[c], by, old[c]) : sum[c] * by;
     if constexpr (ANY)
       store_columns(out, col, a.cols, sum);
     else
@@ -621,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 4) few_kernel(const FewArgs a) {
     float sum[8] = {};
 #pragma unroll 4
     for (int p = begin; p < end; ++p) add(sum, p, col);
-    store(sum, row, col);
+    store(sum, row, col, begin == end ? 0.0f : a.scale);
   }
   if (n <= kFewLong) return;
   for (int r = 0; r < rows; ++r) {
@@ -650,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 4) few_kernel(const FewArgs a) {
 #pragma unroll
         for (int c = 0; c < 8; ++c) sum[c] += t[c];
       }
-      store(sum, row, col);
+      store(sum, row, col, a.scale);
     }
   }
 }

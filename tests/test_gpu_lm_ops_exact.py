@@ -7,9 +7,35 @@ import pytest
 import torch
 
 import fsdp_layout_aware_gb300 as tide
-from test_gpu_lm_ops import BF, DEV, FP, logits, put, randn
+from test_gpu_lm_ops import BF, DEV, FP, logits, put, randn, tokens
 
 pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- embedding
+
+def all_zero_bits(x):
+    return not x.contiguous().view(torch.uint8).any()
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("scale", [-1.5, math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("lead,extra", [(0, 0), (1, 0), (3, 5)])
+@pytest.mark.parametrize("n,vocab,cols", [(40, 300, 64), (40, 300, 61), (900, 2000, 64), (900, 2000, 61), (3000, 40, 24)])
+def test_padding_is_zeros_whatever_the_scale(n, vocab, cols, lead, extra, scale, dtype):
+    """Rows that no token stands for are +0 on rows of any alignment, for few tokens and many."""
+    ids = tokens(n, vocab, n).to(DEV)
+    here = (ids >= 0) & (ids < vocab)
+    w, _ = put(randn((vocab, cols), dtype, 1), lead, extra)
+    out, _ = put(torch.full((n, cols), 9.0, dtype=dtype), lead, extra)
+    tide.tide_embedding(ids, w, out, scale=scale)
+    assert all_zero_bits(out[~here]) and not all_zero_bits(out[here])
+    dw, _ = put(torch.full((vocab, cols), 9.0, dtype=dtype), lead, extra)
+    ids = torch.where(ids == vocab // 2, 0, ids)
+    tide.tide_embedding_backward(ids, put(randn((n, cols), dtype, 2), lead, extra)[0], dw, scale=scale)
+    named = torch.zeros(vocab, dtype=torch.bool, device=DEV)
+    named[ids[(ids >= 0) & (ids < vocab)]] = True
+    assert not named.all() and all_zero_bits(dw[~named]) and not all_zero_bits(dw[named])
 
 
 # ---------------------------------------------------------------- alternatives
