@@ -29,8 +29,8 @@ typedef enum tide_index { TIDE_I32 = 0, TIDE_I64 = 1 } tide_index;
 /* ---- token embedding ------------------------------------------------------
  * out[t] = scale * weight[ids[t]]: ids [tokens] of type `index`, weight
  * [vocab, cols] and out [tokens, cols] of `dtype`.  An id outside 0..vocab-1
- * (padding) gives a row of zeros.  tokens and vocab below 2^31, cols at
- * most 2^24 (UNIMPLEMENTED beyond). */
+ * (padding) gives a row of zeros.  At most 2^31 - 1 tokens, 2^31 - 2 rows of weight
+ * and 2^24 columns (UNIMPLEMENTED beyond). */
 tide_status tide_embedding(int64_t tokens, int64_t vocab, int64_t cols, int32_t index, const void* ids, int32_t dtype,
                            const void* weight, int64_t ldw, float scale, void* out, int64_t ldo, void* stream);
 
@@ -38,8 +38,7 @@ tide_status tide_embedding(int64_t tokens, int64_t vocab, int64_t cols, int32_t 
  * where there are none; ids outside 0..vocab-1 take no part.  With accumulate
  * not 0 that is added to what dweight holds (the sum in fp32, rounded once), and rows
  * that no id names are left as they are.  dy [tokens, cols] and dweight
- * [vocab, cols] are of `dtype`.  The sum runs in a fixed order.  Limits as above, and
- * cols at most 2^24. */
+ * [vocab, cols] are of `dtype`.  The sum runs in a fixed order.  Limits as above. */
 int64_t tide_embedding_backward_workspace(int64_t tokens, int64_t vocab, int64_t cols);
 tide_status tide_embedding_backward(int64_t tokens, int64_t vocab, int64_t cols, int32_t index, const void* ids,
                                     int32_t dtype, const void* dy, int64_t lddy, float scale, void* dweight,
@@ -62,7 +61,7 @@ tide_status tide_embedding_backward(int64_t tokens, int64_t vocab, int64_t cols,
  * and top_logp -inf.  A row that holds +inf or NaN has NaN in all of them (and in
  * lse_parts' second) but for targets outside; its top_tokens still go by its logits,
  * NaN counting as -inf.
- * vocab below 2^31, rows below 2^31 (UNIMPLEMENTED beyond). */
+ * At most 2^31 - 1 rows of 2^31 - 17 logits (UNIMPLEMENTED beyond), here and for the gradient. */
 tide_status tide_log_probs(int64_t rows, int64_t vocab, int32_t dtype, const void* logits, int64_t ldl, float scale,
                            int32_t index, const void* targets, float* logp, float* lse, float* lse_parts,
                            float* entropy, int32_t top, float* top_logp, int64_t ld_top_logp, int32_t* top_tokens, int64_t ld_top_tokens,
@@ -85,7 +84,7 @@ tide_status tide_log_probs_backward(int64_t rows, int64_t vocab, int32_t dtype, 
 /* ---- gradient norm and clipping -------------------------------------------
  * Lists of `count` tensors: host arrays, read during the call only, of device
  * addresses, numbers of (contiguous) elements and element types (tide_dtype).
- * An address may be NULL where the number is 0. */
+ * An address may be NULL where the number is 0.  At most 2^40 elements a tensor (UNIMPLEMENTED beyond). */
 
 /* norm[0] = the square root of the sum of all tensors' squared elements.
  * Squares are never lost to fp32's range.  An infinity gives +inf, NaN gives NaN (also beside one).
