@@ -294,18 +294,20 @@ __global__ void __launch_bounds__(PER_ROW == 32 ? 256 : PER_ROW, 1024 / (PER_ROW
 
   const bool empty = sums.s == 0.0f;
   const float log_s = logf(sums.s);
+  // A logit's log probability.  Of the halves, whose difference is in fp32's range where the logits' is not.
+  auto logp_of = [&](float logit) { return fmaf(0.5f * logit - 0.5f * sums.m, 2.0f * a.scale, -log_s); };
   if (x == 0 && rank == 0) {
     if (a.lse) a.lse[row] = empty ? -INFINITY : fmaf(sums.m, a.scale, log_s);
     if (a.lse_parts) a.lse_parts[2 * row] = empty ? -INFINITY : sums.m, a.lse_parts[2 * row + 1] = log_s;
     if (ENTROPY) a.entropy[row] = empty ? 0.0f : log_s - kLn2 * (sums.e / sums.s);
-    if (a.logp) a.logp[row] = target < 0 ? 0.0f : empty ? -INFINITY : fmaf(target_logit - sums.m, a.scale, -log_s);
+    if (a.logp) a.logp[row] = target < 0 ? 0.0f : empty ? -INFINITY : logp_of(target_logit);
   }
   if constexpr (TOP) {
     const int top = a.top;
     auto put = [&](int at, uint64_t key) {
       if (a.top_logp)
         a.top_logp[row * a.ld_logp + at] =
-            empty ? -INFINITY : fmaf(of_ordered((uint32_t)(key >> 32)) - sums.m, a.scale, -log_s);
+            empty ? -INFINITY : logp_of(of_ordered((uint32_t)(key >> 32)));
       if (a.top_tokens) a.top_tokens[row * a.ld_tokens + at] = (int32_t)~(uint32_t)key;
     };
     auto load = [&](Raw8<T>& r, int at) {
@@ -673,7 +675,8 @@ tide_status log_probs_grad(GradArgs a, int64_t rows, cudaStream_t stream) {
 tide_status check_logits(int64_t rows, int64_t vocab, int32_t dtype, const void* logits, int64_t ldl, float scale) {
   TIDE_TRY(check_sizes(rows, vocab, "log probabilities"));
   TIDE_TRY(check_dtype(dtype));
-  if (!(scale > 0.0f && scale <= 0x1p64f)) return fail(TIDE_ERR_INVALID_ARG, "scale is not above 0 and at most 2^64");
+  // A logit whose distance from the largest leaves fp32's range (above) has p = 0: so it must at this scale.
+  if (!(scale >= 0x1p-120f && scale <= 0x1p64f)) return fail(TIDE_ERR_INVALID_ARG, "scale is not between 2^-120 and 2^64");
   if (rows > INT32_MAX || vocab > INT32_MAX - 16) return fail(TIDE_ERR_UNIMPLEMENTED, "log probabilities: 2^31 rows or logits a row");
   return check_matrix(logits, rows, vocab, ldl, elem_bytes_of(dtype), "logits");
 }

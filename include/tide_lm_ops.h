@@ -47,7 +47,7 @@ tide_status tide_embedding_backward(int64_t tokens, int64_t vocab, int64_t cols,
 
 /* ---- log probabilities ----------------------------------------------------
  * For each row of logits [rows, vocab] (`dtype`), with z = scale * logits
- * (scale above 0, at most 2^64: 1 / temperature) and p = exp(z - lse):
+ * (scale 2^-120 to 2^64: 1 / temperature) and p = exp(z - lse):
  *   lse [rows]                log(sum over v of exp(z[v]))
  *   lse_parts [rows, 2]       the largest logit, and lse less scale times that
  *   logp [rows]               z[targets] - lse; 0 for a target outside 0..vocab-1

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import fsdp_layout_aware_gb300 as tide
-from test_gpu_lm_ops import BF, DEV, FP, logits, put, randn, tokens
+from test_gpu_lm_ops import BF, DEV, FP, check_log_probs, logits, put, randn, tokens
 
 pytestmark = pytest.mark.gpu
 
@@ -74,6 +74,22 @@ def test_alternatives_of_few_tokens_every_time(rows, vocab, dtype):
         far = (values.double() - logp).abs() > 4 * 2.0 ** -24 * 13
         wrong += (torch.where(logp.isinf(), values != logp.float(), far)).sum()
     assert wrong.item() == 0
+
+
+# ---------------------------------------------------------------- log probabilities
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("scale", [2.0 ** -120, 2.0 ** -100, 2.0 ** -64, 0.25])
+@pytest.mark.parametrize("vocab", [9, 4999, 30000])
+def test_logits_further_apart_than_fp32_reaches(vocab, scale, dtype):
+    """logp and top_logp of a logit that lies more than fp32's range below the largest, at a scale that brings it back."""
+    big = torch.finfo(dtype).max
+    x = logits(3, vocab, dtype, 1)
+    x[0, 3], x[0, 5] = big, -big
+    x[1] = -big
+    x[1, vocab - 1] = big / 2
+    x[2, 1:] = -big
+    check_log_probs(x, torch.tensor([5, 0, 2]), scale, min(vocab, 9))
 
 
 # ---------------------------------------------------------------- the gradient

@@ -30,3 +30,11 @@ def test_the_last_size_taken_and_the_first_refused(call, size, last, other, then
     assert at(last) == then, lib().tide_last_error()
     assert at(last + 1) == UNIMPLEMENTED
     assert lib().tide_last_error()
+
+
+@pytest.mark.parametrize("call", [probs, probs_grad])
+def test_scales_that_are_taken(call):
+    for scale in (2.0 ** -120, 1.0, 2.0 ** 64):
+        assert call(scale=scale, rows=0) == OK
+    for scale in (2.0 ** -121, 1e-40, 2.0 ** 65):
+        assert call(scale=scale, rows=0) == INVALID
