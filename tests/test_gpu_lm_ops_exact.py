@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import fsdp_layout_aware_gb300 as tide
-from test_gpu_lm_ops import BF, DEV, FP, check_log_probs, logits, put, randn, tokens
+from test_gpu_lm_ops import BF, DEV, FP, check_log_probs, gen, logits, put, randn, tokens
 
 pytestmark = pytest.mark.gpu
 
@@ -36,6 +36,42 @@ def test_padding_is_zeros_whatever_the_scale(n, vocab, cols, lead, extra, scale,
     named = torch.zeros(vocab, dtype=torch.bool, device=DEV)
     named[ids[(ids >= 0) & (ids < vocab)]] = True
     assert not named.all() and all_zero_bits(dw[~named]) and not all_zero_bits(dw[named])
+
+
+def runs_of(tile, n, vocab, seed):
+    """n ids whose runs, sorted, are of one place up to more than 512 tiles, begin anywhere in a tile, and leave rows out;
+    in any order."""
+    lengths = [1, tile - 1, tile, tile + 1, 2, 2 * tile - 1, 2 * tile, 3, 2 * tile + 1, 3 * tile + 5, 1, 10 * tile + 1, 17 * tile]
+    if n > 520 * tile + 7:
+        lengths.append(520 * tile + 7)
+    ids, at = [], 0
+    while at < n:
+        length = min(lengths[len(ids) % len(lengths)], n - at)
+        ids.append(torch.full((length,), 2 * len(ids) % vocab))  # beyond vocab / 2 runs: the same ids again
+        at += length
+    return torch.cat(ids)[torch.randperm(n, generator=gen(seed))]
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("lead,extra", [(0, 0), (3, 5)])
+@pytest.mark.parametrize("n,cols,tile", [(20011, 8, 8), (20011, 2056, 16), (20011, 4104, 32), (20011, 8200, 64), (400000, 16, 8),
+                                         (400000, 104, 16), (400000, 208, 32), (400000, 408, 64), (513, 40, 8), (700, 33, 8)])
+def test_embedding_gradient_adds_every_row_once(n, cols, tile, lead, extra, dtype):
+    """Small whole numbers, whose sums fp32 holds exactly in any order, by tiles of each size on a GPU of 152 SMs."""
+    vocab = 4001
+    ids = runs_of(tile, n, vocab, n + cols).to(DEV)
+    row, col = torch.arange(n, device=DEV)[:, None], torch.arange(cols, device=DEV)
+    value = ((row * 7 + col * 3) % 11 - 4).to(dtype)  # not 0 on average: one row more or less shows
+    dy, _ = put(value, lead, extra)
+    dw, _ = put(torch.full((vocab, cols), 9.0, dtype=dtype), (lead * 3) % 7, extra)
+    tide.tide_embedding_backward(ids.int() if lead else ids, dy, dw)
+    want = torch.zeros(vocab, cols, dtype=torch.float64, device=DEV).index_add_(0, ids, value.double())
+    assert want.abs().max() < 1 << 24
+    assert torch.equal(dw, want.to(dtype))
+    old = (torch.arange(vocab, device=DEV) % 5 - 2).to(dtype)[:, None].expand(vocab, cols)
+    dw.copy_(old)
+    tide.tide_embedding_backward(ids, dy, dw, scale=-2.0, accumulate=True)
+    assert torch.equal(dw, (old.double() - 2 * want).to(dtype))
 
 
 # ---------------------------------------------------------------- alternatives
@@ -77,6 +113,50 @@ def test_alternatives_of_few_tokens_every_time(rows, vocab, dtype):
 
 
 # ---------------------------------------------------------------- log probabilities
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("lead", [0, 1, 3])
+@pytest.mark.parametrize("top", [0, 3])
+@pytest.mark.parametrize("rows,vocab", [(2000, 1000), (300, 4003), (64, 4096), (400, 13001), (400, 20000), (200, 32005), (64, 20000),
+                                        (37, 131077), (2, 131072), (1, 500009)])
+def test_every_logit_counts_once(rows, vocab, top, lead, dtype):
+    """Rows of equal logits, a few of them masked: the sum is their number, which fp32 holds, and lse is its logarithm."""
+    x = torch.full((rows, vocab), 1.5, dtype=dtype, device=DEV)
+    hole = torch.arange(rows, device=DEV)
+    at = torch.stack([(hole * 7919) % vocab, vocab - 1 - hole % 40, (hole * 8) % vocab, (hole * 4096 + 4095) % vocab], 1)
+    for r in range(4):  # rows of no hole, one, two, and four
+        some = hole % 4 == r
+        x[some] = x[some].scatter(1, at[some][:, :r if r < 3 else 4], -math.inf)
+    x, _ = put(x, lead, lead)
+    count = (x == 1.5).sum(1).double()
+    parts, (lse, entropy) = torch.empty(rows, 2, device=DEV), (torch.empty(rows, device=DEV) for _ in range(2))
+    best = (torch.empty(rows, top, device=DEV), torch.empty(rows, top, dtype=torch.int32, device=DEV)) if top else None
+    tide.tide_log_probs(x, lse=lse, lse_parts=parts, entropy=entropy, top=best)
+    alone = torch.empty(rows, device=DEV)
+    tide.tide_log_probs(x, lse=alone)
+    # ln of a number below 2^19 to one step and a half, 2^-20 each; lse is rounded once more.
+    log_count = torch.log(count)
+    off = 1.5 * 2.0 ** -20
+    assert bool((parts[:, 0] == 1.5).all())
+    assert ((parts[:, 1].double() - log_count).abs() <= off).all()
+    assert ((entropy.double() - log_count).abs() <= off).all()  # no logit is away from the largest
+    for v in (lse, alone):
+        assert ((v.double() - 1.5 - log_count).abs() <= off + 2.0 ** -21).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("rows,vocab", SHARED)
+def test_rows_without_a_token_are_exact(rows, vocab, dtype):
+    x = torch.full((rows, vocab), -math.inf, dtype=dtype, device=DEV)
+    x[1::2] = 0.0
+    t = torch.tensor([-1, -1, vocab, 5, 3, vocab + 7], device=DEV).repeat(rows)[:rows]
+    logp, lse, entropy, parts = *(torch.full((rows,), 9.0, device=DEV) for _ in range(3)), torch.full((rows, 2), 9.0, device=DEV)
+    tide.tide_log_probs(x, t, logp, lse=lse, entropy=entropy, lse_parts=parts)
+    outside = (t < 0) | (t >= vocab)
+    assert bool((logp[outside] == 0).all())
+    assert bool((logp[::2][~outside[::2]] == -math.inf).all()) and bool((lse[::2] == -math.inf).all())
+    assert bool((entropy[::2] == 0).all()) and bool((parts[::2] == -math.inf).all())
+
 
 @pytest.mark.parametrize("dtype", [BF, FP])
 @pytest.mark.parametrize("scale", [2.0 ** -120, 2.0 ** -100, 2.0 ** -64, 0.25])
