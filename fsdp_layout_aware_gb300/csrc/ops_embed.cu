@@ -1,7 +1,7 @@
 // Token embedding, and its gradient by sorted tokens (include/tide_lm_ops.h).
 //
 // Forward: rows of the table are copied, scaled on the way; bound by memory traffic (16384 rows of 8192 bf16, 380 MB
-// with the rows read once: 62 us, 6.1 TB/s).
+// with the rows read once: 62 us, 6.1 TB/s; rows of 8191 104 us: a vector a thread, cut out of two granules).
 //
 // Backward, dweight[v] = scale * sum of dy[t] over the t with token v, is dense: every row
 // of dweight is written once, the rows of dy are read once, and both dwarf the ids.
@@ -13,8 +13,9 @@
 //      Where a run is longer than that, every tile leaves its part of it in the workspace.
 //   3. The parts of such runs (padding, separators, articles) are joined, a block at a time.
 // 16384 tokens into 131072 x 8192 bf16 (2.4 GB): 370 us, 6.5 TB/s; zeros 298 beside the sort's 18, sums 63, parts 10.
-// Small and odd ones are bound by latency: 4093 tokens into 4999 x 4095 fp32 (110 MB) 54 us, of which 20 are zeros
-// beside the sort's 12, 30 sums and 9 parts.
+// Small and odd ones wait for memory, not for its bandwidth: 4093 tokens into 4999 x 4095 fp32 (110 MB) 54 us, of which
+// 20 are zeros beside the sort's 12, 30 sums and 9 parts, one behind the other.  The sums read at a fifth of DRAM's rate:
+// 64 registers a thread leave half of an SM's warps, and 1026 blocks are 1.7 turns of the 608 that run at once.
 
 #include <algorithm>
 #include <type_traits>

@@ -28,8 +28,10 @@ constexpr int kThreads = 256;
 constexpr int kGranules = 8;
 constexpr int64_t kChunk = 16 * kThreads * kGranules;    // 32 KB
 constexpr int kPerSm = 4;                                // blocks an SM: 128 KB of loads in flight
-// The norm asks L2 to keep the last 64 MB of a list, from which clipping begins, and to let what
-// is before go first (norm and clipping of 200 MB 103 us without, 100 with; of 1.4 GB 654 and 648).
+// The norm asks L2 to keep the last 64 MB of a launch's tensors, from which clipping begins, and to let what
+// is before go first (norm and clipping of 200 MB 103 us without, 100 with; of 1.4 GB 654 and 648).  That helps lists
+// of one launch: of more tensors than a table holds, launches follow one another from the list's front, in the norm
+// and in clipping, so that clipping begins with what left L2 long ago.
 constexpr int kKept = (64 << 20) / (int)kChunk;
 
 // Tensors of a launch, by the room that a kernel's 32,764 bytes of arguments leave;
@@ -233,7 +235,7 @@ __global__ void __launch_bounds__(kThreads) norm_join_kernel(const double* parti
   if (threadIdx.x == 0) *norm = (float)sqrt(sum);
 }
 
-// The last chunks first: the norm's pass has left them in L2.
+// The last chunks first: where the list is one launch's, the norm's pass has left them in L2.
 template <int CAP>
 __global__ void __launch_bounds__(kThreads, kPerSm) clip_kernel(const __grid_constant__ ClipTable<CAP> t, const float* norm,
                                                                float max_norm, float eps) {
@@ -267,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) clip_kernel(const __grid_con
           }
         }
       }
-    } else {  // another phase within 16 bytes: element by element
+    } else {  // another phase within 16 bytes: element by element (1.4 GB of fp32 1237 us, against 474 of one phase)
       const int step = r.fp32 ? 4 : 2;
       const int64_t lo = r.at > r.first ? r.at : r.first, hi = r.at + kChunk < r.last ? r.at + kChunk : r.last;
       for (int64_t b = lo + (int64_t)threadIdx.x * step; b < hi; b += kThreads * step) {

@@ -19,9 +19,12 @@
 
 // Backward: element by element, one exponential each.
 //
-// Both are bound by memory traffic while rows are long and many: 4096 x 131072 bf16 (1.07 GB) forward 156 us, 6.9
-// TB/s, with entropy 166, with 20 alternatives too 192 (an exponential and some ten instructions an element, and
-// of its own a row what the joining of its threads costs); backward 308 us, 7.0 TB/s.
+// Both are bound by memory traffic while rows are long and many: 4096 x 131072 bf16 (1.07 GB) forward 156 to 160 us, 6.7
+// to 6.9 TB/s, with entropy 166 to 169, with 20 alternatives too 190 to 194 (an exponential and some ten instructions an
+// element, and of its own a row what the joining of its threads costs); backward 308 us, 7.0 TB/s.  Shorter rows pay for
+// that joining, and for alternatives' bounds, lists and ranks, more often: 8192 x 32000 bf16 90 us (5.8 TB/s), with 20
+// alternatives 114; 16384 x 4999 37 and 72; 16384 x 1000 14 and 33.  Odd rows cost the backward pass a vector a
+// thread and edges by elements: 8192 x 131071 bf16 891 us, 4.8 TB/s (131072: 611).
 
 #include <algorithm>
 #include <cmath>

@@ -94,7 +94,7 @@ tide_status tide_grad_norm(int32_t count, const void* const* tensors, const int6
                            float* norm, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* outs[i] = tensors[i] * c, c = max_norm / (norm[0] + eps) where that is
- * below 1, 1 elsewhere, and NaN where norm[0] is NaN (so +inf clips to zeros, infinite
+ * below 1 (an fp32 number), 1 elsewhere, and NaN where norm[0] is NaN (so +inf clips to zeros, infinite
  * elements to NaN).  outs[i] may be tensors[i] (all of them, then with c = 1 nothing is
  * touched); it has the same number and type of elements.  norm is read on the
  * device.  max_norm and eps are not negative and not NaN. */
